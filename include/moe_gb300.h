@@ -64,7 +64,8 @@ typedef enum {
     MOE_ERR_UNSUPPORTED = 2,
     MOE_ERR_WORKSPACE = 3,
     MOE_ERR_CUDA = 4,
-    MOE_ERR_DEVICE_TIMEOUT = 5
+    MOE_ERR_DEVICE_TIMEOUT = 5,
+    MOE_ERR_INDEX = 6
 } moe_status;
 
 /* Byte offsets of the intermediates inside the workspace (R = T*top_k).
@@ -326,9 +327,62 @@ moe_status moe_forward_mxfp4_profiled(const void* x, const void* router_w, const
 moe_status moe_pack_weights_mxfp4(const float* w13_f32, const float* w2_f32, int H, int I, int E, uint8_t* w13,
                                   uint8_t* s13, uint8_t* w2, uint8_t* s2, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Decoder-block operators beside the layer.
+ * ------------------------------------------------------------------------- */
+
+/* Element types of tensors that may have several. */
+typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2, MOE_E4M3 = 3 } moe_dtype;
+
+/*
+ * Expert choice from router logits ("GPT-OSS on Day 0", MoE routing: the
+ * scheme is what differs between models -- softmax after top-k here, softmax
+ * over all experts for others).  With l the logits of a token:
+ *   s_e = softmax(l)_e (MOE_SCORE_SOFTMAX) or 1 / (1 + exp(-l_e)) (MOE_SCORE_SIGMOID)
+ *   c_e = s_e + bias[e]                       (bias fp32 [E]; NULL: c = s)
+ *   the E experts are `groups` runs of E / groups; a group's score is the sum
+ *   of its group_top (1 or 2) largest c; the top_groups best groups stay open
+ *   (groups = 1: all open); the top_k largest c in them are chosen
+ *   w_j = s_j, divided by (sum_j s_j + 1e-20) if renormalize, times scale
+ * Ties go to the lower index (of the group, of the expert); choices are those
+ * of the formula in 64 bits.  The chosen are stored in ascending expert order.
+ * A NaN logit counts as -inf, +inf as the largest finite value; scores of a
+ * softmax row that is -inf throughout are 0.
+ * Limits: those of the layer for E and top_k; groups <= 32 divides E,
+ * group_top <= E / groups, top_groups * E / groups >= top_k.
+ */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+typedef struct {
+    int score;
+    int groups, top_groups, group_top;
+    int renormalize;
+    float scale;
+    const float* bias; /* device, fp32 [E], or NULL */
+} moe_gate;
+
+/* logits: bf16, fp16 or fp32 [T, E], rows ld elements apart (any alignment of
+ * the type's own; rows aligned to 16 bytes load fastest).  topk_idx int32 [T, top_k],
+ * topk_w fp32 [T, top_k].  Asynchronous on `stream`; no workspace. */
+moe_status moe_route_experts(const moe_gate* gate, const void* logits, int logits_dtype, int64_t ld, int T, int E,
+                             int top_k, int32_t* topk_idx, float* topk_w, void* stream);
+
+/*
+ * The layer with the experts chosen by moe_route_experts' rule from the
+ * caller's logits instead of by its own router; weights rounded to bf16 for
+ * the combine as in moe_forward.  weight_format says which packer wrote the
+ * weights and which workspace size applies (moe_workspace_size for
+ * MOE_W_BLOCK128, else moe_workspace_size_mx); everything else as in the
+ * moe_forward of that format.
+ */
+enum { MOE_W_BLOCK128 = 0, MOE_W_MXFP8 = 1, MOE_W_MXFP4 = 2 };
+moe_status moe_forward_gated(const moe_gate* gate, const void* logits, int logits_dtype, int64_t ld, const void* x,
+                             int weight_format, const uint8_t* w13, const void* s13, const void* b13,
+                             const uint8_t* w2, const void* s2, const void* b2, int T, int H, int I, int E, int top_k,
+                             void* out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then reads and clears the device error word of
- * `workspace`: MOE_OK, MOE_ERR_DEVICE_TIMEOUT (a bounded wait ran out), or
- * MOE_ERR_CUDA. */
+ * `workspace`: MOE_OK, MOE_ERR_DEVICE_TIMEOUT (a bounded wait ran out),
+ * MOE_ERR_INDEX (a page, slot or length was out of range), or MOE_ERR_CUDA. */
 moe_status moe_read_device_status(void* workspace, void* stream);
 
 /*

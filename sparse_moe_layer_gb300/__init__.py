@@ -20,10 +20,11 @@ __all__ = ["MoeError", "build", "lib", "workspace_size", "workspace_layout", "wo
            "read_device_status", "test_bounded_wait", "MoeLayer", "pad128", "pack_weights_mx",
            "pack_weights_into_mx", "s13_mx_shape", "s2_mx_shape", "unblock_scales_mx", "quantize_rows_mx",
            "pack_weights_mxfp4", "pack_weights_into_mxfp4", "w13_shape_fp4", "w2_shape_fp4", "unblock_fp4",
-           "weight_format", "route_debug", "block_weights", "read_static_scratch_status"]
+           "weight_format", "route_debug", "block_weights", "read_static_scratch_status",
+           "route_experts", "forward_gated"]
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace too small", 4: "CUDA error",
-          5: "device wait timed out"}
+          5: "device wait timed out", 6: "a page, slot or length was out of range"}
 
 
 class MoeError(RuntimeError):
@@ -51,6 +52,7 @@ def lib():
             raise RuntimeError(f"{LIB} is not built: run `python -c 'import __graft_entry__ as g; g.build()'`")
         L = ctypes.CDLL(LIB)
         vp, i32, sz, u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64
+        i64 = ctypes.c_int64
         L.moe_workspace_size.argtypes = [i32] * 5
         L.moe_workspace_size.restype = sz
         L.moe_get_workspace_layout.argtypes = [i32] * 5 + [ctypes.POINTER(_Layout)]
@@ -91,6 +93,10 @@ def lib():
         L.moe_forward_mxfp4_profiled.restype = i32
         L.moe_pack_weights_mxfp4.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, vp, vp]
         L.moe_pack_weights_mxfp4.restype = i32
+        L.moe_route_experts.argtypes = [vp, vp, i32, i64, i32, i32, i32, vp, vp, vp]
+        L.moe_route_experts.restype = i32
+        L.moe_forward_gated.argtypes = [vp, vp, i32, i64, vp, i32] + [vp] * 6 + [i32] * 5 + [vp, vp, sz, vp]
+        L.moe_forward_gated.restype = i32
         L.moe_read_device_status.argtypes = [vp, vp]
         L.moe_read_device_status.restype = i32
         L.moe_test_bounded_wait.argtypes = [u64, i32, vp, vp]
@@ -196,6 +202,19 @@ def weight_format(w13: torch.Tensor, s13: torch.Tensor) -> str:
     return "mxfp4" if w13.shape[-1] == 64 else "mxfp8"
 
 
+def _check_weights(fmt: str, w13, s13, w2, s2, E: int, H: int, I: int):
+    Hp, Ip = pad128(H), pad128(I)
+    shapes = (w13_shape_fp4(E, H, I), w2_shape_fp4(E, H, I)) if fmt == "mxfp4" else (w13_shape(E, H, I),
+                                                                                     w2_shape(E, H, I))
+    if (tuple(w13.shape), tuple(w2.shape)) != shapes:
+        raise ValueError(f"packed weight shapes {tuple(w13.shape)}, {tuple(w2.shape)} do not match H={H} I={I} E={E}")
+    if fmt != "block128":
+        if tuple(s13.shape) != s13_mx_shape(E, H, I) or tuple(s2.shape) != s2_mx_shape(E, H, I):
+            raise ValueError("MX scale atom shapes do not match")
+    elif tuple(s13.shape) != (E, 2 * Ip // 128, Hp // 128) or tuple(s2.shape) != (E, Hp // 128, Ip // 128):
+        raise ValueError("block scale shapes do not match")
+
+
 def forward(x, router_w, router_b, w13, s13, b13, w2, s2, b2, top_k: int, out=None, workspace=None, stream=None,
             events=None):
     """out [T, H] bf16 = the MoE layer applied to x [T, H] bf16.
@@ -209,18 +228,9 @@ def forward(x, router_w, router_b, w13, s13, b13, w2, s2, b2, top_k: int, out=No
     T, H = x.shape
     E = router_w.shape[0]
     I = b13.shape[1] // 2
-    Hp, Ip = pad128(H), pad128(I)
     fmt = weight_format(w13, s13)
     mx = fmt != "block128"
-    shapes = (w13_shape_fp4(E, H, I), w2_shape_fp4(E, H, I)) if fmt == "mxfp4" else (w13_shape(E, H, I),
-                                                                                     w2_shape(E, H, I))
-    if (tuple(w13.shape), tuple(w2.shape)) != shapes:
-        raise ValueError(f"packed weight shapes {tuple(w13.shape)}, {tuple(w2.shape)} do not match H={H} I={I} E={E}")
-    if mx:
-        if tuple(s13.shape) != s13_mx_shape(E, H, I) or tuple(s2.shape) != s2_mx_shape(E, H, I):
-            raise ValueError("MX scale atom shapes do not match")
-    elif tuple(s13.shape) != (E, 2 * Ip // 128, Hp // 128) or tuple(s2.shape) != (E, Hp // 128, Ip // 128):
-        raise ValueError("block scale shapes do not match")
+    _check_weights(fmt, w13, s13, w2, s2, E, H, I)
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
     if workspace is None:
@@ -461,6 +471,84 @@ def test_bounded_wait(timeout_ns: int, arrivals: int, stream=None) -> int:
            "moe_test_bounded_wait")
     torch.cuda.synchronize()
     return int(r.item())
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.uint8: 3}
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_FORMATS = {"block128": 0, "mxfp8": 1, "mxfp4": 2}
+
+
+class _Gate(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("groups", ctypes.c_int), ("top_groups", ctypes.c_int),
+                ("group_top", ctypes.c_int), ("renormalize", ctypes.c_int), ("scale", ctypes.c_float),
+                ("bias", ctypes.c_void_p)]
+
+
+def _gate(logits, score, bias, groups, top_groups, group_top, renormalize, scale):
+    """Checked logits and gate: (moe_gate, logits dtype code, T, E)."""
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    dt = _DTYPES.get(logits.dtype, 3)
+    if dt == 3:
+        raise ValueError(f"logits must be bf16, fp16 or fp32, got {logits.dtype}")
+    if logits.dim() != 2 or logits.stride(1) != 1:
+        raise ValueError("logits must be [T, E] with contiguous rows")
+    T, E = logits.shape
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    if bias is not None:
+        if tuple(bias.shape) != (E,):
+            raise ValueError("bias must be [E]")
+        bias = _dev(bias, torch.float32, "bias")
+    return _Gate(_SCORES[score], groups, top_groups, group_top, renormalize, scale, bias), dt, T, E
+
+
+def route_experts(logits, top_k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+                  group_top: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None):
+    """Expert choice from router logits [T, E] (bf16, fp16 or fp32; rows may be strided):
+    (topk_idx [T, k] int32 ascending, topk_w [T, k] fp32).
+
+    score "softmax" (over all experts) or "sigmoid"; bias [E] fp32 moves the choice, not the
+    weights; with groups > 1 only the top_groups groups with the largest sum of their
+    group_top (1 or 2) best choices stay open; renormalize divides the weights by their sum.
+    The defaults are the layer's own rule, softmax over the chosen logits.  Ties go to the
+    lower index."""
+    g, dt, T, E = _gate(logits, score, bias, groups, top_groups, group_top, renormalize, scale)
+    idx = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+    w = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+    if T:
+        _check(lib().moe_route_experts(ctypes.byref(g), logits.data_ptr(), dt, logits.stride(0) if T > 1 else E, T, E,
+                                       top_k, idx.data_ptr(), w.data_ptr(), _stream(stream)), "moe_route_experts")
+    return idx, w
+
+
+def forward_gated(x, logits, w13, s13, b13, w2, s2, b2, top_k: int, score: str = "softmax", bias=None, groups: int = 1,
+                  top_groups: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0, out=None,
+                  workspace=None, stream=None):
+    """The layer (`forward`) with the experts chosen from the caller's logits [T, E] by the rule of
+    `route_experts`; weights of any of the three formats."""
+    g, dt, T, E = _gate(logits, score, bias, groups, top_groups, group_top, renormalize, scale)
+    H, I = x.shape[1], b13.shape[1] // 2
+    fmt = weight_format(w13, s13)
+    mx = fmt != "block128"
+    if x.shape[0] != T:
+        raise ValueError("x and logits must have the same number of tokens")
+    _check_weights(fmt, w13, s13, w2, s2, E, H, I)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    if T == 0:
+        return out
+    if workspace is None:
+        workspace = new_workspace(T, H, I, E, top_k, x.device, mx)
+    sdt = torch.uint8 if mx else torch.float32
+    _check(lib().moe_forward_gated(ctypes.byref(g), logits.data_ptr(), dt, logits.stride(0) if T > 1 else E,
+                                   _dev(x, torch.bfloat16, "x"), _FORMATS[fmt], _dev(w13, torch.uint8, "w13"),
+                                   _dev(s13, sdt, "s13"), _dev(b13, torch.bfloat16, "b13"),
+                                   _dev(w2, torch.uint8, "w2"), _dev(s2, sdt, "s2"), _dev(b2, torch.bfloat16, "b2"),
+                                   T, H, I, E, top_k, _dev(out, torch.bfloat16, "out"),
+                                   _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)),
+           "moe_forward_gated")
+    return out
 
 
 class MoeLayer:

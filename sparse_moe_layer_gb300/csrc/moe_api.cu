@@ -141,7 +141,7 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 // Weight formats of forward_impl.
-enum WeightFormat { kBlock128 = 0, kMxfp8 = 1, kMxfp4 = 2 };
+enum WeightFormat { kBlock128 = MOE_W_BLOCK128, kMxfp8 = MOE_W_MXFP8, kMxfp4 = MOE_W_MXFP4 };
 
 }  // namespace
 
@@ -164,13 +164,53 @@ struct RoutingBuffers {
     float* sx;            // [Hp/128, R] (MXFP8: scale atoms)
 };
 
+// What the gate kernel needs in place of the router.
+struct GateInput {
+    const void* logits;
+    int dtype;
+    size_t ld_bytes;
+    const moe_gate* gate;
+};
+
+static bool gate_ok(const moe_gate* g, int E, int k) {
+    if (g->score != MOE_SCORE_SOFTMAX && g->score != MOE_SCORE_SIGMOID) return false;
+    if (g->groups < 1 || g->groups > 32 || E % g->groups) return false;
+    if (g->top_groups < 1 || g->top_groups > g->groups) return false;
+    if (g->group_top < 1 || g->group_top > 2 || g->group_top > E / g->groups) return false;
+    return g->top_groups * (E / g->groups) >= k && g->scale == g->scale;
+}
+
+static GateParams gate_params(const GateInput& in, int T, int E, int k) {
+    GateParams p;
+    memset(&p, 0, sizeof(p));
+    p.logits = in.logits;
+    p.ld_bytes = in.ld_bytes;
+    p.T = T;
+    p.E = E;
+    p.k = k;
+    p.score = in.gate->score;
+    p.bias = in.gate->bias;
+    p.groups = in.gate->groups;
+    p.top_groups = in.gate->top_groups;
+    p.group_top = in.gate->group_top;
+    p.renorm = in.gate->renormalize != 0;
+    p.scale = in.gate->scale;
+    return p;
+}
+
+// Bytes of a logit element, 0 for a type the gate does not read.
+static int logit_bytes(int dtype) {
+    return dtype == MOE_FP32 ? 4 : (dtype == MOE_BF16 || dtype == MOE_FP16 ? 2 : 0);
+}
+
 // Steps a1-a4 on `st`: the status words and the histogram cleared, the router
-// (top-k, softmax, per-chunk expert histogram), then the permutation with the
+// (top-k, softmax, per-chunk expert histogram; with `gate`, the gate kernel on
+// the caller's logits), then the permutation with the
 // x quantisation (1x128, or 1x32 MX when mx).  bm, nt1, nt2 size the GEMM tile
 // lists the scan writes.  `mid` (optional) is recorded between the two kernels.
 static moe_status launch_routing(const void* x, const void* router_w, const void* router_b, int T, int H, int E,
                                  int top_k, int bm, int nt1, int nt2, bool mx, const RoutingBuffers& b,
-                                 cudaStream_t st, cudaEvent_t mid) {
+                                 cudaStream_t st, cudaEvent_t mid, const GateInput* gate = nullptr) {
     const int Hp = pad128(H);
     const int nch = (T + kChunkTokens - 1) / kChunkTokens;
     // status words, the (chunk, expert) histogram with its arrival counter, and
@@ -199,8 +239,13 @@ static moe_status launch_routing(const void* x, const void* router_w, const void
     rp.tiles1 = b.tiles1;
     rp.tiles2 = b.tiles2;
     rp.status = b.status;
+    if (gate) {
+        GateParams gp = gate_params(*gate, T, E, top_k);
+        gp.r = rp;
+        if (launch_gate(gp, gate->dtype, st) != cudaSuccess) return MOE_ERR_CUDA;
+    }
     // large batches with 16-byte aligned rows: the tensor-core router
-    if (const int np = router_tc_experts(T, H, E)) {
+    else if (const int np = router_tc_experts(T, H, E)) {
         CUtensorMap tmX, tmW;
         if (!make_map_bf16(&tmX, x, T, H, 128) || !make_map_bf16(&tmW, router_w, E, H, (uint32_t)np))
             return MOE_ERR_CUDA;
@@ -256,7 +301,8 @@ static int decode_down_pairs(int RB, int active, int sms) {
 static moe_status forward_impl(const void* x, const void* router_w, const void* router_b, const uint8_t* w13,
                                const void* s13, const void* b13, const uint8_t* w2, const void* s2, const void* b2,
                                int T, int H, int I, int E, int top_k, void* out, void* workspace,
-                               size_t workspace_bytes, void* stream, void* const* ev, int fmt = kBlock128);
+                               size_t workspace_bytes, void* stream, void* const* ev, int fmt = kBlock128,
+                               const GateInput* gate = nullptr);
 
 extern "C" {
 
@@ -347,12 +393,13 @@ moe_status moe_forward_mxfp4_profiled(const void* x, const void* router_w, const
 static moe_status forward_impl(const void* x, const void* router_w, const void* router_b, const uint8_t* w13,
                                const void* s13, const void* b13, const uint8_t* w2, const void* s2, const void* b2,
                                int T, int H, int I, int E, int top_k, void* out, void* workspace,
-                               size_t workspace_bytes, void* stream, void* const* ev, int fmt) {
+                               size_t workspace_bytes, void* stream, void* const* ev, int fmt,
+                               const GateInput* gate) {
     const bool mx = fmt != kBlock128;
     auto mark = [&](int i) {
         if (ev) cudaEventRecord(static_cast<cudaEvent_t>(ev[i]), static_cast<cudaStream_t>(stream));
     };
-    if (!x || !router_w || !router_b || !w13 || !s13 || !b13 || !w2 || !s2 || !b2 || !out || !workspace)
+    if (!x || (!gate && (!router_w || !router_b)) || !w13 || !s13 || !b13 || !w2 || !s2 || !b2 || !out || !workspace)
         return MOE_ERR_INVALID_ARG;
     if (!sizes_ok(T, H, I, E, top_k)) return MOE_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(router_w) || !aligned16(w13) || !aligned16(w2) || !aligned16(out) ||
@@ -400,7 +447,7 @@ static moe_status forward_impl(const void* x, const void* router_w, const void* 
     rb.sx = reinterpret_cast<float*>(ws + L.sx);
     {
         const moe_status rs = launch_routing(x, router_w, router_b, T, H, E, top_k, bm, nt1, nt2, mx, rb, st,
-                                             ev ? static_cast<cudaEvent_t>(ev[1]) : nullptr);
+                                             ev ? static_cast<cudaEvent_t>(ev[1]) : nullptr, gate);
         if (rs != MOE_OK) return rs;
     }
     mark(2);
@@ -705,6 +752,47 @@ extern "C" moe_status moe_block_weights(const uint8_t* w13_rm, const uint8_t* w2
     return MOE_OK;
 }
 
+// Checks shared by the two gate entry points; *elem_bytes gets the logit's size.
+static moe_status check_gate(const moe_gate* gate, const void* logits, int dtype, int64_t ld, int T, int E, int top_k,
+                             int* elem_bytes) {
+    if (!gate || !logits) return MOE_ERR_INVALID_ARG;
+    if (!sizes_ok(T, 1, 1, E, top_k) || ld < E || ld > (int64_t)1 << 31 || !gate_ok(gate, E, top_k))
+        return MOE_ERR_INVALID_ARG;
+    *elem_bytes = logit_bytes(dtype);
+    if (!*elem_bytes) return MOE_ERR_UNSUPPORTED;
+    if (reinterpret_cast<uintptr_t>(logits) % *elem_bytes || (reinterpret_cast<uintptr_t>(gate->bias) & 3u))
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+extern "C" moe_status moe_route_experts(const moe_gate* gate, const void* logits, int logits_dtype, int64_t ld, int T,
+                                        int E, int top_k, int32_t* topk_idx, float* topk_w, void* stream) {
+    int bytes = 0;
+    const moe_status cs = check_gate(gate, logits, logits_dtype, ld, T, E, top_k, &bytes);
+    if (cs != MOE_OK) return cs;
+    if (!topk_idx || !topk_w) return MOE_ERR_INVALID_ARG;
+    const GateInput in = {logits, logits_dtype, (size_t)ld * bytes, gate};
+    GateParams p = gate_params(in, T, E, top_k);
+    p.r.topk_idx = topk_idx;
+    p.r.topk_w = topk_w;
+    return launch_gate(p, logits_dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+extern "C" moe_status moe_forward_gated(const moe_gate* gate, const void* logits, int logits_dtype, int64_t ld,
+                                        const void* x, int weight_format, const uint8_t* w13, const void* s13,
+                                        const void* b13, const uint8_t* w2, const void* s2, const void* b2, int T,
+                                        int H, int I, int E, int top_k, void* out, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+    int bytes = 0;
+    const moe_status cs = check_gate(gate, logits, logits_dtype, ld, T, E, top_k, &bytes);
+    if (cs != MOE_OK) return cs;
+    if (weight_format != MOE_W_BLOCK128 && weight_format != MOE_W_MXFP8 && weight_format != MOE_W_MXFP4)
+        return MOE_ERR_INVALID_ARG;
+    const GateInput in = {logits, logits_dtype, (size_t)ld * bytes, gate};
+    return forward_impl(x, nullptr, nullptr, w13, s13, b13, w2, s2, b2, T, H, I, E, top_k, out, workspace,
+                        workspace_bytes, stream, nullptr, weight_format, &in);
+}
+
 extern "C" {
 
 moe_status moe_pack_weights(const float* w13_f32, const float* w2_f32, int H, int I, int E, uint8_t* w13, float* s13,
@@ -775,6 +863,7 @@ moe_status moe_read_device_status(void* workspace, void* stream) {
     uint32_t word = 0;
     if (cudaMemcpy(&word, workspace, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
     if (cudaMemset(workspace, 0, 4) != cudaSuccess) return MOE_ERR_CUDA;
+    if (word & kErrBadIndex) return MOE_ERR_INDEX;
     return word ? MOE_ERR_DEVICE_TIMEOUT : MOE_OK;
 }
 
@@ -793,6 +882,7 @@ const char* moe_status_str(moe_status s) {
         case MOE_ERR_WORKSPACE: return "workspace too small";
         case MOE_ERR_CUDA: return "CUDA launch or runtime error";
         case MOE_ERR_DEVICE_TIMEOUT: return "a bounded device-side wait timed out";
+        case MOE_ERR_INDEX: return "a page, slot or length was out of range";
     }
     return "unknown status";
 }

@@ -22,7 +22,7 @@ enum : int {
     kStatusTileRows = 3,
     kStatusWords = 64
 };
-enum : uint32_t { kErrTimeoutProducer = 1u, kErrTimeoutMma = 2u, kErrTimeoutEpilogue = 4u };
+enum : uint32_t { kErrTimeoutProducer = 1u, kErrTimeoutMma = 2u, kErrTimeoutEpilogue = 4u, kErrBadIndex = 8u };
 
 // ------------------------------------------------------------ conversion ----
 __device__ __forceinline__ float bf16_bits_to_f32(uint16_t b) { return __uint_as_float(((uint32_t)b) << 16); }

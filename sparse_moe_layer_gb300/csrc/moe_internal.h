@@ -33,6 +33,24 @@ struct RouteParams {
     uint32_t* status;
 };
 
+// Element types of the tensors that may have several (the moe_dtype of the C ABI).
+enum : int { kDtBf16 = 0, kDtFp16 = 1, kDtFp32 = 2, kDtE4m3 = 3 };
+
+// The gate kernel: expert choice from logits.  r: topk_idx and topk_w, and for
+// the layer's routing step (hist non-null) everything a router writes.
+struct GateParams {
+    const void* logits;  // [T, E], rows ld_bytes apart
+    size_t ld_bytes;
+    int T, E, k;
+    int score;  // 0 softmax, 1 sigmoid
+    const float* bias;  // [E] or null
+    int groups, top_groups, group_top;
+    int renorm;
+    float scale;
+    int vec, gsize, lanes_per_group;  // set at launch
+    RouteParams r;
+};
+
 struct PermuteParams {
     const uint16_t* x;
     int T, H, Hp, E, k;
@@ -156,6 +174,7 @@ cudaError_t launch_router(const RouteParams& p, cudaStream_t st);
 // 64 x NP boxes (128-byte swizzle).
 int router_tc_experts(int T, int H, int E);
 cudaError_t launch_router_tc(const RouteParams& p, const CUtensorMap& tmX, const CUtensorMap& tmW, cudaStream_t st);
+cudaError_t launch_gate(const GateParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_permute_quant(const PermuteParams& p, cudaStream_t st);
 cudaError_t launch_combine(const float* part, int T, int H, int ldp, int k, uint16_t* out, int num_sms,
                            cudaStream_t st);
