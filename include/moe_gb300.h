@@ -380,6 +380,51 @@ moe_status moe_forward_gated(const moe_gate* gate, const void* logits, int logit
                              const uint8_t* w2, const void* s2, const void* b2, int T, int H, int I, int E, int top_k,
                              void* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * A paged key-value cache: key (value) d of head h at slot t of page p is
+ * element p * stride[0] + h * stride[1] + t * stride[2] + d.  Any order of
+ * pages, heads and tokens ("Hosting Qwen on Blackwell" keeps it heads-major,
+ * tokens contiguous: [pages, heads, page_size, head_dim]).  dtype MOE_BF16,
+ * MOE_FP16, or MOE_E4M3: codes with one fp32 scale per token and head (of k
+ * and of v, both with scale_stride), value = code * scale.
+ * Limits: head_dim a multiple of 16 up to 256; 1 <= kv_heads <= 256; num_pages *
+ * page_size < 2^31; pointers and strides multiples of 16 bytes (scales: 4).
+ */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t k_stride[3], v_stride[3], scale_stride[3];
+    int dtype, num_pages, page_size, kv_heads, head_dim;
+} moe_kv_cache;
+
+/*
+ * Rotation by position and append to a paged cache ("GPT-OSS on Day 0",
+ * architecture list: rotary positions, YaRN).  For each of N tokens, with
+ * a_i = positions[n] * inv_freq[i] (64 bits) and pairs (x_i, y_i) of the
+ * first rot_dim dims of every head of q and k -- (i, i + rot_dim/2), or with
+ * `neighbours` (2i, 2i+1) --
+ *   (x_i, y_i) -> rope_scale (x_i cos a_i - y_i sin a_i, x_i sin a_i + y_i cos a_i)
+ * in fp32; the other dims of q and k, and v, stay as they are.  q_out gets the
+ * rotated q (it may be q itself); k and v go to slot slots[n] = page *
+ * page_size + place of the cache.  An e4m3 cache gets s = amax / 448 (1 for an
+ * all-zero head) and e4m3(value / s) of the fp32 values (moe_quantize_rows on
+ * a head).  A negative slot appends nothing; one past the last page neither,
+ * and sets the error word.  Slots of one call are distinct.
+ *   q [N, q_heads, D], k and v [N, kv_heads, D]: bf16 or fp16 (`dtype`, that of a
+ *   16-bit cache), strides in elements between tokens and heads, D contiguous;
+ *   positions, slots int64 [N]; inv_freq fp64 [rot_dim / 2]
+ *   status: a device error word for moe_read_device_status, or NULL
+ * Limits: rot_dim a multiple of 16, at most head_dim; 1 <= q_heads <= 4096;
+ * pointers and strides multiples of 16 bytes.  Asynchronous on `stream`.
+ */
+moe_status moe_rotate_append(const moe_kv_cache* cache, const void* q, const void* k, const void* v, int dtype,
+                             int64_t q_token, int64_t q_head, int64_t k_token, int64_t k_head, int64_t v_token,
+                             int64_t v_head, const int64_t* positions, const int64_t* slots, const double* inv_freq,
+                             int rot_dim, int neighbours, float rope_scale, int N, int q_heads, void* q_out,
+                             int64_t out_token, int64_t out_head, uint32_t* status, void* stream);
+
 /* Synchronises `stream`, then reads and clears the device error word of
  * `workspace`: MOE_OK, MOE_ERR_DEVICE_TIMEOUT (a bounded wait ran out),
  * MOE_ERR_INDEX (a page, slot or length was out of range), or MOE_ERR_CUDA. */

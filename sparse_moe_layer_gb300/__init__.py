@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -21,7 +22,7 @@ __all__ = ["MoeError", "build", "lib", "workspace_size", "workspace_layout", "wo
            "pack_weights_into_mx", "s13_mx_shape", "s2_mx_shape", "unblock_scales_mx", "quantize_rows_mx",
            "pack_weights_mxfp4", "pack_weights_into_mxfp4", "w13_shape_fp4", "w2_shape_fp4", "unblock_fp4",
            "weight_format", "route_debug", "block_weights", "read_static_scratch_status",
-           "route_experts", "forward_gated"]
+           "route_experts", "forward_gated", "rotate_append", "new_status"]
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace too small", 4: "CUDA error",
           5: "device wait timed out", 6: "a page, slot or length was out of range"}
@@ -97,6 +98,10 @@ def lib():
         L.moe_route_experts.restype = i32
         L.moe_forward_gated.argtypes = [vp, vp, i32, i64, vp, i32] + [vp] * 6 + [i32] * 5 + [vp, vp, sz, vp]
         L.moe_forward_gated.restype = i32
+        f32 = ctypes.c_float
+        L.moe_rotate_append.argtypes = [vp] * 4 + [i32] + [i64] * 6 + [vp] * 3 + [i32, i32, f32, i32, i32, vp, i64, i64,
+                                                                                vp, vp]
+        L.moe_rotate_append.restype = i32
         L.moe_read_device_status.argtypes = [vp, vp]
         L.moe_read_device_status.restype = i32
         L.moe_test_bounded_wait.argtypes = [u64, i32, vp, vp]
@@ -549,6 +554,93 @@ def forward_gated(x, logits, w13, s13, b13, w2, s2, b2, top_k: int, score: str =
                                    _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)),
            "moe_forward_gated")
     return out
+
+
+_KV = struct.Struct("4P9q5i4x")  # moe_kv_cache
+
+
+def new_status(device=None) -> torch.Tensor:
+    """A zeroed device error word for `rotate_append` and `paged_attention` (read it with `read_device_status`)."""
+    return torch.zeros(4, dtype=torch.uint8, device=device or "cuda")
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale):
+    """Checked cache tensors [pages, heads, page, D]: (moe_kv_cache, heads, page, D, dtype code)."""
+    dt = _DTYPES.get(k_cache.dtype, 2)
+    if not k_cache.is_cuda or not v_cache.is_cuda:
+        raise ValueError("k_cache and v_cache must be CUDA tensors")
+    if dt == 2 or v_cache.dtype != k_cache.dtype:
+        raise ValueError(f"k_cache and v_cache must both be bf16, fp16 or uint8 (e4m3 codes), got {k_cache.dtype}, "
+                         f"{v_cache.dtype}")
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must both be [pages, heads, page, D]")
+    ks, vs = k_cache.stride(), v_cache.stride()
+    if ks[3] != 1 or vs[3] != 1:
+        raise ValueError("the last dim of k_cache and v_cache must be contiguous")
+    kp = vp = 0
+    ss = (0, 0, 0)
+    if dt == 3:
+        if k_scale is None or v_scale is None or k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 \
+                or not k_scale.is_cuda or not v_scale.is_cuda:
+            raise ValueError("an e4m3 cache needs k_scale and v_scale, fp32 CUDA tensors")
+        ss = k_scale.stride()
+        if k_scale.shape != shape[:3] or v_scale.shape != shape[:3] or v_scale.stride() != ss:
+            raise ValueError("k_scale and v_scale must be [pages, heads, page] with equal strides")
+        kp, vp = k_scale.data_ptr(), v_scale.data_ptr()
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("scales belong to an e4m3 cache (uint8)")
+    P, H, S, D = shape
+    return (_KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), kp, vp, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], *ss, dt,
+                     P, S, H, D), H, S, D, dt)
+
+
+def _index(t, n: int, dtype, name: str) -> int:
+    if not t.is_cuda or t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor [{n}]")
+    return t.data_ptr()
+
+
+def _status_ptr(status):
+    return None if status is None else _dev(status, torch.uint8, "status")
+
+
+def rotate_append(q, k, v, positions, slots, k_cache, v_cache, inv_freq, k_scale=None, v_scale=None,
+                  interleaved: bool = False, rope_scale: float = 1.0, q_out=None, status=None, stream=None):
+    """Rotate q [N, Hq, D] and k [N, Hkv, D] by position and append k and v to a paged cache; returns
+    the rotated q (a new tensor, or `q_out`, which may be q itself).
+
+    q, k, v: bf16 or fp16, last dim contiguous (views of a fused projection are fine).  positions,
+    slots int64 [N]; slot = page * page_size + place, negative: not appended.  Cache [pages, Hkv,
+    page, D] of the same type, or uint8 (e4m3 codes) with k_scale, v_scale fp32 [pages, Hkv, page];
+    any strides with the last dim contiguous.  inv_freq fp64 [R / 2] rotates the first R dims, in
+    pairs (i, i + R/2) or, interleaved, (2i, 2i + 1); cos and sin are multiplied by rope_scale.
+    status (`new_status`): set by a slot past the last page."""
+    kv, Hkv, _, D, cdt = _cache(k_cache, v_cache, k_scale, v_scale)
+    if not (q.is_cuda and k.is_cuda and v.is_cuda):
+        raise ValueError("q, k and v must be CUDA tensors")
+    dt = _DTYPES.get(q.dtype, 3)
+    if dt > 1 or k.dtype != q.dtype or v.dtype != q.dtype or (cdt != 3 and cdt != dt):
+        raise ValueError("q, k and v must be bf16 or fp16 alike, and a 16-bit cache of their type")
+    N, Hq = q.shape[0], q.shape[1]
+    if q.dim() != 3 or q.shape[2] != D or k.shape != (N, Hkv, D) or v.shape != (N, Hkv, D):
+        raise ValueError(f"q must be [N, Hq, {D}], k and v [N, {Hkv}, {D}]")
+    if q_out is None:
+        q_out = torch.empty((N, Hq, D), dtype=q.dtype, device=q.device)
+    elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_cuda:
+        raise ValueError("q_out must be like q")
+    qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), q_out.stride()
+    if qs[2] != 1 or ks[2] != 1 or vs[2] != 1 or os_[2] != 1:
+        raise ValueError("the last dim of q, k, v and q_out must be contiguous")
+    if inv_freq.dtype != torch.float64 or not inv_freq.is_cuda or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous fp64 CUDA tensor")
+    pos, sl = _index(positions, N, torch.int64, "positions"), _index(slots, N, torch.int64, "slots")
+    if N:
+        _check(lib().moe_rotate_append(kv, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, qs[0], qs[1], ks[0], ks[1],
+                                       vs[0], vs[1], pos, sl, inv_freq.data_ptr(), 2 * inv_freq.numel(), interleaved,
+                                       rope_scale, N, Hq, q_out.data_ptr(), os_[0], os_[1], _status_ptr(status),
+                                       _stream(stream)), "moe_rotate_append")
+    return q_out
 
 
 class MoeLayer:

@@ -793,6 +793,96 @@ extern "C" moe_status moe_forward_gated(const moe_gate* gate, const void* logits
                         workspace_bytes, stream, nullptr, weight_format, &in);
 }
 
+// Checks of a paged cache; *out gets its device form.
+static moe_status check_cache(const moe_kv_cache* c, KvCache* out) {
+    if (!c || !c->k || !c->v) return MOE_ERR_INVALID_ARG;
+    if (c->num_pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->kv_heads > 256) return MOE_ERR_INVALID_ARG;
+    if ((long long)c->num_pages * c->page_size >= (1LL << 31)) return MOE_ERR_INVALID_ARG;
+    if (c->head_dim < 16 || c->head_dim > 256 || c->head_dim % 16) return MOE_ERR_INVALID_ARG;
+    if (c->dtype != MOE_BF16 && c->dtype != MOE_FP16 && c->dtype != MOE_E4M3) return MOE_ERR_UNSUPPORTED;
+    const bool e4m3 = c->dtype == MOE_E4M3;
+    if (e4m3 && (!c->k_scale || !c->v_scale)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(c->k) || !aligned16(c->v)) return MOE_ERR_UNSUPPORTED;
+    if (e4m3 && ((reinterpret_cast<uintptr_t>(c->k_scale) | reinterpret_cast<uintptr_t>(c->v_scale)) & 3u))
+        return MOE_ERR_UNSUPPORTED;
+    out->k = c->k;
+    out->v = c->v;
+    out->k_scale = e4m3 ? c->k_scale : nullptr;
+    out->v_scale = e4m3 ? c->v_scale : nullptr;
+    const int el = e4m3 ? 16 : 8;  // elements in 16 bytes
+    const int extent[3] = {c->num_pages, c->kv_heads, c->page_size};
+    long long* ks[3] = {&out->k_page, &out->k_head, &out->k_token};
+    long long* vs[3] = {&out->v_page, &out->v_head, &out->v_token};
+    long long* ss[3] = {&out->s_page, &out->s_head, &out->s_token};
+    for (int i = 0; i < 3; ++i) {
+        *ks[i] = *vs[i] = *ss[i] = 0;
+        if (extent[i] == 1) continue;  // a dim of one has no stride
+        if (c->k_stride[i] < 0 || c->v_stride[i] < 0 || (e4m3 && c->scale_stride[i] < 0)) return MOE_ERR_INVALID_ARG;
+        if (c->k_stride[i] % el || c->v_stride[i] % el) return MOE_ERR_UNSUPPORTED;
+        *ks[i] = c->k_stride[i];
+        *vs[i] = c->v_stride[i];
+        if (e4m3) *ss[i] = c->scale_stride[i];
+    }
+    return MOE_OK;
+}
+
+// Element strides of n tokens (rows) and h heads: MOE_OK with dims of one set to 0.
+static moe_status check_strides(int n, int h, int64_t* token, int64_t* head) {
+    if (n == 1) *token = 0;
+    if (h == 1) *head = 0;
+    if (*token < 0 || *head < 0) return MOE_ERR_INVALID_ARG;
+    return *token % 8 || *head % 8 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+extern "C" moe_status moe_rotate_append(const moe_kv_cache* cache, const void* q, const void* k, const void* v,
+                                        int dtype, int64_t q_token, int64_t q_head, int64_t k_token, int64_t k_head,
+                                        int64_t v_token, int64_t v_head, const int64_t* positions,
+                                        const int64_t* slots, const double* inv_freq, int rot_dim, int neighbours,
+                                        float rope_scale, int N, int q_heads, void* q_out, int64_t out_token,
+                                        int64_t out_head, uint32_t* status, void* stream) {
+    AppendParams p;
+    memset(&p, 0, sizeof(p));
+    const moe_status cs = check_cache(cache, &p.cache);
+    if (cs != MOE_OK) return cs;
+    if (!q || !k || !v || !positions || !slots || !q_out || N < 1 || q_heads < 1 || q_heads > 4096)
+        return MOE_ERR_INVALID_ARG;
+    if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 16 || (rot_dim && !inv_freq)) return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_BF16 && dtype != MOE_FP16) return MOE_ERR_UNSUPPORTED;
+    if (cache->dtype != MOE_E4M3 && cache->dtype != dtype) return MOE_ERR_UNSUPPORTED;
+    const moe_status ss[] = {check_strides(N, q_heads, &q_token, &q_head), check_strides(N, cache->kv_heads, &k_token, &k_head),
+                             check_strides(N, cache->kv_heads, &v_token, &v_head),
+                             check_strides(N, q_heads, &out_token, &out_head)};
+    for (moe_status e : ss)
+        if (e != MOE_OK) return e;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out)) return MOE_ERR_UNSUPPORTED;
+    if (((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slots) |
+          reinterpret_cast<uintptr_t>(inv_freq)) & 7u) || (reinterpret_cast<uintptr_t>(status) & 3u))
+        return MOE_ERR_UNSUPPORTED;
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = static_cast<const uint16_t*>(k);
+    p.v = static_cast<const uint16_t*>(v);
+    p.q_out = static_cast<uint16_t*>(q_out);
+    p.q_token = q_token, p.q_head = q_head, p.k_token = k_token, p.k_head = k_head;
+    p.v_token = v_token, p.v_head = v_head, p.o_token = out_token, p.o_head = out_head;
+    p.positions = positions;
+    p.slots = slots;
+    p.inv_freq = inv_freq;
+    p.N = N;
+    p.Hq = q_heads;
+    p.Hkv = cache->kv_heads;
+    p.D = cache->head_dim;
+    p.rot = rot_dim;
+    p.neighbours = neighbours != 0;
+    p.rope_scale = rope_scale;
+    p.num_pages = cache->num_pages;
+    p.page_size = cache->page_size;
+    p.status = status;
+    return launch_rotate_append(p, dtype == MOE_FP16, cache->dtype == MOE_E4M3, num_sms(),
+                                static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
 extern "C" {
 
 moe_status moe_pack_weights(const float* w13_f32, const float* w2_f32, int H, int I, int E, uint8_t* w13, float* s13,

@@ -51,6 +51,35 @@ struct GateParams {
     RouteParams r;
 };
 
+// A paged key-value cache on the device; strides in elements.
+struct KvCache {
+    void* k;
+    void* v;
+    float* k_scale;  // e4m3 caches: [pages, heads, page], else null
+    float* v_scale;
+    long long k_page, k_head, k_token;
+    long long v_page, v_head, v_token;
+    long long s_page, s_head, s_token;  // of both scales
+};
+
+struct AppendParams {
+    const uint16_t* q;  // [N, Hq, D], [N, Hkv, D] twice; strides in elements, D contiguous
+    const uint16_t* k;
+    const uint16_t* v;
+    uint16_t* q_out;
+    long long q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
+    const int64_t* positions;  // [N]
+    const int64_t* slots;      // [N]; < 0: not appended
+    const double* inv_freq;    // [rot / 2]
+    int N, Hq, Hkv, D, rot;
+    int neighbours;  // pairs (2i, 2i+1) instead of (i, i + rot/2)
+    float rope_scale;
+    int num_pages, page_size;
+    KvCache cache;
+    uint32_t* status;                // error word or null
+    int lpr_shift, tokens_per_cta;   // set at launch
+};
+
 struct PermuteParams {
     const uint16_t* x;
     int T, H, Hp, E, k;
@@ -175,6 +204,7 @@ cudaError_t launch_router(const RouteParams& p, cudaStream_t st);
 int router_tc_experts(int T, int H, int E);
 cudaError_t launch_router_tc(const RouteParams& p, const CUtensorMap& tmX, const CUtensorMap& tmW, cudaStream_t st);
 cudaError_t launch_gate(const GateParams& p, int dtype, cudaStream_t st);
+cudaError_t launch_rotate_append(const AppendParams& p, bool fp16, bool e4m3, int sms, cudaStream_t st);
 cudaError_t launch_permute_quant(const PermuteParams& p, cudaStream_t st);
 cudaError_t launch_combine(const float* part, int T, int H, int ldp, int k, uint16_t* out, int num_sms,
                            cudaStream_t st);
