@@ -425,6 +425,37 @@ moe_status moe_rotate_append(const moe_kv_cache* cache, const void* q, const voi
                              int rot_dim, int neighbours, float rope_scale, int N, int q_heads, void* q_out,
                              int64_t out_token, int64_t out_head, uint32_t* status, void* stream);
 
+/*
+ * Attention of one new token per sequence over a paged cache ("GPT-OSS on Day
+ * 0": grouped heads, sink attention, sliding windows).  For sequence b and
+ * query head i, key head i / (q_heads / kv_heads), over the tokens t in
+ * [max(0, lengths[b] - window), lengths[b]) (window 0: from 0):
+ *   s_t = scale * q . k_t
+ *   out = sum_t exp(s_t) v_t / (sum_t exp(s_t) + exp(sinks[i]))
+ * (NULL sinks: no such term), fp32 statistics and sums; the probabilities are
+ * rounded to the cache's 16-bit type (e4m3: fp16) for the product with v.
+ * Token t of sequence b is at place t % page_size of page
+ * page_table[b * table_ld + t / page_size]; entries past the length are not
+ * read, nor are the cache's unused places.  No tokens: out is 0.  A length
+ * outside [0, table_width * page_size] is brought into it, and a token on a page
+ * outside [0, num_pages) is left out; both set the error word.
+ *   q [B, q_heads, D] bf16 or fp16 (`dtype`; that of a 16-bit cache), strides in
+ *   elements, D contiguous; out likewise; page_table, lengths int32; sinks fp32
+ *   workspace: moe_attention_workspace_size bytes, 256-byte aligned, any contents;
+ *   calls that may overlap need one each
+ *   status: a device error word for moe_read_device_status, or NULL
+ * Limits: those of the cache; q_heads a multiple of kv_heads, at most 4096;
+ * 1 <= B <= 65536, B * q_heads < 2^27; table_width * page_size < 2^31; q and out:
+ * pointers and strides multiples of 4 bytes.  The result is the same for every
+ * run of the same call.  Asynchronous on `stream`.
+ */
+size_t moe_attention_workspace_size(int B, int q_heads, int kv_heads, int head_dim);
+moe_status moe_paged_attention(const moe_kv_cache* cache, const void* q, int dtype, int64_t q_token, int64_t q_head,
+                               const int32_t* page_table, int64_t table_ld, int table_width, const int32_t* lengths,
+                               int B, int q_heads, float scale, const float* sinks, int window, void* out,
+                               int64_t out_token, int64_t out_head, void* workspace, size_t workspace_bytes,
+                               uint32_t* status, void* stream);
+
 /* Synchronises `stream`, then reads and clears the device error word of
  * `workspace`: MOE_OK, MOE_ERR_DEVICE_TIMEOUT (a bounded wait ran out),
  * MOE_ERR_INDEX (a page, slot or length was out of range), or MOE_ERR_CUDA. */

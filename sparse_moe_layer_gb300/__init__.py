@@ -22,7 +22,8 @@ __all__ = ["MoeError", "build", "lib", "workspace_size", "workspace_layout", "wo
            "pack_weights_into_mx", "s13_mx_shape", "s2_mx_shape", "unblock_scales_mx", "quantize_rows_mx",
            "pack_weights_mxfp4", "pack_weights_into_mxfp4", "w13_shape_fp4", "w2_shape_fp4", "unblock_fp4",
            "weight_format", "route_debug", "block_weights", "read_static_scratch_status",
-           "route_experts", "forward_gated", "rotate_append", "new_status"]
+           "route_experts", "forward_gated", "rotate_append", "new_status",
+           "paged_attention", "attention_workspace"]
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace too small", 4: "CUDA error",
           5: "device wait timed out", 6: "a page, slot or length was out of range"}
@@ -102,6 +103,11 @@ def lib():
         L.moe_rotate_append.argtypes = [vp] * 4 + [i32] + [i64] * 6 + [vp] * 3 + [i32, i32, f32, i32, i32, vp, i64, i64,
                                                                                 vp, vp]
         L.moe_rotate_append.restype = i32
+        L.moe_attention_workspace_size.argtypes = [i32] * 4
+        L.moe_attention_workspace_size.restype = sz
+        L.moe_paged_attention.argtypes = [vp, vp, i32, i64, i64, vp, i64, i32, vp, i32, i32, f32, vp, i32, vp, i64, i64,
+                                          vp, sz, vp, vp]
+        L.moe_paged_attention.restype = i32
         L.moe_read_device_status.argtypes = [vp, vp]
         L.moe_read_device_status.restype = i32
         L.moe_test_bounded_wait.argtypes = [u64, i32, vp, vp]
@@ -641,6 +647,53 @@ def rotate_append(q, k, v, positions, slots, k_cache, v_cache, inv_freq, k_scale
                                        rope_scale, N, Hq, q_out.data_ptr(), os_[0], os_[1], _status_ptr(status),
                                        _stream(stream)), "moe_rotate_append")
     return q_out
+
+
+def attention_workspace(B: int, q_heads: int, kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
+    """A workspace for `paged_attention` calls of these sizes that do not overlap."""
+    n = int(lib().moe_attention_workspace_size(B, q_heads, kv_heads, head_dim))
+    if n == 0:
+        raise MoeError(1, "moe_attention_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def paged_attention(q, k_cache, v_cache, page_table, lengths, scale: float, k_scale=None, v_scale=None, sinks=None,
+                    window: int = 0, out=None, workspace=None, status=None, stream=None):
+    """Attention of one new token per sequence, q [B, Hq, D] (bf16 or fp16), over a paged cache (see
+    `rotate_append` for its forms); returns out [B, Hq, D] of q's type.
+
+    page_table int32 [B, pages]: page of each page_size tokens (entries past the length are not
+    read); lengths int32 [B]: tokens of each sequence, the new one included, 0 for none (out is 0).
+    sinks fp32 [Hq]: a logit per head that joins the softmax sum without a value.  window > 0:
+    only the last `window` tokens.  status (`new_status`): set by a page or length out of range."""
+    kv, Hkv, page, D, cdt = _cache(k_cache, v_cache, k_scale, v_scale)
+    dt = _DTYPES.get(q.dtype, 3)
+    if not q.is_cuda or dt > 1 or (cdt != 3 and cdt != dt):
+        raise ValueError("q must be a bf16 or fp16 CUDA tensor, and a 16-bit cache of its type")
+    if q.dim() != 3 or q.shape[2] != D or q.stride(2) != 1:
+        raise ValueError(f"q must be [B, Hq, {D}] with a contiguous last dim")
+    B, Hq = q.shape[0], q.shape[1]
+    if not page_table.is_cuda or page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B \
+            or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError(f"page_table must be an int32 CUDA tensor [{B}, pages] with contiguous rows")
+    lens = _index(lengths, B, torch.int32, "lengths")
+    if sinks is not None and sinks.shape != (Hq,):
+        raise ValueError(f"sinks must be [{Hq}]")
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_cuda or out.stride(2) != 1:
+        raise ValueError("out must be like q, its last dim contiguous")
+    if B == 0:
+        return out
+    if workspace is None:
+        workspace = attention_workspace(B, Hq, Hkv, D, q.device)
+    qs, os_ = q.stride(), out.stride()
+    _check(lib().moe_paged_attention(kv, q.data_ptr(), dt, qs[0], qs[1], page_table.data_ptr(), page_table.stride(0),
+                                     page_table.shape[1], lens, B, Hq, scale,
+                                     None if sinks is None else _dev(sinks, torch.float32, "sinks"), window,
+                                     out.data_ptr(), os_[0], os_[1], _dev(workspace, torch.uint8, "workspace"),
+                                     workspace.numel(), _status_ptr(status), _stream(stream)), "moe_paged_attention")
+    return out
 
 
 class MoeLayer:

@@ -883,6 +883,69 @@ extern "C" moe_status moe_rotate_append(const moe_kv_cache* cache, const void* q
                : MOE_ERR_CUDA;
 }
 
+static bool attention_ok(int B, int q_heads, int kv_heads, int head_dim) {
+    return B >= 1 && B <= 65536 && kv_heads >= 1 && kv_heads <= 256 && q_heads >= 1 && q_heads <= 4096 &&
+           q_heads % kv_heads == 0 && (long long)B * q_heads < (1LL << 27) && head_dim >= 16 && head_dim <= 256 &&
+           head_dim % 16 == 0;
+}
+
+extern "C" size_t moe_attention_workspace_size(int B, int q_heads, int kv_heads, int head_dim) {
+    if (!attention_ok(B, q_heads, kv_heads, head_dim)) return 0;
+    AttendWorkspace w;
+    return attend_workspace(B, q_heads, kv_heads, head_dim, num_sms(), &w);
+}
+
+extern "C" moe_status moe_paged_attention(const moe_kv_cache* cache, const void* q, int dtype, int64_t q_token,
+                                          int64_t q_head, const int32_t* page_table, int64_t table_ld, int table_width,
+                                          const int32_t* lengths, int B, int q_heads, float scale, const float* sinks,
+                                          int window, void* out, int64_t out_token, int64_t out_head, void* workspace,
+                                          size_t workspace_bytes, uint32_t* status, void* stream) {
+    AttendParams p;
+    memset(&p, 0, sizeof(p));
+    const moe_status cs = check_cache(cache, &p.cache);
+    if (cs != MOE_OK) return cs;
+    if (!q || !page_table || !lengths || !out || !workspace) return MOE_ERR_INVALID_ARG;
+    if (!attention_ok(B, q_heads, cache->kv_heads, cache->head_dim) || table_width < 1 || window < 0 || scale != scale)
+        return MOE_ERR_INVALID_ARG;
+    if ((long long)table_width * cache->page_size >= (1LL << 31) || (B > 1 && table_ld < table_width))
+        return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_BF16 && dtype != MOE_FP16) return MOE_ERR_UNSUPPORTED;
+    if (cache->dtype != MOE_E4M3 && cache->dtype != dtype) return MOE_ERR_UNSUPPORTED;
+    if (B == 1) q_token = out_token = table_ld = 0;
+    if (q_heads == 1) q_head = out_head = 0;
+    if (q_token < 0 || q_head < 0 || out_token < 0 || out_head < 0) return MOE_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(page_table) |
+          reinterpret_cast<uintptr_t>(lengths) | reinterpret_cast<uintptr_t>(sinks) |
+          reinterpret_cast<uintptr_t>(status)) & 3u) ||
+        ((q_token | q_head | out_token | out_head) & 1) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return MOE_ERR_UNSUPPORTED;
+    const int sms = num_sms();
+    AttendWorkspace w;
+    if (workspace_bytes < attend_workspace(B, q_heads, cache->kv_heads, cache->head_dim, sms, &w))
+        return MOE_ERR_WORKSPACE;
+    p.q = static_cast<const uint16_t*>(q);
+    p.out = static_cast<uint16_t*>(out);
+    p.q_token = q_token, p.q_head = q_head, p.o_token = out_token, p.o_head = out_head;
+    p.table = page_table;
+    p.table_ld = table_ld;
+    p.lengths = lengths;
+    p.sinks = sinks;
+    p.B = B;
+    p.Hq = q_heads;
+    p.Hkv = cache->kv_heads;
+    p.D = cache->head_dim;
+    p.num_pages = cache->num_pages;
+    p.page_size = cache->page_size;
+    p.max_tokens = table_width * cache->page_size;
+    p.window = window;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.status = status;
+    return launch_attend(p, cache->dtype, dtype == MOE_FP16, sms, workspace, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
 extern "C" {
 
 moe_status moe_pack_weights(const float* w13_f32, const float* w2_f32, int H, int I, int E, uint8_t* w13, float* s13,

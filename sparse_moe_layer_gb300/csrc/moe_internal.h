@@ -80,6 +80,34 @@ struct AppendParams {
     int lpr_shift, tokens_per_cta;   // set at launch
 };
 
+struct AttendParams {
+    const uint16_t* q;  // [B, Hq, D]
+    uint16_t* out;
+    long long q_token, q_head, o_token, o_head;
+    KvCache cache;
+    const int32_t* table;  // [B, *] page ids, rows table_ld apart
+    long long table_ld;
+    const int32_t* lengths;  // [B]
+    const float* sinks;      // [Hq] or null
+    int B, Hq, Hkv, D;
+    int num_pages, page_size, max_tokens;  // max_tokens: table columns * page_size
+    int window;                            // 0: none
+    float scale_log2;                      // scale * log2(e)
+    uint32_t* status;                      // error word or null
+    // set at launch
+    int group, head_blocks, rows_per_seq;  // query heads per key head; blocks of 16 of them; rows of a sequence
+    int page_shift;                        // log2(page_size), -1 if none
+    int by_row, min_units;                 // runs of whole rows; least units of a run
+    int by_row_join, runs, heads_per_cta;
+    int32_t* cont;   // [runs] row that the run continues, -1: it starts one
+    int32_t* first;  // [rows] run that the row begins in, -1: it ends there too (by_row_join)
+    float* partial;  // [runs, 2, 16 (max, sum) + 16 x D]
+};
+struct AttendWorkspace {
+    int runs, by_row_join;
+    size_t cont, first, partial, total;
+};
+
 struct PermuteParams {
     const uint16_t* x;
     int T, H, Hp, E, k;
@@ -205,6 +233,8 @@ int router_tc_experts(int T, int H, int E);
 cudaError_t launch_router_tc(const RouteParams& p, const CUtensorMap& tmX, const CUtensorMap& tmW, cudaStream_t st);
 cudaError_t launch_gate(const GateParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_rotate_append(const AppendParams& p, bool fp16, bool e4m3, int sms, cudaStream_t st);
+size_t attend_workspace(int B, int Hq, int Hkv, int D, int sms, AttendWorkspace* w);
+cudaError_t launch_attend(const AttendParams& p, int kv_dtype, bool fp16, int sms, void* workspace, cudaStream_t st);
 cudaError_t launch_permute_quant(const PermuteParams& p, cudaStream_t st);
 cudaError_t launch_combine(const float* part, int T, int H, int ldp, int k, uint16_t* out, int num_sms,
                            cudaStream_t st);
