@@ -242,7 +242,7 @@ static moe_status launch_routing(const void* x, const void* router_w, const void
     if (gate) {
         GateParams gp = gate_params(*gate, T, E, top_k);
         gp.r = rp;
-        if (launch_gate(gp, gate->dtype, st) != cudaSuccess) return MOE_ERR_CUDA;
+        if (launch_gate(gp, gate->dtype, num_sms(), st) != cudaSuccess) return MOE_ERR_CUDA;
     }
     // large batches with 16-byte aligned rows: the tensor-core router
     else if (const int np = router_tc_experts(T, H, E)) {
@@ -775,7 +775,7 @@ extern "C" moe_status moe_route_experts(const moe_gate* gate, const void* logits
     GateParams p = gate_params(in, T, E, top_k);
     p.r.topk_idx = topk_idx;
     p.r.topk_w = topk_w;
-    return launch_gate(p, logits_dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return launch_gate(p, logits_dtype, num_sms(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 extern "C" moe_status moe_forward_gated(const moe_gate* gate, const void* logits, int logits_dtype, int64_t ld,

@@ -47,7 +47,7 @@ struct GateParams {
     int groups, top_groups, group_top;
     int renorm;
     float scale;
-    int vec, gsize, lanes_per_group;  // set at launch
+    int vec, gsize, inv_gsize, aligned, lanes_per_group;  // set at launch
     RouteParams r;
 };
 
@@ -231,7 +231,7 @@ cudaError_t launch_router(const RouteParams& p, cudaStream_t st);
 // 64 x NP boxes (128-byte swizzle).
 int router_tc_experts(int T, int H, int E);
 cudaError_t launch_router_tc(const RouteParams& p, const CUtensorMap& tmX, const CUtensorMap& tmW, cudaStream_t st);
-cudaError_t launch_gate(const GateParams& p, int dtype, cudaStream_t st);
+cudaError_t launch_gate(const GateParams& p, int dtype, int sms, cudaStream_t st);
 cudaError_t launch_rotate_append(const AppendParams& p, bool fp16, bool e4m3, int sms, cudaStream_t st);
 size_t attend_workspace(int B, int Hq, int Hkv, int D, int sms, AttendWorkspace* w);
 cudaError_t launch_attend(const AttendParams& p, int kv_dtype, bool fp16, int sms, void* workspace, cudaStream_t st);

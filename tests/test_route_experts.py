@@ -173,6 +173,22 @@ def test_borders_below_fp32_resolution_follow_64_bits(score):
 
 
 @gpu
+def test_logits_and_choices_apart_in_the_last_bits():
+    """fp32 logits one step apart (0 to 40 steps, shuffled), in one binade, across two, negative, and
+    around zero; the same as biases of equal scores, and as whole groups."""
+    g = torch.Generator().manual_seed(2)
+    for E in (16, 64, 160, 256):
+        steps = torch.stack([torch.randperm(E, generator=g) % 41 for _ in range(40)])
+        for base in (1.0, 2.0 - 2.0 ** -22, -3.0, 0.0):
+            l = (base + steps.double() * 2.0 ** (-23 if base else -140)).float().cuda()
+            check(l, 8)
+            check(l, 8, groups=8, top_groups=5, group_top=1)
+            check(l, 8, score="sigmoid", groups=8, top_groups=4, group_top=2)
+            check(torch.zeros(3, E, device="cuda"), 8, score="sigmoid", bias=l[0], groups=4, top_groups=2, group_top=2)
+            check(l, 8, score="sigmoid", bias=l[0])
+
+
+@gpu
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_masked_logits(score):
     l = draw(12, 40, seed=7)
