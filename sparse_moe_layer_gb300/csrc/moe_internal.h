@@ -77,7 +77,7 @@ struct AppendParams {
     int num_pages, page_size;
     KvCache cache;
     uint32_t* status;                // error word or null
-    int lpr_shift, tokens_per_cta;   // set at launch
+    int lpr_shift, parts, groups_per_part;  // set at launch
 };
 
 struct AttendParams {
