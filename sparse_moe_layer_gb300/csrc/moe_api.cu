@@ -891,8 +891,10 @@ static bool attention_ok(int B, int q_heads, int kv_heads, int head_dim) {
 
 extern "C" size_t moe_attention_workspace_size(int B, int q_heads, int kv_heads, int head_dim) {
     if (!attention_ok(B, q_heads, kv_heads, head_dim)) return 0;
-    AttendWorkspace w;
-    return attend_workspace(B, q_heads, kv_heads, head_dim, num_sms(), &w);
+    AttendWorkspace w, w8;  // of either cache type
+    const size_t a = attend_workspace(B, q_heads, kv_heads, head_dim, false, num_sms(), &w);
+    const size_t b = attend_workspace(B, q_heads, kv_heads, head_dim, true, num_sms(), &w8);
+    return a > b ? a : b;
 }
 
 extern "C" moe_status moe_paged_attention(const moe_kv_cache* cache, const void* q, int dtype, int64_t q_token,
@@ -921,7 +923,7 @@ extern "C" moe_status moe_paged_attention(const moe_kv_cache* cache, const void*
         return MOE_ERR_UNSUPPORTED;
     const int sms = num_sms();
     AttendWorkspace w;
-    if (workspace_bytes < attend_workspace(B, q_heads, cache->kv_heads, cache->head_dim, sms, &w))
+    if (workspace_bytes < attend_workspace(B, q_heads, cache->kv_heads, cache->head_dim, cache->dtype == MOE_E4M3, sms, &w))
         return MOE_ERR_WORKSPACE;
     p.q = static_cast<const uint16_t*>(q);
     p.out = static_cast<uint16_t*>(out);

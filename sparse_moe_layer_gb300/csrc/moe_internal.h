@@ -96,7 +96,8 @@ struct AttendParams {
     uint32_t* status;                      // error word or null
     // set at launch
     int group, head_blocks, rows_per_seq;  // query heads per key head; blocks of 16 of them; rows of a sequence
-    int page_shift;                        // log2(page_size), -1 if none
+    int page_shift, page16;                // log2(page_size), -1 if none; whether 16 divides it
+    int team;                              // a CTA per row
     int by_row, min_units;                 // runs of whole rows; least units of a run
     int by_row_join, runs, heads_per_cta;
     int32_t* cont;   // [runs] row that the run continues, -1: it starts one
@@ -233,7 +234,7 @@ int router_tc_experts(int T, int H, int E);
 cudaError_t launch_router_tc(const RouteParams& p, const CUtensorMap& tmX, const CUtensorMap& tmW, cudaStream_t st);
 cudaError_t launch_gate(const GateParams& p, int dtype, int sms, cudaStream_t st);
 cudaError_t launch_rotate_append(const AppendParams& p, bool fp16, bool e4m3, int sms, cudaStream_t st);
-size_t attend_workspace(int B, int Hq, int Hkv, int D, int sms, AttendWorkspace* w);
+size_t attend_workspace(int B, int Hq, int Hkv, int D, bool e4m3, int sms, AttendWorkspace* w);
 cudaError_t launch_attend(const AttendParams& p, int kv_dtype, bool fp16, int sms, void* workspace, cudaStream_t st);
 cudaError_t launch_permute_quant(const PermuteParams& p, cudaStream_t st);
 cudaError_t launch_combine(const float* part, int T, int H, int ldp, int k, uint16_t* out, int num_sms,
