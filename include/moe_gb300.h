@@ -441,15 +441,17 @@ moe_status moe_rotate_append(const moe_kv_cache* cache, const void* q, const voi
  * outside [0, num_pages) is left out; both set the error word.
  *   q [B, q_heads, D] bf16 or fp16 (`dtype`; that of a 16-bit cache), strides in
  *   elements, D contiguous; out likewise; page_table, lengths int32; sinks fp32
- *   workspace: moe_attention_workspace_size bytes, 256-byte aligned, any contents;
- *   calls that may overlap need one each
+ *   workspace: for the parts of rows cut over several warps, 256-byte aligned, any
+ *   contents; calls that may overlap need one each.  moe_attention_workspace_size
+ *   gives its bytes for rows of at most max_tokens (the window, or table_width *
+ *   page_size if that is less); 256: such rows are not cut, and it may be NULL
  *   status: a device error word for moe_read_device_status, or NULL
  * Limits: those of the cache; q_heads a multiple of kv_heads, at most 4096;
  * 1 <= B <= 65536, B * q_heads < 2^27; table_width * page_size < 2^31; q and out:
  * pointers and strides multiples of 4 bytes.  The result is the same for every
  * run of the same call.  Asynchronous on `stream`.
  */
-size_t moe_attention_workspace_size(int B, int q_heads, int kv_heads, int head_dim);
+size_t moe_attention_workspace_size(int B, int q_heads, int kv_heads, int head_dim, int cache_dtype, int max_tokens);
 moe_status moe_paged_attention(const moe_kv_cache* cache, const void* q, int dtype, int64_t q_token, int64_t q_head,
                                const int32_t* page_table, int64_t table_ld, int table_width, const int32_t* lengths,
                                int B, int q_heads, float scale, const float* sinks, int window, void* out,

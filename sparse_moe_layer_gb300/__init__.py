@@ -9,6 +9,7 @@ library is missing, importing the binding's functions raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 
@@ -103,7 +104,7 @@ def lib():
         L.moe_rotate_append.argtypes = [vp] * 4 + [i32] + [i64] * 6 + [vp] * 3 + [i32, i32, f32, i32, i32, vp, i64, i64,
                                                                                 vp, vp]
         L.moe_rotate_append.restype = i32
-        L.moe_attention_workspace_size.argtypes = [i32] * 4
+        L.moe_attention_workspace_size.argtypes = [i32] * 6
         L.moe_attention_workspace_size.restype = sz
         L.moe_paged_attention.argtypes = [vp, vp, i32, i64, i64, vp, i64, i32, vp, i32, i32, f32, vp, i32, vp, i64, i64,
                                           vp, sz, vp, vp]
@@ -649,9 +650,16 @@ def rotate_append(q, k, v, positions, slots, k_cache, v_cache, inv_freq, k_scale
     return q_out
 
 
-def attention_workspace(B: int, q_heads: int, kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
-    """A workspace for `paged_attention` calls of these sizes that do not overlap."""
-    n = int(lib().moe_attention_workspace_size(B, q_heads, kv_heads, head_dim))
+@functools.lru_cache(maxsize=4096)
+def _attention_bytes(B: int, q_heads: int, kv_heads: int, head_dim: int, dtype: int, tokens: int) -> int:
+    return int(lib().moe_attention_workspace_size(B, q_heads, kv_heads, head_dim, dtype, tokens))
+
+
+def attention_workspace(B: int, q_heads: int, kv_heads: int, head_dim: int, max_tokens: int, dtype=torch.bfloat16,
+                        device=None) -> torch.Tensor:
+    """A workspace for `paged_attention` calls of these sizes that do not overlap: max_tokens is the
+    window, or the page table's columns times the page size if that is less; dtype the cache's."""
+    n = _attention_bytes(B, q_heads, kv_heads, head_dim, _DTYPES.get(dtype, -1), max_tokens)
     if n == 0:
         raise MoeError(1, "moe_attention_workspace_size")
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
@@ -685,14 +693,20 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, scale: float, k_sc
         raise ValueError("out must be like q, its last dim contiguous")
     if B == 0:
         return out
-    if workspace is None:
-        workspace = attention_workspace(B, Hq, Hkv, D, q.device)
+    if workspace is not None:
+        ws, ws_bytes = _dev(workspace, torch.uint8, "workspace"), workspace.numel()
+    else:
+        most = page_table.shape[1] * page
+        ws, ws_bytes = None, _attention_bytes(B, Hq, Hkv, D, cdt, window if 0 < window < most else most)
+        if ws_bytes > 256:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            ws = workspace.data_ptr()
     qs, os_ = q.stride(), out.stride()
     _check(lib().moe_paged_attention(kv, q.data_ptr(), dt, qs[0], qs[1], page_table.data_ptr(), page_table.stride(0),
                                      page_table.shape[1], lens, B, Hq, scale,
                                      None if sinks is None else _dev(sinks, torch.float32, "sinks"), window,
-                                     out.data_ptr(), os_[0], os_[1], _dev(workspace, torch.uint8, "workspace"),
-                                     workspace.numel(), _status_ptr(status), _stream(stream)), "moe_paged_attention")
+                                     out.data_ptr(), os_[0], os_[1], ws, ws_bytes, _status_ptr(status),
+                                     _stream(stream)), "moe_paged_attention")
     return out
 
 

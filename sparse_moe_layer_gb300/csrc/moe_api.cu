@@ -8,6 +8,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "../../include/moe_gb300.h"
@@ -131,9 +132,13 @@ bool make_map_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t col
 }
 
 int num_sms() {
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
+    static std::atomic<int> known[64];  // by device; a device's count does not change
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
     cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (n > 0) known[dev].store(n, std::memory_order_relaxed);
     return n > 0 ? n : 1;
 }
 
@@ -889,12 +894,13 @@ static bool attention_ok(int B, int q_heads, int kv_heads, int head_dim) {
            head_dim % 16 == 0;
 }
 
-extern "C" size_t moe_attention_workspace_size(int B, int q_heads, int kv_heads, int head_dim) {
-    if (!attention_ok(B, q_heads, kv_heads, head_dim)) return 0;
-    AttendWorkspace w, w8;  // of either cache type
-    const size_t a = attend_workspace(B, q_heads, kv_heads, head_dim, false, num_sms(), &w);
-    const size_t b = attend_workspace(B, q_heads, kv_heads, head_dim, true, num_sms(), &w8);
-    return a > b ? a : b;
+extern "C" size_t moe_attention_workspace_size(int B, int q_heads, int kv_heads, int head_dim, int cache_dtype,
+                                               int max_tokens) {
+    if (!attention_ok(B, q_heads, kv_heads, head_dim) || max_tokens < 1) return 0;
+    if (cache_dtype != MOE_BF16 && cache_dtype != MOE_FP16 && cache_dtype != MOE_E4M3) return 0;
+    AttendPlan w;
+    attend_plan(B, q_heads, kv_heads, head_dim, cache_dtype == MOE_E4M3, max_tokens, num_sms(), &w);
+    return w.total ? w.total : 256;
 }
 
 extern "C" moe_status moe_paged_attention(const moe_kv_cache* cache, const void* q, int dtype, int64_t q_token,
@@ -906,7 +912,7 @@ extern "C" moe_status moe_paged_attention(const moe_kv_cache* cache, const void*
     memset(&p, 0, sizeof(p));
     const moe_status cs = check_cache(cache, &p.cache);
     if (cs != MOE_OK) return cs;
-    if (!q || !page_table || !lengths || !out || !workspace) return MOE_ERR_INVALID_ARG;
+    if (!q || !page_table || !lengths || !out) return MOE_ERR_INVALID_ARG;
     if (!attention_ok(B, q_heads, cache->kv_heads, cache->head_dim) || table_width < 1 || window < 0 || scale != scale)
         return MOE_ERR_INVALID_ARG;
     if ((long long)table_width * cache->page_size >= (1LL << 31) || (B > 1 && table_ld < table_width))
@@ -921,10 +927,12 @@ extern "C" moe_status moe_paged_attention(const moe_kv_cache* cache, const void*
           reinterpret_cast<uintptr_t>(status)) & 3u) ||
         ((q_token | q_head | out_token | out_head) & 1) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return MOE_ERR_UNSUPPORTED;
-    const int sms = num_sms();
-    AttendWorkspace w;
-    if (workspace_bytes < attend_workspace(B, q_heads, cache->kv_heads, cache->head_dim, cache->dtype == MOE_E4M3, sms, &w))
-        return MOE_ERR_WORKSPACE;
+    p.max_tokens = table_width * cache->page_size;
+    AttendPlan w;
+    attend_plan(B, q_heads, cache->kv_heads, cache->head_dim, cache->dtype == MOE_E4M3,
+                window > 0 && window < p.max_tokens ? window : p.max_tokens, num_sms(), &w);
+    if (w.total && !workspace) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < w.total) return MOE_ERR_WORKSPACE;
     p.q = static_cast<const uint16_t*>(q);
     p.out = static_cast<uint16_t*>(out);
     p.q_token = q_token, p.q_head = q_head, p.o_token = out_token, p.o_head = out_head;
@@ -938,11 +946,10 @@ extern "C" moe_status moe_paged_attention(const moe_kv_cache* cache, const void*
     p.D = cache->head_dim;
     p.num_pages = cache->num_pages;
     p.page_size = cache->page_size;
-    p.max_tokens = table_width * cache->page_size;
     p.window = window;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.status = status;
-    return launch_attend(p, cache->dtype, dtype == MOE_FP16, sms, workspace, static_cast<cudaStream_t>(stream)) ==
+    return launch_attend(p, w, cache->dtype, dtype == MOE_FP16, workspace, static_cast<cudaStream_t>(stream)) ==
                    cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;

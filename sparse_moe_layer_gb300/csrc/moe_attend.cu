@@ -887,29 +887,28 @@ cudaError_t launch_attend_d(const AttendParams& p, int grid, cudaStream_t st) {
 
 }  // namespace
 
-size_t attend_workspace(int B, int Hq, int Hkv, int D, bool e4m3, int sms, AttendWorkspace* w) {
-    const int runs = sms * ctas_per_sm(dp_of(D), e4m3) * kAttWarps;
+// How the rows are given to warps; the workspace is for the parts of cut rows.
+void attend_plan(int B, int Hq, int Hkv, int D, bool e4m3, int most, int sms, AttendPlan* w) {
+    const int ctas = sms * ctas_per_sm(dp_of(D), e4m3), runs = ctas * kAttWarps;
     const long long rows = (long long)B * Hkv * ((Hq / Hkv + kAttRows - 1) / kAttRows);
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     w->runs = runs;
+    w->team = rows <= ctas && most <= kTeamTokens;
+    w->by_row = !w->team && most <= kWholeTokens;
     w->by_row_join = rows <= runs;
     w->cont = 0;
     w->first = up((size_t)runs * 4);
     w->partial = w->first + up((size_t)(rows <= runs ? rows : 1) * 4);
-    w->total = w->partial + (size_t)runs * 2 * kAttRows * (D + 2) * 4;
-    return w->total;
+    w->total = w->team || w->by_row ? 0 : w->partial + (size_t)runs * 2 * kAttRows * (D + 2) * 4;
 }
 
-cudaError_t launch_attend(const AttendParams& p_in, int kv_dtype, bool fp16, int sms, void* workspace, cudaStream_t st) {
+cudaError_t launch_attend(const AttendParams& p_in, const AttendPlan& w, int kv_dtype, bool fp16, void* workspace,
+                          cudaStream_t st) {
     AttendParams p = p_in;
     const bool e4m3 = kv_dtype == kDtE4m3;
-    AttendWorkspace w;
-    attend_workspace(p.B, p.Hq, p.Hkv, p.D, e4m3, sms, &w);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.runs = w.runs;
-    p.cont = reinterpret_cast<int32_t*>(ws + w.cont);
-    p.first = reinterpret_cast<int32_t*>(ws + w.first);
-    p.partial = reinterpret_cast<float*>(ws + w.partial);
+    p.team = w.team;
+    p.by_row = w.by_row;
     p.group = p.Hq / p.Hkv;
     p.head_blocks = (p.group + kAttRows - 1) / kAttRows;
     p.rows_per_seq = p.Hkv * p.head_blocks;
@@ -918,14 +917,15 @@ cudaError_t launch_attend(const AttendParams& p_in, int kv_dtype, bool fp16, int
     if ((p.page_size & (p.page_size - 1)) == 0)
         for (p.page_shift = 0; (1 << p.page_shift) < p.page_size;) ++p.page_shift;
     const long long rows = (long long)p.B * p.rows_per_seq;
-    int grid = w.runs / kAttWarps;
-    const int most = p.window > 0 && p.window < p.max_tokens ? p.window : p.max_tokens;
-    p.team = rows <= grid && most <= kTeamTokens;
-    p.by_row = !p.team && most <= kWholeTokens;
-    p.by_row_join = w.by_row_join;
     p.min_units = p.by_row ? 1 : kMinTokens / tile_tokens(dp_of(p.D), e4m3);
-    if (p.by_row || p.team) p.cont = nullptr, p.by_row_join = 0;
-    if (p.team) grid = (int)rows;
+    if (w.total) {
+        uint8_t* ws = static_cast<uint8_t*>(workspace);
+        p.by_row_join = w.by_row_join;
+        p.cont = reinterpret_cast<int32_t*>(ws + w.cont);
+        p.first = reinterpret_cast<int32_t*>(ws + w.first);
+        p.partial = reinterpret_cast<float*>(ws + w.partial);
+    }
+    const int grid = p.team ? (int)rows : w.runs / kAttWarps;
     cudaError_t e;
     if (e4m3)
         e = fp16 ? launch_attend_d<kKvE4m3, true>(p, grid, st) : launch_attend_d<kKvE4m3, false>(p, grid, st);

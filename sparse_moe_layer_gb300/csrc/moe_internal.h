@@ -104,9 +104,9 @@ struct AttendParams {
     int32_t* first;  // [rows] run that the row begins in, -1: it ends there too (by_row_join)
     float* partial;  // [runs, 2, 16 (max, sum) + 16 x D]
 };
-struct AttendWorkspace {
-    int runs, by_row_join;
-    size_t cont, first, partial, total;
+struct AttendPlan {
+    int runs, team, by_row, by_row_join;
+    size_t cont, first, partial, total;  // workspace; total 0: none needed
 };
 
 struct PermuteParams {
@@ -234,8 +234,10 @@ int router_tc_experts(int T, int H, int E);
 cudaError_t launch_router_tc(const RouteParams& p, const CUtensorMap& tmX, const CUtensorMap& tmW, cudaStream_t st);
 cudaError_t launch_gate(const GateParams& p, int dtype, int sms, cudaStream_t st);
 cudaError_t launch_rotate_append(const AppendParams& p, bool fp16, bool e4m3, int sms, cudaStream_t st);
-size_t attend_workspace(int B, int Hq, int Hkv, int D, bool e4m3, int sms, AttendWorkspace* w);
-cudaError_t launch_attend(const AttendParams& p, int kv_dtype, bool fp16, int sms, void* workspace, cudaStream_t st);
+// most: tokens that a row can have (its window, or the page table's columns)
+void attend_plan(int B, int Hq, int Hkv, int D, bool e4m3, int most, int sms, AttendPlan* plan);
+cudaError_t launch_attend(const AttendParams& p, const AttendPlan& plan, int kv_dtype, bool fp16, void* workspace,
+                          cudaStream_t st);
 cudaError_t launch_permute_quant(const PermuteParams& p, cudaStream_t st);
 cudaError_t launch_combine(const float* part, int T, int H, int ldp, int k, uint16_t* out, int num_sms,
                            cudaStream_t st);

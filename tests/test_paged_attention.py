@@ -43,8 +43,9 @@ def test_refusals_on_the_host():
         return L.moe_paged_attention(kv_bytes(**cache) if kv is None else kv, q, dt, *qst, table, ld, width, lens, B, Hq,
                                      scale, sinks, window, out, *ost, ws, wsb, status, None)
 
-    for name in ("q", "table", "lens", "out", "ws"):
+    for name in ("q", "table", "lens", "out"):
         assert call(**{name: None}) == 1, name
+    assert call(width=100, ld=100, ws=None) == 1  # rows that may be cut need a workspace
     assert call(kv=kv_bytes(k=0)) == 1 and call(B=0) == 1 and call(B=65537) == 1 and call(Hq=0) == 1
     assert call(Hq=3) == 1 and call(Hq=4098) == 1  # not a multiple of the key heads; too many
     assert call(D=72) == 1 and call(D=272) == 1 and call(S=0) == 1 and call(H=300) == 1
@@ -56,9 +57,11 @@ def test_refusals_on_the_host():
     assert call(sinks=258) == 2 and call(status=258) == 2 and call(ws=264) == 2
     assert call(qst=(256, 65)) == 2 and call(ost=(255, 64)) == 2 and call(qst=(-256, 64)) == 1
     assert call(kv=kv_bytes(k=264)) == 2 and call(kv=kv_bytes(strides=(2048, 1024, 68))) == 2
-    assert call(wsb=64) == 3
-    assert L.moe_attention_workspace_size(0, 4, 2, 64) == 0 and L.moe_attention_workspace_size(1, 3, 2, 64) == 0
-    assert L.moe_attention_workspace_size(1, 4, 2, 72) == 0 and L.moe_attention_workspace_size(1, 4, 2, 64) > 0
+    assert call(width=100, ld=100, wsb=64) == 3
+    size = L.moe_attention_workspace_size
+    assert size(0, 4, 2, 64, 0, 99) == 0 and size(1, 3, 2, 64, 0, 99) == 0 and size(1, 4, 2, 72, 0, 99) == 0
+    assert size(1, 4, 2, 64, 2, 99) == 0 and size(1, 4, 2, 64, 0, 0) == 0
+    assert size(1, 4, 2, 64, 0, 99) == 256 and size(1, 4, 2, 64, 3, 99999) > 256
 
 
 def test_binding_refuses():
@@ -274,7 +277,7 @@ def test_strided_q_and_out():
     fused = torch.randn(3, 12, 64, device="cuda").bfloat16()
     q = fused[:, :8]
     out = torch.zeros(3, 10, 64, dtype=torch.bfloat16, device="cuda")
-    ws = moe.attention_workspace(3, 8, 2, 64)
+    ws = moe.attention_workspace(3, 8, 2, 64, 100000)
     ws.fill_(0xFF)
     got = c.run(q=q, out=out[:, 1:9], workspace=ws)
     c.check(got, q=q)
@@ -286,7 +289,7 @@ def test_strided_q_and_out():
 @gpu
 def test_repeated_calls_and_graph_replay_agree():
     c = Case([6000, 0, 1, 800, 77], 16, 2, 64)
-    ws = moe.attention_workspace(5, 16, 2, 64)
+    ws = moe.attention_workspace(5, 16, 2, 64, 6000)
     a = c.run(sinks=True, workspace=ws)
     for _ in range(3):
         ws.random_(0, 256)
@@ -399,7 +402,9 @@ def test_shape_refusals():
     refuse("status 1", q=torch.cat((c.q, c.q), 1)[:, :9].contiguous())
     refuse("lengths", lens=c.lens.long())
     refuse("lengths", lens=c.lens[:1])
-    refuse("status 3", workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    long = Case([5000], 8, 2, 64)
+    with pytest.raises(moe.MoeError, match="status 3"):
+        long.run(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     refuse("like q", out=torch.empty(2, 8, 64, device="cuda"))
     refuse("status 1", window=-1)
     refuse("status 1", scale=math.nan)
