@@ -195,6 +195,21 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
         it.tile = warp;
         step = kAttWarps;
         left = it.ntiles > warp ? (it.ntiles - warp + kAttWarps - 1) / kAttWarps : 0;
+    } else if (p.by_row) {  // whole rows
+        const int rows = p.B * p.rows_per_seq, n = rows < nwarps ? rows : nwarps;
+        if (gw >= n) return;
+        const int u0 = (int)((long long)rows * gw / n), u1 = (int)((long long)rows * (gw + 1) / n);
+        it.b = u0 / p.rows_per_seq;
+        it.h = u0 - it.b * p.rows_per_seq;
+        it.seq(p);
+        it.tile = 0;
+        left = 0;
+        TileIt<TT> t = it;
+        for (int r = u1 - u0; r > 0; --r) {
+            left += t.ntiles;
+            t.tile = t.ntiles - 1;
+            t.next(p, 1);
+        }
     } else {
         // each thread sums the tiles of a slice of the sequences (rows_per_seq rows each)
         const int slice = (p.B + kAttWarps * 32 - 1) / (kAttWarps * 32);
@@ -204,7 +219,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             if (b < p.B) {
                 int st;
                 const int len = seen_tokens(p, b, &st);
-                mine += p.by_row ? 1 : tiles_of<TT>(st, len);
+                mine += tiles_of<TT>(st, len);
             }
         }
         int inc = mine;
@@ -226,7 +241,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
         const long long want = (total + p.min_units - 1) / p.min_units;
         const int n = (int)(want < nwarps ? want : nwarps);
         if (gw >= n) {
-            if (lane == 0 && p.cont) p.cont[gw] = -1;
+            if (lane == 0) p.cont[gw] = -1;
             return;
         }
         const long long u0 = total * gw / n, u1 = total * (gw + 1) / n;
@@ -240,27 +255,15 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
         it.b = sl * slice;
         while (true) {
             it.seq(p);
-            const long long here = (long long)(p.by_row ? 1 : it.ntiles) * p.rows_per_seq;
+            const long long here = (long long)it.ntiles * p.rows_per_seq;
             if (u < here) break;
             u -= here;
             ++it.b;
         }
-        if (p.by_row) {  // whole rows: their tiles
-            it.h = (int)u;
-            it.tile = 0;
-            left = 0;
-            TileIt<TT> t = it;
-            for (int r = (int)(u1 - u0); r > 0; --r) {
-                left += t.ntiles;
-                t.tile = t.ntiles - 1;
-                t.next(p, 1);
-            }
-        } else {
-            it.h = (int)(u / it.ntiles);
-            it.tile = (int)(u - (long long)it.h * it.ntiles);
-            left = (int)(u1 - u0);
-            if (lane == 0) p.cont[gw] = it.tile ? it.b * p.rows_per_seq + it.h : -1;
-        }
+        it.h = (int)(u / it.ntiles);
+        it.tile = (int)(u - (long long)it.h * it.ntiles);
+        left = (int)(u1 - u0);
+        if (lane == 0) p.cont[gw] = it.tile ? it.b * p.rows_per_seq + it.h : -1;
     }
 
     // --- the ring ---
@@ -352,6 +355,10 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             *reinterpret_cast<int4*>(ring + slot * C::STAGE + 2 * C::TILE + C::SC) = m;
         }
     };
+    // dims past D (D < DP) are products of zeros: no branch in the tile loop
+    if (p.D < DP)
+        for (int i = lane * 16; i < S * C::STAGE; i += 32 * 16) *reinterpret_cast<uint4*>(ring + i) = make_uint4(0, 0, 0, 0);
+    __syncwarp();
     int to_issue = left;
     if (left > 0) fetch();
     auto issue_next = [&](int slot) {
@@ -488,16 +495,14 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             const int r = (lane & 7) + ((lane >> 4) << 3), hi = (lane >> 3) & 1;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                if (k * 16 < p.D) {
-                    uint32_t a[4];
-                    qfrag(k, a);
+                uint32_t a[4];
+                qfrag(k, a);
 #pragma unroll
-                    for (int t = 0; t < KT; ++t) {
-                        uint32_t b[4];
-                        ldsm4(ks_s + swz<C::CH>(16 * t + r, 2 * k + hi), b);
-                        mma16816<F16>(s[2 * t], a, b[0], b[1]);
-                        mma16816<F16>(s[2 * t + 1], a, b[2], b[3]);
-                    }
+                for (int t = 0; t < KT; ++t) {
+                    uint32_t b[4];
+                    ldsm4(ks_s + swz<C::CH>(16 * t + r, 2 * k + hi), b);
+                    mma16816<F16>(s[2 * t], a, b[0], b[1]);
+                    mma16816<F16>(s[2 * t + 1], a, b[2], b[3]);
                 }
             }
         } else {
@@ -505,14 +510,12 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             const int r = lane;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                if (k * 16 < p.D) {
-                    uint32_t a[4], b[4];
-                    qfrag(k, a);
-                    ldsm4(ks_s + swz<C::CH>(r, k), b);
+                uint32_t a[4], b[4];
+                qfrag(k, a);
+                ldsm4(ks_s + swz<C::CH>(r, k), b);
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        mma16816<F16>(s[t], a, e4m3x2_to_f16x2(b[t]), e4m3x2_to_f16x2(b[t] >> 16));
-                }
+                for (int t = 0; t < 4; ++t)
+                    mma16816<F16>(s[t], a, e4m3x2_to_f16x2(b[t]), e4m3x2_to_f16x2(b[t] >> 16));
             }
         }
         // --- scale, mask, running maximum ---
@@ -570,12 +573,10 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             l1 *= c1;
 #pragma unroll
             for (int d = 0; d < DP / 8; ++d) {
-                if (d * 8 < p.D) {
-                    o[d][0] *= c0 * cv;
-                    o[d][1] *= c0 * cv;
-                    o[d][2] *= c1 * cv;
-                    o[d][3] *= c1 * cv;
-                }
+                o[d][0] *= c0 * cv;
+                o[d][1] *= c0 * cv;
+                o[d][2] *= c1 * cv;
+                o[d][3] *= c1 * cv;
             }
             m0 = t0;
             m1 = t1;
@@ -608,14 +609,12 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             const int r = (lane & 7) + (((lane >> 3) & 1) << 3), hi = lane >> 4;
 #pragma unroll
             for (int d = 0; d < KS; ++d) {
-                if (d * 16 < p.D) {
 #pragma unroll
-                    for (int t = 0; t < KT; ++t) {
-                        uint32_t b[4];
-                        ldsm4_t(vs_s + swz<C::CH>(16 * t + r, 2 * d + hi), b);
-                        mma16816<F16>(o[2 * d], pa[t], b[0], b[1]);
-                        mma16816<F16>(o[2 * d + 1], pa[t], b[2], b[3]);
-                    }
+                for (int t = 0; t < KT; ++t) {
+                    uint32_t b[4];
+                    ldsm4_t(vs_s + swz<C::CH>(16 * t + r, 2 * d + hi), b);
+                    mma16816<F16>(o[2 * d], pa[t], b[0], b[1]);
+                    mma16816<F16>(o[2 * d + 1], pa[t], b[2], b[3]);
                 }
             }
         } else {
@@ -624,15 +623,13 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             const int r = lane;
 #pragma unroll
             for (int d = 0; d < KS; ++d) {
-                if (d * 16 < p.D) {
-                    uint32_t b[4];
-                    ldsm4_t(vs_s + swz<C::CH>(r, d), b);
+                uint32_t b[4];
+                ldsm4_t(vs_s + swz<C::CH>(r, d), b);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t lo = __byte_perm(b[2 * k], 0, 0x3120), hi = __byte_perm(b[2 * k + 1], 0, 0x3120);
-                        mma16816<F16>(o[2 * d], pa[k], e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(hi));
-                        mma16816<F16>(o[2 * d + 1], pa[k], e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi >> 16));
-                    }
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t lo = __byte_perm(b[2 * k], 0, 0x3120), hi = __byte_perm(b[2 * k + 1], 0, 0x3120);
+                    mma16816<F16>(o[2 * d], pa[k], e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(hi));
+                    mma16816<F16>(o[2 * d + 1], pa[k], e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi >> 16));
                 }
             }
         }
@@ -917,7 +914,7 @@ cudaError_t launch_attend(const AttendParams& p_in, const AttendPlan& w, int kv_
     if ((p.page_size & (p.page_size - 1)) == 0)
         for (p.page_shift = 0; (1 << p.page_shift) < p.page_size;) ++p.page_shift;
     const long long rows = (long long)p.B * p.rows_per_seq;
-    p.min_units = p.by_row ? 1 : kMinTokens / tile_tokens(dp_of(p.D), e4m3);
+    p.min_units = kMinTokens / tile_tokens(dp_of(p.D), e4m3);
     if (w.total) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);
         p.by_row_join = w.by_row_join;

@@ -98,7 +98,7 @@ struct AttendParams {
     int group, head_blocks, rows_per_seq;  // query heads per key head; blocks of 16 of them; rows of a sequence
     int page_shift, page16;                // log2(page_size), -1 if none; whether 16 divides it
     int team;                              // a CTA per row
-    int by_row, min_units;                 // runs of whole rows; least units of a run
+    int by_row, min_units;                 // runs of whole rows; least tiles of a run
     int by_row_join, runs, heads_per_cta;
     int32_t* cont;   // [runs] row that the run continues, -1: it starts one
     int32_t* first;  // [rows] run that the row begins in, -1: it ends there too (by_row_join)
