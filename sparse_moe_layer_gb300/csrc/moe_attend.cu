@@ -14,12 +14,14 @@
 // 128-row tcgen05 tile would be 4 to 16 times padding here and hand the scores
 // through tensor memory.
 //
-// Every warp works alone: the (sequence, key head, token tile) list is cut into
-// equal runs, one per resident warp, so a batch of very different lengths loads
-// all SMs alike; a warp streams its tiles through its own cp.async ring with
-// running maximum and sum, and only a row cut by a run's border leaves fp32
-// partials, which a second, dependent launch joins in a fixed order (results
-// do not depend on scheduling).
+// The (sequence, key head, token tile) list is cut into equal runs, one per
+// resident warp (many rows) or CTA (few), so a batch of very different lengths
+// loads all SMs alike.  A warp streams its tiles through its own cp.async ring (the
+// copies run on over the borders of rows) with its own running maximum and sum; a
+// CTA's warps take its run's tiles in turn and join in shared memory where a row
+// or the run ends.  Only a row cut by a run's border leaves fp32 parts, which a second, dependent launch joins in a
+// fixed order (results do not depend on scheduling).  Rows of a tile or a few
+// take a warp each, or a CTA each if there are few.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -44,7 +46,7 @@ struct AttCfg {
     static constexpr int STAGES = DP == 64 && KV == kKvE4m3 ? 4 : DP == 256 && KV == kKvE4m3 ? 2 : 3;
     static constexpr int TILE = TT * ROW;                  // bytes of a K (or V) tile
     static constexpr int SC = KV == kKvE4m3 ? 2 * TT * 4 : 0;
-    static constexpr int STAGE = 2 * TILE + SC + 16;       // + meta
+    static constexpr int STAGE = 2 * TILE + SC + 16;       // + the mask of valid tokens
     static constexpr int QS = DP == 256 ? DP / 16 * 512 : 0;  // Q fragments, where registers do not hold them
     static constexpr int WARP = (STAGES * STAGE + QS + 127) / 128 * 128;
     static constexpr int SMEM = kAttWarps * WARP;
@@ -133,9 +135,8 @@ __device__ __forceinline__ int tiles_of(int start, int len) {
     return max(1, (len + TT - 1) / TT - start / TT);
 }
 
-// Where a warp stands in the list of tiles: sequence b, row h of it (key head
-// and block of 16 query heads), tile of the row.  step: tiles apart (a team's
-// warps take a row's tiles in turn).
+// A place in the list of tiles: sequence b, row h of it (key head and block of
+// 16 query heads), tile of the row.
 template <int TT>
 struct TileIt {
     int b, h, tile, ntiles, start, len;
@@ -143,15 +144,33 @@ struct TileIt {
         len = seen_tokens(p, b, &start);
         ntiles = tiles_of<TT>(start, len);
     }
-    __device__ __forceinline__ void next(const AttendParams& p, int step) {
+    __device__ __forceinline__ void advance(const AttendParams& p, int step) {
         tile += step;
-        if (tile < ntiles) return;
-        tile = 0;
-        if (++h < p.rows_per_seq) return;
-        h = 0;
-        if (++b < p.B) seq(p);
+        while (tile >= ntiles) {
+            tile -= ntiles;
+            if (++h < p.rows_per_seq) continue;
+            h = 0;
+            if (++b >= p.B) return;
+            seq(p);
+        }
     }
 };
+
+// A lane's four values of a 16-dim block of one row (half 0: row g, 1: row g + 8)
+// from its two accumulators, times w, in memory order: dims quad_at, + 1 and, 8
+// on (e4m3: 2 on), two more.
+struct Quad {
+    float a, b, c, d;
+};
+template <int KV>
+__device__ __forceinline__ Quad quad(const float (&u)[4], const float (&v)[4], int half, float w) {
+    if (KV == kKvE4m3) return {u[2 * half] * w, v[2 * half] * w, u[2 * half + 1] * w, v[2 * half + 1] * w};
+    return {u[2 * half] * w, u[2 * half + 1] * w, v[2 * half] * w, v[2 * half + 1] * w};
+}
+template <int KV>
+__device__ __forceinline__ int quad_at(int c) {
+    return KV == kKvE4m3 ? 4 * c : 2 * c;
+}
 
 // 1 / (sum with the head's sink), about the larger of the two exponents: what
 // sums taken about m are multiplied by.  0 for a row without tokens.
@@ -179,36 +198,35 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
     __shared__ int s_wsum[kAttWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
-    const int nwarps = gridDim.x * kAttWarps;
-    const int gw = warp * gridDim.x + blockIdx.x;  // neighbouring runs on different SMs
+    __shared__ float2 s_ml[kAttWarps][kAttRows];  // a segment's maxima and sums
+    __shared__ int s_slot[kAttWarps];             // and the ring slot of its values
     pdl_allow_dependents();
 
-    // --- this warp's run of the tile list ---
-    TileIt<TT> it;
-    int left;  // tiles of the run
-    int step = 1;
-    if (p.team) {
-        // few rows, none long: a CTA per row, its warps take the tiles in turn
-        it.b = blockIdx.x / p.rows_per_seq;
-        it.h = blockIdx.x - it.b * p.rows_per_seq;
+    // --- the run: tiles of one warp (solo), or tiles that the CTA's warps take in turn ---
+    TileIt<TT> it;  // of the copies
+    int rem;        // tiles of the run
+    // neighbouring runs on different SMs
+    const int run = p.solo ? warp * gridDim.x + blockIdx.x : blockIdx.x;
+    const int nruns = p.solo ? gridDim.x * kAttWarps : gridDim.x;
+    if (p.team) {  // few rows, none long: one to a CTA
+        it.b = run / p.rows_per_seq;
+        it.h = run - it.b * p.rows_per_seq;
+        it.tile = 0;
         it.seq(p);
-        it.tile = warp;
-        step = kAttWarps;
-        left = it.ntiles > warp ? (it.ntiles - warp + kAttWarps - 1) / kAttWarps : 0;
+        rem = it.ntiles;
     } else if (p.by_row) {  // whole rows
-        const int rows = p.B * p.rows_per_seq, n = rows < nwarps ? rows : nwarps;
-        if (gw >= n) return;
-        const int u0 = (int)((long long)rows * gw / n), u1 = (int)((long long)rows * (gw + 1) / n);
+        const int rows = p.B * p.rows_per_seq, n = rows < nruns ? rows : nruns;
+        if (run >= n) return;
+        const int u0 = (int)((long long)rows * run / n), u1 = (int)((long long)rows * (run + 1) / n);
         it.b = u0 / p.rows_per_seq;
         it.h = u0 - it.b * p.rows_per_seq;
-        it.seq(p);
         it.tile = 0;
-        left = 0;
+        it.seq(p);
+        rem = 0;
         TileIt<TT> t = it;
         for (int r = u1 - u0; r > 0; --r) {
-            left += t.ntiles;
-            t.tile = t.ntiles - 1;
-            t.next(p, 1);
+            rem += t.ntiles;
+            t.advance(p, t.ntiles);
         }
     } else {
         // each thread sums the tiles of a slice of the sequences (rows_per_seq rows each)
@@ -238,13 +256,15 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
         if (tid == 0) s_pre[0] = 0;
         __syncthreads();
         const long long total = (long long)s_pre[kAttWarps * 32] * p.rows_per_seq;
-        const long long want = (total + p.min_units - 1) / p.min_units;
-        const int n = (int)(want < nwarps ? want : nwarps);
-        if (gw >= n) {
-            if (lane == 0) p.cont[gw] = -1;
+        const long long want = (total + p.min_tiles - 1) / p.min_tiles;
+        const int n = (int)(want < nruns ? want : nruns);
+        const bool lead = p.solo ? lane == 0 : tid == 0;
+        if (run >= n) {  // a whole CTA, or a warp that meets no barrier any more
+            if (lead) p.cont[run] = -1;
             return;
         }
-        const long long u0 = total * gw / n, u1 = total * (gw + 1) / n;
+        const long long u0 = total * run / n;
+        rem = (int)(total * (run + 1) / n - u0);
         // the slice, then the sequence, that holds u0
         int sl = 0;
         for (int base = 0; base < kAttWarps * 32; base += 32) {
@@ -262,9 +282,12 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
         }
         it.h = (int)(u / it.ntiles);
         it.tile = (int)(u - (long long)it.h * it.ntiles);
-        left = (int)(u1 - u0);
-        if (lane == 0) p.cont[gw] = it.tile ? it.b * p.rows_per_seq + it.h : -1;
+        if (lead) p.cont[run] = it.tile ? it.b * p.rows_per_seq + it.h : -1;
     }
+    TileIt<TT> row = it;  // of the products: the tile that the current segment (a row's tiles in the run) begins with
+    const int step = p.solo ? 1 : kAttWarps;
+    int to_issue = p.solo ? rem : rem > warp ? (rem - warp + kAttWarps - 1) / kAttWarps : 0;  // tiles of this warp
+    if (!p.solo && to_issue > 0) it.advance(p, warp);
 
     // --- the ring ---
     uint8_t* ring = smem + warp * C::WARP;
@@ -275,35 +298,38 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
     // byte offsets of the lane's chunk in a group of 16 tokens, and of a step
     const long long k_lane = (long long)r0 * p.cache.k_token * C::ES + ch * 16, k_step = RPS * p.cache.k_token * C::ES;
     const long long v_lane = (long long)r0 * p.cache.v_token * C::ES + ch * 16, v_step = RPS * p.cache.v_token * C::ES;
-    // tile `it`: tokens of the lanes and their pages, fetched one tile ahead of the copies
-    int f_pid = -1, f_off = 0;
-    bool f_ok = false;
+    // tile `it`: tokens of the lanes and their pages, looked up before the copies need them
+    struct Fetched {
+        int h, pid, off;
+        bool ok;
+    };
     auto fetch = [&]() {
+        Fetched f = {it.h, -1, 0, false};
         const int tok = (it.start / TT + it.tile) * TT + (lane & (TT - 1));
-        f_pid = -1;
         if (tok < it.len) {
             const int pi = p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_size;
-            f_off = tok - pi * p.page_size;
+            f.off = tok - pi * p.page_size;
             // a token before the window shares its group's page; with smaller pages it is not looked up
-            if (tok >= it.start || p.page16) f_pid = __ldg(p.table + (long long)it.b * p.table_ld + pi);
+            if (tok >= it.start || p.page16) f.pid = __ldg(p.table + (long long)it.b * p.table_ld + pi);
         }
-        f_ok = tok >= it.start && tok < it.len;
+        f.ok = tok >= it.start && tok < it.len;
+        return f;
     };
-    auto issue = [&](int slot) {
+    auto issue = [&](int slot, Fetched f) {
         const uint32_t dst = ring_s + slot * C::STAGE;
-        const int kvh = p.head_blocks == 1 ? it.h : it.h / p.head_blocks;
-        if ((uint32_t)f_pid >= (uint32_t)p.num_pages) {
-            if (f_ok && p.status) atomicOr(p.status, kErrBadIndex);
-            f_pid = 0;
-            f_ok = false;
+        const int kvh = p.head_blocks == 1 ? f.h : f.h / p.head_blocks;
+        if ((uint32_t)f.pid >= (uint32_t)p.num_pages) {
+            if (f.ok && p.status) atomicOr(p.status, kErrBadIndex);
+            f.pid = 0;
+            f.ok = false;
         }
-        const uint32_t mask = __ballot_sync(kAllLanes, f_ok);
+        const uint32_t mask = __ballot_sync(kAllLanes, f.ok);
         const uint8_t* kb = static_cast<const uint8_t*>(p.cache.k) + (long long)kvh * p.cache.k_head * C::ES;
         const uint8_t* vb = static_cast<const uint8_t*>(p.cache.v) + (long long)kvh * p.cache.v_head * C::ES;
         if (p.page16) {  // a group of 16 tokens lies on one page
 #pragma unroll
             for (int hh = 0; hh < KT; ++hh) {
-                const long long pid = __shfl_sync(kAllLanes, f_pid, hh * 16), off = __shfl_sync(kAllLanes, f_off, hh * 16);
+                const long long pid = __shfl_sync(kAllLanes, f.pid, hh * 16), off = __shfl_sync(kAllLanes, f.off, hh * 16);
                 const uint8_t* ks = kb + (pid * p.cache.k_page + off * p.cache.k_token) * C::ES + k_lane;
                 const uint8_t* vs = vb + (pid * p.cache.v_page + off * p.cache.v_token) * C::ES + v_lane;
                 if (((mask >> (16 * hh)) & 0xffffu) == 0xffffu) {
@@ -330,7 +356,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
 #pragma unroll
             for (int i = 0; i < TT / RPS; ++i) {
                 const int r = r0 + i * RPS;
-                const long long pid = __shfl_sync(kAllLanes, f_pid, r), off = __shfl_sync(kAllLanes, f_off, r);
+                const long long pid = __shfl_sync(kAllLanes, f.pid, r), off = __shfl_sync(kAllLanes, f.off, r);
                 const bool ok = (mask >> r) & 1u;
                 const uint32_t at = dst + swz<C::CH>(r, ch);
                 if (in) {
@@ -341,39 +367,47 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
         }
         if constexpr (KV == kKvE4m3) {  // lane = token (TT == 32)
             const long long at =
-                f_ok ? f_pid * p.cache.s_page + kvh * p.cache.s_head + f_off * p.cache.s_token : 0;
-            cp_async4z(dst + 2 * C::TILE + lane * 4, p.cache.k_scale + at, f_ok);
-            cp_async4z(dst + 2 * C::TILE + TT * 4 + lane * 4, p.cache.v_scale + at, f_ok);
+                f.ok ? f.pid * p.cache.s_page + kvh * p.cache.s_head + f.off * p.cache.s_token : 0;
+            cp_async4z(dst + 2 * C::TILE + lane * 4, p.cache.k_scale + at, f.ok);
+            cp_async4z(dst + 2 * C::TILE + TT * 4 + lane * 4, p.cache.v_scale + at, f.ok);
         }
-        if (lane == 0) {
-            // b, h, valid tokens, flags: 1 first tile of its row, 2 last tile of its row
-            int4 m;
-            m.x = it.b;
-            m.y = it.h;
-            m.z = (int)(mask & kAllTokens);
-            m.w = (it.tile == 0 ? 1 : 0) | (it.tile == it.ntiles - 1 ? 2 : 0);
-            *reinterpret_cast<int4*>(ring + slot * C::STAGE + 2 * C::TILE + C::SC) = m;
-        }
+        if (lane == 0)  // valid tokens
+            *reinterpret_cast<uint32_t*>(ring + slot * C::STAGE + 2 * C::TILE + C::SC) = mask & kAllTokens;
     };
     // dims past D (D < DP) are products of zeros: no branch in the tile loop
-    if (p.D < DP)
-        for (int i = lane * 16; i < S * C::STAGE; i += 32 * 16) *reinterpret_cast<uint4*>(ring + i) = make_uint4(0, 0, 0, 0);
-    __syncwarp();
-    int to_issue = left;
-    if (left > 0) fetch();
+    auto zero_pad = [&](int slot) {
+        if (p.D < DP)
+            for (int i = lane * 16; i < 2 * C::TILE; i += 32 * 16)
+                *reinterpret_cast<uint4*>(ring + slot * C::STAGE + i) = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+    };
+    for (int s = 0; s < S; ++s) zero_pad(s);
+    // S tiles' pages are looked up at once, S - 1 of them copied
+    Fetched ahead[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        if (s < to_issue) {
+            if (s > 0) it.advance(p, step);
+            ahead[s] = fetch();
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) {
+        if (s < to_issue) issue(s, ahead[s]);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    Fetched next = ahead[S - 1];
+    to_issue -= S - 1;
     auto issue_next = [&](int slot) {
         if (to_issue > 0) {
-            issue(slot);
+            issue(slot, next);
             if (--to_issue > 0) {
-                it.next(p, step);
-                fetch();
+                it.advance(p, step);
+                next = fetch();
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    const int row_b = it.b, row_h = it.h;  // a team's row
-#pragma unroll
-    for (int s = 0; s < S - 1; ++s) issue_next(s);
 
     float o[DP / 8][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // rows g and g + 8
@@ -424,65 +458,64 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             set_qfrag(k, a);
         }
     };
-    auto meta_at = [&](int slot) { return *reinterpret_cast<const int4*>(ring + slot * C::STAGE + 2 * C::TILE + C::SC); };
-    __syncwarp();
-    if (left > 0) load_q(row_b, row_h);  // in flight with the first tiles
+    load_q(row.b, row.h);  // in flight with the first tiles
+    int slot = 0, fill = S - 1, pos = 0;
+    while (rem > 0) {
+    // --- a segment ---
+    const int nseg = min(row.ntiles - row.tile, rem);
+    m0 = m1 = -INFINITY;
+    l0 = l1 = 0.f;
+    vref = 0x1p-100f;
 #pragma unroll
     for (int d = 0; d < DP / 8; ++d)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[d][j] = 0.f;
-    bool fresh = true, whole = true;
-    int slot = 0, fill = S - 1;
-    for (int i = 0; i < left; ++i) {
+    if constexpr (KV == kKvE4m3) {
+        // the products run in fp16: each query row is scaled by a power of two to
+        // below 2 (exact but for values 2^-24 below the largest)
+        float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            uint32_t a[4];
+            qfrag(k, a);
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                const float2 x = unpack2<QF16>(a[j]), y = unpack2<QF16>(a[j + 1]);
+                a0 = fmaxf(a0, fmaxf(fabsf(x.x), fabsf(x.y)));
+                a1 = fmaxf(a1, fmaxf(fabsf(y.x), fabsf(y.y)));
+            }
+        }
+        a0 = fmaxf(a0, __shfl_xor_sync(kAllLanes, a0, 1));
+        a0 = fmaxf(a0, __shfl_xor_sync(kAllLanes, a0, 2));
+        a1 = fmaxf(a1, __shfl_xor_sync(kAllLanes, a1, 1));
+        a1 = fmaxf(a1, __shfl_xor_sync(kAllLanes, a1, 2));
+        // 2^-floor(log2 amax), exponent field kept within [1, 253]
+        const uint32_t e0 = min(max(__float_as_uint(a0) >> 23, 1u), 253u);
+        const uint32_t e1 = min(max(__float_as_uint(a1) >> 23, 1u), 253u);
+        const float f0 = __uint_as_float((254u - e0) << 23), f1 = __uint_as_float((254u - e1) << 23);
+        qf0 = p.scale_log2 * __uint_as_float(e0 << 23);
+        qf1 = p.scale_log2 * __uint_as_float(e1 << 23);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            uint32_t a[4];
+            qfrag(k, a);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 x = unpack2<QF16>(a[j]);
+                const float f = j & 1 ? f1 : f0;
+                a[j] = pack2<true>(x.x * f, x.y * f);
+            }
+            set_qfrag(k, a);
+        }
+    }
+    // a warp's tiles of the segment: places of the run that are its own modulo the warps
+    for (int j = p.solo ? 0 : (warp - pos) & (kAttWarps - 1); j < nseg; j += step) {
         cp_async_wait<S - 2>();
         __syncwarp();
         issue_next(fill);
         fill = fill + 1 == S ? 0 : fill + 1;
         const uint8_t* stage = ring + slot * C::STAGE;
         const uint32_t ks_s = ring_s + slot * C::STAGE, vs_s = ks_s + C::TILE;
-        const int4 meta = meta_at(slot);
-        if (fresh) {  // a new row
-            fresh = false;
-            whole = (meta.w & 1) != 0;
-            if constexpr (KV == kKvE4m3) {
-                // the products run in fp16: each query row is scaled by a power of two to
-                // below 2 (exact but for values 2^-24 below the largest)
-                float a0 = 0.f, a1 = 0.f;
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    uint32_t a[4];
-                    qfrag(k, a);
-#pragma unroll
-                    for (int j = 0; j < 4; j += 2) {
-                        const float2 x = unpack2<QF16>(a[j]), y = unpack2<QF16>(a[j + 1]);
-                        a0 = fmaxf(a0, fmaxf(fabsf(x.x), fabsf(x.y)));
-                        a1 = fmaxf(a1, fmaxf(fabsf(y.x), fabsf(y.y)));
-                    }
-                }
-                a0 = fmaxf(a0, __shfl_xor_sync(kAllLanes, a0, 1));
-                a0 = fmaxf(a0, __shfl_xor_sync(kAllLanes, a0, 2));
-                a1 = fmaxf(a1, __shfl_xor_sync(kAllLanes, a1, 1));
-                a1 = fmaxf(a1, __shfl_xor_sync(kAllLanes, a1, 2));
-                // 2^-floor(log2 amax), exponent field kept within [1, 253]
-                const uint32_t e0 = min(max(__float_as_uint(a0) >> 23, 1u), 253u);
-                const uint32_t e1 = min(max(__float_as_uint(a1) >> 23, 1u), 253u);
-                const float f0 = __uint_as_float((254u - e0) << 23), f1 = __uint_as_float((254u - e1) << 23);
-                qf0 = p.scale_log2 * __uint_as_float(e0 << 23);
-                qf1 = p.scale_log2 * __uint_as_float(e1 << 23);
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    uint32_t a[4];
-                    qfrag(k, a);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 x = unpack2<QF16>(a[j]);
-                        const float f = j & 1 ? f1 : f0;
-                        a[j] = pack2<true>(x.x * f, x.y * f);
-                    }
-                    set_qfrag(k, a);
-                }
-            }
-        }
 
         // --- scores of the tile: S[16 heads, TT tokens] ---
         float s[NT][4];
@@ -541,7 +574,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[t][j] *= p.scale_log2;
         }
-        const uint32_t valid = (uint32_t)meta.z;
+        const uint32_t valid = *reinterpret_cast<const uint32_t*>(stage + 2 * C::TILE + C::SC);
         if (valid != kAllTokens) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -634,37 +667,38 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             }
         }
         slot = slot + 1 == S ? 0 : slot + 1;
+    }
 
-        if (p.team) continue;  // joined after the loop
-        const bool row_ends = (meta.w & 2) != 0;
-        if (!row_ends && i + 1 < left) continue;
-        // --- the row, or the run's part of it, is done ---
-        if (i + 1 < left) {  // the next row's queries come while this one is written
-            __syncwarp();
-            const int4 nm = meta_at(slot);
-            load_q(nm.x, nm.y);
-        }
-        const int kvh = p.head_blocks == 1 ? meta.y : meta.y / p.head_blocks, hb = meta.y - kvh * p.head_blocks;
-        const int head0 = kvh * p.group + hb * kAttRows;           // first query head of the row
-        const int heads = min(kAttRows, p.group - hb * kAttRows);  // of 16 rows used
-        fresh = true;
-        l0 += __shfl_xor_sync(kAllLanes, l0, 1);
-        l1 += __shfl_xor_sync(kAllLanes, l1, 1);
-        l0 += __shfl_xor_sync(kAllLanes, l0, 2);
-        l1 += __shfl_xor_sync(kAllLanes, l1, 2);
-        const bool done = whole && row_ends;
+    // --- the segment is done: the row, or the run's part of it ---
+    const int b = row.b, h = row.h;
+    const bool starts = row.tile == 0, ends = row.tile + nseg == row.ntiles;
+    rem -= nseg;
+    pos += nseg;
+    row.advance(p, nseg);
+    if (rem > 0) load_q(row.b, row.h);  // the next row's queries come while this one is written
+    const int kvh = p.head_blocks == 1 ? h : h / p.head_blocks, hb = h - kvh * p.head_blocks;
+    const int head0 = kvh * p.group + hb * kAttRows;           // first query head of the row
+    const int heads = min(kAttRows, p.group - hb * kAttRows);  // of 16 rows used
+    l0 += __shfl_xor_sync(kAllLanes, l0, 1);
+    l1 += __shfl_xor_sync(kAllLanes, l1, 1);
+    l0 += __shfl_xor_sync(kAllLanes, l0, 2);
+    l1 += __shfl_xor_sync(kAllLanes, l1, 2);
+    const bool done = starts && ends;
+    float* part = done ? nullptr : p.partial + ((long long)run * 2 + (starts ? 1 : 0)) * (kAttRows * (p.D + 2));
+    // the runs that a row begins and ends in, for the join (first -1: one run has all of it)
+    if (p.by_row_join && (p.solo ? lane == 0 : tid == 0)) {
+        const int at = b * p.rows_per_seq + h;
+        if (starts) p.first[at] = ends ? -1 : run;
+        if (ends && !starts) p.last[at] = run;
+    }
+    if (p.solo) {
         float w0 = 1.f, w1 = 1.f;
-        float* part = nullptr;
         if (done) {
             w0 = g < heads ? final_weight(p, head0 + g, m0, l0) : 0.f;
             w1 = g + 8 < heads ? final_weight(p, head0 + g + 8, m1, l1) : 0.f;
-        } else {
-            part = p.partial + ((long long)gw * 2 + (whole ? 1 : 0)) * (kAttRows * (p.D + 2));
-            if (c == 0) {
-                if (g < heads) part[2 * g] = m0, part[2 * g + 1] = l0;
-                if (g + 8 < heads) part[2 * g + 16] = m1, part[2 * g + 17] = l1;
-            }
-            part += 2 * kAttRows;
+        } else if (c == 0) {
+            if (g < heads) *reinterpret_cast<float2*>(part + 2 * g) = make_float2(m0, l0);
+            if (g + 8 < heads) *reinterpret_cast<float2*>(part + 2 * g + 16) = make_float2(m1, l1);
         }
         if constexpr (KV == kKvE4m3) {
             w0 *= vref;
@@ -675,194 +709,209 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             if (d * 16 >= p.D) continue;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int row = g + 8 * half;
-                const float w = half ? w1 : w0;
-                if (row >= heads) continue;
-                // a lane's dims: 16 d + 2c, + 1 and 8 on, or (e4m3) 16 d + 4c .. + 3
-                const float lo = o[2 * d][2 * half] * w, hi = o[2 * d + 1][2 * half + 1] * w;
-                const float u = (KV == kKvE4m3 ? o[2 * d + 1][2 * half] : o[2 * d][2 * half + 1]) * w;
-                const float v = (KV == kKvE4m3 ? o[2 * d][2 * half + 1] : o[2 * d + 1][2 * half]) * w;
-                const int d0 = d * 16 + (KV == kKvE4m3 ? 4 * c : 2 * c), d1 = d0 + (KV == kKvE4m3 ? 2 : 8);
+                const int r = g + 8 * half;
+                if (r >= heads) continue;
+                const Quad q = quad<KV>(o[2 * d], o[2 * d + 1], half, half ? w1 : w0);
+                const int d0 = d * 16 + quad_at<KV>(c), d1 = d0 + (KV == kKvE4m3 ? 2 : 8);
                 if (done) {
-                    uint16_t* dst = p.out + meta.x * p.o_token + (long long)(head0 + row) * p.o_head;
-                    *reinterpret_cast<uint32_t*>(dst + d0) = pack2<QF16>(lo, u);
-                    *reinterpret_cast<uint32_t*>(dst + d1) = pack2<QF16>(v, hi);
+                    uint16_t* dst = p.out + b * p.o_token + (long long)(head0 + r) * p.o_head;
+                    *reinterpret_cast<uint32_t*>(dst + d0) = pack2<QF16>(q.a, q.b);
+                    *reinterpret_cast<uint32_t*>(dst + d1) = pack2<QF16>(q.c, q.d);
                 } else {
-                    *reinterpret_cast<float2*>(part + row * p.D + d0) = make_float2(lo, u);
-                    *reinterpret_cast<float2*>(part + row * p.D + d1) = make_float2(v, hi);
+                    float* dst = part + 2 * kAttRows + r * p.D;
+                    *reinterpret_cast<float2*>(dst + d0) = make_float2(q.a, q.b);
+                    *reinterpret_cast<float2*>(dst + d1) = make_float2(q.c, q.d);
                 }
             }
         }
-        // the run that a row begins in, for the join (-1: it ends there too)
-        if (p.by_row_join && whole && lane == 0) p.first[meta.x * p.rows_per_seq + meta.y] = row_ends ? -1 : gw;
-        m0 = m1 = -INFINITY;
-        l0 = l1 = 0.f;
-        vref = 0x1p-100f;
-#pragma unroll
-        for (int d = 0; d < DP / 8; ++d)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[d][j] = 0.f;
+        continue;
     }
-    if (!p.team) return;
-
-    // --- a team: the warps' parts of the row meet in the ring's memory ---
-    l0 += __shfl_xor_sync(kAllLanes, l0, 1);
-    l1 += __shfl_xor_sync(kAllLanes, l1, 1);
-    l0 += __shfl_xor_sync(kAllLanes, l0, 2);
-    l1 += __shfl_xor_sync(kAllLanes, l1, 2);
-    cp_async_wait<0>();
-    __syncthreads();
-    float2* s_ml = reinterpret_cast<float2*>(smem);                      // [warps][16]
-    float* s_o = reinterpret_cast<float*>(smem + kAttWarps * 16 * 8);    // [warps][16][D + 4]: rows on other banks
-    const int ld = p.D + 4;
+    // the warps' parts meet in the ring slots that hold no tile (one of each warp); columns of a
+    // row are moved by 4 (row mod 8) to spread the rows over the banks
+    if (lane == 0) s_slot[warp] = fill;
     if (c == 0) {
-        s_ml[warp * 16 + g] = make_float2(m0, l0);
-        s_ml[warp * 16 + g + 8] = make_float2(m1, l1);
+        s_ml[warp][g] = make_float2(m0, l0);
+        s_ml[warp][g + 8] = make_float2(m1, l1);
     }
-    const float f = KV == kKvE4m3 ? vref : 1.f;
+    {
+        float* mine = reinterpret_cast<float*>(ring + fill * C::STAGE);
+        const float f = KV == kKvE4m3 ? vref : 1.f;
 #pragma unroll
-    for (int d = 0; d < KS; ++d) {
-        if (d * 16 >= p.D) continue;
+        for (int d = 0; d < KS; ++d) {
+            if (d * 16 >= p.D) continue;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float* dst = s_o + (warp * 16 + g + 8 * half) * ld + d * 16 + (KV == kKvE4m3 ? 4 * c : 2 * c);
-            const float lo = o[2 * d][2 * half] * f, hi = o[2 * d + 1][2 * half + 1] * f;
-            const float u = (KV == kKvE4m3 ? o[2 * d + 1][2 * half] : o[2 * d][2 * half + 1]) * f;
-            const float v = (KV == kKvE4m3 ? o[2 * d][2 * half + 1] : o[2 * d + 1][2 * half]) * f;
-            *reinterpret_cast<float2*>(dst) = make_float2(lo, u);
-            *reinterpret_cast<float2*>(dst + (KV == kKvE4m3 ? 2 : 8)) = make_float2(v, hi);
+            for (int half = 0; half < 2; ++half) {
+                if (g + 8 * half >= heads) continue;
+                const Quad q = quad<KV>(o[2 * d], o[2 * d + 1], half, f);
+                float* dst = mine + (g + 8 * half) * DP;
+                const int d0 = d * 16 + quad_at<KV>(c), d1 = d0 + (KV == kKvE4m3 ? 2 : 8);
+                *reinterpret_cast<float2*>(dst + (d0 ^ (g << 2))) = make_float2(q.a, q.b);
+                *reinterpret_cast<float2*>(dst + (d1 ^ (g << 2))) = make_float2(q.c, q.d);
+            }
         }
     }
     __syncthreads();
-    const int kvh = row_h / p.head_blocks, hb = row_h - kvh * p.head_blocks;
-    const int head0 = kvh * p.group + hb * kAttRows, heads = min(kAttRows, p.group - hb * kAttRows);
-    for (int row = warp; row < heads; row += kAttWarps) {
-        float m = -INFINITY, l = 0.f;
-#pragma unroll
-        for (int w = 0; w < kAttWarps; ++w) m = fmaxf(m, s_ml[w * 16 + row].x);
-        float e[kAttWarps];
+    for (int r = warp; r < heads; r += kAttWarps) {
+        float m = -INFINITY, l = 0.f, e[kAttWarps];
+        const float* src[kAttWarps];
 #pragma unroll
         for (int w = 0; w < kAttWarps; ++w) {
-            e[w] = m == -INFINITY ? 0.f : ex2_approx(s_ml[w * 16 + row].x - m);
-            l += e[w] * s_ml[w * 16 + row].y;
+            m = fmaxf(m, s_ml[w][r].x);
+            src[w] = reinterpret_cast<const float*>(smem + w * C::WARP + s_slot[w] * C::STAGE) + r * DP;
         }
-        const float fw = final_weight(p, head0 + row, m, l);
-        uint16_t* dst = p.out + row_b * p.o_token + (long long)(head0 + row) * p.o_head;
+#pragma unroll
+        for (int w = 0; w < kAttWarps; ++w) {
+            e[w] = m == -INFINITY ? 0.f : ex2_approx(s_ml[w][r].x - m);
+            l += e[w] * s_ml[w][r].y;
+        }
+        const float fw = done ? final_weight(p, head0 + r, m, l) : 1.f;
+        if (!done && lane == 0) *reinterpret_cast<float2*>(part + 2 * r) = make_float2(m, l);
         for (int d = 2 * lane; d < p.D; d += 64) {
             float x = 0.f, y = 0.f;
 #pragma unroll
             for (int w = 0; w < kAttWarps; ++w) {
-                const float2 v = *reinterpret_cast<const float2*>(s_o + (w * 16 + row) * ld + d);
+                const float2 v = *reinterpret_cast<const float2*>(src[w] + (d ^ ((r & 7) << 2)));
                 x += e[w] * v.x;
                 y += e[w] * v.y;
             }
-            *reinterpret_cast<uint32_t*>(dst + d) = pack2<QF16>(x * fw, y * fw);
+            if (done)
+                *reinterpret_cast<uint32_t*>(p.out + b * p.o_token + (long long)(head0 + r) * p.o_head + d) =
+                    pack2<QF16>(x * fw, y * fw);
+            else
+                *reinterpret_cast<float2*>(part + 2 * kAttRows + r * p.D + d) = make_float2(x, y);
         }
+    }
+    if (rem > 0) {
+        __syncthreads();  // the slots are free again
+        zero_pad(fill);
+    }
     }
 }
 
 // Joins the parts of rows cut by a run's border.  Job j: row j (by_row_join: its
-// first run in first[j], -1 if one run did it all), or the row that run j
-// continues as the first to do so.  Parts: slot 1 of the first run, slot 0 of
-// the runs that continue the row.  A CTA takes heads_per_cta heads, its 8 warps
-// split over heads and, where those are fewer, over the parts.
+// first and last run), or the row that run j continues as the first to do so.
+// Parts: slot 1 of the first run, slot 0 of the runs that continue the row.  A job's
+// head is the work of join_warps warps: a lane has 4 dims (two times 4 past 128)
+// of every n-th part, and the lanes' running sums meet by shuffles, then in
+// shared memory, always in the same order.
+constexpr int kJoinWarps = 8;  // per CTA
+
+struct Sums {
+    float m, l;
+    float4 v[2];
+};
+__device__ __forceinline__ void add_scaled(float4& a, float f, const float4& b, float h) {
+    a.x = a.x * f + b.x * h;
+    a.y = a.y * f + b.y * h;
+    a.z = a.z * f + b.z * h;
+    a.w = a.w * f + b.w * h;
+}
+// a += b, each about its own maximum
+__device__ __forceinline__ void join(Sums& a, const Sums& b) {
+    const float m = fmaxf(a.m, b.m);
+    const float f = m == -INFINITY ? 0.f : ex2_approx(a.m - m), h = m == -INFINITY ? 0.f : ex2_approx(b.m - m);
+    a.m = m;
+    a.l = a.l * f + b.l * h;
+    add_scaled(a.v[0], f, b.v[0], h);
+    add_scaled(a.v[1], f, b.v[1], h);
+}
+
 template <bool QF16>
-__global__ void __launch_bounds__(256) attend_join_kernel(AttendParams p) {
-    __shared__ float s_m[8], s_l[8];
-    __shared__ float s_o[8 * 256];
+__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendParams p) {
+    __shared__ float s_ml[kJoinWarps][2];
+    __shared__ __align__(16) float s_v[kJoinWarps][256];
     pdl_wait();
-    const int j = blockIdx.x;
-    const int nruns = p.runs;
-    int run0, row;
-    if (p.by_row_join) {
-        run0 = p.first[j];
-        row = j;
-        if (run0 < 0) return;
-    } else {
-        row = p.cont[j];
-        if (row < 0 || p.cont[j - 1] == row) return;  // run 0 starts a row: cont[0] is -1
-        run0 = j - 1;
-    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int nparts = 1;
-    for (uint32_t same = kAllLanes; same == kAllLanes;) {
-        const int r = run0 + nparts + lane;
-        same = __ballot_sync(kAllLanes, r < nruns && p.cont[r] == row);
-        nparts += same == kAllLanes ? 32 : __ffs(~same) - 1;
-    }
-    const int b = row / p.rows_per_seq, h = row - b * p.rows_per_seq;
-    const int hb = h % p.head_blocks, head0 = (h / p.head_blocks) * p.group + hb * kAttRows;
-    const int heads = min(kAttRows, p.group - hb * kAttRows);
-    const int psize = kAttRows * (p.D + 2);
-    auto part = [&](int i) { return p.partial + ((long long)(run0 + i) * 2 + (i == 0 ? 1 : 0)) * psize; };
-    const int pw = p.heads_per_cta >= 8 ? 1 : 8 / p.heads_per_cta;  // warps per head
-    const int hw = 8 / pw;
-    const int h_end = min(heads, ((int)blockIdx.y + 1) * p.heads_per_cta);
-    for (int hh = blockIdx.y * p.heads_per_cta; hh < h_end; hh += hw) {
-        const int head = hh + warp / pw, sub = warp % pw;
-        float m = -INFINITY, l = 0.f;
-        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (head < h_end) {
-            const int i0 = nparts * sub / pw, i1 = nparts * (sub + 1) / pw;
-            for (int i = i0 + lane; i < i1; i += 32) m = fmaxf(m, part(i)[2 * head]);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAllLanes, m, o));
-            const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-            for (int i = i0; i < i1; ++i) {
-                const float* q = part(i);
-                const float w = ex2_approx(q[2 * head] - base);
-                l += w * q[2 * head + 1];
-                const float* src = q + 2 * kAttRows + head * p.D;
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k * 32 + lane < p.D) acc[k] += w * src[k * 32 + lane];
-            }
-        }
-        if (pw > 1) {  // the warps of a head join in shared memory, in order
-            if (lane == 0) s_m[warp] = m, s_l[warp] = l;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k * 32 + lane < p.D) s_o[warp * 256 + k * 32 + lane] = acc[k];
-            __syncthreads();
-            if (sub == 0 && head < h_end) {
-                float top = -INFINITY;
-                for (int w = 0; w < pw; ++w) top = fmaxf(top, s_m[warp + w]);
-                m = top;
-                l = 0.f;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-                for (int w = 0; w < pw; ++w) {
-                    const float f = top == -INFINITY ? 0.f : ex2_approx(s_m[warp + w] - top);
-                    l += f * s_l[warp + w];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (k * 32 + lane < p.D) acc[k] += f * s_o[(warp + w) * 256 + k * 32 + lane];
+    const int per = min(kAttRows, p.group);  // heads of a row
+    const int item = (blockIdx.x * kJoinWarps + warp) / p.join_warps, sub = warp % p.join_warps;
+    const int j = item / per, head = item - j * per;
+    int run0 = -1, row = -1, nparts = 0;
+    if (j < p.jobs) {
+        if (p.by_row_join) {
+            run0 = p.first[j];
+            row = j;
+            if (run0 >= 0) nparts = p.last[j] - run0 + 1;  // (not set where one run has the row)
+        } else {
+            row = p.cont[j];
+            if (row >= 0 && p.cont[j - 1] != row) {  // run 0 starts a row: cont[0] is -1
+                run0 = j - 1;
+                nparts = 1;
+                for (uint32_t same = kAllLanes; same == kAllLanes;) {
+                    const int r = run0 + nparts + lane;
+                    same = __ballot_sync(kAllLanes, r < p.runs && p.cont[r] == row);
+                    nparts += same == kAllLanes ? 32 : __ffs(~same) - 1;
                 }
             }
-            __syncthreads();
         }
-        if (sub == 0 && head < h_end) {
-            const float w = final_weight(p, head0 + head, m, l);
-            uint16_t* dst = p.out + b * p.o_token + (long long)(head0 + head) * p.o_head;
+    }
+    const int b = nparts ? row / p.rows_per_seq : 0, h = nparts ? row - b * p.rows_per_seq : 0;
+    const int hb = h % p.head_blocks, head0 = (h / p.head_blocks) * p.group + hb * kAttRows;
+    if (head >= p.group - hb * kAttRows) nparts = 0;  // a last block of fewer heads
+    const int psize = kAttRows * (p.D + 2);
+    // lanes of a part: a power of two of 4 dims each, at most the warp
+    const int lp = p.D <= 16 ? 4 : p.D <= 32 ? 8 : p.D <= 64 ? 16 : 32;
+    const int d = (lane & (lp - 1)) * 4, splits = (32 / lp) * p.join_warps, at = sub * (32 / lp) + lane / lp;
+    Sums a = {-INFINITY, 0.f, {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)}};
+#pragma unroll 4
+    for (int i = at; i < nparts; i += splits) {
+        const float* q = p.partial + ((long long)(run0 + i) * 2 + (i == 0 ? 1 : 0)) * psize;
+        const float2 ml = *reinterpret_cast<const float2*>(q + 2 * head);
+        const float* src = q + 2 * kAttRows + head * p.D + d;
+        Sums x = {ml.x, ml.y, {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)}};
+        if (d < p.D) x.v[0] = *reinterpret_cast<const float4*>(src);
+        if (d + 128 < p.D) x.v[1] = *reinterpret_cast<const float4*>(src + 128);
+        join(a, x);
+    }
+    for (int o = lp; o < 32; o <<= 1) {
+        Sums x;
+        x.m = __shfl_xor_sync(kAllLanes, a.m, o);
+        x.l = __shfl_xor_sync(kAllLanes, a.l, o);
+        x.v[0] = make_float4(__shfl_xor_sync(kAllLanes, a.v[0].x, o), __shfl_xor_sync(kAllLanes, a.v[0].y, o),
+                             __shfl_xor_sync(kAllLanes, a.v[0].z, o), __shfl_xor_sync(kAllLanes, a.v[0].w, o));
+        x.v[1] = a.v[1];  // only past 128 dims, where a part takes the warp
+        join(a, x);
+    }
+    if (p.join_warps > 1) {
+        if (lane == 0) s_ml[warp][0] = a.m, s_ml[warp][1] = a.l;
+        if (lane < lp && d < p.D) *reinterpret_cast<float4*>(&s_v[warp][d]) = a.v[0];
+        if (d + 128 < p.D) *reinterpret_cast<float4*>(&s_v[warp][d + 128]) = a.v[1];
+        __syncthreads();
+        if (sub == 0 && d < p.D)
+            for (int w = 1; w < p.join_warps; ++w) {
+                Sums x = {s_ml[warp + w][0], s_ml[warp + w][1], {*reinterpret_cast<const float4*>(&s_v[warp + w][d]), a.v[1]}};
+                if (d + 128 < p.D) x.v[1] = *reinterpret_cast<const float4*>(&s_v[warp + w][d + 128]);
+                join(a, x);
+            }
+    }
+    if (nparts && sub == 0 && lane < lp) {
+        const float w = final_weight(p, head0 + head, a.m, a.l);
+        uint16_t* dst = p.out + b * p.o_token + (long long)(head0 + head) * p.o_head + d;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (k * 32 + lane < p.D) dst[k * 32 + lane] = (uint16_t)pack2<QF16>(acc[k] * w, 0.f);
-        }
+        for (int k = 0; k < 2; ++k)
+            if (d + 128 * k < p.D) {
+                *reinterpret_cast<uint32_t*>(dst + 128 * k) = pack2<QF16>(a.v[k].x * w, a.v[k].y * w);
+                *reinterpret_cast<uint32_t*>(dst + 128 * k + 2) = pack2<QF16>(a.v[k].z * w, a.v[k].w * w);
+            }
     }
 }
 
 namespace {
 
-// Runs are at least this many tokens; rows of at most this many are not cut; a
-// CTA takes a row of its own where all rows fit at once and none is longer.
-constexpr int kMinTokens = 64;
+// A CTA's run is at least this many tiles (one per warp), a warp's two; rows of at
+// most kWholeTokens take a warp each; a CTA takes a row of its own where all rows
+// fit at once and none is longer than kTeamTokens; from kSoloRows rows on, runs
+// are a warp's: fewer waits at the rows' ends, and few parts to a row anyway.
+constexpr int kMinTiles = kAttWarps;
+constexpr int kMinSoloTiles = 2;
+#ifndef MOE_SOLO_ROWS
+#define MOE_SOLO_ROWS 96
+#endif
+constexpr int kSoloRows = MOE_SOLO_ROWS;
 constexpr int kWholeTokens = 128;
 constexpr int kTeamTokens = 512;
 
 int dp_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 int ctas_per_sm(int dp, bool e4m3) { return dp == 64 && e4m3 ? 3 : dp == 256 ? 1 : 2; }
-int tile_tokens(int dp, bool e4m3) { return e4m3 || dp == 64 ? 32 : 16; }
 
 template <int DP, int KV, bool QF16>
 cudaError_t launch_attend_t(const AttendParams& p, int grid, cudaStream_t st) {
@@ -886,16 +935,20 @@ cudaError_t launch_attend_d(const AttendParams& p, int grid, cudaStream_t st) {
 
 // How the rows are given to warps; the workspace is for the parts of cut rows.
 void attend_plan(int B, int Hq, int Hkv, int D, bool e4m3, int most, int sms, AttendPlan* w) {
-    const int ctas = sms * ctas_per_sm(dp_of(D), e4m3), runs = ctas * kAttWarps;
+    const int ctas = sms * ctas_per_sm(dp_of(D), e4m3);
     const long long rows = (long long)B * Hkv * ((Hq / Hkv + kAttRows - 1) / kAttRows);
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-    w->runs = runs;
     w->team = rows <= ctas && most <= kTeamTokens;
     w->by_row = !w->team && most <= kWholeTokens;
+    w->solo = w->by_row || (!w->team && rows >= kSoloRows);
+    const int runs = w->solo ? ctas * kAttWarps : ctas;
+    w->runs = runs;
+    w->ctas = w->team ? (int)rows : ctas;
     w->by_row_join = rows <= runs;
     w->cont = 0;
     w->first = up((size_t)runs * 4);
-    w->partial = w->first + up((size_t)(rows <= runs ? rows : 1) * 4);
+    w->last = w->first + up((size_t)(rows <= runs ? rows : 1) * 4);
+    w->partial = w->last + up((size_t)(rows <= runs ? rows : 1) * 4);
     w->total = w->team || w->by_row ? 0 : w->partial + (size_t)runs * 2 * kAttRows * (D + 2) * 4;
 }
 
@@ -906,6 +959,7 @@ cudaError_t launch_attend(const AttendParams& p_in, const AttendPlan& w, int kv_
     p.runs = w.runs;
     p.team = w.team;
     p.by_row = w.by_row;
+    p.solo = w.solo;
     p.group = p.Hq / p.Hkv;
     p.head_blocks = (p.group + kAttRows - 1) / kAttRows;
     p.rows_per_seq = p.Hkv * p.head_blocks;
@@ -914,28 +968,30 @@ cudaError_t launch_attend(const AttendParams& p_in, const AttendPlan& w, int kv_
     if ((p.page_size & (p.page_size - 1)) == 0)
         for (p.page_shift = 0; (1 << p.page_shift) < p.page_size;) ++p.page_shift;
     const long long rows = (long long)p.B * p.rows_per_seq;
-    p.min_units = kMinTokens / tile_tokens(dp_of(p.D), e4m3);
+    p.min_tiles = p.solo ? kMinSoloTiles : kMinTiles;
     if (w.total) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);
         p.by_row_join = w.by_row_join;
         p.cont = reinterpret_cast<int32_t*>(ws + w.cont);
         p.first = reinterpret_cast<int32_t*>(ws + w.first);
+        p.last = reinterpret_cast<int32_t*>(ws + w.last);
         p.partial = reinterpret_cast<float*>(ws + w.partial);
     }
-    const int grid = p.team ? (int)rows : w.runs / kAttWarps;
+    const int grid = w.ctas;
     cudaError_t e;
     if (e4m3)
         e = fp16 ? launch_attend_d<kKvE4m3, true>(p, grid, st) : launch_attend_d<kKvE4m3, false>(p, grid, st);
     else
         e = fp16 ? launch_attend_d<kKvFp16, true>(p, grid, st) : launch_attend_d<kKvBf16, false>(p, grid, st);
     if (e != cudaSuccess || p.by_row || p.team) return e;
-    // few rows: a CTA per head, its warps over the parts; many: a CTA per row
+    // warps per head by the parts that a row can have on average
     const int heads = p.group < kAttRows ? p.group : kAttRows;
-    const int jobs = p.by_row_join ? (int)rows : p.runs;
-    p.heads_per_cta = jobs <= 256 ? 1 : 8;
-    const dim3 jg(jobs, (heads + p.heads_per_cta - 1) / p.heads_per_cta);
-    return fp16 ? launch_pdl(attend_join_kernel<true>, jg, dim3(256), 0, st, p)
-                : launch_pdl(attend_join_kernel<false>, jg, dim3(256), 0, st, p);
+    p.jobs = p.by_row_join ? (int)rows : p.runs;
+    p.join_warps = 1;
+    while (p.join_warps < kJoinWarps && (long long)p.join_warps * 8 * p.jobs <= p.runs) p.join_warps *= 2;
+    const dim3 jg((unsigned)(((long long)p.jobs * heads * p.join_warps + kJoinWarps - 1) / kJoinWarps));
+    return fp16 ? launch_pdl(attend_join_kernel<true>, jg, dim3(kJoinWarps * 32), 0, st, p)
+                : launch_pdl(attend_join_kernel<false>, jg, dim3(kJoinWarps * 32), 0, st, p);
 }
 
 }  // namespace moe
