@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -947,7 +948,9 @@ extern "C" moe_status moe_paged_attention(const moe_kv_cache* cache, const void*
     p.num_pages = cache->num_pages;
     p.page_size = cache->page_size;
     p.window = window;
-    p.scale_log2 = scale * 1.4426950408889634f;
+    // a scale of 0 becomes the smallest normal: the scores' factor must not turn -inf into NaN
+    p.scale_log2 = fmaxf(fabsf(scale) * 1.4426950408889634f, 1.17549435e-38f);
+    p.q_sign = scale < 0.f ? 0x80008000u : 0u;
     p.status = status;
     return launch_attend(p, w, cache->dtype, dtype == MOE_FP16, workspace, static_cast<cudaStream_t>(stream)) ==
                    cudaSuccess

@@ -41,8 +41,10 @@ template <int DP, int KV>
 struct AttCfg {
     static constexpr int ES = KV == kKvE4m3 ? 1 : 2;       // bytes of a cached value
     static constexpr int TT = KV == kKvE4m3 || DP == 64 ? 32 : 16;  // tokens per tile
-    static constexpr int ROW = DP * ES;                    // bytes of a token's row in shared memory
-    static constexpr int CH = ROW / 16;                    // its 16-byte chunks
+    static constexpr int CH = DP * ES / 16;                // 16-byte chunks of a token's row
+    static constexpr int LANES = CH <= 4 ? 4 : CH <= 8 ? 8 : CH <= 16 ? 16 : 32;  // lanes that copy it
+    static constexpr int PITCH = DP == 96 ? CH | 1 : CH;   // chunks from row to row in shared memory
+    static constexpr int ROW = PITCH * 16;
     static constexpr int STAGES = DP == 64 && KV == kKvE4m3 ? 4 : DP == 256 && KV == kKvE4m3 ? 2 : 3;
     static constexpr int TILE = TT * ROW;                  // bytes of a K (or V) tile
     static constexpr int SC = KV == kKvE4m3 ? 2 * TT * 4 : 0;
@@ -114,10 +116,11 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
 
 // Byte of chunk c (16 bytes) of token row r in a tile: 8 rows of one chunk
 // column fall on 8 different bank groups, for the loads and for ldmatrix.
-template <int CH>
+template <typename C>
 __device__ __forceinline__ uint32_t swz(int r, int c) {
-    if (CH >= 8) return (uint32_t)(r * CH + ((c & ~7) | ((c ^ r) & 7))) * 16u;
-    return (uint32_t)(r * CH + (c ^ ((r >> 1) & 3))) * 16u;  // CH == 4: two rows per 128 bytes
+    if (C::PITCH & 1) return (uint32_t)(r * C::PITCH + c) * 16u;  // an odd pitch does it alone
+    if (C::CH >= 8) return (uint32_t)(r * C::CH + ((c & ~7) | ((c ^ r) & 7))) * 16u;
+    return (uint32_t)(r * C::CH + (c ^ ((r >> 1) & 3))) * 16u;  // CH == 4: two rows per 128 bytes
 }
 
 __device__ __forceinline__ int seen_tokens(const AttendParams& p, int b, int* start) {
@@ -292,8 +295,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
     // --- the ring ---
     uint8_t* ring = smem + warp * C::WARP;
     const uint32_t ring_s = smem_u32(ring);
-    constexpr int RPS = 32 / (C::CH < 32 ? C::CH : 32);  // token rows per step of the warp
-    const int ch = lane % C::CH, r0 = lane / C::CH;
+    constexpr int RPS = 32 / C::LANES;  // token rows per step of the warp
+    const int ch = lane % C::LANES, r0 = lane / C::LANES;
     const bool in = ch * (16 / C::ES) < p.D;
     // byte offsets of the lane's chunk in a group of 16 tokens, and of a step
     const long long k_lane = (long long)r0 * p.cache.k_token * C::ES + ch * 16, k_step = RPS * p.cache.k_token * C::ES;
@@ -336,7 +339,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
                     if (in) {
 #pragma unroll
                         for (int i = 0; i < 16 / RPS; ++i) {
-                            const uint32_t at = dst + swz<C::CH>(16 * hh + r0 + i * RPS, ch);
+                            const uint32_t at = dst + swz<C>(16 * hh + r0 + i * RPS, ch);
                             cp_async16(at, ks + i * k_step);
                             cp_async16(at + C::TILE, vs + i * v_step);
                         }
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
 #pragma unroll
                     for (int i = 0; i < 16 / RPS; ++i) {
                         const int r = 16 * hh + r0 + i * RPS;
-                        const uint32_t at = dst + swz<C::CH>(r, ch);
+                        const uint32_t at = dst + swz<C>(r, ch);
                         const bool ok = (mask >> r) & 1u;
                         cp_async16z(at, ok ? ks + i * k_step : kb, ok);
                         cp_async16z(at + C::TILE, ok ? vs + i * v_step : vb, ok);
@@ -358,7 +361,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
                 const int r = r0 + i * RPS;
                 const long long pid = __shfl_sync(kAllLanes, f.pid, r), off = __shfl_sync(kAllLanes, f.off, r);
                 const bool ok = (mask >> r) & 1u;
-                const uint32_t at = dst + swz<C::CH>(r, ch);
+                const uint32_t at = dst + swz<C>(r, ch);
                 if (in) {
                     cp_async16z(at, ok ? kb + (pid * p.cache.k_page + off * p.cache.k_token) * C::ES + ch * 16 : kb, ok);
                     cp_async16z(at + C::TILE, ok ? vb + (pid * p.cache.v_page + off * p.cache.v_token) * C::ES + ch * 16 : vb, ok);
@@ -411,7 +414,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
 
     float o[DP / 8][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // rows g and g + 8
-    float qf0 = p.scale_log2, qf1 = p.scale_log2;              // times the query row's power of two (e4m3)
+    // positive factors of the scores: |scale| log2 e, times the query row's power of two (e4m3)
+    float qf0 = p.scale_log2, qf1 = p.scale_log2;
     float vref = 0x1p-100f;                                    // e4m3: the accumulator's value scale
     uint32_t qr[DP <= 128 ? KS : 1][4];
     uint32_t* qs = reinterpret_cast<uint32_t*>(ring + S * C::STAGE);
@@ -455,6 +459,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
                     a[3] = *reinterpret_cast<const uint32_t*>(q1 + cb);
                 }
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[j] ^= p.q_sign;
             set_qfrag(k, a);
         }
     };
@@ -533,7 +539,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
 #pragma unroll
                 for (int t = 0; t < KT; ++t) {
                     uint32_t b[4];
-                    ldsm4(ks_s + swz<C::CH>(16 * t + r, 2 * k + hi), b);
+                    ldsm4(ks_s + swz<C>(16 * t + r, 2 * k + hi), b);
                     mma16816<F16>(s[2 * t], a, b[0], b[1]);
                     mma16816<F16>(s[2 * t + 1], a, b[2], b[3]);
                 }
@@ -545,13 +551,13 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             for (int k = 0; k < KS; ++k) {
                 uint32_t a[4], b[4];
                 qfrag(k, a);
-                ldsm4(ks_s + swz<C::CH>(r, k), b);
+                ldsm4(ks_s + swz<C>(r, k), b);
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
                     mma16816<F16>(s[t], a, e4m3x2_to_f16x2(b[t]), e4m3x2_to_f16x2(b[t] >> 16));
             }
         }
-        // --- scale, mask, running maximum ---
+        // --- key scales, mask, running maximum (of scores before the positive factors qf) ---
         float vr[NT][2];  // e4m3: value scale of the lane's tokens over the accumulator's
         float vmax = 0.f;
         if constexpr (KV == kKvE4m3) {
@@ -560,19 +566,14 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             for (int t = 0; t < NT; ++t) {
                 const float2 kk = *reinterpret_cast<const float2*>(sck + t * 8 + 2 * c);
                 const float2 vv = *reinterpret_cast<const float2*>(sck + TT + t * 8 + 2 * c);
-                s[t][0] *= kk.x * qf0;
-                s[t][1] *= kk.y * qf0;
-                s[t][2] *= kk.x * qf1;
-                s[t][3] *= kk.y * qf1;
+                s[t][0] *= kk.x;
+                s[t][1] *= kk.y;
+                s[t][2] *= kk.x;
+                s[t][3] *= kk.y;
                 vr[t][0] = vv.x;
                 vr[t][1] = vv.y;
                 vmax = fmaxf(vmax, fmaxf(vv.x, vv.y));
             }
-        } else {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[t][j] *= p.scale_log2;
         }
         const uint32_t valid = *reinterpret_cast<const uint32_t*>(stage + 2 * C::TILE + C::SC);
         if (valid != kAllTokens) {
@@ -598,9 +599,9 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             vmax = fmaxf(vmax, __shfl_xor_sync(kAllLanes, vmax, 2));
             vnew = fmaxf(vref, vmax);
         }
-        const float b0 = t0 == -INFINITY ? 0.f : t0, b1 = t1 == -INFINITY ? 0.f : t1;
+        const float b0 = t0 == -INFINITY ? 0.f : t0 * qf0, b1 = t1 == -INFINITY ? 0.f : t1 * qf1;
         if (__any_sync(kAllLanes, t0 != m0 || t1 != m1 || vnew != vref)) {
-            const float c0 = ex2_approx(m0 - b0), c1 = ex2_approx(m1 - b1);
+            const float c0 = ex2_approx(m0 * qf0 - b0), c1 = ex2_approx(m1 * qf1 - b1);
             const float cv = KV == kKvE4m3 ? vref / vnew : 1.f;
             l0 *= c0;
             l1 *= c1;
@@ -621,10 +622,10 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             float e[4];
-            e[0] = ex2_approx(s[t][0] - b0);
-            e[1] = ex2_approx(s[t][1] - b0);
-            e[2] = ex2_approx(s[t][2] - b1);
-            e[3] = ex2_approx(s[t][3] - b1);
+            e[0] = ex2_approx(fmaf(s[t][0], qf0, -b0));
+            e[1] = ex2_approx(fmaf(s[t][1], qf0, -b0));
+            e[2] = ex2_approx(fmaf(s[t][2], qf1, -b1));
+            e[3] = ex2_approx(fmaf(s[t][3], qf1, -b1));
             l0 += e[0] + e[1];
             l1 += e[2] + e[3];
             if constexpr (KV == kKvE4m3) {
@@ -645,7 +646,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
 #pragma unroll
                 for (int t = 0; t < KT; ++t) {
                     uint32_t b[4];
-                    ldsm4_t(vs_s + swz<C::CH>(16 * t + r, 2 * d + hi), b);
+                    ldsm4_t(vs_s + swz<C>(16 * t + r, 2 * d + hi), b);
                     mma16816<F16>(o[2 * d], pa[t], b[0], b[1]);
                     mma16816<F16>(o[2 * d + 1], pa[t], b[2], b[3]);
                 }
@@ -657,7 +658,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
 #pragma unroll
             for (int d = 0; d < KS; ++d) {
                 uint32_t b[4];
-                ldsm4_t(vs_s + swz<C::CH>(r, d), b);
+                ldsm4_t(vs_s + swz<C>(r, d), b);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t lo = __byte_perm(b[2 * k], 0, 0x3120), hi = __byte_perm(b[2 * k + 1], 0, 0x3120);
@@ -683,6 +684,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
     l1 += __shfl_xor_sync(kAllLanes, l1, 1);
     l0 += __shfl_xor_sync(kAllLanes, l0, 2);
     l1 += __shfl_xor_sync(kAllLanes, l1, 2);
+    m0 *= qf0;  // from here on in powers of two
+    m1 *= qf1;
     const bool done = starts && ends;
     float* part = done ? nullptr : p.partial + ((long long)run * 2 + (starts ? 1 : 0)) * (kAttRows * (p.D + 2));
     // the runs that a row begins and ends in, for the join (first -1: one run has all of it)
@@ -910,7 +913,7 @@ constexpr int kSoloRows = MOE_SOLO_ROWS;
 constexpr int kWholeTokens = 128;
 constexpr int kTeamTokens = 512;
 
-int dp_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+int dp_of(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
 int ctas_per_sm(int dp, bool e4m3) { return dp == 64 && e4m3 ? 3 : dp == 256 ? 1 : 2; }
 
 template <int DP, int KV, bool QF16>
@@ -926,6 +929,7 @@ template <int KV, bool QF16>
 cudaError_t launch_attend_d(const AttendParams& p, int grid, cudaStream_t st) {
     switch (dp_of(p.D)) {
         case 64: return launch_attend_t<64, KV, QF16>(p, grid, st);
+        case 96: return launch_attend_t<96, KV, QF16>(p, grid, st);
         case 128: return launch_attend_t<128, KV, QF16>(p, grid, st);
         default: return launch_attend_t<256, KV, QF16>(p, grid, st);
     }

@@ -92,7 +92,8 @@ struct AttendParams {
     int B, Hq, Hkv, D;
     int num_pages, page_size, max_tokens;  // max_tokens: table columns * page_size
     int window;                            // 0: none
-    float scale_log2;                      // scale * log2(e)
+    float scale_log2;                      // |scale| log2(e), not 0
+    uint32_t q_sign;                       // the queries' sign bits to flip (a negative scale)
     uint32_t* status;                      // error word or null
     // set at launch
     int group, head_blocks, rows_per_seq;  // query heads per key head; blocks of 16 of them; rows of a sequence
