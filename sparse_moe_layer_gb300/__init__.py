@@ -9,9 +9,7 @@ library is missing, importing the binding's functions raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
-import struct
 
 import torch
 
@@ -101,6 +99,7 @@ def lib():
         L.moe_forward_gated.argtypes = [vp, vp, i32, i64, vp, i32] + [vp] * 6 + [i32] * 5 + [vp, vp, sz, vp]
         L.moe_forward_gated.restype = i32
         f32 = ctypes.c_float
+        # (called through _binding below; these serve direct callers of the C ABI)
         L.moe_rotate_append.argtypes = [vp] * 4 + [i32] + [i64] * 6 + [vp] * 3 + [i32, i32, f32, i32, i32, vp, i64, i64,
                                                                                 vp, vp]
         L.moe_rotate_append.restype = i32
@@ -117,6 +116,20 @@ def lib():
         L.moe_status_str.restype = ctypes.c_char_p
         _lib = L
     return _lib
+
+
+_calls = None
+
+
+def _entries():
+    """The compiled entries of the decoder-block operators (csrc/binding.cpp)."""
+    global _calls
+    if _calls is None:
+        lib()
+        from . import _binding as b
+        b.set_error(MoeError)
+        _calls = b
+    return _calls
 
 
 def pad128(n: int) -> int:
@@ -525,13 +538,8 @@ def route_experts(logits, top_k: int, score: str = "softmax", bias=None, groups:
     group_top (1 or 2) best choices stay open; renormalize divides the weights by their sum.
     The defaults are the layer's own rule, softmax over the chosen logits.  Ties go to the
     lower index."""
-    g, dt, T, E = _gate(logits, score, bias, groups, top_groups, group_top, renormalize, scale)
-    idx = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
-    w = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
-    if T:
-        _check(lib().moe_route_experts(ctypes.byref(g), logits.data_ptr(), dt, logits.stride(0) if T > 1 else E, T, E,
-                                       top_k, idx.data_ptr(), w.data_ptr(), _stream(stream)), "moe_route_experts")
-    return idx, w
+    return (_calls or _entries()).route_experts(logits, top_k, _SCORES.get(score, -1), bias, groups, top_groups, group_top,
+                                                renormalize, scale, None if stream is None else stream.cuda_stream)
 
 
 def forward_gated(x, logits, w13, s13, b13, w2, s2, b2, top_k: int, score: str = "softmax", bias=None, groups: int = 1,
@@ -563,53 +571,9 @@ def forward_gated(x, logits, w13, s13, b13, w2, s2, b2, top_k: int, score: str =
     return out
 
 
-_KV = struct.Struct("4P9q5i4x")  # moe_kv_cache
-
-
 def new_status(device=None) -> torch.Tensor:
     """A zeroed device error word for `rotate_append` and `paged_attention` (read it with `read_device_status`)."""
     return torch.zeros(4, dtype=torch.uint8, device=device or "cuda")
-
-
-def _cache(k_cache, v_cache, k_scale, v_scale):
-    """Checked cache tensors [pages, heads, page, D]: (moe_kv_cache, heads, page, D, dtype code)."""
-    dt = _DTYPES.get(k_cache.dtype, 2)
-    if not k_cache.is_cuda or not v_cache.is_cuda:
-        raise ValueError("k_cache and v_cache must be CUDA tensors")
-    if dt == 2 or v_cache.dtype != k_cache.dtype:
-        raise ValueError(f"k_cache and v_cache must both be bf16, fp16 or uint8 (e4m3 codes), got {k_cache.dtype}, "
-                         f"{v_cache.dtype}")
-    shape = k_cache.shape
-    if len(shape) != 4 or v_cache.shape != shape:
-        raise ValueError("k_cache and v_cache must both be [pages, heads, page, D]")
-    ks, vs = k_cache.stride(), v_cache.stride()
-    if ks[3] != 1 or vs[3] != 1:
-        raise ValueError("the last dim of k_cache and v_cache must be contiguous")
-    kp = vp = 0
-    ss = (0, 0, 0)
-    if dt == 3:
-        if k_scale is None or v_scale is None or k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 \
-                or not k_scale.is_cuda or not v_scale.is_cuda:
-            raise ValueError("an e4m3 cache needs k_scale and v_scale, fp32 CUDA tensors")
-        ss = k_scale.stride()
-        if k_scale.shape != shape[:3] or v_scale.shape != shape[:3] or v_scale.stride() != ss:
-            raise ValueError("k_scale and v_scale must be [pages, heads, page] with equal strides")
-        kp, vp = k_scale.data_ptr(), v_scale.data_ptr()
-    elif k_scale is not None or v_scale is not None:
-        raise ValueError("scales belong to an e4m3 cache (uint8)")
-    P, H, S, D = shape
-    return (_KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), kp, vp, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], *ss, dt,
-                     P, S, H, D), H, S, D, dt)
-
-
-def _index(t, n: int, dtype, name: str) -> int:
-    if not t.is_cuda or t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor [{n}]")
-    return t.data_ptr()
-
-
-def _status_ptr(status):
-    return None if status is None else _dev(status, torch.uint8, "status")
 
 
 def rotate_append(q, k, v, positions, slots, k_cache, v_cache, inv_freq, k_scale=None, v_scale=None,
@@ -623,43 +587,16 @@ def rotate_append(q, k, v, positions, slots, k_cache, v_cache, inv_freq, k_scale
     any strides with the last dim contiguous.  inv_freq fp64 [R / 2] rotates the first R dims, in
     pairs (i, i + R/2) or, interleaved, (2i, 2i + 1); cos and sin are multiplied by rope_scale.
     status (`new_status`): set by a slot past the last page."""
-    kv, Hkv, _, D, cdt = _cache(k_cache, v_cache, k_scale, v_scale)
-    if not (q.is_cuda and k.is_cuda and v.is_cuda):
-        raise ValueError("q, k and v must be CUDA tensors")
-    dt = _DTYPES.get(q.dtype, 3)
-    if dt > 1 or k.dtype != q.dtype or v.dtype != q.dtype or (cdt != 3 and cdt != dt):
-        raise ValueError("q, k and v must be bf16 or fp16 alike, and a 16-bit cache of their type")
-    N, Hq = q.shape[0], q.shape[1]
-    if q.dim() != 3 or q.shape[2] != D or k.shape != (N, Hkv, D) or v.shape != (N, Hkv, D):
-        raise ValueError(f"q must be [N, Hq, {D}], k and v [N, {Hkv}, {D}]")
-    if q_out is None:
-        q_out = torch.empty((N, Hq, D), dtype=q.dtype, device=q.device)
-    elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_cuda:
-        raise ValueError("q_out must be like q")
-    qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), q_out.stride()
-    if qs[2] != 1 or ks[2] != 1 or vs[2] != 1 or os_[2] != 1:
-        raise ValueError("the last dim of q, k, v and q_out must be contiguous")
-    if inv_freq.dtype != torch.float64 or not inv_freq.is_cuda or not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be a contiguous fp64 CUDA tensor")
-    pos, sl = _index(positions, N, torch.int64, "positions"), _index(slots, N, torch.int64, "slots")
-    if N:
-        _check(lib().moe_rotate_append(kv, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, qs[0], qs[1], ks[0], ks[1],
-                                       vs[0], vs[1], pos, sl, inv_freq.data_ptr(), 2 * inv_freq.numel(), interleaved,
-                                       rope_scale, N, Hq, q_out.data_ptr(), os_[0], os_[1], _status_ptr(status),
-                                       _stream(stream)), "moe_rotate_append")
-    return q_out
-
-
-@functools.lru_cache(maxsize=4096)
-def _attention_bytes(B: int, q_heads: int, kv_heads: int, head_dim: int, dtype: int, tokens: int) -> int:
-    return int(lib().moe_attention_workspace_size(B, q_heads, kv_heads, head_dim, dtype, tokens))
+    return (_calls or _entries()).rotate_append(q, k, v, positions, slots, k_cache, v_cache, inv_freq, k_scale, v_scale,
+                                                interleaved, rope_scale, q_out, status,
+                                                None if stream is None else stream.cuda_stream)
 
 
 def attention_workspace(B: int, q_heads: int, kv_heads: int, head_dim: int, max_tokens: int, dtype=torch.bfloat16,
                         device=None) -> torch.Tensor:
     """A workspace for `paged_attention` calls of these sizes that do not overlap: max_tokens is the
     window, or the page table's columns times the page size if that is less; dtype the cache's."""
-    n = _attention_bytes(B, q_heads, kv_heads, head_dim, _DTYPES.get(dtype, -1), max_tokens)
+    n = int(lib().moe_attention_workspace_size(B, q_heads, kv_heads, head_dim, _DTYPES.get(dtype, -1), max_tokens))
     if n == 0:
         raise MoeError(1, "moe_attention_workspace_size")
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
@@ -674,40 +611,9 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, scale: float, k_sc
     read); lengths int32 [B]: tokens of each sequence, the new one included, 0 for none (out is 0).
     sinks fp32 [Hq]: a logit per head that joins the softmax sum without a value.  window > 0:
     only the last `window` tokens.  status (`new_status`): set by a page or length out of range."""
-    kv, Hkv, page, D, cdt = _cache(k_cache, v_cache, k_scale, v_scale)
-    dt = _DTYPES.get(q.dtype, 3)
-    if not q.is_cuda or dt > 1 or (cdt != 3 and cdt != dt):
-        raise ValueError("q must be a bf16 or fp16 CUDA tensor, and a 16-bit cache of its type")
-    if q.dim() != 3 or q.shape[2] != D or q.stride(2) != 1:
-        raise ValueError(f"q must be [B, Hq, {D}] with a contiguous last dim")
-    B, Hq = q.shape[0], q.shape[1]
-    if not page_table.is_cuda or page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B \
-            or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError(f"page_table must be an int32 CUDA tensor [{B}, pages] with contiguous rows")
-    lens = _index(lengths, B, torch.int32, "lengths")
-    if sinks is not None and sinks.shape != (Hq,):
-        raise ValueError(f"sinks must be [{Hq}]")
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_cuda or out.stride(2) != 1:
-        raise ValueError("out must be like q, its last dim contiguous")
-    if B == 0:
-        return out
-    if workspace is not None:
-        ws, ws_bytes = _dev(workspace, torch.uint8, "workspace"), workspace.numel()
-    else:
-        most = page_table.shape[1] * page
-        ws, ws_bytes = None, _attention_bytes(B, Hq, Hkv, D, cdt, window if 0 < window < most else most)
-        if ws_bytes > 256:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-            ws = workspace.data_ptr()
-    qs, os_ = q.stride(), out.stride()
-    _check(lib().moe_paged_attention(kv, q.data_ptr(), dt, qs[0], qs[1], page_table.data_ptr(), page_table.stride(0),
-                                     page_table.shape[1], lens, B, Hq, scale,
-                                     None if sinks is None else _dev(sinks, torch.float32, "sinks"), window,
-                                     out.data_ptr(), os_[0], os_[1], ws, ws_bytes, _status_ptr(status),
-                                     _stream(stream)), "moe_paged_attention")
-    return out
+    return (_calls or _entries()).paged_attention(q, k_cache, v_cache, page_table, lengths, scale, k_scale, v_scale, sinks,
+                                                  window, out, workspace, status,
+                                                  None if stream is None else stream.cuda_stream)
 
 
 class MoeLayer:

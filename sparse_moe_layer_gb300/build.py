@@ -1,8 +1,10 @@
-"""Build libmoe_gb300.so in-tree for sm_103a (nvcc, one -gencode, parallel TUs)."""
+"""Build libmoe_gb300.so in-tree for sm_103a (nvcc, one -gencode, parallel TUs), and
+_binding.so, the Python entries of the decoder-block operators (g++, against torch)."""
 from __future__ import annotations
 
 import os
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -10,6 +12,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_gb300.so")
+BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["moe_api.cu", "moe_route.cu", "moe_gemm.cu", "moe_gemm_decode.cu", "moe_gemm_mx.cu", "moe_gate.cu", "moe_append.cu",
            "moe_attend.cu"]
 HEADERS = ["moe_device.cuh", "moe_internal.h", "moe_scan.cuh"]
@@ -23,10 +26,10 @@ def _nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "moe_gb300.h")]
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + ["binding.cpp"]] + [os.path.join(ROOT, "include", "moe_gb300.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
@@ -46,6 +49,32 @@ def _check_gemm_registers(log_path: str) -> None:
         raise RuntimeError("ptxas ignored setmaxnreg in a prefill GEMM")
 
 
+def _compile_binding() -> str:
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD, "binding.o")
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
+    r = subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj, "-I" + inc,
+                        "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
+                        "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"),
+                        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stderr[-4000:]}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    r = subprocess.run(["g++", "-shared", "-o", tmp, obj, "-L" + HERE, "-l:libmoe_gb300.so", "-Wl,-rpath,$ORIGIN", "-L" + lib,
+                        "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"], capture_output=True,
+                       text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
@@ -62,8 +91,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr[-4000:]}")
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding = binding.result()
     _check_gemm_registers(os.path.join(BUILD, "moe_gemm.cu.log"))
     tmp = LIB + ".tmp"
     r = subprocess.run([nvcc, "-shared", "-gencode", "arch=compute_103a,code=sm_103a", "-o", tmp, *objs],
@@ -71,6 +102,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     if verbose:
         for src in SOURCES:
             print(open(os.path.join(BUILD, src + ".log")).read())

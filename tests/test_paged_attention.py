@@ -14,12 +14,14 @@ bf16, 2^-11 fp16; A = sum_t p_t |v_td| with p summing to at most 1):
               times sum_t |v| (e4m3: of the largest value scale)        2^-25 L max|v|
   out         half a step                                                 h |out|"""
 import math
+import struct
 
 import pytest
 import torch
 
 import sparse_moe_layer_gb300 as moe
 
+KV = struct.Struct("4P9q5i4x")  # moe_kv_cache
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
 HALF = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
 
@@ -32,7 +34,7 @@ def built():
 # ------------------------------------------------------------- on the CPU ----
 def kv_bytes(dt=0, P=4, S=16, H=2, D=64, k=256, v=512, ks=0, vs=0, strides=None):
     st = strides or (H * S * D, S * D, D)
-    return moe._KV.pack(k, v, ks, vs, *st, *st, H * S, S, 1, dt, P, S, H, D)
+    return KV.pack(k, v, ks, vs, *st, *st, H * S, S, 1, dt, P, S, H, D)
 
 
 def test_refusals_on_the_host():

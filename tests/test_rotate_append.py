@@ -12,12 +12,14 @@ e4m3: 2^-4 of the value, or half its smallest step (2^-10 of a scale); a scale i
 rounded to 2^-24 of itself, or half the smallest fp32 step (2^-150)."""
 import ctypes
 import math
+import struct
 
 import pytest
 import torch
 
 import sparse_moe_layer_gb300 as moe
 
+KV = struct.Struct("4P9q5i4x")  # moe_kv_cache
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
 HALF = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
 
@@ -34,7 +36,7 @@ def inv_freq(rot):
 # ------------------------------------------------------------- on the CPU ----
 def kv_bytes(dt=0, P=4, S=16, H=2, D=64, k=256, v=512, ks=0, vs=0, strides=None, sstr=(32, 16, 1)):
     st = strides or (H * S * D, S * D, D)
-    return moe._KV.pack(k, v, ks, vs, *st, *st, *sstr, dt, P, S, H, D)
+    return KV.pack(k, v, ks, vs, *st, *st, *sstr, dt, P, S, H, D)
 
 
 def test_refusals_on_the_host():
