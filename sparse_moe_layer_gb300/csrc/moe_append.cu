@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) rotate_append_kernel(Append
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long job = (long long)blockIdx.x * kAppendWarps + warp;
     const int n = (int)(job / p.parts), part = (int)(job - (long long)n * p.parts);
+    pdl_wait();
     if (n >= p.N) return;
     const int rows = p.Hq + 2 * p.Hkv;
     const int lpr = 1 << p.lpr_shift;
@@ -191,11 +192,10 @@ __global__ void __launch_bounds__(kAppendWarps * 32) rotate_append_kernel(Append
 }
 
 template <bool FP16, bool E4M3>
-static void launch_append_t(const AppendParams& p, int grid, cudaStream_t st) {
-    if (p.neighbours)
-        rotate_append_kernel<FP16, E4M3, true><<<grid, kAppendWarps * 32, 0, st>>>(p);
-    else
-        rotate_append_kernel<FP16, E4M3, false><<<grid, kAppendWarps * 32, 0, st>>>(p);
+static cudaError_t launch_append_t(const AppendParams& p, int grid, cudaStream_t st) {
+    const dim3 g(grid), b(kAppendWarps * 32);
+    return p.neighbours ? launch_pdl(rotate_append_kernel<FP16, E4M3, true>, g, b, 0, st, p)
+                        : launch_pdl(rotate_append_kernel<FP16, E4M3, false>, g, b, 0, st, p);
 }
 
 cudaError_t launch_rotate_append(const AppendParams& p_in, bool fp16, bool e4m3, int sms, cudaStream_t st) {
@@ -212,11 +212,8 @@ cudaError_t launch_rotate_append(const AppendParams& p_in, bool fp16, bool e4m3,
     p.groups_per_part = (groups + parts - 1) / parts;
     p.parts = (groups + p.groups_per_part - 1) / p.groups_per_part;
     const int grid = (int)(((long long)p.N * p.parts + kAppendWarps - 1) / kAppendWarps);
-    if (fp16)
-        e4m3 ? launch_append_t<true, true>(p, grid, st) : launch_append_t<true, false>(p, grid, st);
-    else
-        e4m3 ? launch_append_t<false, true>(p, grid, st) : launch_append_t<false, false>(p, grid, st);
-    return cudaGetLastError();
+    if (fp16) return e4m3 ? launch_append_t<true, true>(p, grid, st) : launch_append_t<true, false>(p, grid, st);
+    return e4m3 ? launch_append_t<false, true>(p, grid, st) : launch_append_t<false, false>(p, grid, st);
 }
 
 }  // namespace moe

@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
     const int g = lane >> 2, c = lane & 3;
     __shared__ float2 s_ml[kAttWarps][kAttRows];  // a segment's maxima and sums
     __shared__ int s_slot[kAttWarps];             // and the ring slot of its values
+    pdl_wait();
     pdl_allow_dependents();
 
     // --- the run: tiles of one warp (solo), or tiles that the CTA's warps take in turn ---
@@ -922,8 +923,7 @@ cudaError_t launch_attend_t(const AttendParams& p, int grid, cudaStream_t st) {
     static_assert(C::SMEM * C::CTAS <= 226 * 1024, "shared memory of the resident CTAs");
     cudaError_t e = cudaFuncSetAttribute(attend_kernel<DP, KV, QF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    attend_kernel<DP, KV, QF16><<<grid, kAttWarps * 32, C::SMEM, st>>>(p);
-    return cudaGetLastError();
+    return launch_pdl(attend_kernel<DP, KV, QF16>, dim3(grid), dim3(kAttWarps * 32), C::SMEM, st, p);
 }
 template <int KV, bool QF16>
 cudaError_t launch_attend_d(const AttendParams& p, int grid, cudaStream_t st) {

@@ -371,6 +371,8 @@ __global__ void __launch_bounds__(kGateWarps * 32, kGateCtas) gate_kernel(GatePa
     const int step = gridDim.x * kGateWarps;
     const bool scored = p.bias != nullptr || (p.groups > 1 && p.group_top == 2);  // fp32 scores are compared
     const bool gridded = DT == kDtFp32 || p.bias;  // of experts
+    pdl_wait();
+    pdl_allow_dependents();  // one wave: what follows may take its place beside it
     const float reach = p.bias ? kReachScore : kReachLogit;
     float bias[VPL];
     load_bias<VPL>(p, e0, bias);
@@ -562,12 +564,11 @@ static cudaError_t launch_gate_v(const GateParams& p, int dtype, int sms, cudaSt
     const int want = (p.T + kGateWarps - 1) / kGateWarps;
     const int grid = want < kGateCtas * sms ? want : kGateCtas * sms;
     if (dtype == kDtFp32)
-        gate_kernel<VPL, kDtFp32><<<grid, kGateWarps * 32, 0, st>>>(p);
+        return launch_pdl(gate_kernel<VPL, kDtFp32>, dim3(grid), dim3(kGateWarps * 32), 0, st, p);
     else if (dtype == kDtFp16)
-        gate_kernel<VPL, kDtFp16><<<grid, kGateWarps * 32, 0, st>>>(p);
+        return launch_pdl(gate_kernel<VPL, kDtFp16>, dim3(grid), dim3(kGateWarps * 32), 0, st, p);
     else
-        gate_kernel<VPL, kDtBf16><<<grid, kGateWarps * 32, 0, st>>>(p);
-    return cudaGetLastError();
+        return launch_pdl(gate_kernel<VPL, kDtBf16>, dim3(grid), dim3(kGateWarps * 32), 0, st, p);
 }
 
 cudaError_t launch_gate(const GateParams& p_in, int dtype, int sms, cudaStream_t st) {
