@@ -66,11 +66,17 @@ __device__ __forceinline__ float logit_at(const void* row, int e) {
 
 // Lane l holds experts [l*VPL, (l+1)*VPL), so the lowest lane and then the
 // lowest register of a tie is the lowest expert, and a row is one or two wide
-// loads per lane when its start is aligned and no lane straddles E.
+// loads per lane when its start is aligned and no lane straddles E.  What is past
+// E holds -inf: set once by clear(), and left alone by the wide loads.
 template <int VPL, int DT>
 struct RawRow {
     static constexpr int BYTES = VPL * (DT == kDtFp32 ? 4 : 2);
+    static constexpr uint32_t kAbsent = DT == kDtFp32 ? 0xff800000u : DT == kDtFp16 ? 0xfc00fc00u : 0xff80ff80u;  // -inf
     uint32_t w[(BYTES + 3) / 4];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < (BYTES + 3) / 4; ++i) w[i] = kAbsent;
+    }
 };
 template <int VPL, int DT>
 __device__ __forceinline__ void load_row(const GateParams& p, const uint8_t* row, int lane, RawRow<VPL, DT>& v) {
@@ -101,16 +107,16 @@ __device__ __forceinline__ void load_row(const GateParams& p, const uint8_t* row
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             if (DT == kDtFp32) {
-                v.w[j] = e0 + j < p.E ? reinterpret_cast<const uint32_t*>(row)[e0 + j] : 0u;
+                v.w[j] = e0 + j < p.E ? reinterpret_cast<const uint32_t*>(row)[e0 + j] : RawRow<VPL, DT>::kAbsent;
             } else {
-                const uint32_t h = e0 + j < p.E ? reinterpret_cast<const uint16_t*>(row)[e0 + j] : 0u;
+                const uint32_t h = e0 + j < p.E ? reinterpret_cast<const uint16_t*>(row)[e0 + j] : RawRow<VPL, DT>::kAbsent & 0xffffu;
                 v.w[j / 2] = j & 1 ? v.w[j / 2] | (h << 16) : h;
             }
         }
     }
 }
 template <int VPL, int DT>
-__device__ __forceinline__ void unpack_row(const GateParams& p, const RawRow<VPL, DT>& v, int e0, float (&x)[VPL]) {
+__device__ __forceinline__ void unpack_row(const RawRow<VPL, DT>& v, float (&x)[VPL]) {
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
         float f;
@@ -120,7 +126,7 @@ __device__ __forceinline__ void unpack_row(const GateParams& p, const RawRow<VPL
             const uint16_t h = (uint16_t)(v.w[j / 2] >> (16 * (j & 1)));
             f = DT == kDtFp16 ? __half2float(__ushort_as_half(h)) : bf16_bits_to_f32(h);
         }
-        x[j] = e0 + j < p.E ? clean(f) : -INFINITY;
+        x[j] = f;
     }
 }
 
@@ -140,22 +146,24 @@ __device__ __forceinline__ void top2_lanes(T& a, T& b, int width) {
 // the sum and the reciprocal: below 2^-21.7; softmax -- relative, 2 + 1.2 d
 // steps of exp(-d), 8 of the sum z, 2 more: below 2^-19.4 of the largest.
 template <int VPL>
-__device__ __forceinline__ void choices(const GateParams& p, const float (&x)[VPL], const float (&bias)[VPL], int e0,
+__device__ __forceinline__ void choices(const GateParams& p, const float (&x)[VPL], const float (&bias)[VPL],
                                         bool scored, float m, float rz, float (&c)[VPL]) {
+    if (!scored) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-        c[j] = x[j];
-        if (scored) {
-            const float s = p.score == 0 ? (m == -INFINITY ? 0.f : __expf(x[j] - m) * rz)
-                                         : rcp_approx(1.0f + __expf(-x[j]));
-            c[j] = e0 + j < p.E ? s + bias[j] : -INFINITY;
-        }
+        for (int j = 0; j < VPL; ++j) c[j] = x[j];
+    } else if (p.score == 0) {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) c[j] = (m == -INFINITY ? 0.f : __expf(x[j] - m) * rz) + bias[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) c[j] = rcp_approx(1.0f + __expf(-x[j])) + bias[j];
     }
 }
 template <int VPL>
 __device__ __forceinline__ void load_bias(const GateParams& p, int e0, float (&bias)[VPL]) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) bias[j] = p.bias && e0 + j < p.E ? __ldg(p.bias + e0 + j) : 0.f;
+    for (int j = 0; j < VPL; ++j)  // -inf past E: so are the choices
+        bias[j] = e0 + j >= p.E ? -INFINITY : p.bias ? __ldg(p.bias + e0 + j) : 0.f;
 }
 // Bound of the error of an fp32 choice of size |c|; rz: the largest softmax score.
 __device__ __forceinline__ float choice_error(const GateParams& p, float rz, float c) {
@@ -208,14 +216,17 @@ __device__ __noinline__ int choose_close(const GateParams& p, const uint8_t* row
     const int e0 = lane * VPL;
     {
         RawRow<VPL, DT> raw;
+        raw.clear();
         load_row<VPL, DT>(p, row, lane, raw);
-        unpack_row<VPL, DT>(p, raw, e0, x);
+        unpack_row<VPL, DT>(raw, x);
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) x[j] = clean(x[j]);
     }
     const bool scored = p.bias != nullptr || (p.groups > 1 && p.group_top == 2);
     {
         float bias[VPL];
         load_bias<VPL>(p, e0, bias);
-        choices<VPL>(p, x, bias, e0, scored, m, rz, c);
+        choices<VPL>(p, x, bias, scored, m, rz, c);
     }
     double z64 = 1.0;
     if (scored && p.score == 0) {
@@ -358,7 +369,8 @@ __device__ __forceinline__ bool grid_close(uint32_t w, uint32_t next, float reac
     return (w >> 9) <= kGridFloor || (w >> 9) - (next >> 9) < apart;
 }
 
-// Warps take tokens in turn, the next token's logits in flight.
+// A CTA's warps take its tokens as they come free (a close row holds up one warp
+// only), the next token's logits in flight.
 // p.r.hist != nullptr: the layer's routing step, which also counts the chunk
 // histogram and lets the last CTA scan it.
 template <int VPL, int DT>
@@ -368,7 +380,7 @@ __global__ void __launch_bounds__(kGateWarps * 32, kGateCtas) gate_kernel(GatePa
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e0 = lane * VPL;
     int* scratch = s_scan + warp * kScratch<VPL>;
-    const int step = gridDim.x * kGateWarps;
+    __shared__ int s_next;
     const bool scored = p.bias != nullptr || (p.groups > 1 && p.group_top == 2);  // fp32 scores are compared
     const bool gridded = DT == kDtFp32 || p.bias;  // of experts
     pdl_wait();
@@ -376,15 +388,31 @@ __global__ void __launch_bounds__(kGateWarps * 32, kGateCtas) gate_kernel(GatePa
     const float reach = p.bias ? kReachScore : kReachLogit;
     float bias[VPL];
     load_bias<VPL>(p, e0, bias);
-    int t = warp * gridDim.x + blockIdx.x;
+    if (threadIdx.x == 0) s_next = kGateWarps;
+    __syncthreads();
+    int t = warp * gridDim.x + blockIdx.x, ahead = 0;
+    auto take = [&]() {  // the next of the CTA's tokens that no warp has
+        int j = 0;
+        if (lane == 0) j = atomicAdd(&s_next, 1);
+        return (int)min((long long)__shfl_sync(kFull, j, 0) * gridDim.x + blockIdx.x, (long long)p.T);
+    };
     RawRow<VPL, DT> raw;
+    raw.clear();
+    // Without scores and with a grid a NaN needs no care (maxima pass it over, grid_key puts it on the
+    // floor) and +inf puts the whole row there; elsewhere logits are made finite first
+    const bool clean_first = scored || !gridded || (p.score == 0 && !p.renorm);
     auto row_of = [&](int i) { return static_cast<const uint8_t*>(p.logits) + (size_t)i * p.ld_bytes; };
     if (t < p.T) load_row<VPL, DT>(p, row_of(t), lane, raw);
-    for (; t < p.T; t += step) {
+    for (; t < p.T; t = ahead) {
         const uint8_t* row = row_of(t);
+        ahead = take();
         float x[VPL], c[VPL];
-        unpack_row<VPL, DT>(p, raw, e0, x);
-        if (t + step < p.T) load_row<VPL, DT>(p, row_of(t + step), lane, raw);
+        unpack_row<VPL, DT>(raw, x);
+        if (clean_first) {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) x[j] = clean(x[j]);
+        }
+        if (ahead < p.T) load_row<VPL, DT>(p, row_of(ahead), lane, raw);
         float m = 0.f, rz = 1.f;
         if (p.score == 0 && (scored || !p.renorm)) {  // softmax over all experts
             float mx = x[0];
@@ -398,9 +426,10 @@ __global__ void __launch_bounds__(kGateWarps * 32, kGateCtas) gate_kernel(GatePa
             for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
             rz = z > 0.f ? 1.0f / z : 0.f;
         }
-        choices<VPL>(p, x, bias, e0, scored, m, rz, c);
+        choices<VPL>(p, x, bias, scored, m, rz, c);
         bool close = false;
         uint32_t in = kFull;  // the lane's experts in open groups
+        bool open = true;     // all of them
         if (p.groups > 1) {
             const int P = p.lanes_per_group;
             float a = -INFINITY, b = -INFINITY;
@@ -446,23 +475,38 @@ __global__ void __launch_bounds__(kGateWarps * 32, kGateCtas) gate_kernel(GatePa
                 close = grid_close(w, next, kReachGroup, scored ? 2.f * choice_error(p, rz, warp_max(mag)) : 0.f);
             }
             if (p.aligned) {
-                in = gkey >= w ? kFull : 0u;
+                open = gkey >= w;
+                in = open ? kFull : 0u;
             } else {
-                const uint32_t open = __ballot_sync(kFull, lane % P == 0 && gkey >= w);  // bit g * P
+                const uint32_t groups = __ballot_sync(kFull, lane % P == 0 && gkey >= w);  // bit g * P
                 in = 0;
 #pragma unroll
                 for (int j = 0; j < VPL; ++j)  // (e * ceil(2^16 / gsize)) >> 16 = e / gsize for e < 256
-                    in |= ((open >> ((((e0 + j) * p.inv_gsize) >> 16) * P)) & 1u) << j;
+                    in |= ((groups >> ((((e0 + j) * p.inv_gsize) >> 16) * P)) & 1u) << j;
             }
         }
         const bool settle = close;
         uint32_t key[VPL];
         float top = 0.f;
-        if (e0 + VPL > p.E) in &= (1u << max(p.E - e0, 0)) - 1u;
         if (gridded) {
             float v[VPL];
+            if (p.bias) {
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) v[j] = (in >> j) & 1u ? (p.bias ? c[j] : x[j]) : -INFINITY;
+                for (int j = 0; j < VPL; ++j) v[j] = c[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) v[j] = x[j];
+            }
+            if (p.groups > 1) {
+                if (p.aligned) {
+                    const float shut = open ? 0.f : -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < VPL; ++j) v[j] += shut;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < VPL; ++j) v[j] = (in >> j) & 1u ? v[j] : -INFINITY;
+                }
+            }
             top = v[0];
 #pragma unroll
             for (int j = 1; j < VPL; ++j) top = fmaxf(top, v[j]);
@@ -473,7 +517,7 @@ __global__ void __launch_bounds__(kGateWarps * 32, kGateCtas) gate_kernel(GatePa
         } else {
 #pragma unroll
             for (int j = 0; j < VPL; ++j)
-                key[j] = (in >> j) & 1u ? (order_key(x[j]) & ~255u) | (255u - (e0 + j)) : 0u;
+                key[j] = (in >> j) & 1u && e0 + j < p.E ? (order_key(x[j]) & ~255u) | (255u - (e0 + j)) : 0u;
         }
         // each lane's keys in falling order, then k rounds of the warp's largest head
         if constexpr (VPL == 2) {
@@ -508,15 +552,17 @@ __global__ void __launch_bounds__(kGateWarps * 32, kGateCtas) gate_kernel(GatePa
 #pragma unroll
                 for (int j = 0; j < VPL && j + r < kMaxTopK; ++j)  // what later rounds and the border can see
                     key[j] = pop ? (j + 1 < VPL ? key[j + 1] : 0u) : key[j];
-                if (lane == r) mine = 255 - (int)(w & 255u);
+                if (lane == r) mine = (int)w;
             }
         }
+        mine = 255 - (mine & 255);
         if (gridded) {
             const uint32_t next = warp_max(key[0]);
             const float mag = fmaxf(fabsf(top), fabsf(top - reach));
             close = close || grid_close(w, next, reach, p.bias ? choice_error(p, rz, mag) : 0.f);
         }
         if (close) {
+            if (e0 + VPL > p.E) in &= (1u << max(p.E - e0, 0)) - 1u;
             mine = choose_close<VPL, DT>(p, row, lane, m, rz, in, settle, scratch);
             for (int q = 0; q < p.k; ++q) slot += __shfl_sync(kFull, mine, q) < mine;
         } else {
@@ -531,18 +577,18 @@ __global__ void __launch_bounds__(kGateWarps * 32, kGateCtas) gate_kernel(GatePa
         if (p.score == 0) {
             if (!scored && p.renorm) {  // the sum over all experts cancels
                 m = warp_max(xe);
-                s = has && m != -INFINITY ? expf(xe - m) : 0.f;
+                s = has && m != -INFINITY ? __expf(xe - m) : 0.f;
             } else {
-                s = has && m != -INFINITY ? expf(xe - m) * rz : 0.f;
+                s = has && m != -INFINITY ? __expf(xe - m) * rz : 0.f;
             }
         } else {
-            s = has ? 1.0f / (1.0f + expf(-xe)) : 0.f;
+            s = has ? rcp_approx(1.0f + __expf(-xe)) : 0.f;
         }
         if (p.renorm) {
             float sum = s;
 #pragma unroll
             for (int o = kMaxTopK / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-            s = s / (sum + 1e-20f);
+            s = __fdividef(s, sum + 1e-20f);
         }
         s *= p.scale;
         if (has) {
