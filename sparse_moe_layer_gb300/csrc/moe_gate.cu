@@ -541,13 +541,11 @@ __global__ void __launch_bounds__(kGateWarps * 32, kGateCtas) gate_kernel(GatePa
             }
         }
         int mine = 0, slot = 0;  // lane r: the expert of round r, and its place in ascending order
-        uint32_t won[kMaxTopK], w = 0;
+        uint32_t w = 0;
 #pragma unroll
         for (int r = 0; r < kMaxTopK; ++r) {
-            won[r] = 0;
             if (r < p.k) {
                 w = warp_max(key[0]);
-                won[r] = w;
                 const bool pop = key[0] == w;
 #pragma unroll
                 for (int j = 0; j < VPL && j + r < kMaxTopK; ++j)  // what later rounds and the border can see
@@ -564,11 +562,8 @@ __global__ void __launch_bounds__(kGateWarps * 32, kGateCtas) gate_kernel(GatePa
         if (close) {
             if (e0 + VPL > p.E) in &= (1u << max(p.E - e0, 0)) - 1u;
             mine = choose_close<VPL, DT>(p, row, lane, m, rz, in, settle, scratch);
-            for (int q = 0; q < p.k; ++q) slot += __shfl_sync(kFull, mine, q) < mine;
-        } else {
-#pragma unroll
-            for (int r = 0; r < kMaxTopK; ++r) slot += r < p.k && 255 - (int)(won[r] & 255u) < mine;
         }
+        for (int q = 0; q < p.k; ++q) slot += __shfl_sync(kFull, mine, q) < mine;
 
         // weights: lane r < k has one chosen expert
         const bool has = lane < p.k;
