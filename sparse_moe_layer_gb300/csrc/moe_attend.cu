@@ -35,6 +35,7 @@ namespace {
 constexpr uint32_t kAllLanes = 0xffffffffu;
 constexpr int kAttWarps = 4;  // warps per CTA
 constexpr int kAttRows = 16;  // query heads per row (m16 of the products)
+constexpr float kSlack = 8.f;
 enum : int { kKvBf16 = 0, kKvFp16 = 1, kKvE4m3 = 2 };
 
 template <int DP, int KV>
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // rows g and g + 8
     // positive factors of the scores: |scale| log2 e, times the query row's power of two (e4m3)
     float qf0 = p.scale_log2, qf1 = p.scale_log2;
-    float vref = 0x1p-100f;                                    // e4m3: the accumulator's value scale
+    float vref = 0x1p-100f, ivref = 0x1p100f;                  // e4m3: the accumulator's value scale, and over it
     uint32_t qr[DP <= 128 ? KS : 1][4];
     uint32_t* qs = reinterpret_cast<uint32_t*>(ring + S * C::STAGE);
     auto qfrag = [&](int k, uint32_t (&a)[4]) {
@@ -473,6 +474,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
     m0 = m1 = -INFINITY;
     l0 = l1 = 0.f;
     vref = 0x1p-100f;
+    ivref = 0x1p100f;
 #pragma unroll
     for (int d = 0; d < DP / 8; ++d)
 #pragma unroll
@@ -594,32 +596,38 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
         t1 = fmaxf(t1, __shfl_xor_sync(kAllLanes, t1, 1));
         t0 = fmaxf(t0, __shfl_xor_sync(kAllLanes, t0, 2));
         t1 = fmaxf(t1, __shfl_xor_sync(kAllLanes, t1, 2));
-        float vnew = vref;
+        // The sums stay about an older maximum until a score passes it by kSlack powers of two (one
+        // warp-wide rescaling then): probabilities reach 2^kSlack, exact in the same number of bits.
+        bool far = (t0 - m0) * qf0 > kSlack || (t1 - m1) * qf1 > kSlack;  // NaN (both -inf): no
         if constexpr (KV == kKvE4m3) {
             vmax = fmaxf(vmax, __shfl_xor_sync(kAllLanes, vmax, 1));
             vmax = fmaxf(vmax, __shfl_xor_sync(kAllLanes, vmax, 2));
-            vnew = fmaxf(vref, vmax);
+            far = far || vmax > vref;
         }
-        const float b0 = t0 == -INFINITY ? 0.f : t0 * qf0, b1 = t1 == -INFINITY ? 0.f : t1 * qf1;
-        if (__any_sync(kAllLanes, t0 != m0 || t1 != m1 || vnew != vref)) {
-            const float c0 = ex2_approx(m0 * qf0 - b0), c1 = ex2_approx(m1 * qf1 - b1);
-            const float cv = KV == kKvE4m3 ? vref / vnew : 1.f;
+        if (__any_sync(kAllLanes, far)) {
+            const float n0 = t0 == -INFINITY ? 0.f : t0 * qf0, n1 = t1 == -INFINITY ? 0.f : t1 * qf1;
+            float c0 = ex2_approx(m0 * qf0 - n0), c1 = ex2_approx(m1 * qf1 - n1);
             l0 *= c0;
             l1 *= c1;
+            if (KV == kKvE4m3 && vmax > vref) {  // the accumulator's scale: room for values 4 times as large
+                c0 *= vref / (4.f * vmax);
+                c1 *= vref / (4.f * vmax);
+                vref = 4.f * vmax;
+                ivref = 1.0f / vref;
+            }
 #pragma unroll
             for (int d = 0; d < DP / 8; ++d) {
-                o[d][0] *= c0 * cv;
-                o[d][1] *= c0 * cv;
-                o[d][2] *= c1 * cv;
-                o[d][3] *= c1 * cv;
+                o[d][0] *= c0;
+                o[d][1] *= c0;
+                o[d][2] *= c1;
+                o[d][3] *= c1;
             }
             m0 = t0;
             m1 = t1;
-            vref = vnew;
         }
+        const float b0 = m0 == -INFINITY ? 0.f : m0 * qf0, b1 = m1 == -INFINITY ? 0.f : m1 * qf1;
         // --- probabilities (fp32 sums; rounded to 16 bits for the second product) ---
         uint32_t pa[KT][4];
-        const float ivref = KV == kKvE4m3 ? 1.0f / vref : 1.f;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             float e[4];
