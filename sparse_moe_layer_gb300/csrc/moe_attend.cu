@@ -387,22 +387,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
         __syncwarp();
     };
     for (int s = 0; s < S; ++s) zero_pad(s);
-    // S tiles' pages are looked up at once, S - 1 of them copied
-    Fetched ahead[S];
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-        if (s < to_issue) {
-            if (s > 0) it.advance(p, step);
-            ahead[s] = fetch();
-        }
-    }
-#pragma unroll
-    for (int s = 0; s < S - 1; ++s) {
-        if (s < to_issue) issue(s, ahead[s]);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-    Fetched next = ahead[S - 1];
-    to_issue -= S - 1;
+    Fetched next = {0, -1, 0, false};
+    if (to_issue > 0) next = fetch();
     auto issue_next = [&](int slot) {
         if (to_issue > 0) {
             issue(slot, next);
@@ -413,6 +399,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+#pragma unroll 1  // (a tile's pages are in the cache line of the one before, as a rule)
+    for (int s = 0; s < S - 1; ++s) issue_next(s);
 
     float o[DP / 8][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // rows g and g + 8
@@ -466,9 +454,126 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             set_qfrag(k, a);
         }
     };
-    load_q(row.b, row.h);  // in flight with the first tiles
     int slot = 0, fill = S - 1, pos = 0;
-    while (rem > 0) {
+    int b = 0, h = 0;  // the segment done last
+    bool starts = false, ends = false;
+    for (bool first = true;; first = false) {
+    // the row's queries come with its first tiles, or while the row before is written
+    if (rem > 0) load_q(row.b, row.h);
+    if (!first) {
+    const int kvh = p.head_blocks == 1 ? h : h / p.head_blocks, hb = h - kvh * p.head_blocks;
+    const int head0 = kvh * p.group + hb * kAttRows;           // first query head of the row
+    const int heads = min(kAttRows, p.group - hb * kAttRows);  // of 16 rows used
+    l0 += __shfl_xor_sync(kAllLanes, l0, 1);
+    l1 += __shfl_xor_sync(kAllLanes, l1, 1);
+    l0 += __shfl_xor_sync(kAllLanes, l0, 2);
+    l1 += __shfl_xor_sync(kAllLanes, l1, 2);
+    m0 *= qf0;  // from here on in powers of two
+    m1 *= qf1;
+    const bool done = starts && ends;
+    float* part = done ? nullptr : p.partial + ((long long)run * 2 + (starts ? 1 : 0)) * (kAttRows * (p.D + 2));
+    // the runs that a row begins and ends in, for the join (first -1: one run has all of it)
+    if (p.by_row_join && (p.solo ? lane == 0 : tid == 0)) {
+        const int at = b * p.rows_per_seq + h;
+        if (starts) p.first[at] = ends ? -1 : run;
+        if (ends && !starts) p.last[at] = run;
+    }
+    if (p.solo) {
+        float w0 = 1.f, w1 = 1.f;
+        if (done) {
+            w0 = g < heads ? final_weight(p, head0 + g, m0, l0) : 0.f;
+            w1 = g + 8 < heads ? final_weight(p, head0 + g + 8, m1, l1) : 0.f;
+        } else if (c == 0) {
+            if (g < heads) *reinterpret_cast<float2*>(part + 2 * g) = make_float2(m0, l0);
+            if (g + 8 < heads) *reinterpret_cast<float2*>(part + 2 * g + 16) = make_float2(m1, l1);
+        }
+        if constexpr (KV == kKvE4m3) {
+            w0 *= vref;
+            w1 *= vref;
+        }
+#pragma unroll
+        for (int d = 0; d < KS; ++d) {
+            if (d * 16 >= p.D) continue;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int r = g + 8 * half;
+                if (r >= heads) continue;
+                const Quad q = quad<KV>(o[2 * d], o[2 * d + 1], half, half ? w1 : w0);
+                const int d0 = d * 16 + quad_at<KV>(c), d1 = d0 + (KV == kKvE4m3 ? 2 : 8);
+                if (done) {
+                    uint16_t* dst = p.out + b * p.o_token + (long long)(head0 + r) * p.o_head;
+                    *reinterpret_cast<uint32_t*>(dst + d0) = pack2<QF16>(q.a, q.b);
+                    *reinterpret_cast<uint32_t*>(dst + d1) = pack2<QF16>(q.c, q.d);
+                } else {
+                    float* dst = part + 2 * kAttRows + r * p.D;
+                    *reinterpret_cast<float2*>(dst + d0) = make_float2(q.a, q.b);
+                    *reinterpret_cast<float2*>(dst + d1) = make_float2(q.c, q.d);
+                }
+            }
+        }
+    } else {
+    // the warps' parts meet in the ring slots that hold no tile (one of each warp); columns of a
+    // row are moved by 4 (row mod 8) to spread the rows over the banks
+    if (lane == 0) s_slot[warp] = fill;
+    if (c == 0) {
+        s_ml[warp][g] = make_float2(m0, l0);
+        s_ml[warp][g + 8] = make_float2(m1, l1);
+    }
+    {
+        float* mine = reinterpret_cast<float*>(ring + fill * C::STAGE);
+        const float f = KV == kKvE4m3 ? vref : 1.f;
+#pragma unroll
+        for (int d = 0; d < KS; ++d) {
+            if (d * 16 >= p.D) continue;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (g + 8 * half >= heads) continue;
+                const Quad q = quad<KV>(o[2 * d], o[2 * d + 1], half, f);
+                float* dst = mine + (g + 8 * half) * DP;
+                const int d0 = d * 16 + quad_at<KV>(c), d1 = d0 + (KV == kKvE4m3 ? 2 : 8);
+                *reinterpret_cast<float2*>(dst + (d0 ^ (g << 2))) = make_float2(q.a, q.b);
+                *reinterpret_cast<float2*>(dst + (d1 ^ (g << 2))) = make_float2(q.c, q.d);
+            }
+        }
+    }
+    __syncthreads();
+    for (int r = warp; r < heads; r += kAttWarps) {
+        float m = -INFINITY, l = 0.f, e[kAttWarps];
+        const float* src[kAttWarps];
+#pragma unroll
+        for (int w = 0; w < kAttWarps; ++w) {
+            m = fmaxf(m, s_ml[w][r].x);
+            src[w] = reinterpret_cast<const float*>(smem + w * C::WARP + s_slot[w] * C::STAGE) + r * DP;
+        }
+#pragma unroll
+        for (int w = 0; w < kAttWarps; ++w) {
+            e[w] = m == -INFINITY ? 0.f : ex2_approx(s_ml[w][r].x - m);
+            l += e[w] * s_ml[w][r].y;
+        }
+        const float fw = done ? final_weight(p, head0 + r, m, l) : 1.f;
+        if (!done && lane == 0) *reinterpret_cast<float2*>(part + 2 * r) = make_float2(m, l);
+        for (int d = 2 * lane; d < p.D; d += 64) {
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int w = 0; w < kAttWarps; ++w) {
+                const float2 v = *reinterpret_cast<const float2*>(src[w] + (d ^ ((r & 7) << 2)));
+                x += e[w] * v.x;
+                y += e[w] * v.y;
+            }
+            if (done)
+                *reinterpret_cast<uint32_t*>(p.out + b * p.o_token + (long long)(head0 + r) * p.o_head + d) =
+                    pack2<QF16>(x * fw, y * fw);
+            else
+                *reinterpret_cast<float2*>(part + 2 * kAttRows + r * p.D + d) = make_float2(x, y);
+        }
+    }
+    if (rem > 0) {
+        __syncthreads();  // the slots are free again
+        zero_pad(fill);
+    }
+    }
+    }
+    if (rem == 0) return;
     // --- a segment ---
     const int nseg = min(row.ntiles - row.tile, rem);
     m0 = m1 = -INFINITY;
@@ -680,123 +785,13 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
     }
 
     // --- the segment is done: the row, or the run's part of it ---
-    const int b = row.b, h = row.h;
-    const bool starts = row.tile == 0, ends = row.tile + nseg == row.ntiles;
+    b = row.b;
+    h = row.h;
+    starts = row.tile == 0;
+    ends = row.tile + nseg == row.ntiles;
     rem -= nseg;
     pos += nseg;
     row.advance(p, nseg);
-    if (rem > 0) load_q(row.b, row.h);  // the next row's queries come while this one is written
-    const int kvh = p.head_blocks == 1 ? h : h / p.head_blocks, hb = h - kvh * p.head_blocks;
-    const int head0 = kvh * p.group + hb * kAttRows;           // first query head of the row
-    const int heads = min(kAttRows, p.group - hb * kAttRows);  // of 16 rows used
-    l0 += __shfl_xor_sync(kAllLanes, l0, 1);
-    l1 += __shfl_xor_sync(kAllLanes, l1, 1);
-    l0 += __shfl_xor_sync(kAllLanes, l0, 2);
-    l1 += __shfl_xor_sync(kAllLanes, l1, 2);
-    m0 *= qf0;  // from here on in powers of two
-    m1 *= qf1;
-    const bool done = starts && ends;
-    float* part = done ? nullptr : p.partial + ((long long)run * 2 + (starts ? 1 : 0)) * (kAttRows * (p.D + 2));
-    // the runs that a row begins and ends in, for the join (first -1: one run has all of it)
-    if (p.by_row_join && (p.solo ? lane == 0 : tid == 0)) {
-        const int at = b * p.rows_per_seq + h;
-        if (starts) p.first[at] = ends ? -1 : run;
-        if (ends && !starts) p.last[at] = run;
-    }
-    if (p.solo) {
-        float w0 = 1.f, w1 = 1.f;
-        if (done) {
-            w0 = g < heads ? final_weight(p, head0 + g, m0, l0) : 0.f;
-            w1 = g + 8 < heads ? final_weight(p, head0 + g + 8, m1, l1) : 0.f;
-        } else if (c == 0) {
-            if (g < heads) *reinterpret_cast<float2*>(part + 2 * g) = make_float2(m0, l0);
-            if (g + 8 < heads) *reinterpret_cast<float2*>(part + 2 * g + 16) = make_float2(m1, l1);
-        }
-        if constexpr (KV == kKvE4m3) {
-            w0 *= vref;
-            w1 *= vref;
-        }
-#pragma unroll
-        for (int d = 0; d < KS; ++d) {
-            if (d * 16 >= p.D) continue;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int r = g + 8 * half;
-                if (r >= heads) continue;
-                const Quad q = quad<KV>(o[2 * d], o[2 * d + 1], half, half ? w1 : w0);
-                const int d0 = d * 16 + quad_at<KV>(c), d1 = d0 + (KV == kKvE4m3 ? 2 : 8);
-                if (done) {
-                    uint16_t* dst = p.out + b * p.o_token + (long long)(head0 + r) * p.o_head;
-                    *reinterpret_cast<uint32_t*>(dst + d0) = pack2<QF16>(q.a, q.b);
-                    *reinterpret_cast<uint32_t*>(dst + d1) = pack2<QF16>(q.c, q.d);
-                } else {
-                    float* dst = part + 2 * kAttRows + r * p.D;
-                    *reinterpret_cast<float2*>(dst + d0) = make_float2(q.a, q.b);
-                    *reinterpret_cast<float2*>(dst + d1) = make_float2(q.c, q.d);
-                }
-            }
-        }
-        continue;
-    }
-    // the warps' parts meet in the ring slots that hold no tile (one of each warp); columns of a
-    // row are moved by 4 (row mod 8) to spread the rows over the banks
-    if (lane == 0) s_slot[warp] = fill;
-    if (c == 0) {
-        s_ml[warp][g] = make_float2(m0, l0);
-        s_ml[warp][g + 8] = make_float2(m1, l1);
-    }
-    {
-        float* mine = reinterpret_cast<float*>(ring + fill * C::STAGE);
-        const float f = KV == kKvE4m3 ? vref : 1.f;
-#pragma unroll
-        for (int d = 0; d < KS; ++d) {
-            if (d * 16 >= p.D) continue;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (g + 8 * half >= heads) continue;
-                const Quad q = quad<KV>(o[2 * d], o[2 * d + 1], half, f);
-                float* dst = mine + (g + 8 * half) * DP;
-                const int d0 = d * 16 + quad_at<KV>(c), d1 = d0 + (KV == kKvE4m3 ? 2 : 8);
-                *reinterpret_cast<float2*>(dst + (d0 ^ (g << 2))) = make_float2(q.a, q.b);
-                *reinterpret_cast<float2*>(dst + (d1 ^ (g << 2))) = make_float2(q.c, q.d);
-            }
-        }
-    }
-    __syncthreads();
-    for (int r = warp; r < heads; r += kAttWarps) {
-        float m = -INFINITY, l = 0.f, e[kAttWarps];
-        const float* src[kAttWarps];
-#pragma unroll
-        for (int w = 0; w < kAttWarps; ++w) {
-            m = fmaxf(m, s_ml[w][r].x);
-            src[w] = reinterpret_cast<const float*>(smem + w * C::WARP + s_slot[w] * C::STAGE) + r * DP;
-        }
-#pragma unroll
-        for (int w = 0; w < kAttWarps; ++w) {
-            e[w] = m == -INFINITY ? 0.f : ex2_approx(s_ml[w][r].x - m);
-            l += e[w] * s_ml[w][r].y;
-        }
-        const float fw = done ? final_weight(p, head0 + r, m, l) : 1.f;
-        if (!done && lane == 0) *reinterpret_cast<float2*>(part + 2 * r) = make_float2(m, l);
-        for (int d = 2 * lane; d < p.D; d += 64) {
-            float x = 0.f, y = 0.f;
-#pragma unroll
-            for (int w = 0; w < kAttWarps; ++w) {
-                const float2 v = *reinterpret_cast<const float2*>(src[w] + (d ^ ((r & 7) << 2)));
-                x += e[w] * v.x;
-                y += e[w] * v.y;
-            }
-            if (done)
-                *reinterpret_cast<uint32_t*>(p.out + b * p.o_token + (long long)(head0 + r) * p.o_head + d) =
-                    pack2<QF16>(x * fw, y * fw);
-            else
-                *reinterpret_cast<float2*>(part + 2 * kAttRows + r * p.D + d) = make_float2(x, y);
-        }
-    }
-    if (rem > 0) {
-        __syncthreads();  // the slots are free again
-        zero_pad(fill);
-    }
     }
 }
 
