@@ -124,6 +124,12 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
     return (uint32_t)(r * C::CH + (c ^ ((r >> 1) & 3))) * 16u;  // CH == 4: two rows per 128 bytes
 }
 
+// a / b of numbers >= 0: 32-bit where they fit, as they nearly always do (the
+// 64-bit division is a routine of a few hundred cycles)
+__device__ __forceinline__ long long quotient(long long a, int b) {
+    return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
 __device__ __forceinline__ int seen_tokens(const AttendParams& p, int b, int* start) {
     const int raw = __ldg(p.lengths + b);
     const int len = min(max(raw, 0), p.max_tokens);
@@ -174,6 +180,14 @@ __device__ __forceinline__ Quad quad(const float (&u)[4], const float (&v)[4], i
 template <int KV>
 __device__ __forceinline__ int quad_at(int c) {
     return KV == kKvE4m3 ? 4 * c : 2 * c;
+}
+
+// a = a f + b h
+__device__ __forceinline__ void add_scaled(float4& a, float f, const float4& b, float h) {
+    a.x = a.x * f + b.x * h;
+    a.y = a.y * f + b.y * h;
+    a.z = a.z * f + b.z * h;
+    a.w = a.w * f + b.w * h;
 }
 
 // 1 / (sum with the head's sink), about the larger of the two exponents: what
@@ -261,15 +275,18 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
         if (tid == 0) s_pre[0] = 0;
         __syncthreads();
         const long long total = (long long)s_pre[kAttWarps * 32] * p.rows_per_seq;
-        const long long want = (total + p.min_tiles - 1) / p.min_tiles;
+        const long long want = (total + (1 << p.min_tiles_shift) - 1) >> p.min_tiles_shift;
         const int n = (int)(want < nruns ? want : nruns);
         const bool lead = p.solo ? lane == 0 : tid == 0;
         if (run >= n) {  // a whole CTA, or a warp that meets no barrier any more
             if (lead) p.cont[run] = -1;
             return;
         }
-        const long long u0 = total * run / n;
-        rem = (int)(total * (run + 1) / n - u0);
+        // run r starts at total * r / n: longer runs spread evenly, not first (2 us on 16 rows of 8000)
+        const long long each = quotient(total, n);
+        const int more = (int)(total - each * n), from = more * run / n;  // n <= runs: small products
+        const long long u0 = each * run + from;
+        rem = (int)each + more * (run + 1) / n - from;
         // the slice, then the sequence, that holds u0
         int sl = 0;
         for (int base = 0; base < kAttWarps * 32; base += 32) {
@@ -285,7 +302,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             u -= here;
             ++it.b;
         }
-        it.h = (int)(u / it.ntiles);
+        it.h = (int)quotient(u, it.ntiles);
         it.tile = (int)(u - (long long)it.h * it.ntiles);
         if (lead) p.cont[run] = it.tile ? it.b * p.rows_per_seq + it.h : -1;
     }
@@ -537,7 +554,12 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
         }
     }
     __syncthreads();
-    for (int r = warp; r < heads; r += kAttWarps) {
+    constexpr int LPR = DP == 64 ? 16 : 32;  // lanes of a row, 4 dims each
+    constexpr int RPW = 32 / LPR;
+#pragma unroll 4
+    for (int r0 = 0; r0 < kAttRows; r0 += kAttWarps * RPW) {
+        const int r = r0 + warp * RPW + lane / LPR;
+        if (r >= heads) break;
         float m = -INFINITY, l = 0.f, e[kAttWarps];
         const float* src[kAttWarps];
 #pragma unroll
@@ -551,20 +573,22 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             l += e[w] * s_ml[w][r].y;
         }
         const float fw = done ? final_weight(p, head0 + r, m, l) : 1.f;
-        if (!done && lane == 0) *reinterpret_cast<float2*>(part + 2 * r) = make_float2(m, l);
-        for (int d = 2 * lane; d < p.D; d += 64) {
-            float x = 0.f, y = 0.f;
+        if (!done && lane % LPR == 0) *reinterpret_cast<float2*>(part + 2 * r) = make_float2(m, l);
 #pragma unroll
-            for (int w = 0; w < kAttWarps; ++w) {
-                const float2 v = *reinterpret_cast<const float2*>(src[w] + (d ^ ((r & 7) << 2)));
-                x += e[w] * v.x;
-                y += e[w] * v.y;
+        for (int q = 0; q < (DP + 127) / 128; ++q) {
+            const int d = 4 * (lane % LPR) + 128 * q;
+            if (d >= p.D) continue;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kAttWarps; ++w)
+                add_scaled(x, 1.f, *reinterpret_cast<const float4*>(src[w] + (d ^ ((r & 7) << 2))), e[w]);
+            if (done) {
+                uint16_t* dst = p.out + b * p.o_token + (long long)(head0 + r) * p.o_head + d;
+                *reinterpret_cast<uint32_t*>(dst) = pack2<QF16>(x.x * fw, x.y * fw);
+                *reinterpret_cast<uint32_t*>(dst + 2) = pack2<QF16>(x.z * fw, x.w * fw);
+            } else {
+                *reinterpret_cast<float4*>(part + 2 * kAttRows + r * p.D + d) = x;
             }
-            if (done)
-                *reinterpret_cast<uint32_t*>(p.out + b * p.o_token + (long long)(head0 + r) * p.o_head + d) =
-                    pack2<QF16>(x * fw, y * fw);
-            else
-                *reinterpret_cast<float2*>(part + 2 * kAttRows + r * p.D + d) = make_float2(x, y);
         }
     }
     if (rem > 0) {
@@ -807,12 +831,6 @@ struct Sums {
     float m, l;
     float4 v[2];
 };
-__device__ __forceinline__ void add_scaled(float4& a, float f, const float4& b, float h) {
-    a.x = a.x * f + b.x * h;
-    a.y = a.y * f + b.y * h;
-    a.z = a.z * f + b.z * h;
-    a.w = a.w * f + b.w * h;
-}
 // a += b, each about its own maximum
 __device__ __forceinline__ void join(Sums& a, const Sums& b) {
     const float m = fmaxf(a.m, b.m);
@@ -908,8 +926,8 @@ namespace {
 // most kWholeTokens take a warp each; a CTA takes a row of its own where all rows
 // fit at once and none is longer than kTeamTokens; from kSoloRows rows on, runs
 // are a warp's: fewer waits at the rows' ends, and few parts to a row anyway.
-constexpr int kMinTiles = kAttWarps;
-constexpr int kMinSoloTiles = 2;
+constexpr int kMinTilesLog2 = 2;
+constexpr int kMinSoloTilesLog2 = 1;
 #ifndef MOE_SOLO_ROWS
 #define MOE_SOLO_ROWS 96
 #endif
@@ -975,7 +993,7 @@ cudaError_t launch_attend(const AttendParams& p_in, const AttendPlan& w, int kv_
     if ((p.page_size & (p.page_size - 1)) == 0)
         for (p.page_shift = 0; (1 << p.page_shift) < p.page_size;) ++p.page_shift;
     const long long rows = (long long)p.B * p.rows_per_seq;
-    p.min_tiles = p.solo ? kMinSoloTiles : kMinTiles;
+    p.min_tiles_shift = p.solo ? kMinSoloTilesLog2 : kMinTilesLog2;
     if (w.total) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);
         p.by_row_join = w.by_row_join;

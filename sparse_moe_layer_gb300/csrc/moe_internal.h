@@ -99,7 +99,7 @@ struct AttendParams {
     int group, head_blocks, rows_per_seq;  // query heads per key head; blocks of 16 of them; rows of a sequence
     int page_shift, page16;                // log2(page_size), -1 if none; whether 16 divides it
     int team;                              // a CTA per row
-    int solo, by_row, min_tiles;           // runs of a warp (else of a CTA); of whole rows; least tiles of a run
+    int solo, by_row, min_tiles_shift;     // runs of a warp (else of a CTA); of whole rows; log2 of a run's least tiles
     int by_row_join, runs, jobs, join_warps;
     int32_t* cont;   // [runs] row that the run continues, -1: it starts one
     int32_t* first;  // [rows] run that the row begins in, -1: it ends there too (by_row_join)
