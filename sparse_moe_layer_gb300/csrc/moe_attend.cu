@@ -15,13 +15,13 @@
 // through tensor memory.
 //
 // The (sequence, key head, token tile) list is cut into equal runs, one per
-// resident warp (many rows) or CTA (few), so a batch of very different lengths
-// loads all SMs alike.  A warp streams its tiles through its own cp.async ring (the
-// copies run on over the borders of rows) with its own running maximum and sum; a
-// CTA's warps take its run's tiles in turn and join in shared memory where a row
-// or the run ends.  Only a row cut by a run's border leaves fp32 parts, which a second, dependent launch joins in a
-// fixed order (results do not depend on scheduling).  Rows of a tile or a few
-// take a warp each, or a CTA each if there are few.
+// resident CTA, so a batch of very different lengths loads all SMs alike.  A
+// CTA's warps take the run's tiles in turn, each through its own cp.async ring
+// (the copies run on over the borders of rows) with its own running maximum and
+// sum; where a row or the run ends they join in shared memory.  Only a row cut by
+// a run's border leaves fp32 parts, which a second, dependent launch joins in a
+// fixed order (results do not depend on scheduling).  Short rows are not cut: a
+// CTA or a warp takes whole ones (attend_plan).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -221,22 +221,21 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
     pdl_wait();
     pdl_allow_dependents();
 
-    // --- the run: tiles of one warp (solo), or tiles that the CTA's warps take in turn ---
+    // --- the run: tiles that the CTA's warps take in turn, or whole rows of one warp ---
     TileIt<TT> it;  // of the copies
     int rem;        // tiles of the run
-    // neighbouring runs on different SMs
-    const int run = p.solo ? warp * gridDim.x + blockIdx.x : blockIdx.x;
-    const int nruns = p.solo ? gridDim.x * kAttWarps : gridDim.x;
+    const int run = blockIdx.x;
     if (p.team) {  // few rows, none long: one to a CTA
         it.b = run / p.rows_per_seq;
         it.h = run - it.b * p.rows_per_seq;
         it.tile = 0;
         it.seq(p);
         rem = it.ntiles;
-    } else if (p.by_row) {  // whole rows
-        const int rows = p.B * p.rows_per_seq, n = rows < nruns ? rows : nruns;
-        if (run >= n) return;
-        const int u0 = (int)((long long)rows * run / n), u1 = (int)((long long)rows * (run + 1) / n);
+    } else if (p.by_row) {  // neighbouring warps' rows on different SMs
+        const int nwarps = gridDim.x * kAttWarps, w = warp * gridDim.x + blockIdx.x;
+        const int rows = p.B * p.rows_per_seq, n = rows < nwarps ? rows : nwarps;
+        if (w >= n) return;
+        const int u0 = (int)((long long)rows * w / n), u1 = (int)((long long)rows * (w + 1) / n);
         it.b = u0 / p.rows_per_seq;
         it.h = u0 - it.b * p.rows_per_seq;
         it.tile = 0;
@@ -275,11 +274,10 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
         if (tid == 0) s_pre[0] = 0;
         __syncthreads();
         const long long total = (long long)s_pre[kAttWarps * 32] * p.rows_per_seq;
-        const long long want = (total + (1 << p.min_tiles_shift) - 1) >> p.min_tiles_shift;
-        const int n = (int)(want < nruns ? want : nruns);
-        const bool lead = p.solo ? lane == 0 : tid == 0;
-        if (run >= n) {  // a whole CTA, or a warp that meets no barrier any more
-            if (lead) p.cont[run] = -1;
+        const long long want = (total + kAttWarps - 1) / kAttWarps;
+        const int n = (int)(want < (int)gridDim.x ? want : gridDim.x);
+        if (run >= n) {
+            if (tid == 0) p.cont[run] = -1;
             return;
         }
         // run r starts at total * r / n: longer runs spread evenly, not first (2 us on 16 rows of 8000)
@@ -304,12 +302,12 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
         }
         it.h = (int)quotient(u, it.ntiles);
         it.tile = (int)(u - (long long)it.h * it.ntiles);
-        if (lead) p.cont[run] = it.tile ? it.b * p.rows_per_seq + it.h : -1;
+        if (tid == 0) p.cont[run] = it.tile ? it.b * p.rows_per_seq + it.h : -1;
     }
     TileIt<TT> row = it;  // of the products: the tile that the current segment (a row's tiles in the run) begins with
-    const int step = p.solo ? 1 : kAttWarps;
-    int to_issue = p.solo ? rem : rem > warp ? (rem - warp + kAttWarps - 1) / kAttWarps : 0;  // tiles of this warp
-    if (!p.solo && to_issue > 0) it.advance(p, warp);
+    const int step = p.by_row ? 1 : kAttWarps;
+    int to_issue = p.by_row ? rem : rem > warp ? (rem - warp + kAttWarps - 1) / kAttWarps : 0;  // tiles of this warp
+    if (!p.by_row && to_issue > 0) it.advance(p, warp);
 
     // --- the ring ---
     uint8_t* ring = smem + warp * C::WARP;
@@ -476,360 +474,348 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
     int b = 0, h = 0;  // the segment done last
     bool starts = false, ends = false;
     for (bool first = true;; first = false) {
-    // the row's queries come with its first tiles, or while the row before is written
-    if (rem > 0) load_q(row.b, row.h);
-    if (!first) {
-    const int kvh = p.head_blocks == 1 ? h : h / p.head_blocks, hb = h - kvh * p.head_blocks;
-    const int head0 = kvh * p.group + hb * kAttRows;           // first query head of the row
-    const int heads = min(kAttRows, p.group - hb * kAttRows);  // of 16 rows used
-    if constexpr (KV == kKvE4m3) {
-        l0 += __shfl_xor_sync(kAllLanes, l0, 1);
-        l1 += __shfl_xor_sync(kAllLanes, l1, 1);
-        l0 += __shfl_xor_sync(kAllLanes, l0, 2);
-        l1 += __shfl_xor_sync(kAllLanes, l1, 2);
-    } else {
-        l0 = ls[0];
-        l1 = ls[2];
-    }
-    m0 *= qf0;  // from here on in powers of two
-    m1 *= qf1;
-    const bool done = starts && ends;
-    float* part = done ? nullptr : p.partial + ((long long)run * 2 + (starts ? 1 : 0)) * (kAttRows * (p.D + 2));
-    // the runs that a row begins and ends in, for the join (first -1: one run has all of it)
-    if (p.by_row_join && (p.solo ? lane == 0 : tid == 0)) {
-        const int at = b * p.rows_per_seq + h;
-        if (starts) p.first[at] = ends ? -1 : run;
-        if (ends && !starts) p.last[at] = run;
-    }
-    if (p.solo) {
-        float w0 = 1.f, w1 = 1.f;
-        if (done) {
-            w0 = g < heads ? final_weight(p, head0 + g, m0, l0) : 0.f;
-            w1 = g + 8 < heads ? final_weight(p, head0 + g + 8, m1, l1) : 0.f;
-        } else if (c == 0) {
-            if (g < heads) *reinterpret_cast<float2*>(part + 2 * g) = make_float2(m0, l0);
-            if (g + 8 < heads) *reinterpret_cast<float2*>(part + 2 * g + 16) = make_float2(m1, l1);
-        }
-        if constexpr (KV == kKvE4m3) {
-            w0 *= vref;
-            w1 *= vref;
-        }
+        // the row's queries come with its first tiles, or while the row before is written
+        if (rem > 0) load_q(row.b, row.h);
+        if (!first) {
+            const int kvh = p.head_blocks == 1 ? h : h / p.head_blocks, hb = h - kvh * p.head_blocks;
+            const int head0 = kvh * p.group + hb * kAttRows;           // first query head of the row
+            const int heads = min(kAttRows, p.group - hb * kAttRows);  // of 16 rows used
+            if constexpr (KV == kKvE4m3) {
+                l0 += __shfl_xor_sync(kAllLanes, l0, 1);
+                l1 += __shfl_xor_sync(kAllLanes, l1, 1);
+                l0 += __shfl_xor_sync(kAllLanes, l0, 2);
+                l1 += __shfl_xor_sync(kAllLanes, l1, 2);
+            } else {
+                l0 = ls[0];
+                l1 = ls[2];
+            }
+            m0 *= qf0;  // from here on in powers of two
+            m1 *= qf1;
+            const bool done = starts && ends;
+            float* part = done ? nullptr : p.partial + ((long long)run * 2 + (starts ? 1 : 0)) * (kAttRows * (p.D + 2));
+            // the runs that a row begins and ends in, for the join (first -1: one run has all of it)
+            if (p.by_row_join && tid == 0) {
+                const int at = b * p.rows_per_seq + h;
+                if (starts) p.first[at] = ends ? -1 : run;
+                if (ends && !starts) p.last[at] = run;
+            }
+            if (p.by_row) {
+                float w0 = g < heads ? final_weight(p, head0 + g, m0, l0) : 0.f;
+                float w1 = g + 8 < heads ? final_weight(p, head0 + g + 8, m1, l1) : 0.f;
+                if constexpr (KV == kKvE4m3) {
+                    w0 *= vref;
+                    w1 *= vref;
+                }
 #pragma unroll
-        for (int d = 0; d < KS; ++d) {
-            if (d * 16 >= p.D) continue;
+                for (int d = 0; d < KS; ++d) {
+                    if (d * 16 >= p.D) continue;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int r = g + 8 * half;
-                if (r >= heads) continue;
-                const Quad q = quad<KV>(o[2 * d], o[2 * d + 1], half, half ? w1 : w0);
-                const int d0 = d * 16 + quad_at<KV>(c), d1 = d0 + (KV == kKvE4m3 ? 2 : 8);
-                if (done) {
-                    uint16_t* dst = p.out + b * p.o_token + (long long)(head0 + r) * p.o_head;
-                    *reinterpret_cast<uint32_t*>(dst + d0) = pack2<QF16>(q.a, q.b);
-                    *reinterpret_cast<uint32_t*>(dst + d1) = pack2<QF16>(q.c, q.d);
-                } else {
-                    float* dst = part + 2 * kAttRows + r * p.D;
-                    *reinterpret_cast<float2*>(dst + d0) = make_float2(q.a, q.b);
-                    *reinterpret_cast<float2*>(dst + d1) = make_float2(q.c, q.d);
+                    for (int half = 0; half < 2; ++half) {
+                        const int r = g + 8 * half;
+                        if (r >= heads) continue;
+                        const Quad q = quad<KV>(o[2 * d], o[2 * d + 1], half, half ? w1 : w0);
+                        uint16_t* dst =
+                            p.out + b * p.o_token + (long long)(head0 + r) * p.o_head + d * 16 + quad_at<KV>(c);
+                        *reinterpret_cast<uint32_t*>(dst) = pack2<QF16>(q.a, q.b);
+                        *reinterpret_cast<uint32_t*>(dst + (KV == kKvE4m3 ? 2 : 8)) = pack2<QF16>(q.c, q.d);
+                    }
+                }
+            } else {
+                // the warps' parts meet in the ring slots that hold no tile (one of each warp); columns of a
+                // row are moved by 4 (row mod 8) to spread the rows over the banks
+                if (lane == 0) s_slot[warp] = fill;
+                if (c == 0) {
+                    s_ml[warp][g] = make_float2(m0, l0);
+                    s_ml[warp][g + 8] = make_float2(m1, l1);
+                }
+                {
+                    float* mine = reinterpret_cast<float*>(ring + fill * C::STAGE);
+                    const float f = KV == kKvE4m3 ? vref : 1.f;
+#pragma unroll
+                    for (int d = 0; d < KS; ++d) {
+                        if (d * 16 >= p.D) continue;
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            if (g + 8 * half >= heads) continue;
+                            const Quad q = quad<KV>(o[2 * d], o[2 * d + 1], half, f);
+                            float* dst = mine + (g + 8 * half) * DP;
+                            const int d0 = d * 16 + quad_at<KV>(c), d1 = d0 + (KV == kKvE4m3 ? 2 : 8);
+                            *reinterpret_cast<float2*>(dst + (d0 ^ (g << 2))) = make_float2(q.a, q.b);
+                            *reinterpret_cast<float2*>(dst + (d1 ^ (g << 2))) = make_float2(q.c, q.d);
+                        }
+                    }
+                }
+                __syncthreads();
+                constexpr int LPR = DP == 64 ? 16 : 32;  // lanes of a row, 4 dims each
+                constexpr int RPW = 32 / LPR;
+#pragma unroll 4
+                for (int r0 = 0; r0 < kAttRows; r0 += kAttWarps * RPW) {
+                    const int r = r0 + warp * RPW + lane / LPR;
+                    if (r >= heads) break;
+                    float m = -INFINITY, l = 0.f, e[kAttWarps];
+                    const float* src[kAttWarps];
+#pragma unroll
+                    for (int w = 0; w < kAttWarps; ++w) {
+                        m = fmaxf(m, s_ml[w][r].x);
+                        src[w] = reinterpret_cast<const float*>(smem + w * C::WARP + s_slot[w] * C::STAGE) + r * DP;
+                    }
+#pragma unroll
+                    for (int w = 0; w < kAttWarps; ++w) {
+                        e[w] = m == -INFINITY ? 0.f : ex2_approx(s_ml[w][r].x - m);
+                        l += e[w] * s_ml[w][r].y;
+                    }
+                    const float fw = done ? final_weight(p, head0 + r, m, l) : 1.f;
+                    if (!done && lane % LPR == 0) *reinterpret_cast<float2*>(part + 2 * r) = make_float2(m, l);
+#pragma unroll
+                    for (int q = 0; q < (DP + 127) / 128; ++q) {
+                        const int d = 4 * (lane % LPR) + 128 * q;
+                        if (d >= p.D) continue;
+                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int w = 0; w < kAttWarps; ++w)
+                            add_scaled(x, 1.f, *reinterpret_cast<const float4*>(src[w] + (d ^ ((r & 7) << 2))), e[w]);
+                        if (done) {
+                            uint16_t* dst = p.out + b * p.o_token + (long long)(head0 + r) * p.o_head + d;
+                            *reinterpret_cast<uint32_t*>(dst) = pack2<QF16>(x.x * fw, x.y * fw);
+                            *reinterpret_cast<uint32_t*>(dst + 2) = pack2<QF16>(x.z * fw, x.w * fw);
+                        } else {
+                            *reinterpret_cast<float4*>(part + 2 * kAttRows + r * p.D + d) = x;
+                        }
+                    }
+                }
+                if (rem > 0) {
+                    __syncthreads();  // the slots are free again
+                    zero_pad(fill);
                 }
             }
         }
-    } else {
-    // the warps' parts meet in the ring slots that hold no tile (one of each warp); columns of a
-    // row are moved by 4 (row mod 8) to spread the rows over the banks
-    if (lane == 0) s_slot[warp] = fill;
-    if (c == 0) {
-        s_ml[warp][g] = make_float2(m0, l0);
-        s_ml[warp][g + 8] = make_float2(m1, l1);
-    }
-    {
-        float* mine = reinterpret_cast<float*>(ring + fill * C::STAGE);
-        const float f = KV == kKvE4m3 ? vref : 1.f;
+        if (rem == 0) return;
+        // --- a segment ---
+        const int nseg = min(row.ntiles - row.tile, rem);
+        m0 = m1 = -INFINITY;
+        l0 = l1 = ls[0] = ls[2] = 0.f;
+        vref = 0x1p-100f;
+        ivref = 0x1p100f;
 #pragma unroll
-        for (int d = 0; d < KS; ++d) {
-            if (d * 16 >= p.D) continue;
+        for (int d = 0; d < DP / 8; ++d)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (g + 8 * half >= heads) continue;
-                const Quad q = quad<KV>(o[2 * d], o[2 * d + 1], half, f);
-                float* dst = mine + (g + 8 * half) * DP;
-                const int d0 = d * 16 + quad_at<KV>(c), d1 = d0 + (KV == kKvE4m3 ? 2 : 8);
-                *reinterpret_cast<float2*>(dst + (d0 ^ (g << 2))) = make_float2(q.a, q.b);
-                *reinterpret_cast<float2*>(dst + (d1 ^ (g << 2))) = make_float2(q.c, q.d);
-            }
-        }
-    }
-    __syncthreads();
-    constexpr int LPR = DP == 64 ? 16 : 32;  // lanes of a row, 4 dims each
-    constexpr int RPW = 32 / LPR;
-#pragma unroll 4
-    for (int r0 = 0; r0 < kAttRows; r0 += kAttWarps * RPW) {
-        const int r = r0 + warp * RPW + lane / LPR;
-        if (r >= heads) break;
-        float m = -INFINITY, l = 0.f, e[kAttWarps];
-        const float* src[kAttWarps];
-#pragma unroll
-        for (int w = 0; w < kAttWarps; ++w) {
-            m = fmaxf(m, s_ml[w][r].x);
-            src[w] = reinterpret_cast<const float*>(smem + w * C::WARP + s_slot[w] * C::STAGE) + r * DP;
-        }
-#pragma unroll
-        for (int w = 0; w < kAttWarps; ++w) {
-            e[w] = m == -INFINITY ? 0.f : ex2_approx(s_ml[w][r].x - m);
-            l += e[w] * s_ml[w][r].y;
-        }
-        const float fw = done ? final_weight(p, head0 + r, m, l) : 1.f;
-        if (!done && lane % LPR == 0) *reinterpret_cast<float2*>(part + 2 * r) = make_float2(m, l);
-#pragma unroll
-        for (int q = 0; q < (DP + 127) / 128; ++q) {
-            const int d = 4 * (lane % LPR) + 128 * q;
-            if (d >= p.D) continue;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kAttWarps; ++w)
-                add_scaled(x, 1.f, *reinterpret_cast<const float4*>(src[w] + (d ^ ((r & 7) << 2))), e[w]);
-            if (done) {
-                uint16_t* dst = p.out + b * p.o_token + (long long)(head0 + r) * p.o_head + d;
-                *reinterpret_cast<uint32_t*>(dst) = pack2<QF16>(x.x * fw, x.y * fw);
-                *reinterpret_cast<uint32_t*>(dst + 2) = pack2<QF16>(x.z * fw, x.w * fw);
-            } else {
-                *reinterpret_cast<float4*>(part + 2 * kAttRows + r * p.D + d) = x;
-            }
-        }
-    }
-    if (rem > 0) {
-        __syncthreads();  // the slots are free again
-        zero_pad(fill);
-    }
-    }
-    }
-    if (rem == 0) return;
-    // --- a segment ---
-    const int nseg = min(row.ntiles - row.tile, rem);
-    m0 = m1 = -INFINITY;
-    l0 = l1 = ls[0] = ls[2] = 0.f;
-    vref = 0x1p-100f;
-    ivref = 0x1p100f;
-#pragma unroll
-    for (int d = 0; d < DP / 8; ++d)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[d][j] = 0.f;
-    if constexpr (KV == kKvE4m3) {
-        // the products run in fp16: each query row is scaled by a power of two to
-        // below 2 (exact but for values 2^-24 below the largest)
-        float a0 = 0.f, a1 = 0.f;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-            uint32_t a[4];
-            qfrag(k, a);
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-                const float2 x = unpack2<QF16>(a[j]), y = unpack2<QF16>(a[j + 1]);
-                a0 = fmaxf(a0, fmaxf(fabsf(x.x), fabsf(x.y)));
-                a1 = fmaxf(a1, fmaxf(fabsf(y.x), fabsf(y.y)));
-            }
-        }
-        a0 = fmaxf(a0, __shfl_xor_sync(kAllLanes, a0, 1));
-        a0 = fmaxf(a0, __shfl_xor_sync(kAllLanes, a0, 2));
-        a1 = fmaxf(a1, __shfl_xor_sync(kAllLanes, a1, 1));
-        a1 = fmaxf(a1, __shfl_xor_sync(kAllLanes, a1, 2));
-        // 2^-floor(log2 amax), exponent field kept within [1, 253]
-        const uint32_t e0 = min(max(__float_as_uint(a0) >> 23, 1u), 253u);
-        const uint32_t e1 = min(max(__float_as_uint(a1) >> 23, 1u), 253u);
-        const float f0 = __uint_as_float((254u - e0) << 23), f1 = __uint_as_float((254u - e1) << 23);
-        qf0 = p.scale_log2 * __uint_as_float(e0 << 23);
-        qf1 = p.scale_log2 * __uint_as_float(e1 << 23);
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-            uint32_t a[4];
-            qfrag(k, a);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 x = unpack2<QF16>(a[j]);
-                const float f = j & 1 ? f1 : f0;
-                a[j] = pack2<true>(x.x * f, x.y * f);
-            }
-            set_qfrag(k, a);
-        }
-    }
-    // a warp's tiles of the segment: places of the run that are its own modulo the warps
-    for (int j = p.solo ? 0 : (warp - pos) & (kAttWarps - 1); j < nseg; j += step) {
-        cp_async_wait<S - 2>();
-        __syncwarp();
-        issue_next(fill);
-        fill = fill + 1 == S ? 0 : fill + 1;
-        const uint8_t* stage = ring + slot * C::STAGE;
-        const uint32_t ks_s = ring_s + slot * C::STAGE, vs_s = ks_s + C::TILE;
-
-        // --- scores of the tile: S[16 heads, TT tokens] ---
-        float s[NT][4];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[t][j] = 0.f;
-        if constexpr (KV != kKvE4m3) {
-            // matrices of a load: tokens 0-7 and 8-15, dims 0-7 and 8-15 of the step
-            const int r = (lane & 7) + ((lane >> 4) << 3), hi = (lane >> 3) & 1;
+            for (int j = 0; j < 4; ++j) o[d][j] = 0.f;
+        if constexpr (KV == kKvE4m3) {
+            // the products run in fp16: each query row is scaled by a power of two to
+            // below 2 (exact but for values 2^-24 below the largest)
+            float a0 = 0.f, a1 = 0.f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 uint32_t a[4];
                 qfrag(k, a);
 #pragma unroll
-                for (int t = 0; t < KT; ++t) {
-                    uint32_t b[4];
-                    ldsm4(ks_s + swz<C>(16 * t + r, 2 * k + hi), b);
-                    mma16816<F16>(s[2 * t], a, b[0], b[1]);
-                    mma16816<F16>(s[2 * t + 1], a, b[2], b[3]);
+                for (int j = 0; j < 4; j += 2) {
+                    const float2 x = unpack2<QF16>(a[j]), y = unpack2<QF16>(a[j + 1]);
+                    a0 = fmaxf(a0, fmaxf(fabsf(x.x), fabsf(x.y)));
+                    a1 = fmaxf(a1, fmaxf(fabsf(y.x), fabsf(y.y)));
                 }
             }
-        } else {
-            // a matrix: 8 tokens x 16 dims of codes; a load takes 4 groups of 8 tokens
-            const int r = lane;
+            a0 = fmaxf(a0, __shfl_xor_sync(kAllLanes, a0, 1));
+            a0 = fmaxf(a0, __shfl_xor_sync(kAllLanes, a0, 2));
+            a1 = fmaxf(a1, __shfl_xor_sync(kAllLanes, a1, 1));
+            a1 = fmaxf(a1, __shfl_xor_sync(kAllLanes, a1, 2));
+            // 2^-floor(log2 amax), exponent field kept within [1, 253]
+            const uint32_t e0 = min(max(__float_as_uint(a0) >> 23, 1u), 253u);
+            const uint32_t e1 = min(max(__float_as_uint(a1) >> 23, 1u), 253u);
+            const float f0 = __uint_as_float((254u - e0) << 23), f1 = __uint_as_float((254u - e1) << 23);
+            qf0 = p.scale_log2 * __uint_as_float(e0 << 23);
+            qf1 = p.scale_log2 * __uint_as_float(e1 << 23);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                uint32_t a[4], b[4];
+                uint32_t a[4];
                 qfrag(k, a);
-                ldsm4(ks_s + swz<C>(r, k), b);
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    mma16816<F16>(s[t], a, e4m3x2_to_f16x2(b[t]), e4m3x2_to_f16x2(b[t] >> 16));
+                for (int j = 0; j < 4; ++j) {
+                    const float2 x = unpack2<QF16>(a[j]);
+                    const float f = j & 1 ? f1 : f0;
+                    a[j] = pack2<true>(x.x * f, x.y * f);
+                }
+                set_qfrag(k, a);
             }
         }
-        // --- key scales, mask, running maximum (of scores before the positive factors qf) ---
-        float vr[NT][2];  // e4m3: value scale of the lane's tokens over the accumulator's
-        float vmax = 0.f;
-        if constexpr (KV == kKvE4m3) {
-            const float* sck = reinterpret_cast<const float*>(stage + 2 * C::TILE);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const float2 kk = *reinterpret_cast<const float2*>(sck + t * 8 + 2 * c);
-                const float2 vv = *reinterpret_cast<const float2*>(sck + TT + t * 8 + 2 * c);
-                s[t][0] *= kk.x;
-                s[t][1] *= kk.y;
-                s[t][2] *= kk.x;
-                s[t][3] *= kk.y;
-                vr[t][0] = vv.x;
-                vr[t][1] = vv.y;
-                vmax = fmaxf(vmax, fmaxf(vv.x, vv.y));
-            }
-        }
-        const uint32_t valid = *reinterpret_cast<const uint32_t*>(stage + 2 * C::TILE + C::SC);
-        if (valid != kAllTokens) {
+        // a warp's tiles of the segment: places of the run that are its own modulo the warps
+        for (int j = p.by_row ? 0 : (warp - pos) & (kAttWarps - 1); j < nseg; j += step) {
+            cp_async_wait<S - 2>();
+            __syncwarp();
+            issue_next(fill);
+            fill = fill + 1 == S ? 0 : fill + 1;
+            const uint8_t* stage = ring + slot * C::STAGE;
+            const uint32_t ks_s = ring_s + slot * C::STAGE, vs_s = ks_s + C::TILE;
+
+            // --- scores of the tile: S[16 heads, TT tokens] ---
+            float s[NT][4];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (!((valid >> (t * 8 + 2 * c + (j & 1))) & 1u)) s[t][j] = -INFINITY;
-        }
-        float t0 = m0, t1 = m1;
+                for (int j = 0; j < 4; ++j) s[t][j] = 0.f;
+            if constexpr (KV != kKvE4m3) {
+                // matrices of a load: tokens 0-7 and 8-15, dims 0-7 and 8-15 of the step
+                const int r = (lane & 7) + ((lane >> 4) << 3), hi = (lane >> 3) & 1;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            t0 = fmaxf(t0, fmaxf(s[t][0], s[t][1]));
-            t1 = fmaxf(t1, fmaxf(s[t][2], s[t][3]));
-        }
-        t0 = fmaxf(t0, __shfl_xor_sync(kAllLanes, t0, 1));
-        t1 = fmaxf(t1, __shfl_xor_sync(kAllLanes, t1, 1));
-        t0 = fmaxf(t0, __shfl_xor_sync(kAllLanes, t0, 2));
-        t1 = fmaxf(t1, __shfl_xor_sync(kAllLanes, t1, 2));
-        // The sums stay about an older maximum until a score passes it by kSlack powers of two (one
-        // warp-wide rescaling then): probabilities reach 2^kSlack, exact in the same number of bits.
-        bool far = (t0 - m0) * qf0 > kSlack || (t1 - m1) * qf1 > kSlack;  // NaN (both -inf): no
-        if constexpr (KV == kKvE4m3) {
-            vmax = fmaxf(vmax, __shfl_xor_sync(kAllLanes, vmax, 1));
-            vmax = fmaxf(vmax, __shfl_xor_sync(kAllLanes, vmax, 2));
-            far = far || vmax > vref;
-        }
-        if (__any_sync(kAllLanes, far)) {
-            const float n0 = t0 == -INFINITY ? 0.f : t0 * qf0, n1 = t1 == -INFINITY ? 0.f : t1 * qf1;
-            float c0 = ex2_approx(m0 * qf0 - n0), c1 = ex2_approx(m1 * qf1 - n1);
-            l0 *= c0;
-            l1 *= c1;
-            ls[0] *= c0;
-            ls[2] *= c1;
-            if (KV == kKvE4m3 && vmax > vref) {  // the accumulator's scale: room for values 4 times as large
-                c0 *= vref / (4.f * vmax);
-                c1 *= vref / (4.f * vmax);
-                vref = 4.f * vmax;
-                ivref = 1.0f / vref;
+                for (int k = 0; k < KS; ++k) {
+                    uint32_t a[4];
+                    qfrag(k, a);
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) {
+                        uint32_t b[4];
+                        ldsm4(ks_s + swz<C>(16 * t + r, 2 * k + hi), b);
+                        mma16816<F16>(s[2 * t], a, b[0], b[1]);
+                        mma16816<F16>(s[2 * t + 1], a, b[2], b[3]);
+                    }
+                }
+            } else {
+                // a matrix: 8 tokens x 16 dims of codes; a load takes 4 groups of 8 tokens
+                const int r = lane;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    uint32_t a[4], b[4];
+                    qfrag(k, a);
+                    ldsm4(ks_s + swz<C>(r, k), b);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        mma16816<F16>(s[t], a, e4m3x2_to_f16x2(b[t]), e4m3x2_to_f16x2(b[t] >> 16));
+                }
             }
-#pragma unroll
-            for (int d = 0; d < DP / 8; ++d) {
-                o[d][0] *= c0;
-                o[d][1] *= c0;
-                o[d][2] *= c1;
-                o[d][3] *= c1;
-            }
-            m0 = t0;
-            m1 = t1;
-        }
-        const float b0 = m0 == -INFINITY ? 0.f : m0 * qf0, b1 = m1 == -INFINITY ? 0.f : m1 * qf1;
-        // --- probabilities (fp32 sums; rounded to 16 bits for the second product) ---
-        uint32_t pa[KT][4];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float e[4];
-            e[0] = ex2_approx(fmaf(s[t][0], qf0, -b0));
-            e[1] = ex2_approx(fmaf(s[t][1], qf0, -b0));
-            e[2] = ex2_approx(fmaf(s[t][2], qf1, -b1));
-            e[3] = ex2_approx(fmaf(s[t][3], qf1, -b1));
+            // --- key scales, mask, running maximum (of scores before the positive factors qf) ---
+            float vr[NT][2];  // e4m3: value scale of the lane's tokens over the accumulator's
+            float vmax = 0.f;
             if constexpr (KV == kKvE4m3) {
-                l0 += e[0] + e[1];
-                l1 += e[2] + e[3];
-                const float x = vr[t][0] * ivref, y = vr[t][1] * ivref;
-                e[0] *= x;
-                e[1] *= y;
-                e[2] *= x;
-                e[3] *= y;
+                const float* sck = reinterpret_cast<const float*>(stage + 2 * C::TILE);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const float2 kk = *reinterpret_cast<const float2*>(sck + t * 8 + 2 * c);
+                    const float2 vv = *reinterpret_cast<const float2*>(sck + TT + t * 8 + 2 * c);
+                    s[t][0] *= kk.x;
+                    s[t][1] *= kk.y;
+                    s[t][2] *= kk.x;
+                    s[t][3] *= kk.y;
+                    vr[t][0] = vv.x;
+                    vr[t][1] = vv.y;
+                    vmax = fmaxf(vmax, fmaxf(vv.x, vv.y));
+                }
             }
-            pa[t >> 1][(t & 1) * 2] = pack2<F16>(e[0], e[1]);
-            pa[t >> 1][(t & 1) * 2 + 1] = pack2<F16>(e[2], e[3]);
-        }
-        // --- O += P V ---
-        if constexpr (KV != kKvE4m3) {
-            // the sums (fp32) are of the rounded probabilities, P times a column of ones: a weight's
-            // rounding then cancels where it dominates its row (relative error of a window of 128
-            // tokens against 64 bits 2.2e-3 -> 2.0e-3, of which 1.7e-3 is the output type)
-            constexpr uint32_t kOnes = F16 ? 0x3c003c00u : 0x3f803f80u;
+            const uint32_t valid = *reinterpret_cast<const uint32_t*>(stage + 2 * C::TILE + C::SC);
+            if (valid != kAllTokens) {
 #pragma unroll
-            for (int t = 0; t < KT; ++t) mma16816<F16>(ls, pa[t], kOnes, kOnes);
-            const int r = (lane & 7) + (((lane >> 3) & 1) << 3), hi = lane >> 4;
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int d = 0; d < KS; ++d) {
+                    for (int j = 0; j < 4; ++j)
+                        if (!((valid >> (t * 8 + 2 * c + (j & 1))) & 1u)) s[t][j] = -INFINITY;
+            }
+            float t0 = m0, t1 = m1;
 #pragma unroll
-                for (int t = 0; t < KT; ++t) {
+            for (int t = 0; t < NT; ++t) {
+                t0 = fmaxf(t0, fmaxf(s[t][0], s[t][1]));
+                t1 = fmaxf(t1, fmaxf(s[t][2], s[t][3]));
+            }
+            t0 = fmaxf(t0, __shfl_xor_sync(kAllLanes, t0, 1));
+            t1 = fmaxf(t1, __shfl_xor_sync(kAllLanes, t1, 1));
+            t0 = fmaxf(t0, __shfl_xor_sync(kAllLanes, t0, 2));
+            t1 = fmaxf(t1, __shfl_xor_sync(kAllLanes, t1, 2));
+            // The sums stay about an older maximum until a score passes it by kSlack powers of two (one
+            // warp-wide rescaling then): probabilities reach 2^kSlack, exact in the same number of bits.
+            bool far = (t0 - m0) * qf0 > kSlack || (t1 - m1) * qf1 > kSlack;  // NaN (both -inf): no
+            if constexpr (KV == kKvE4m3) {
+                vmax = fmaxf(vmax, __shfl_xor_sync(kAllLanes, vmax, 1));
+                vmax = fmaxf(vmax, __shfl_xor_sync(kAllLanes, vmax, 2));
+                far = far || vmax > vref;
+            }
+            if (__any_sync(kAllLanes, far)) {
+                const float n0 = t0 == -INFINITY ? 0.f : t0 * qf0, n1 = t1 == -INFINITY ? 0.f : t1 * qf1;
+                float c0 = ex2_approx(m0 * qf0 - n0), c1 = ex2_approx(m1 * qf1 - n1);
+                l0 *= c0;
+                l1 *= c1;
+                ls[0] *= c0;
+                ls[2] *= c1;
+                if (KV == kKvE4m3 && vmax > vref) {  // the accumulator's scale: room for values 4 times as large
+                    c0 *= vref / (4.f * vmax);
+                    c1 *= vref / (4.f * vmax);
+                    vref = 4.f * vmax;
+                    ivref = 1.0f / vref;
+                }
+#pragma unroll
+                for (int d = 0; d < DP / 8; ++d) {
+                    o[d][0] *= c0;
+                    o[d][1] *= c0;
+                    o[d][2] *= c1;
+                    o[d][3] *= c1;
+                }
+                m0 = t0;
+                m1 = t1;
+            }
+            const float b0 = m0 == -INFINITY ? 0.f : m0 * qf0, b1 = m1 == -INFINITY ? 0.f : m1 * qf1;
+            // --- probabilities (fp32 sums; rounded to 16 bits for the second product) ---
+            uint32_t pa[KT][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float e[4];
+                e[0] = ex2_approx(fmaf(s[t][0], qf0, -b0));
+                e[1] = ex2_approx(fmaf(s[t][1], qf0, -b0));
+                e[2] = ex2_approx(fmaf(s[t][2], qf1, -b1));
+                e[3] = ex2_approx(fmaf(s[t][3], qf1, -b1));
+                if constexpr (KV == kKvE4m3) {
+                    l0 += e[0] + e[1];
+                    l1 += e[2] + e[3];
+                    const float x = vr[t][0] * ivref, y = vr[t][1] * ivref;
+                    e[0] *= x;
+                    e[1] *= y;
+                    e[2] *= x;
+                    e[3] *= y;
+                }
+                pa[t >> 1][(t & 1) * 2] = pack2<F16>(e[0], e[1]);
+                pa[t >> 1][(t & 1) * 2 + 1] = pack2<F16>(e[2], e[3]);
+            }
+            // --- O += P V ---
+            if constexpr (KV != kKvE4m3) {
+                // the sums (fp32) are of the rounded probabilities, P times a column of ones: a weight's
+                // rounding then cancels where it dominates its row (relative error of a window of 128
+                // tokens against 64 bits 2.2e-3 -> 2.0e-3, of which 1.7e-3 is the output type)
+                constexpr uint32_t kOnes = F16 ? 0x3c003c00u : 0x3f803f80u;
+#pragma unroll
+                for (int t = 0; t < KT; ++t) mma16816<F16>(ls, pa[t], kOnes, kOnes);
+                const int r = (lane & 7) + (((lane >> 3) & 1) << 3), hi = lane >> 4;
+#pragma unroll
+                for (int d = 0; d < KS; ++d) {
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) {
+                        uint32_t b[4];
+                        ldsm4_t(vs_s + swz<C>(16 * t + r, 2 * d + hi), b);
+                        mma16816<F16>(o[2 * d], pa[t], b[0], b[1]);
+                        mma16816<F16>(o[2 * d + 1], pa[t], b[2], b[3]);
+                    }
+                }
+            } else {
+                // a transposed matrix hands a lane dims 2g, 2g+1 of tokens 2c, 2c+1: one product
+                // takes the even dims of a 16-dim block, one the odd
+                const int r = lane;
+#pragma unroll
+                for (int d = 0; d < KS; ++d) {
                     uint32_t b[4];
-                    ldsm4_t(vs_s + swz<C>(16 * t + r, 2 * d + hi), b);
-                    mma16816<F16>(o[2 * d], pa[t], b[0], b[1]);
-                    mma16816<F16>(o[2 * d + 1], pa[t], b[2], b[3]);
+                    ldsm4_t(vs_s + swz<C>(r, d), b);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t lo = __byte_perm(b[2 * k], 0, 0x3120), hi = __byte_perm(b[2 * k + 1], 0, 0x3120);
+                        mma16816<F16>(o[2 * d], pa[k], e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(hi));
+                        mma16816<F16>(o[2 * d + 1], pa[k], e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi >> 16));
+                    }
                 }
             }
-        } else {
-            // a transposed matrix hands a lane dims 2g, 2g+1 of tokens 2c, 2c+1: one product
-            // takes the even dims of a 16-dim block, one the odd
-            const int r = lane;
-#pragma unroll
-            for (int d = 0; d < KS; ++d) {
-                uint32_t b[4];
-                ldsm4_t(vs_s + swz<C>(r, d), b);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t lo = __byte_perm(b[2 * k], 0, 0x3120), hi = __byte_perm(b[2 * k + 1], 0, 0x3120);
-                    mma16816<F16>(o[2 * d], pa[k], e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(hi));
-                    mma16816<F16>(o[2 * d + 1], pa[k], e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi >> 16));
-                }
-            }
+            slot = slot + 1 == S ? 0 : slot + 1;
         }
-        slot = slot + 1 == S ? 0 : slot + 1;
-    }
 
-    // --- the segment is done: the row, or the run's part of it ---
-    b = row.b;
-    h = row.h;
-    starts = row.tile == 0;
-    ends = row.tile + nseg == row.ntiles;
-    rem -= nseg;
-    pos += nseg;
-    row.advance(p, nseg);
+        // --- the segment is done: the row, or the run's part of it ---
+        b = row.b;
+        h = row.h;
+        starts = row.tile == 0;
+        ends = row.tile + nseg == row.ntiles;
+        rem -= nseg;
+        pos += nseg;
+        row.advance(p, nseg);
     }
 }
 
@@ -936,20 +922,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendPara
 
 namespace {
 
-// A CTA's run is at least this many tiles (one per warp), a warp's two; rows of at
-// most kWholeTokens take a warp each; a CTA takes a row of its own where all rows
-// fit at once and none is longer than kTeamTokens; from kSoloRows rows on, runs
-// are a warp's: fewer waits at the rows' ends, and few parts to a row anyway.
-constexpr int kMinTilesLog2 = 2;
-constexpr int kMinSoloTilesLog2 = 1;
-#ifndef MOE_SOLO_ROWS
-#define MOE_SOLO_ROWS 96
-#endif
-constexpr int kSoloRows = MOE_SOLO_ROWS;
-constexpr int kWholeTokens = 128;
-constexpr int kTeamTokens = 512;
+// Rows of at most kWholeTokens are not cut where that costs little: a CTA takes a
+// row (all rows resident at once), or a warp takes rows, if the tiles that the
+// busiest has beyond the average are fewer than what runs over borders, their
+// joins and the second launch cost: kTeamTiles for a CTA, kRowTiles for a warp.
+// bf16, D = 64, 8 rows a sequence, us not cut / cut: 8 rows of 500 tokens 6.8 / 8.3,
+// of 1000 10.3 / 8.3; 64 rows of 1000 10.7 / 11.3; 256 rows of 1000 14.5 / 20.2; 2048
+// rows of 128 tokens 16.7 / 23.8, of 256 28.4 / 36.4; 512 rows of 256 11.7 / 14.9.
+constexpr int kWholeTokens = 1024;
+constexpr int kTeamTiles = 24;
+constexpr int kRowTiles = 6;
 
 int dp_of(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
+int tile_tokens(int dp, bool e4m3) { return e4m3 || dp == 64 ? 32 : 16; }
 int ctas_per_sm(int dp, bool e4m3) { return dp == 64 && e4m3 ? 3 : dp == 256 ? 1 : 2; }
 
 template <int DP, int KV, bool QF16>
@@ -977,10 +962,12 @@ void attend_plan(int B, int Hq, int Hkv, int D, bool e4m3, int most, int sms, At
     const int ctas = sms * ctas_per_sm(dp_of(D), e4m3);
     const long long rows = (long long)B * Hkv * ((Hq / Hkv + kAttRows - 1) / kAttRows);
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-    w->team = rows <= ctas && most <= kTeamTokens;
-    w->by_row = !w->team && most <= kWholeTokens;
-    w->solo = w->by_row || (!w->team && rows >= kSoloRows);
-    const int runs = w->solo ? ctas * kAttWarps : ctas;
+    const long long warps = (long long)ctas * kAttWarps, waves = (rows + warps - 1) / warps;
+    const long long tiles = (most + tile_tokens(dp_of(D), e4m3) - 1) / tile_tokens(dp_of(D), e4m3);
+    const bool whole = most <= kWholeTokens;
+    w->team = whole && rows <= ctas && tiles * (ctas - rows) <= (long long)kTeamTiles * ctas;
+    w->by_row = whole && !w->team && tiles * (waves * warps - rows) <= kRowTiles * warps;
+    const int runs = ctas;
     w->runs = runs;
     w->ctas = w->team ? (int)rows : ctas;
     w->by_row_join = rows <= runs;
@@ -998,7 +985,6 @@ cudaError_t launch_attend(const AttendParams& p_in, const AttendPlan& w, int kv_
     p.runs = w.runs;
     p.team = w.team;
     p.by_row = w.by_row;
-    p.solo = w.solo;
     p.group = p.Hq / p.Hkv;
     p.head_blocks = (p.group + kAttRows - 1) / kAttRows;
     p.rows_per_seq = p.Hkv * p.head_blocks;
@@ -1007,7 +993,6 @@ cudaError_t launch_attend(const AttendParams& p_in, const AttendPlan& w, int kv_
     if ((p.page_size & (p.page_size - 1)) == 0)
         for (p.page_shift = 0; (1 << p.page_shift) < p.page_size;) ++p.page_shift;
     const long long rows = (long long)p.B * p.rows_per_seq;
-    p.min_tiles_shift = p.solo ? kMinSoloTilesLog2 : kMinTilesLog2;
     if (w.total) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);
         p.by_row_join = w.by_row_join;
