@@ -38,10 +38,21 @@ constexpr int kAttRows = 16;  // query heads per row (m16 of the products)
 constexpr float kSlack = 8.f;
 enum : int { kKvBf16 = 0, kKvFp16 = 1, kKvE4m3 = 2 };
 
-template <int DP, int KV>
+// How the rows are given out: equal runs of tiles, one per CTA; a row per CTA; rows
+// per warp.  attend_plan chooses.
+enum : int { kRuns = 0, kTeam = 1, kRows = 2 };
+
+// Tokens per tile and CTAs per SM.  light (16-bit caches of up to 64 dims): half the
+// tile and twice the warps, for whole rows that one wave of these takes.
+constexpr int tile_tokens(int dp, bool e4m3, bool light) { return e4m3 || (dp == 64 && !light) ? 32 : 16; }
+constexpr int ctas_per_sm(int dp, bool e4m3, bool light) {
+    return dp == 64 ? (e4m3 ? 3 : light ? 4 : 2) : dp == 256 ? 1 : 2;
+}
+
+template <int DP, int KV, bool LIGHT>
 struct AttCfg {
     static constexpr int ES = KV == kKvE4m3 ? 1 : 2;       // bytes of a cached value
-    static constexpr int TT = KV == kKvE4m3 || DP == 64 ? 32 : 16;  // tokens per tile
+    static constexpr int TT = tile_tokens(DP, KV == kKvE4m3, LIGHT);  // tokens per tile
     static constexpr int CH = DP * ES / 16;                // 16-byte chunks of a token's row
     static constexpr int LANES = CH <= 4 ? 4 : CH <= 8 ? 8 : CH <= 16 ? 16 : 32;  // lanes that copy it
     static constexpr int PITCH = DP == 96 ? CH | 1 : CH;   // chunks from row to row in shared memory
@@ -53,7 +64,7 @@ struct AttCfg {
     static constexpr int QS = DP == 256 ? DP / 16 * 512 : 0;  // Q fragments, where registers do not hold them
     static constexpr int WARP = (STAGES * STAGE + QS + 127) / 128 * 128;
     static constexpr int SMEM = kAttWarps * WARP;
-    static constexpr int CTAS = DP == 64 && KV == kKvE4m3 ? 3 : DP == 256 ? 1 : 2;  // resident per SM
+    static constexpr int CTAS = ctas_per_sm(DP, KV == kKvE4m3, LIGHT);
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -205,9 +216,10 @@ __device__ __forceinline__ float final_weight(const AttendParams& p, int head, f
 
 }  // namespace
 
-template <int DP, int KV, bool QF16>
-__global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_kernel(AttendParams p) {
-    using C = AttCfg<DP, KV>;
+template <int DP, int KV, bool QF16, int MODE, bool LIGHT>
+__global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) attend_kernel(AttendParams p) {
+    using C = AttCfg<DP, KV, LIGHT>;
+    constexpr bool ROWS = MODE == kRows;
     constexpr bool F16 = KV != kKvBf16;  // type of the products
     constexpr int TT = C::TT, NT = TT / 8, KT = TT / 16, KS = DP / 16, S = C::STAGES;
     constexpr uint32_t kAllTokens = TT == 32 ? 0xffffffffu : 0xffffu;
@@ -225,13 +237,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
     TileIt<TT> it;  // of the copies
     int rem;        // tiles of the run
     const int run = blockIdx.x;
-    if (p.team) {  // few rows, none long: one to a CTA
-        it.b = run / p.rows_per_seq;
-        it.h = run - it.b * p.rows_per_seq;
-        it.tile = 0;
-        it.seq(p);
-        rem = it.ntiles;
-    } else if (p.by_row) {  // neighbouring warps' rows on different SMs
+    if constexpr (ROWS) {  // neighbouring warps' rows on different SMs
         const int nwarps = gridDim.x * kAttWarps, w = warp * gridDim.x + blockIdx.x;
         const int rows = p.B * p.rows_per_seq, n = rows < nwarps ? rows : nwarps;
         if (w >= n) return;
@@ -246,6 +252,12 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             rem += t.ntiles;
             t.advance(p, t.ntiles);
         }
+    } else if constexpr (MODE == kTeam) {  // few rows, none long: one to a CTA
+        it.b = run / p.rows_per_seq;
+        it.h = run - it.b * p.rows_per_seq;
+        it.tile = 0;
+        it.seq(p);
+        rem = it.ntiles;
     } else {
         // each thread sums the tiles of a slice of the sequences (rows_per_seq rows each)
         const int slice = (p.B + kAttWarps * 32 - 1) / (kAttWarps * 32);
@@ -305,9 +317,9 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
         if (tid == 0) p.cont[run] = it.tile ? it.b * p.rows_per_seq + it.h : -1;
     }
     TileIt<TT> row = it;  // of the products: the tile that the current segment (a row's tiles in the run) begins with
-    const int step = p.by_row ? 1 : kAttWarps;
-    int to_issue = p.by_row ? rem : rem > warp ? (rem - warp + kAttWarps - 1) / kAttWarps : 0;  // tiles of this warp
-    if (!p.by_row && to_issue > 0) it.advance(p, warp);
+    constexpr int step = ROWS ? 1 : kAttWarps;
+    int to_issue = ROWS ? rem : rem > warp ? (rem - warp + kAttWarps - 1) / kAttWarps : 0;  // tiles of this warp
+    if (!ROWS && to_issue > 0) it.advance(p, warp);
 
     // --- the ring ---
     uint8_t* ring = smem + warp * C::WARP;
@@ -491,15 +503,15 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             }
             m0 *= qf0;  // from here on in powers of two
             m1 *= qf1;
-            const bool done = starts && ends;
+            const bool done = MODE != kRuns || (starts && ends);
             float* part = done ? nullptr : p.partial + ((long long)run * 2 + (starts ? 1 : 0)) * (kAttRows * (p.D + 2));
             // the runs that a row begins and ends in, for the join (first -1: one run has all of it)
-            if (p.by_row_join && tid == 0) {
+            if (MODE == kRuns && p.by_row_join && tid == 0) {
                 const int at = b * p.rows_per_seq + h;
                 if (starts) p.first[at] = ends ? -1 : run;
                 if (ends && !starts) p.last[at] = run;
             }
-            if (p.by_row) {
+            if constexpr (ROWS) {
                 float w0 = g < heads ? final_weight(p, head0 + g, m0, l0) : 0.f;
                 float w1 = g + 8 < heads ? final_weight(p, head0 + g + 8, m1, l1) : 0.f;
                 if constexpr (KV == kKvE4m3) {
@@ -639,7 +651,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV>::CTAS) attend_k
             }
         }
         // a warp's tiles of the segment: places of the run that are its own modulo the warps
-        for (int j = p.by_row ? 0 : (warp - pos) & (kAttWarps - 1); j < nseg; j += step) {
+        for (int j = ROWS ? 0 : (warp - pos) & (kAttWarps - 1); j < nseg; j += step) {
             cp_async_wait<S - 2>();
             __syncwarp();
             issue_next(fill);
@@ -922,60 +934,102 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendPara
 
 namespace {
 
-// Rows of at most kWholeTokens are not cut where that costs little: a CTA takes a
-// row (all rows resident at once), or a warp takes rows, if the tiles that the
-// busiest has beyond the average are fewer than what runs over borders, their
-// joins and the second launch cost: kTeamTiles for a CTA, kRowTiles for a warp.
-// bf16, D = 64, 8 rows a sequence, us not cut / cut: 8 rows of 500 tokens 6.8 / 8.3,
-// of 1000 10.3 / 8.3; 64 rows of 1000 10.7 / 11.3; 256 rows of 1000 14.5 / 20.2; 2048
-// rows of 128 tokens 16.7 / 23.8, of 256 28.4 / 36.4; 512 rows of 256 11.7 / 14.9.
+// Rows of at most kWholeTokens are not cut where that costs little.  A CTA takes a
+// row, all rows resident at once: up to one wave of the wide kernel if the tiles
+// that its idle CTAs miss are few (kTeamTiles each on average), up to one of the
+// light kernel (between the two, us of the light team / warps with rows / cut: 320 rows
+// of 128 tokens 6.3 / 7.0 / 11.2, 600 of 512 15.9 / 19.8 / 23.3, of 1000 27.9 / 35.7 / 34.6;
+// below, the wide team wins: 256 rows of 300 7.1 / 7.7).  Else a warp takes rows, if the
+// tiles that the busiest has beyond the average are fewer than what the alternative
+// costs: borders, joins and the second launch (kRowTiles) and a meeting of the
+// CTA's warps at every row's end (kEndTiles), both twice as many where a warp's
+// tile counts half (light) or a CTA has the SM for itself (more than 128 dims).
+// us whole / cut, bf16, D = 64: 1024 rows of 128 tokens 8.1 / 19.2, of 1000 45.5 / 52.2; 2600
+// of 256 38.5 / 46.8, of 512 69.6 / 68.1, of 1000 130 / 111; light: 1296 of 128 11.1 / 20.6, of
+// 1000 60.9 / 62.8; D = 128, e4m3: 320 of 256 15.9 / 19.3, of 512 27.2 / 22.5, 4096 of 512 116 / 158;
+// D = 256: 320 of 512 42.9 / 56.9, 1300 of 1000 277 / 251.
 constexpr int kWholeTokens = 1024;
 constexpr int kTeamTiles = 24;
-constexpr int kRowTiles = 6;
+constexpr int kRowTiles = 9, kEndTiles = 3;
 
 int dp_of(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
-int tile_tokens(int dp, bool e4m3) { return e4m3 || dp == 64 ? 32 : 16; }
-int ctas_per_sm(int dp, bool e4m3) { return dp == 64 && e4m3 ? 3 : dp == 256 ? 1 : 2; }
 
-template <int DP, int KV, bool QF16>
-cudaError_t launch_attend_t(const AttendParams& p, int grid, cudaStream_t st) {
-    using C = AttCfg<DP, KV>;
+template <int DP, int KV, bool QF16, int MODE, bool LIGHT>
+cudaError_t launch_attend_m(const AttendParams& p, int grid, cudaStream_t st) {
+    using C = AttCfg<DP, KV, LIGHT>;
     static_assert(C::SMEM * C::CTAS <= 226 * 1024, "shared memory of the resident CTAs");
-    cudaError_t e = cudaFuncSetAttribute(attend_kernel<DP, KV, QF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    const auto kernel = attend_kernel<DP, KV, QF16, MODE, LIGHT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attend_kernel<DP, KV, QF16>, dim3(grid), dim3(kAttWarps * 32), C::SMEM, st, p);
+    return launch_pdl(kernel, dim3(grid), dim3(kAttWarps * 32), C::SMEM, st, p);
+}
+template <int DP, int KV, bool QF16>
+cudaError_t launch_attend_t(const AttendParams& p, const AttendPlan& w, cudaStream_t st) {
+    if constexpr (DP == 64 && KV != kKvE4m3) {
+        if (w.light)
+            return w.mode == kRows ? launch_attend_m<DP, KV, QF16, kRows, true>(p, w.ctas, st)
+                                   : launch_attend_m<DP, KV, QF16, kTeam, true>(p, w.ctas, st);
+    }
+    return w.mode == kRows   ? launch_attend_m<DP, KV, QF16, kRows, false>(p, w.ctas, st)
+           : w.mode == kTeam ? launch_attend_m<DP, KV, QF16, kTeam, false>(p, w.ctas, st)
+                             : launch_attend_m<DP, KV, QF16, kRuns, false>(p, w.ctas, st);
 }
 template <int KV, bool QF16>
-cudaError_t launch_attend_d(const AttendParams& p, int grid, cudaStream_t st) {
+cudaError_t launch_attend_d(const AttendParams& p, const AttendPlan& w, cudaStream_t st) {
     switch (dp_of(p.D)) {
-        case 64: return launch_attend_t<64, KV, QF16>(p, grid, st);
-        case 96: return launch_attend_t<96, KV, QF16>(p, grid, st);
-        case 128: return launch_attend_t<128, KV, QF16>(p, grid, st);
-        default: return launch_attend_t<256, KV, QF16>(p, grid, st);
+        case 64: return launch_attend_t<64, KV, QF16>(p, w, st);
+        case 96: return launch_attend_t<96, KV, QF16>(p, w, st);
+        case 128: return launch_attend_t<128, KV, QF16>(p, w, st);
+        default: return launch_attend_t<256, KV, QF16>(p, w, st);
     }
 }
 
 }  // namespace
 
-// How the rows are given to warps; the workspace is for the parts of cut rows.
+// The workspace is for the parts of cut rows.
 void attend_plan(int B, int Hq, int Hkv, int D, bool e4m3, int most, int sms, AttendPlan* w) {
-    const int ctas = sms * ctas_per_sm(dp_of(D), e4m3);
+    const int dp = dp_of(D);
     const long long rows = (long long)B * Hkv * ((Hq / Hkv + kAttRows - 1) / kAttRows);
+    const int ctas = sms * ctas_per_sm(dp, e4m3, false), light_ctas = sms * ctas_per_sm(dp, e4m3, true);
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-    const long long warps = (long long)ctas * kAttWarps, waves = (rows + warps - 1) / warps;
-    const long long tiles = (most + tile_tokens(dp_of(D), e4m3) - 1) / tile_tokens(dp_of(D), e4m3);
-    const bool whole = most <= kWholeTokens;
-    w->team = whole && rows <= ctas && tiles * (ctas - rows) <= (long long)kTeamTiles * ctas;
-    w->by_row = whole && !w->team && tiles * (waves * warps - rows) <= kRowTiles * warps;
+    auto tiles = [&](bool light) {
+        const int tt = tile_tokens(dp, e4m3, light);
+        return (long long)((most + tt - 1) / tt);
+    };
+    auto waves = [&](long long n) { return (rows + n * kAttWarps - 1) / (n * kAttWarps); };
+    w->mode = kRuns;
+    w->light = false;
+    w->ctas = ctas;
+    if (most <= kWholeTokens) {
+        if (rows <= ctas) {
+            if (tiles(false) * (ctas - rows) <= (long long)kTeamTiles * ctas) w->mode = kTeam;
+        } else if (rows <= light_ctas) {
+            w->mode = kTeam;
+            w->light = true;
+        }
+        if (w->mode == kTeam) {
+            w->ctas = (int)rows;
+        } else {
+            // twice the warps at half the speed: 2048 rows of 128 tokens 14.8 us light, 16.2 not (one
+            // wave against two), 1024 rows 10.0, 8.1 (one against one)
+            const bool light = light_ctas > ctas && 2 * waves(light_ctas) <= waves(ctas);
+            const int n = light ? light_ctas : ctas;
+            const long long warps = (long long)n * kAttWarps, few = kRowTiles * warps + kEndTiles * rows;
+            if (tiles(light) * (waves(n) * warps - rows) <= (light || dp == 256 ? 2 : 1) * few) {
+                w->mode = kRows;
+                w->light = light;
+                w->ctas = n;
+            }
+        }
+    }
     const int runs = ctas;
     w->runs = runs;
-    w->ctas = w->team ? (int)rows : ctas;
     w->by_row_join = rows <= runs;
     w->cont = 0;
     w->first = up((size_t)runs * 4);
     w->last = w->first + up((size_t)(rows <= runs ? rows : 1) * 4);
     w->partial = w->last + up((size_t)(rows <= runs ? rows : 1) * 4);
-    w->total = w->team || w->by_row ? 0 : w->partial + (size_t)runs * 2 * kAttRows * (D + 2) * 4;
+    w->total = w->mode != kRuns ? 0 : w->partial + (size_t)runs * 2 * kAttRows * (D + 2) * 4;
 }
 
 cudaError_t launch_attend(const AttendParams& p_in, const AttendPlan& w, int kv_dtype, bool fp16, void* workspace,
@@ -983,8 +1037,6 @@ cudaError_t launch_attend(const AttendParams& p_in, const AttendPlan& w, int kv_
     AttendParams p = p_in;
     const bool e4m3 = kv_dtype == kDtE4m3;
     p.runs = w.runs;
-    p.team = w.team;
-    p.by_row = w.by_row;
     p.group = p.Hq / p.Hkv;
     p.head_blocks = (p.group + kAttRows - 1) / kAttRows;
     p.rows_per_seq = p.Hkv * p.head_blocks;
@@ -1001,13 +1053,12 @@ cudaError_t launch_attend(const AttendParams& p_in, const AttendPlan& w, int kv_
         p.last = reinterpret_cast<int32_t*>(ws + w.last);
         p.partial = reinterpret_cast<float*>(ws + w.partial);
     }
-    const int grid = w.ctas;
     cudaError_t e;
     if (e4m3)
-        e = fp16 ? launch_attend_d<kKvE4m3, true>(p, grid, st) : launch_attend_d<kKvE4m3, false>(p, grid, st);
+        e = fp16 ? launch_attend_d<kKvE4m3, true>(p, w, st) : launch_attend_d<kKvE4m3, false>(p, w, st);
     else
-        e = fp16 ? launch_attend_d<kKvFp16, true>(p, grid, st) : launch_attend_d<kKvBf16, false>(p, grid, st);
-    if (e != cudaSuccess || p.by_row || p.team) return e;
+        e = fp16 ? launch_attend_d<kKvFp16, true>(p, w, st) : launch_attend_d<kKvBf16, false>(p, w, st);
+    if (e != cudaSuccess || w.mode != kRuns) return e;
     // warps per head by the parts that a row can have on average
     const int heads = p.group < kAttRows ? p.group : kAttRows;
     p.jobs = p.by_row_join ? (int)rows : p.runs;

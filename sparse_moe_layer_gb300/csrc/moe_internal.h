@@ -98,8 +98,6 @@ struct AttendParams {
     // set at launch
     int group, head_blocks, rows_per_seq;  // query heads per key head; blocks of 16 of them; rows of a sequence
     int page_shift, page16;                // log2(page_size), -1 if none; whether 16 divides it
-    int team;                              // a CTA per row
-    int by_row;                            // a warp's run of whole rows
     int by_row_join, runs, jobs, join_warps;
     int32_t* cont;   // [runs] row that the run continues, -1: it starts one
     int32_t* first;  // [rows] run that the row begins in, -1: it ends there too (by_row_join)
@@ -107,7 +105,7 @@ struct AttendParams {
     float* partial;  // [runs, 2, 16 (max, sum) + 16 x D]
 };
 struct AttendPlan {
-    int ctas, runs, team, by_row, by_row_join;
+    int mode, light, ctas, runs, by_row_join;
     size_t cont, first, last, partial, total;  // workspace; total 0: none needed
 };
 

@@ -232,6 +232,19 @@ def test_ragged_batches(dtype, cache):
 
 
 @gpu
+@pytest.mark.parametrize("dtype,cache", CACHES)
+@pytest.mark.parametrize("D", [48, 64, 128, 256])
+@pytest.mark.parametrize("B", [39, 76, 100, 160, 330])
+def test_many_short_rows(B, D, dtype, cache):
+    """Whole rows by CTA and by warp, below, at and past one wave of each: 8 B rows."""
+    lens = [(i * 53) % 131 for i in range(B)]
+    Case(lens, 16, 8, D, dtype=dtype, cache=cache, seed=B).both(sinks=True)
+    c = Case([n + 60 for n in lens], 16, 8, D, dtype=dtype, cache=cache, seed=B)
+    c.both(window=33, sinks=True)
+    c.both()
+
+
+@gpu
 def test_large_batch_of_slices():
     """More sequences than one per thread: the list is searched by slices."""
     lens = [(i * 37) % 50 for i in range(2500)]
