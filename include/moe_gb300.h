@@ -447,9 +447,10 @@ moe_status moe_rotate_append(const moe_kv_cache* cache, const void* q, const voi
  *   page_size if that is less); 256: such rows are not cut, and it may be NULL
  *   status: a device error word for moe_read_device_status, or NULL
  * Limits: those of the cache; q_heads a multiple of kv_heads, at most 4096;
- * 1 <= B <= 65536, B * q_heads < 2^27; table_width * page_size < 2^31; q and out:
- * pointers and strides multiples of 4 bytes.  The result is the same for every
- * run of the same call.  Asynchronous on `stream`.
+ * 1 <= B <= 65536, B * q_heads < 2^27; table_width * page_size and
+ * B * (max_tokens / 16 + 2) at most 2^31 - 32; q and out: pointers and strides
+ * multiples of 4 bytes.  The result is the same for every run of the same call.
+ * Asynchronous on `stream`.
  */
 size_t moe_attention_workspace_size(int B, int q_heads, int kv_heads, int head_dim, int cache_dtype, int max_tokens);
 moe_status moe_paged_attention(const moe_kv_cache* cache, const void* q, int dtype, int64_t q_token, int64_t q_head,

@@ -889,6 +889,9 @@ extern "C" moe_status moe_rotate_append(const moe_kv_cache* cache, const void* q
                : MOE_ERR_CUDA;
 }
 
+// A sequence's tokens, at most: a multiple of every tile below 2^31.
+constexpr long long kMaxTokens = (1LL << 31) - 32;
+
 static bool attention_ok(int B, int q_heads, int kv_heads, int head_dim) {
     return B >= 1 && B <= 65536 && kv_heads >= 1 && kv_heads <= 256 && q_heads >= 1 && q_heads <= 4096 &&
            q_heads % kv_heads == 0 && (long long)B * q_heads < (1LL << 27) && head_dim >= 16 && head_dim <= 256 &&
@@ -916,8 +919,11 @@ extern "C" moe_status moe_paged_attention(const moe_kv_cache* cache, const void*
     if (!q || !page_table || !lengths || !out) return MOE_ERR_INVALID_ARG;
     if (!attention_ok(B, q_heads, cache->kv_heads, cache->head_dim) || table_width < 1 || window < 0 || scale != scale)
         return MOE_ERR_INVALID_ARG;
-    if ((long long)table_width * cache->page_size >= (1LL << 31) || (B > 1 && table_ld < table_width))
-        return MOE_ERR_INVALID_ARG;
+    // token numbers, rounded up to a tile, and the tiles of all sequences fit 31 bits
+    const long long most = (long long)table_width * cache->page_size;
+    if (most > kMaxTokens || (B > 1 && table_ld < table_width)) return MOE_ERR_INVALID_ARG;
+    const long long seen = window > 0 && window < most ? window : most;
+    if (B * (seen / 16 + 2) > kMaxTokens) return MOE_ERR_INVALID_ARG;
     if (dtype != MOE_BF16 && dtype != MOE_FP16) return MOE_ERR_UNSUPPORTED;
     if (cache->dtype != MOE_E4M3 && cache->dtype != dtype) return MOE_ERR_UNSUPPORTED;
     if (B == 1) q_token = out_token = table_ld = 0;
@@ -928,10 +934,10 @@ extern "C" moe_status moe_paged_attention(const moe_kv_cache* cache, const void*
           reinterpret_cast<uintptr_t>(status)) & 3u) ||
         ((q_token | q_head | out_token | out_head) & 1) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return MOE_ERR_UNSUPPORTED;
-    p.max_tokens = table_width * cache->page_size;
+    p.max_tokens = (int)most;
     AttendPlan w;
-    attend_plan(B, q_heads, cache->kv_heads, cache->head_dim, cache->dtype == MOE_E4M3,
-                window > 0 && window < p.max_tokens ? window : p.max_tokens, num_sms(), &w);
+    attend_plan(B, q_heads, cache->kv_heads, cache->head_dim, cache->dtype == MOE_E4M3, (int)seen,
+                num_sms(), &w);
     if (w.total && !workspace) return MOE_ERR_INVALID_ARG;
     if (workspace_bytes < w.total) return MOE_ERR_WORKSPACE;
     p.q = static_cast<const uint16_t*>(q);

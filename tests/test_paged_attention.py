@@ -66,6 +66,19 @@ def test_refusals_on_the_host():
     assert size(1, 4, 2, 64, 0, 99) == 256 and size(1, 4, 2, 64, 3, 99999) > 256
 
 
+def test_lengths_past_31_bits_are_refused():
+    """Token numbers are rounded up to a tile of 32, and a batch's tiles are counted in 32 bits."""
+    L = moe.lib()
+
+    def call(B, width, page=16, window=0, ws=None):
+        return L.moe_paged_attention(kv_bytes(S=page), 256, 0, 256, 64, 256, width, width, 256, B, 4, 0.125, None, window,
+                                     256, 256, 64, ws, 0, None, None)
+
+    assert call(1, (1 << 27) - 1) == 1 and call(1, (1 << 31) - 17, page=1) == 1
+    assert call(1, (1 << 27) - 2, ws=256) == 3  # passes, for the workspace to be found too small
+    assert call(65536, 1 << 16, ws=256) == 1 and call(65536, 1 << 14, ws=256) == 3
+
+
 def test_binding_refuses():
     q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
     kv = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
