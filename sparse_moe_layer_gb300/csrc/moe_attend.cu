@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
         if (p.page16) {  // a group of 16 tokens lies on one page
 #pragma unroll
             for (int hh = 0; hh < KT; ++hh) {
-                const long long pid = __shfl_sync(kAllLanes, f.pid, hh * 16), off = __shfl_sync(kAllLanes, f.off, hh * 16);
+                const long long pid = __shfl_sync(kAllLanes, f.pid, hh * 16);
+                const long long off = __shfl_sync(kAllLanes, f.off, hh * 16);
                 const uint8_t* ks = kb + (pid * p.cache.k_page + off * p.cache.k_token) * C::ES + k_lane;
                 const uint8_t* vs = vb + (pid * p.cache.v_page + off * p.cache.v_token) * C::ES + v_lane;
                 if (((mask >> (16 * hh)) & 0xffffu) == 0xffffu) {
@@ -391,9 +392,11 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
                 const long long pid = __shfl_sync(kAllLanes, f.pid, r), off = __shfl_sync(kAllLanes, f.off, r);
                 const bool ok = (mask >> r) & 1u;
                 const uint32_t at = dst + swz<C>(r, ch);
+                const long long k_at = (pid * p.cache.k_page + off * p.cache.k_token) * C::ES + ch * 16;
+                const long long v_at = (pid * p.cache.v_page + off * p.cache.v_token) * C::ES + ch * 16;
                 if (in) {
-                    cp_async16z(at, ok ? kb + (pid * p.cache.k_page + off * p.cache.k_token) * C::ES + ch * 16 : kb, ok);
-                    cp_async16z(at + C::TILE, ok ? vb + (pid * p.cache.v_page + off * p.cache.v_token) * C::ES + ch * 16 : vb, ok);
+                    cp_async16z(at, ok ? kb + k_at : kb, ok);
+                    cp_async16z(at + C::TILE, ok ? vb + v_at : vb, ok);
                 }
             }
         }
@@ -635,8 +638,9 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
             const uint32_t e0 = min(max(__float_as_uint(a0) >> 23, 1u), 253u);
             const uint32_t e1 = min(max(__float_as_uint(a1) >> 23, 1u), 253u);
             const float f0 = __uint_as_float((254u - e0) << 23), f1 = __uint_as_float((254u - e1) << 23);
-            qf0 = p.scale_log2 * __uint_as_float(e0 << 23);
-            qf1 = p.scale_log2 * __uint_as_float(e1 << 23);
+            // not 0, which would make NaN of a masked score
+            qf0 = fmaxf(p.scale_log2 * __uint_as_float(e0 << 23), 0x1p-126f);
+            qf1 = fmaxf(p.scale_log2 * __uint_as_float(e1 << 23), 0x1p-126f);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 uint32_t a[4];
@@ -915,8 +919,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendPara
         __syncthreads();
         if (sub == 0 && d < p.D)
             for (int w = 1; w < p.join_warps; ++w) {
-                Sums x = {s_ml[warp + w][0], s_ml[warp + w][1], {*reinterpret_cast<const float4*>(&s_v[warp + w][d]), a.v[1]}};
-                if (d + 128 < p.D) x.v[1] = *reinterpret_cast<const float4*>(&s_v[warp + w][d + 128]);
+                const float* v = s_v[warp + w] + d;
+                Sums x = {s_ml[warp + w][0], s_ml[warp + w][1], {*reinterpret_cast<const float4*>(v), a.v[1]}};
+                if (d + 128 < p.D) x.v[1] = *reinterpret_cast<const float4*>(v + 128);
                 join(a, x);
             }
     }

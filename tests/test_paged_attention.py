@@ -275,6 +275,14 @@ def test_peaked_and_flat_scores():
 
 
 @gpu
+def test_zero_queries_with_a_scale_of_zero():
+    """The scores' factor of such a row stays above 0 (0 times a masked score's -inf is NaN)."""
+    for cache in ("bf16", "e4m3"):
+        Case([1000, 33], 8, 2, 64, cache=cache, spread=0.0).both(scale=0.0)
+        Case([7, 33], 8, 2, 64, cache=cache, spread=0.0).both(scale=-1e-30, sinks=True)
+
+
+@gpu
 def test_extreme_sinks():
     c = Case([0, 1, 50, 3000], 8, 2, 64)
     c.sinks = torch.tensor([-math.inf, 100.0, -100.0, 30.0, 0.0, 1e30, -1e30, 5.0], device="cuda")
