@@ -49,6 +49,35 @@ constexpr int ctas_per_sm(int dp, bool e4m3, bool light) {
     return dp == 64 ? (e4m3 ? 3 : light ? 4 : 2) : dp == 256 ? 1 : 2;
 }
 
+// Rows of at most kWholeTokens are not cut where that costs little.  A CTA takes a
+// row, all rows resident at once: up to one wave of the wide kernel if the tiles
+// that its idle CTAs miss are few (kTeamTiles each on average), up to one of the
+// light kernel (between the two, us of the light team / warps with rows / cut: 320 rows
+// of 128 tokens 6.3 / 7.0 / 11.2, 600 of 512 15.9 / 19.8 / 23.3, of 1000 27.9 / 35.7 / 34.6;
+// below, the wide team wins: 256 rows of 300 7.1 / 7.7).  Else a warp takes rows, if the
+// tiles that the busiest has beyond the average are fewer than what the alternative
+// costs: borders, joins and the second launch (kRowTiles) and a meeting of the
+// CTA's warps at every row's end (kEndTiles), both twice as many where a warp's
+// tile counts half (light) or a CTA has the SM for itself (more than 128 dims).
+// us whole / cut, bf16, D = 64: 1024 rows of 128 tokens 8.1 / 19.2, of 1000 45.5 / 52.2; 2600
+// of 256 38.5 / 46.8, of 512 69.6 / 68.1, of 1000 130 / 111; light: 1296 of 128 11.1 / 20.6, of
+// 1000 60.9 / 62.8; D = 128, e4m3: 320 of 256 15.9 / 19.3, of 512 27.2 / 22.5, 4096 of 512 116 / 158;
+// D = 256: 320 of 512 42.9 / 56.9, 1300 of 1000 277 / 251.
+// kRowTilesFound: the same in a kernel that was launched for long rows and finds short
+// ones, with more rows than CTAs; what it was launched with costs the join's launch either
+// way. us whole / cut, table of 16000 tokens more: bf16, D = 64: 2048 rows of 1-128 tokens
+// 17.1 / 36.9, of 256 32.0 / 38.1, 320 of 64 8.7 / 8.6, of 256 14.2 / 12.8, 64 of 256 12.7 / 7.9;
+// D = 128, e4m3: 2048 of 1-128 23.7 / 71.5, of 1000 111 / 128.
+constexpr int kWholeTokens = 1024;
+constexpr int kTeamTiles = 24;
+constexpr int kRowTiles = 9, kEndTiles = 4;
+constexpr int kRowTilesFound = 4;
+// Whether warps of n CTAs take whole rows of up to `tiles` tiles (allowance, weight: as above).
+__host__ __device__ inline bool rows_fit(long long tiles, long long rows, int n, int allowance, int weight) {
+    const long long warps = (long long)n * kAttWarps, waves = (rows + warps - 1) / warps;
+    return tiles * (waves * warps - rows) <= weight * (allowance * warps + kEndTiles * rows);
+}
+
 template <int DP, int KV, bool LIGHT>
 struct AttCfg {
     static constexpr int ES = KV == kKvE4m3 ? 1 : 2;       // bytes of a cached value
@@ -219,13 +248,13 @@ __device__ __forceinline__ float final_weight(const AttendParams& p, int head, f
 template <int DP, int KV, bool QF16, int MODE, bool LIGHT>
 __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) attend_kernel(AttendParams p) {
     using C = AttCfg<DP, KV, LIGHT>;
-    constexpr bool ROWS = MODE == kRows;
+    bool by_row = MODE == kRows;  // kRuns: if the lengths found are all short
     constexpr bool F16 = KV != kKvBf16;  // type of the products
     constexpr int TT = C::TT, NT = TT / 8, KT = TT / 16, KS = DP / 16, S = C::STAGES;
     constexpr uint32_t kAllTokens = TT == 32 ? 0xffffffffu : 0xffffu;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_pre[kAttWarps * 32 + 1];
-    __shared__ int s_wsum[kAttWarps];
+    __shared__ int s_wsum[kAttWarps], s_wmax[kAttWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
     __shared__ float2 s_ml[kAttWarps][kAttRows];  // a segment's maxima and sums
@@ -237,10 +266,10 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
     TileIt<TT> it;  // of the copies
     int rem;        // tiles of the run
     const int run = blockIdx.x;
-    if constexpr (ROWS) {  // neighbouring warps' rows on different SMs
+    auto whole_rows = [&]() {  // a warp's rows, neighbouring warps' on different SMs; false: none
         const int nwarps = gridDim.x * kAttWarps, w = warp * gridDim.x + blockIdx.x;
         const int rows = p.B * p.rows_per_seq, n = rows < nwarps ? rows : nwarps;
-        if (w >= n) return;
+        if (w >= n) return false;
         const int u0 = (int)((long long)rows * w / n), u1 = (int)((long long)rows * (w + 1) / n);
         it.b = u0 / p.rows_per_seq;
         it.h = u0 - it.b * p.rows_per_seq;
@@ -252,6 +281,10 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
             rem += t.ntiles;
             t.advance(p, t.ntiles);
         }
+        return true;
+    };
+    if constexpr (MODE == kRows) {
+        if (!whole_rows()) return;
     } else if constexpr (MODE == kTeam) {  // few rows, none long: one to a CTA
         it.b = run / p.rows_per_seq;
         it.h = run - it.b * p.rows_per_seq;
@@ -261,13 +294,15 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
     } else {
         // each thread sums the tiles of a slice of the sequences (rows_per_seq rows each)
         const int slice = (p.B + kAttWarps * 32 - 1) / (kAttWarps * 32);
-        int mine = 0;
+        int mine = 0, longest = 0;
         for (int i = 0; i < slice; ++i) {
             const int b = tid * slice + i;
             if (b < p.B) {
                 int st;
                 const int len = seen_tokens(p, b, &st);
-                mine += tiles_of<TT>(st, len);
+                const int nt = tiles_of<TT>(st, len);
+                mine += nt;
+                longest = max(longest, nt);
             }
         }
         int inc = mine;
@@ -276,50 +311,62 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
             const int v = __shfl_up_sync(kAllLanes, inc, o);
             if (lane >= o) inc += v;
         }
-        if (lane == 31) s_wsum[warp] = inc;
+        longest = __reduce_max_sync(kAllLanes, longest);
+        if (lane == 31) s_wsum[warp] = inc, s_wmax[warp] = longest;
         __syncthreads();
         int before = 0;
 #pragma unroll
-        for (int w = 0; w < kAttWarps; ++w)
+        for (int w = 0; w < kAttWarps; ++w) {
             if (w < warp) before += s_wsum[w];
+            longest = max(longest, s_wmax[w]);
+        }
+        // a wide table whose rows turn out short: whole rows by warps after all (kRowTilesFound)
+        const int rows = p.B * p.rows_per_seq;
+        by_row = longest * TT <= kWholeTokens && rows >= (int)gridDim.x &&
+                 rows_fit(longest, rows, gridDim.x, kRowTilesFound, DP == 256 ? 2 : 1);
         s_pre[tid + 1] = before + inc;
         if (tid == 0) s_pre[0] = 0;
         __syncthreads();
-        const long long total = (long long)s_pre[kAttWarps * 32] * p.rows_per_seq;
-        const long long want = (total + kAttWarps - 1) / kAttWarps;
-        const int n = (int)(want < (int)gridDim.x ? want : gridDim.x);
-        if (run >= n) {
+        if (by_row) {
             if (tid == 0) p.cont[run] = -1;
-            return;
+            if (!whole_rows()) return;
+        } else {
+            const long long total = (long long)s_pre[kAttWarps * 32] * p.rows_per_seq;
+            const long long want = (total + kAttWarps - 1) / kAttWarps;
+            const int n = (int)(want < (int)gridDim.x ? want : gridDim.x);
+            if (run >= n) {
+                if (tid == 0) p.cont[run] = -1;
+                return;
+            }
+            // run r starts at total * r / n: longer runs spread evenly, not first (2 us on 16 rows of 8000)
+            const long long each = quotient(total, n);
+            const int more = (int)(total - each * n), from = more * run / n;  // n <= runs: small products
+            const long long u0 = each * run + from;
+            rem = (int)each + more * (run + 1) / n - from;
+            // the slice, then the sequence, that holds u0
+            int sl = 0;
+            for (int base = 0; base < kAttWarps * 32; base += 32) {
+                const bool past = (long long)s_pre[base + lane + 1] * p.rows_per_seq <= u0;
+                sl += __popc(__ballot_sync(kAllLanes, past));
+            }
+            long long u = u0 - (long long)s_pre[sl] * p.rows_per_seq;
+            it.b = sl * slice;
+            while (true) {
+                it.seq(p);
+                const long long here = (long long)it.ntiles * p.rows_per_seq;
+                if (u < here) break;
+                u -= here;
+                ++it.b;
+            }
+            it.h = (int)quotient(u, it.ntiles);
+            it.tile = (int)(u - (long long)it.h * it.ntiles);
+            if (tid == 0) p.cont[run] = it.tile ? it.b * p.rows_per_seq + it.h : -1;
         }
-        // run r starts at total * r / n: longer runs spread evenly, not first (2 us on 16 rows of 8000)
-        const long long each = quotient(total, n);
-        const int more = (int)(total - each * n), from = more * run / n;  // n <= runs: small products
-        const long long u0 = each * run + from;
-        rem = (int)each + more * (run + 1) / n - from;
-        // the slice, then the sequence, that holds u0
-        int sl = 0;
-        for (int base = 0; base < kAttWarps * 32; base += 32) {
-            const bool past = (long long)s_pre[base + lane + 1] * p.rows_per_seq <= u0;
-            sl += __popc(__ballot_sync(kAllLanes, past));
-        }
-        long long u = u0 - (long long)s_pre[sl] * p.rows_per_seq;
-        it.b = sl * slice;
-        while (true) {
-            it.seq(p);
-            const long long here = (long long)it.ntiles * p.rows_per_seq;
-            if (u < here) break;
-            u -= here;
-            ++it.b;
-        }
-        it.h = (int)quotient(u, it.ntiles);
-        it.tile = (int)(u - (long long)it.h * it.ntiles);
-        if (tid == 0) p.cont[run] = it.tile ? it.b * p.rows_per_seq + it.h : -1;
     }
     TileIt<TT> row = it;  // of the products: the tile that the current segment (a row's tiles in the run) begins with
-    constexpr int step = ROWS ? 1 : kAttWarps;
-    int to_issue = ROWS ? rem : rem > warp ? (rem - warp + kAttWarps - 1) / kAttWarps : 0;  // tiles of this warp
-    if (!ROWS && to_issue > 0) it.advance(p, warp);
+    const int step = by_row ? 1 : kAttWarps;
+    int to_issue = by_row ? rem : rem > warp ? (rem - warp + kAttWarps - 1) / kAttWarps : 0;  // tiles of this warp
+    if (!by_row && to_issue > 0) it.advance(p, warp);
 
     // --- the ring ---
     uint8_t* ring = smem + warp * C::WARP;
@@ -509,12 +556,12 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
             const bool done = MODE != kRuns || (starts && ends);
             float* part = done ? nullptr : p.partial + ((long long)run * 2 + (starts ? 1 : 0)) * (kAttRows * (p.D + 2));
             // the runs that a row begins and ends in, for the join (first -1: one run has all of it)
-            if (MODE == kRuns && p.by_row_join && tid == 0) {
+            if (MODE == kRuns && p.by_row_join && (by_row ? lane : tid) == 0) {
                 const int at = b * p.rows_per_seq + h;
                 if (starts) p.first[at] = ends ? -1 : run;
                 if (ends && !starts) p.last[at] = run;
             }
-            if constexpr (ROWS) {
+            if (by_row) {
                 float w0 = g < heads ? final_weight(p, head0 + g, m0, l0) : 0.f;
                 float w1 = g + 8 < heads ? final_weight(p, head0 + g + 8, m1, l1) : 0.f;
                 if constexpr (KV == kKvE4m3) {
@@ -655,7 +702,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
             }
         }
         // a warp's tiles of the segment: places of the run that are its own modulo the warps
-        for (int j = ROWS ? 0 : (warp - pos) & (kAttWarps - 1); j < nseg; j += step) {
+        for (int j = by_row ? 0 : (warp - pos) & (kAttWarps - 1); j < nseg; j += step) {
             cp_async_wait<S - 2>();
             __syncwarp();
             issue_next(fill);
@@ -939,24 +986,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendPara
 
 namespace {
 
-// Rows of at most kWholeTokens are not cut where that costs little.  A CTA takes a
-// row, all rows resident at once: up to one wave of the wide kernel if the tiles
-// that its idle CTAs miss are few (kTeamTiles each on average), up to one of the
-// light kernel (between the two, us of the light team / warps with rows / cut: 320 rows
-// of 128 tokens 6.3 / 7.0 / 11.2, 600 of 512 15.9 / 19.8 / 23.3, of 1000 27.9 / 35.7 / 34.6;
-// below, the wide team wins: 256 rows of 300 7.1 / 7.7).  Else a warp takes rows, if the
-// tiles that the busiest has beyond the average are fewer than what the alternative
-// costs: borders, joins and the second launch (kRowTiles) and a meeting of the
-// CTA's warps at every row's end (kEndTiles), both twice as many where a warp's
-// tile counts half (light) or a CTA has the SM for itself (more than 128 dims).
-// us whole / cut, bf16, D = 64: 1024 rows of 128 tokens 8.1 / 19.2, of 1000 45.5 / 52.2; 2600
-// of 256 38.5 / 46.8, of 512 69.6 / 68.1, of 1000 130 / 111; light: 1296 of 128 11.1 / 20.6, of
-// 1000 60.9 / 62.8; D = 128, e4m3: 320 of 256 15.9 / 19.3, of 512 27.2 / 22.5, 4096 of 512 116 / 158;
-// D = 256: 320 of 512 42.9 / 56.9, 1300 of 1000 277 / 251.
-constexpr int kWholeTokens = 1024;
-constexpr int kTeamTiles = 24;
-constexpr int kRowTiles = 9, kEndTiles = 3;
-
 int dp_of(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : 256; }
 
 template <int DP, int KV, bool QF16, int MODE, bool LIGHT>
@@ -1019,8 +1048,7 @@ void attend_plan(int B, int Hq, int Hkv, int D, bool e4m3, int most, int sms, At
             // wave against two), 1024 rows 10.0, 8.1 (one against one)
             const bool light = light_ctas > ctas && 2 * waves(light_ctas) <= waves(ctas);
             const int n = light ? light_ctas : ctas;
-            const long long warps = (long long)n * kAttWarps, few = kRowTiles * warps + kEndTiles * rows;
-            if (tiles(light) * (waves(n) * warps - rows) <= (light || dp == 256 ? 2 : 1) * few) {
+            if (rows_fit(tiles(light), rows, n, kRowTiles, light || dp == 256 ? 2 : 1)) {
                 w->mode = kRows;
                 w->light = light;
                 w->ctas = n;

@@ -255,6 +255,7 @@ def test_many_short_rows(B, D, dtype, cache):
     c = Case([n + 60 for n in lens], 16, 8, D, dtype=dtype, cache=cache, seed=B)
     c.both(window=33, sinks=True)
     c.both()
+    Case(lens, 16, 8, D, dtype=dtype, cache=cache, seed=B, wide=100).both(sinks=True)  # short only by the lengths
 
 
 @gpu
