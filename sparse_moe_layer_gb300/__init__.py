@@ -554,12 +554,13 @@ def forward_gated(x, logits, w13, s13, b13, w2, s2, b2, top_k: int, score: str =
     if x.shape[0] != T:
         raise ValueError("x and logits must have the same number of tokens")
     _check_weights(fmt, w13, s13, w2, s2, E, H, I)
-    if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    with torch.cuda.stream(stream):  # what is allocated and dropped here stays in that stream's order
+        if out is None:
+            out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        if workspace is None and T:
+            workspace = new_workspace(T, H, I, E, top_k, x.device, mx)
     if T == 0:
         return out
-    if workspace is None:
-        workspace = new_workspace(T, H, I, E, top_k, x.device, mx)
     sdt = torch.uint8 if mx else torch.float32
     _check(lib().moe_forward_gated(ctypes.byref(g), logits.data_ptr(), dt, logits.stride(0) if T > 1 else E,
                                    _dev(x, torch.bfloat16, "x"), _FORMATS[fmt], _dev(w13, torch.uint8, "w13"),

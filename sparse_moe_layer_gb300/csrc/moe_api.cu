@@ -781,7 +781,8 @@ extern "C" moe_status moe_route_experts(const moe_gate* gate, const void* logits
     GateParams p = gate_params(in, T, E, top_k);
     p.r.topk_idx = topk_idx;
     p.r.topk_w = topk_w;
-    return launch_gate(p, logits_dtype, num_sms(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    const cudaError_t e = launch_gate(p, logits_dtype, num_sms(), static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 extern "C" moe_status moe_forward_gated(const moe_gate* gate, const void* logits, int logits_dtype, int64_t ld,
@@ -855,7 +856,8 @@ extern "C" moe_status moe_rotate_append(const moe_kv_cache* cache, const void* q
     if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 16 || (rot_dim && !inv_freq)) return MOE_ERR_INVALID_ARG;
     if (dtype != MOE_BF16 && dtype != MOE_FP16) return MOE_ERR_UNSUPPORTED;
     if (cache->dtype != MOE_E4M3 && cache->dtype != dtype) return MOE_ERR_UNSUPPORTED;
-    const moe_status ss[] = {check_strides(N, q_heads, &q_token, &q_head), check_strides(N, cache->kv_heads, &k_token, &k_head),
+    const moe_status ss[] = {check_strides(N, q_heads, &q_token, &q_head),
+                             check_strides(N, cache->kv_heads, &k_token, &k_head),
                              check_strides(N, cache->kv_heads, &v_token, &v_head),
                              check_strides(N, q_heads, &out_token, &out_head)};
     for (moe_status e : ss)

@@ -115,7 +115,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) rotate_append_kernel(Append
     float2 cs[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float4 v = turns ? *reinterpret_cast<const float4*>(&s_cs[warp][8 * unit + 2 * i]) : make_float4(1.f, 0.f, 1.f, 0.f);
+        float4 v = make_float4(1.f, 0.f, 1.f, 0.f);
+        if (turns) v = *reinterpret_cast<const float4*>(&s_cs[warp][8 * unit + 2 * i]);
         cs[2 * i] = make_float2(v.x, v.y);
         cs[2 * i + 1] = make_float2(v.z, v.w);
     }

@@ -71,7 +71,8 @@ __device__ __forceinline__ float logit_at(const void* row, int e) {
 template <int VPL, int DT>
 struct RawRow {
     static constexpr int BYTES = VPL * (DT == kDtFp32 ? 4 : 2);
-    static constexpr uint32_t kAbsent = DT == kDtFp32 ? 0xff800000u : DT == kDtFp16 ? 0xfc00fc00u : 0xff80ff80u;  // -inf
+    // -inf
+    static constexpr uint32_t kAbsent = DT == kDtFp32 ? 0xff800000u : DT == kDtFp16 ? 0xfc00fc00u : 0xff80ff80u;
     uint32_t w[(BYTES + 3) / 4];
     __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -109,7 +110,8 @@ __device__ __forceinline__ void load_row(const GateParams& p, const uint8_t* row
             if (DT == kDtFp32) {
                 v.w[j] = e0 + j < p.E ? reinterpret_cast<const uint32_t*>(row)[e0 + j] : RawRow<VPL, DT>::kAbsent;
             } else {
-                const uint32_t h = e0 + j < p.E ? reinterpret_cast<const uint16_t*>(row)[e0 + j] : RawRow<VPL, DT>::kAbsent & 0xffffu;
+                const uint32_t h = e0 + j < p.E ? reinterpret_cast<const uint16_t*>(row)[e0 + j]
+                                                : RawRow<VPL, DT>::kAbsent & 0xffffu;
                 v.w[j / 2] = j & 1 ? v.w[j / 2] | (h << 16) : h;
             }
         }
