@@ -3,8 +3,10 @@
 Thin Python binding of the C ABI in ``include/moe_gb300.h`` (library
 ``libmoe_gb300.so``, built in-tree for sm_103a).  Every step of the layer runs
 in the library's CUDA kernels; this module only checks tensors and passes
-pointers, sizes and the current CUDA stream.  There is no CPU fallback: if the
-library is missing, importing the binding's functions raises.
+pointers, sizes and the current CUDA stream.  The operators beside the layer
+(route_experts, rotate_append, paged_attention) do that in a compiled module,
+``_binding.so``.  There is no CPU fallback: if the library is missing, importing
+the binding's functions raises.
 """
 from __future__ import annotations
 

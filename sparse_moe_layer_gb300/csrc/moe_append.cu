@@ -18,6 +18,13 @@
 // warp computes its token's angles once, keeps them in registers and streams
 // rows with kAppendBatch groups of them in flight and no barrier; small batches
 // split a token's rows over more warps.
+//
+// 8192 tokens of 72 heads of 128 into an e4m3 cache: 54.4 us, 5.4 TB/s (80 % of a copy);
+// 256 tokens of 80 heads of 64, 16-bit cache: 3.1 us, 1 token 2.1. A CTA per token with
+// its angles in shared memory took 83 us (a barrier, one round of rows in flight); 2 or
+// 3 groups in flight 60 and 56; more CTAs an SM have fewer registers (58 to 84).
+// Equal runs of batches over the borders of tokens gain where tokens just pass a wave
+// of warps (2600 tokens 21.2 -> 18.5) and lose below one (1200 tokens 8.3 -> 9.3).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -22,6 +22,14 @@
 // a run's border leaves fp32 parts, which a second, dependent launch joins in a
 // fixed order (results do not depend on scheduling).  Short rows are not cut: a
 // CTA or a warp takes whole ones (attend_plan).
+//
+// 64 sequences of 1 to 16384 tokens, 8 key heads of 64, bf16: 164 us, 6.3 TB/s (92 % of a
+// copy). 4 sequences of 100000 to 131072 tokens, 4 key heads of 128, e4m3: 90 us, 5.5 TB/s;
+// 6.8 TB/s while it streams, and 15 us of launch, first tiles, row ends and the join.
+// 256 sequences, window 128, 8 key heads of 64, bf16: 16 us, 4.5 TB/s: latency of the 8
+// tiles that a warp has. One sequence of 90 tokens: 3.5 us, latency.
+// A run per warp instead of per CTA lost 4 % on 128 rows and more; 16-token tiles on
+// e4m3 took 149 us, 12 warps an SM with two stages 132 where this shape took 123.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -887,7 +895,9 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
 // Parts: slot 1 of the first run, slot 0 of the runs that continue the row.  A job's
 // head is the work of join_warps warps: a lane has 4 dims (two times 4 past 128)
 // of every n-th part, and the lanes' running sums meet by shuffles, then in
-// shared memory, always in the same order.
+// shared memory, always in the same order.  Bound by latency: the parts of 304 runs
+// are 1 to 2.5 MB in L2, and the join takes 2 to 3 us behind the first kernel (6.8
+// to 8.5 with cold caches).
 constexpr int kJoinWarps = 8;  // per CTA
 
 struct Sums {
