@@ -348,6 +348,9 @@ typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2, MOE_E4M3 = 3 } moe_dtyp
  * of the formula in 64 bits.  The chosen are stored in ascending expert order.
  * A NaN logit counts as -inf, +inf as the largest finite value; scores of a
  * softmax row that is -inf throughout are 0.
+ * A bias, and a group's sum, count as at most 2^126 and at least -2^126 (NaN as
+ * the least): a bias of -inf leaves an expert out while others are left in the
+ * open groups, +inf opens its group and takes it.
  * Limits: those of the layer for E and top_k; groups <= 32 divides E,
  * group_top <= E / groups, top_groups * E / groups >= top_k.
  */

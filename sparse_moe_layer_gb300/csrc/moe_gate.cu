@@ -161,13 +161,25 @@ __device__ __forceinline__ void choices(const GateParams& p, const float (&x)[VP
         for (int j = 0; j < VPL; ++j) c[j] = rcp_approx(1.0f + __expf(-x[j])) + bias[j];
     }
 }
+// A bias, and the sum of a group, count as at most kMostBias either way (NaN as the
+// least): sums and differences of choices stay finite, all masked experts (-inf) tie,
+// and so do the groups that have one among their best.
+constexpr float kMostBias = 0x1p126f;
+__device__ __forceinline__ float bounded(float b) { return fminf(fmaxf(b, -kMostBias), kMostBias); }
+__device__ __forceinline__ float pair_sum(float a, float b) { return a >= kMostBias ? kMostBias : bounded(a + b); }
+__device__ __forceinline__ double pair_sum(double a, double b) {
+    const double most = kMostBias;
+    return a >= most ? most : fmin(fmax(a + b, -most), most);
+}
 template <int VPL>
 __device__ __forceinline__ void load_bias(const GateParams& p, int e0, float (&bias)[VPL]) {
 #pragma unroll
     for (int j = 0; j < VPL; ++j)  // -inf past E: so are the choices
-        bias[j] = e0 + j >= p.E ? -INFINITY : p.bias ? __ldg(p.bias + e0 + j) : 0.f;
+        bias[j] = e0 + j >= p.E ? -INFINITY : p.bias ? bounded(__ldg(p.bias + e0 + j)) : 0.f;
 }
 // Bound of the error of an fp32 choice of size |c|; rz: the largest softmax score.
+// c less its bound grows with c, and so does c with it added: a choice that is clear
+// of the border by the border's bound is clear by its own.
 __device__ __forceinline__ float choice_error(const GateParams& p, float rz, float c) {
     return (p.score == 0 ? 0x1p-19f * rz : 0x1p-21f) + 0x1p-23f * fabsf(c);
 }
@@ -197,7 +209,7 @@ __device__ __forceinline__ int choices_64(const GateParams& p, const uint8_t* ro
     for (int i = lane; i < n; i += 32) {
         const int e = list[i];
         const double s = score_64(logit_at<DT>(row, e), m, z64, p.score);
-        value[i] = p.bias ? s + (double)p.bias[e] : s;
+        value[i] = p.bias ? s + (double)bounded(p.bias[e]) : s;
     }
     __syncwarp();
     return n;
@@ -211,7 +223,7 @@ __device__ __forceinline__ int choices_64(const GateParams& p, const uint8_t* ro
 template <int VPL, int DT>
 __device__ __noinline__ int choose_close(const GateParams& p, const uint8_t* row, int lane, float m, float rz,
                                          uint32_t live, bool settle_groups, int* scratch) {
-    // the warp's VPL * 36 words: 64-bit values, then the list of their experts
+    // the warp's kScratch words: 64-bit values, then (kListAt) the list of their experts
     double* value = reinterpret_cast<double*>(scratch);
     int* list = scratch + kListAt<VPL>;
     float x[VPL], c[VPL];
@@ -239,7 +251,7 @@ __device__ __noinline__ int choose_close(const GateParams& p, const uint8_t* row
     }
     const int gs = p.gsize;
     if (settle_groups) {
-        float mine = -INFINITY, second = -INFINITY, mag = 0.f;  // of group `lane`
+        float mine = -INFINITY, second = -INFINITY, err = 0.f;  // of group `lane`
         for (int g = 0; g < p.groups; ++g) {
             float a = -INFINITY, b = -INFINITY;
 #pragma unroll
@@ -251,9 +263,9 @@ __device__ __noinline__ int choose_close(const GateParams& p, const uint8_t* row
             }
             top2_lanes(a, b, 32);
             if (lane == g) {
-                mine = p.group_top == 2 ? a + b : a;
+                mine = p.group_top == 2 ? pair_sum(a, b) : a;
                 second = p.group_top == 2 ? b : a;
-                mag = fabsf(a) + (p.group_top == 2 ? fabsf(b) : 0.f);
+                err = 2.f * choice_error(p, rz, fabsf(a) + (p.group_top == 2 ? fabsf(b) : 0.f));
             }
         }
         int rank = 0;
@@ -262,19 +274,20 @@ __device__ __noinline__ int choose_close(const GateParams& p, const uint8_t* row
             rank += v > mine || (v == mine && g < lane);
         }
         uint32_t open = __ballot_sync(kFull, lane < p.groups && rank < p.top_groups);
-        if (scored) {
-            const int at = __ffs(__ballot_sync(kFull, lane < p.groups && rank == p.top_groups - 1)) - 1;
-            const float last = __shfl_sync(kFull, mine, at);
-            float err = lane < p.groups ? 2.f * choice_error(p, rz, mag) : 0.f;
-            for (int o = 16; o > 0; o >>= 1) err = fmaxf(err, __shfl_xor_sync(kFull, err, o));
-            const float above = mine - last;  // one difference for both tests: no value falls between them
-            const uint32_t sure = __ballot_sync(kFull, lane < p.groups && above > 2.f * err);
-            const uint32_t near = __ballot_sync(kFull, lane < p.groups && fabsf(above) <= 2.f * err);
+        if (scored && p.top_groups < p.groups) {
+            // near: groups that their errors may bring past one on the other side of the border
+            const bool in = (open >> lane) & 1u, out = lane < p.groups && !in;
+            const float lowest = -warp_max(in ? err - mine : -INFINITY);
+            const float highest = warp_max(out ? mine + err : -INFINITY);
+            const bool clear = in && mine - err > highest;
+            const uint32_t sure = __ballot_sync(kFull, clear);
+            const uint32_t near = __ballot_sync(kFull, (in && !clear) || (out && mine + err >= lowest));
+            const float from = second - 2.f * err;
             uint32_t want = 0;  // members of near groups that may be among their largest
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
                 const int g = e0 + j < p.E ? (e0 + j) / gs : 0;
-                const float least = __shfl_sync(kFull, second, g) - 2.f * err;
+                const float least = __shfl_sync(kFull, from, g);
                 if (e0 + j < p.E && ((near >> g) & 1u) && c[j] >= least) want |= 1u << j;
             }
             const int n = choices_64<VPL, DT>(p, row, lane, want, m, z64, list, value);
@@ -286,7 +299,7 @@ __device__ __noinline__ int choose_close(const GateParams& p, const uint8_t* row
                     a = fmax(a, value[i]);
                 }
             __syncwarp();
-            const double exact = p.group_top == 2 ? a + b : a;
+            const double exact = p.group_top == 2 ? pair_sum(a, b) : a;
             int before = __popc(sure);
             for (uint32_t left = near; left; left &= left - 1) {
                 const int g = __ffs(left) - 1;
@@ -465,7 +478,7 @@ __global__ void __launch_bounds__(kGateWarps * 32, kGateCtas) gate_kernel(GatePa
             }
             top2_lanes(a, b, P);
             const int g = lane / P;
-            const float score = p.group_top == 2 ? a + b : a;  // -inf past the groups
+            const float score = p.group_top == 2 ? pair_sum(a, b) : a;
             uint32_t gkey = 0;
             float top = 0.f;
             if (DT == kDtFp32 || scored) {
@@ -476,10 +489,13 @@ __global__ void __launch_bounds__(kGateWarps * 32, kGateCtas) gate_kernel(GatePa
             }
             uint32_t w = kFull;
             for (int r = 0; r < p.top_groups; ++r) w = warp_max(gkey < w ? gkey : 0u);
-            const uint32_t next = warp_max(gkey < w ? gkey : 0u);
-            if ((DT == kDtFp32 || scored) && next != 0u) {
-                const float mag = g < p.groups ? fabsf(a) + (p.group_top == 2 ? fabsf(b) : 0.f) : 0.f;
-                close = grid_close(w, next, kReachGroup, scored ? 2.f * choice_error(p, rz, warp_max(mag)) : 0.f);
+            if ((DT == kDtFp32 || scored) && p.top_groups < p.groups) {
+                // close: the errors may bring a group left out past one taken (or equal steps hide their order)
+                const float err =
+                    scored ? 2.f * choice_error(p, rz, fabsf(a) + (p.group_top == 2 ? fabsf(b) : 0.f)) : 0.f;
+                const float lowest = -warp_max(g < p.groups && gkey >= w ? err - score : -INFINITY);
+                const float highest = warp_max(g < p.groups && gkey < w ? score + err : -INFINITY);
+                close = lowest <= highest;
             }
             if (p.aligned) {
                 open = gkey >= w;
