@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
                     s[t][3] *= kk.y;
                     vr[t][0] = vv.x;
                     vr[t][1] = vv.y;
-                    vmax = fmaxf(vmax, fmaxf(vv.x, vv.y));
+                    vmax = fmaxf(vmax, fmaxf(fabsf(vv.x), fabsf(vv.y)));
                 }
             }
             const uint32_t valid = *reinterpret_cast<const uint32_t*>(stage + 2 * C::TILE + C::SC);
