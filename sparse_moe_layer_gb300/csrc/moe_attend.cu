@@ -43,8 +43,17 @@ namespace {
 constexpr uint32_t kAllLanes = 0xffffffffu;
 constexpr int kAttWarps = 4;  // warps per CTA
 constexpr int kAttRows = 16;  // query heads per row (m16 of the products)
-constexpr float kSlack = 8.f;
 enum : int { kKvBf16 = 0, kKvFp16 = 1, kKvE4m3 = 2 };
+
+// Powers of two that a score may stand above the maximum that its row's sums are about.
+template <int KV>
+constexpr float kSlack = KV == kKvE4m3 ? 4.f : 8.f;
+// e4m3: a weight is probability times value scale, and the row's accumulators are about a
+// power of two of their own, so that the largest weight is at least 2^kNewWeight (kMostLift:
+// powers of two of that about the scores' maximum at most, where all weights are tiny).
+// While the tile's scales times 2^(maximum - that power) are at most 2^kMostScale, weights are
+// at most 2^15 (probabilities 2^kSlack) and fit fp16; else the weights are looked at.
+constexpr float kNewWeight = 5.f, kMostScale = 11.f, kMostLift = 104.f;
 
 // How the rows are given out: equal runs of tiles, one per CTA; a row per CTA; rows
 // per warp.  attend_plan chooses.
@@ -492,7 +501,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
     float ls[4] = {0.f, 0.f, 0.f, 0.f};                        // 16-bit caches: the sums, [0] and [2]
     // positive factors of the scores: |scale| log2 e, times the query row's power of two (e4m3)
     float qf0 = p.scale_log2, qf1 = p.scale_log2;
-    float vref = 0x1p-100f, ivref = 0x1p100f;                  // e4m3: the accumulator's value scale, and over it
+    float b0 = 0.f, b1 = 0.f;  // powers of two that sums and accumulators are about
+    float vlim = 0.f;          // e4m3: the largest value scale that weights of any row have room for
     uint32_t qr[DP <= 128 ? KS : 1][4];
     uint32_t* qs = reinterpret_cast<uint32_t*>(ring + S * C::STAGE);
     auto qfrag = [&](int k, uint32_t (&a)[4]) {
@@ -561,6 +571,11 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
             }
             m0 *= qf0;  // from here on in powers of two
             m1 *= qf1;
+            // e4m3: sums and accumulators about the maximum
+            const float f0 = KV != kKvE4m3 ? 1.f : m0 == -INFINITY ? 0.f : ex2_approx(b0 - m0);
+            const float f1 = KV != kKvE4m3 ? 1.f : m1 == -INFINITY ? 0.f : ex2_approx(b1 - m1);
+            l0 *= f0;
+            l1 *= f1;
             const bool done = MODE != kRuns || (starts && ends);
             float* part = done ? nullptr : p.partial + ((long long)run * 2 + (starts ? 1 : 0)) * (kAttRows * (p.D + 2));
             // the runs that a row begins and ends in, for the join (first -1: one run has all of it)
@@ -573,8 +588,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
                 float w0 = g < heads ? final_weight(p, head0 + g, m0, l0) : 0.f;
                 float w1 = g + 8 < heads ? final_weight(p, head0 + g + 8, m1, l1) : 0.f;
                 if constexpr (KV == kKvE4m3) {
-                    w0 *= vref;
-                    w1 *= vref;
+                    w0 *= f0;
+                    w1 *= f1;
                 }
 #pragma unroll
                 for (int d = 0; d < KS; ++d) {
@@ -600,14 +615,13 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
                 }
                 {
                     float* mine = reinterpret_cast<float*>(ring + fill * C::STAGE);
-                    const float f = KV == kKvE4m3 ? vref : 1.f;
 #pragma unroll
                     for (int d = 0; d < KS; ++d) {
                         if (d * 16 >= p.D) continue;
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             if (g + 8 * half >= heads) continue;
-                            const Quad q = quad<KV>(o[2 * d], o[2 * d + 1], half, f);
+                            const Quad q = quad<KV>(o[2 * d], o[2 * d + 1], half, half ? f1 : f0);
                             float* dst = mine + (g + 8 * half) * DP;
                             const int d0 = d * 16 + quad_at<KV>(c), d1 = d0 + (KV == kKvE4m3 ? 2 : 8);
                             *reinterpret_cast<float2*>(dst + (d0 ^ (g << 2))) = make_float2(q.a, q.b);
@@ -664,8 +678,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
         const int nseg = min(row.ntiles - row.tile, rem);
         m0 = m1 = -INFINITY;
         l0 = l1 = ls[0] = ls[2] = 0.f;
-        vref = 0x1p-100f;
-        ivref = 0x1p100f;
+        b0 = b1 = vlim = 0.f;
 #pragma unroll
         for (int d = 0; d < DP / 8; ++d)
 #pragma unroll
@@ -753,7 +766,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
                 }
             }
             // --- key scales, mask, running maximum (of scores before the positive factors qf) ---
-            float vr[NT][2];  // e4m3: value scale of the lane's tokens over the accumulator's
+            float vr[NT][2];  // e4m3: value scales of the lane's tokens
             float vmax = 0.f;
             if constexpr (KV == kKvE4m3) {
                 const float* sck = reinterpret_cast<const float*>(stage + 2 * C::TILE);
@@ -790,25 +803,58 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
             t1 = fmaxf(t1, __shfl_xor_sync(kAllLanes, t1, 2));
             // The sums stay about an older maximum until a score passes it by kSlack powers of two (one
             // warp-wide rescaling then): probabilities reach 2^kSlack, exact in the same number of bits.
-            bool far = (t0 - m0) * qf0 > kSlack || (t1 - m1) * qf1 > kSlack;  // NaN (both -inf): no
-            if constexpr (KV == kKvE4m3) {
-                vmax = fmaxf(vmax, __shfl_xor_sync(kAllLanes, vmax, 1));
-                vmax = fmaxf(vmax, __shfl_xor_sync(kAllLanes, vmax, 2));
-                far = far || vmax > vref;
-            }
+            bool far = (t0 - m0) * qf0 > kSlack<KV> || (t1 - m1) * qf1 > kSlack<KV>;  // NaN (both -inf): no
+            if constexpr (KV == kKvE4m3) far = far || vmax > vlim;
             if (__any_sync(kAllLanes, far)) {
                 const float n0 = t0 == -INFINITY ? 0.f : t0 * qf0, n1 = t1 == -INFINITY ? 0.f : t1 * qf1;
-                float c0 = ex2_approx(m0 * qf0 - n0), c1 = ex2_approx(m1 * qf1 - n1);
+                float c0, c1;
+                if constexpr (KV == kKvE4m3) {
+                    // The accumulators' powers of two rise with the weights seen, not with the scales: a large
+                    // scale without probability costs the others no bits.  An all-zero head has the scale 1,
+                    // which may be far above theirs: it has no weight.
+                    uint4 any = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+                    for (int i = 0; i < C::CH; ++i) {  // lane = token
+                        const uint4 v = *reinterpret_cast<const uint4*>(stage + C::TILE + swz<C>(lane, i));
+                        any.x |= v.x | v.y;
+                        any.y |= v.z | v.w;
+                    }
+                    const uint32_t some = __ballot_sync(kAllLanes, ((any.x | any.y) & 0x7f7f7f7fu) != 0u);
+                    float top0 = 0.f, top1 = 0.f;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            if (!((some >> (t * 8 + 2 * c + j)) & 1u)) vr[t][j] = 0.f;
+                            top0 = fmaxf(top0, ex2_approx(fmaf(s[t][j], qf0, -n0)) * fabsf(vr[t][j]));
+                            top1 = fmaxf(top1, ex2_approx(fmaf(s[t][2 + j], qf1, -n1)) * fabsf(vr[t][j]));
+                        }
+                    top0 = fmaxf(top0, __shfl_xor_sync(kAllLanes, top0, 1));
+                    top1 = fmaxf(top1, __shfl_xor_sync(kAllLanes, top1, 1));
+                    top0 = fmaxf(top0, __shfl_xor_sync(kAllLanes, top0, 2));
+                    top1 = fmaxf(top1, __shfl_xor_sync(kAllLanes, top1, 2));
+                    const float over0 = fmaxf(log2f(top0) - kNewWeight, -kMostLift);  // of the maximum
+                    const float over1 = fmaxf(log2f(top1) - kNewWeight, -kMostLift);
+                    const float r0 = m0 == -INFINITY ? n0 + over0 : fmaxf(b0, n0 + over0);
+                    const float r1 = m1 == -INFINITY ? n1 + over1 : fmaxf(b1, n1 + over1);
+                    c0 = m0 == -INFINITY ? 0.f : ex2_approx(b0 - r0);
+                    c1 = m1 == -INFINITY ? 0.f : ex2_approx(b1 - r1);
+                    b0 = r0;
+                    b1 = r1;
+                    vlim = fminf(t0 == -INFINITY ? INFINITY : ex2_approx(kMostScale + b0 - n0),
+                                 t1 == -INFINITY ? INFINITY : ex2_approx(kMostScale + b1 - n1));
+#pragma unroll
+                    for (int i = 4; i < 32; i <<= 1) vlim = fminf(vlim, __shfl_xor_sync(kAllLanes, vlim, i));
+                } else {
+                    c0 = ex2_approx(m0 * qf0 - n0);
+                    c1 = ex2_approx(m1 * qf1 - n1);
+                    b0 = n0;
+                    b1 = n1;
+                }
                 l0 *= c0;
                 l1 *= c1;
                 ls[0] *= c0;
                 ls[2] *= c1;
-                if (KV == kKvE4m3 && vmax > vref) {  // the accumulator's scale: room for values 4 times as large
-                    c0 *= vref / (4.f * vmax);
-                    c1 *= vref / (4.f * vmax);
-                    vref = 4.f * vmax;
-                    ivref = 1.0f / vref;
-                }
 #pragma unroll
                 for (int d = 0; d < DP / 8; ++d) {
                     o[d][0] *= c0;
@@ -819,8 +865,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
                 m0 = t0;
                 m1 = t1;
             }
-            const float b0 = m0 == -INFINITY ? 0.f : m0 * qf0, b1 = m1 == -INFINITY ? 0.f : m1 * qf1;
-            // --- probabilities (fp32 sums; rounded to 16 bits for the second product) ---
+            // --- probabilities (e4m3: weights), rounded to 16 bits for the second product ---
             uint32_t pa[KT][4];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
@@ -832,11 +877,10 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
                 if constexpr (KV == kKvE4m3) {
                     l0 += e[0] + e[1];
                     l1 += e[2] + e[3];
-                    const float x = vr[t][0] * ivref, y = vr[t][1] * ivref;
-                    e[0] *= x;
-                    e[1] *= y;
-                    e[2] *= x;
-                    e[3] *= y;
+                    e[0] *= vr[t][0];
+                    e[1] *= vr[t][1];
+                    e[2] *= vr[t][0];
+                    e[3] *= vr[t][1];
                 }
                 pa[t >> 1][(t & 1) * 2] = pack2<F16>(e[0], e[1]);
                 pa[t >> 1][(t & 1) * 2 + 1] = pack2<F16>(e[2], e[3]);
