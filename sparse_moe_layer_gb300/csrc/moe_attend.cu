@@ -48,6 +48,11 @@ enum : int { kKvBf16 = 0, kKvFp16 = 1, kKvE4m3 = 2 };
 // Powers of two that a score may stand above the maximum that its row's sums are about.
 template <int KV>
 constexpr float kSlack = KV == kKvE4m3 ? 4.f : 8.f;
+// And powers of two that a 16-bit cache's sums lie below that maximum: fp16 probabilities
+// start at 2^7, reach 2^15, and keep their 11 bits down to 2^-21 of the largest (without
+// it a flat tail of probabilities below 2^-25 was lost, however long).
+template <int KV>
+constexpr float kLift = KV == kKvFp16 ? 7.f : 0.f;
 // e4m3: a weight is probability times value scale, and the row's accumulators are about a
 // power of two of their own, so that the largest weight is at least 2^kNewWeight (kMostLift:
 // powers of two of that about the scores' maximum at most, where all weights are tiny).
@@ -569,8 +574,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
                 l0 = ls[0];
                 l1 = ls[2];
             }
-            m0 *= qf0;  // from here on in powers of two
-            m1 *= qf1;
+            m0 = m0 * qf0 - kLift<KV>;  // from here on in powers of two, what the sums are about
+            m1 = m1 * qf1 - kLift<KV>;
             // e4m3: sums and accumulators about the maximum
             const float f0 = KV != kKvE4m3 ? 1.f : m0 == -INFINITY ? 0.f : ex2_approx(b0 - m0);
             const float f1 = KV != kKvE4m3 ? 1.f : m1 == -INFINITY ? 0.f : ex2_approx(b1 - m1);
@@ -848,8 +853,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
                 } else {
                     c0 = ex2_approx(m0 * qf0 - n0);
                     c1 = ex2_approx(m1 * qf1 - n1);
-                    b0 = n0;
-                    b1 = n1;
+                    b0 = n0 - kLift<KV>;
+                    b1 = n1 - kLift<KV>;
                 }
                 l0 *= c0;
                 l1 *= c1;
