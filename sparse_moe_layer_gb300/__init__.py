@@ -15,7 +15,7 @@ import os
 
 import torch
 
-from .build import LIB, build
+from .build import LIB, binding_current, build
 
 __all__ = ["MoeError", "build", "lib", "workspace_size", "workspace_layout", "workspace_views", "forward",
            "pack_weights", "pack_weights_into", "w13_shape", "w2_shape", "unblock", "quantize_rows",
@@ -128,6 +128,9 @@ def _entries():
     global _calls
     if _calls is None:
         lib()
+        if not binding_current():
+            raise RuntimeError("_binding.so is not built for this torch and Python: run `python -c 'import "
+                               "__graft_entry__ as g; g.build()'` with g++, Python.h and torch's headers")
         from . import _binding as b
         b.set_error(MoeError)
         _calls = b

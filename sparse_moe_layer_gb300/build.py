@@ -1,10 +1,15 @@
 """Build libmoe_gb300.so in-tree for sm_103a (nvcc, one -gencode, parallel TUs), and
-_binding.so, the Python entries of the decoder-block operators (g++, against torch)."""
+_binding.so, the Python entries of the decoder-block operators (g++, against torch).
+The library needs nvcc only: it is linked first, and where the binding's own needs
+(g++, Python.h, torch with its headers) are missing, it is left out with a warning."""
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
+import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -26,11 +31,43 @@ def _nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + ["binding.cpp"]] + [os.path.join(ROOT, "include", "moe_gb300.h")]
-    return any(os.path.getmtime(d) > t for d in deps)
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "moe_gb300.h")]
+    return not os.path.exists(LIB) or any(os.path.getmtime(d) > os.path.getmtime(LIB) for d in deps)
+
+
+def _binding_missing() -> str:
+    """What the binding cannot be built without and is not here, or ''."""
+    if not shutil.which("g++"):
+        return "g++"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    try:
+        import torch
+    except ImportError:
+        return "torch"
+    if not os.path.exists(os.path.join(os.path.dirname(torch.__file__), "include", "torch", "csrc", "Exceptions.h")):
+        return "torch's headers"
+    return ""
+
+
+def _binding_made_for() -> str:
+    import torch
+    return f"torch {torch.__version__} python {sys.version.split()[0]}"
+
+
+def _stamp() -> str:
+    return os.path.join(BUILD, "binding.for")
+
+
+def binding_current() -> bool:
+    """Whether _binding.so is there and was made for this torch and Python (their C++ interfaces
+    change between versions)."""
+    return os.path.exists(BINDING) and os.path.exists(_stamp()) and open(_stamp()).read() == _binding_made_for()
+
+
+def _binding_stale() -> bool:
+    deps = [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "moe_gb300.h")]
+    return not binding_current() or any(os.path.getmtime(d) > os.path.getmtime(BINDING) for d in deps)
 
 
 GEMM_LAUNCH_REGS = 168  # must match GemmCfg<...>::LAUNCH_REGS (setmaxnreg budget)
@@ -73,10 +110,18 @@ def _link_binding(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
     os.replace(tmp, BINDING)
+    with open(_stamp(), "w") as f:
+        f.write(_binding_made_for())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
+    missing = _binding_missing()
+    library = force or _stale()
+    binding = not missing and (force or _binding_stale())
+    if missing:
+        warnings.warn(f"no {missing}: route_experts, rotate_append and paged_attention get no Python entries (the C "
+                      "library is not affected)", stacklevel=2)
+    if not library and not binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -92,18 +137,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_compile_binding)
-        objs = list(ex.map(compile_one, SOURCES))
-        binding = binding.result()
-    _check_gemm_registers(os.path.join(BUILD, "moe_gemm.cu.log"))
-    tmp = LIB + ".tmp"
-    r = subprocess.run([nvcc, "-shared", "-gencode", "arch=compute_103a,code=sm_103a", "-o", tmp, *objs],
-                       capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
-    os.replace(tmp, LIB)
-    _link_binding(binding)
-    if verbose:
+        binding_obj = ex.submit(_compile_binding) if binding else None
+        if library:
+            objs = list(ex.map(compile_one, SOURCES))
+            _check_gemm_registers(os.path.join(BUILD, "moe_gemm.cu.log"))
+            tmp = LIB + ".tmp"
+            r = subprocess.run([nvcc, "-shared", "-gencode", "arch=compute_103a,code=sm_103a", "-o", tmp, *objs],
+                               capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
+            os.replace(tmp, LIB)
+        if binding:
+            _link_binding(binding_obj.result())
+    if verbose and library:
         for src in SOURCES:
             print(open(os.path.join(BUILD, src + ".log")).read())
     return LIB
