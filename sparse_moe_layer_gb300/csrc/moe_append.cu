@@ -215,8 +215,8 @@ cudaError_t launch_rotate_append(const AppendParams& p_in, bool fp16, bool e4m3,
     // computes the angles again): 256 tokens of 80 rows take 3.4 us with 8 warps an SM, 4.7 with
     // 24; 777 of 28 rows 4.3, 4.8 with 4 and 6.1 with 24
     const int rpg = 32 >> p.lpr_shift, groups = (rows + rpg - 1) / rpg;
-    int parts = (8 * sms + p.N - 1) / p.N;
-    if (parts > groups) parts = groups;
+    const long long even = (8LL * sms + p.N - 1) / p.N;  // (N may be close to 2^31)
+    const int parts = even < groups ? (int)even : groups;
     p.groups_per_part = (groups + parts - 1) / parts;
     p.parts = (groups + p.groups_per_part - 1) / p.groups_per_part;
     const int grid = (int)(((long long)p.N * p.parts + kAppendWarps - 1) / kAppendWarps);
