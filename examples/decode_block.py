@@ -26,9 +26,18 @@ def norm(x):
     return (f * torch.rsqrt(f.square().mean(-1, keepdim=True) + 1e-5)).bfloat16()
 
 
+def next_slots(table, at, page, num_pages):
+    """Cache slots of tokens number `at` [B] of the sequences of a page table [B, pages].  A sequence whose
+    pages are full gets the slot past the last page: rotate_append appends nothing and reports it."""
+    column = (at // page).clamp(max=table.shape[1] - 1)
+    slots = table.gather(1, column[:, None])[:, 0].long() * page + at % page
+    return torch.where(at < table.shape[1] * page, slots, num_pages * page)
+
+
 class DecodeBlock:
     """Weights, the paged cache of `batch` sequences of `context` tokens already in it, and the state of
-    the next step.  `gate`: keyword arguments of the expert choice (route_experts)."""
+    the next step.  There are pages for `room` tokens more (rounded up to whole pages); steps past them set
+    `status`.  `gate`: keyword arguments of the expert choice (route_experts)."""
 
     def __init__(self, batch, context, room, H=2880, I=2880, E=32, top_k=4, q_heads=64, kv_heads=8, head_dim=64,
                  page=16, cache="bf16", window=0, gate=None, seed=0):
@@ -61,7 +70,6 @@ class DecodeBlock:
         order = torch.randperm(batch * pages, generator=g, device="cuda")
         self.table = order.int().view(batch, pages)
         self.lengths = torch.full((batch,), context, dtype=torch.int32, device="cuda")
-        self.room = room
         most = window if 0 < window < pages * page else pages * page
         self.att_ws = moe.attention_workspace(batch, q_heads, kv_heads, head_dim, most, self.k.dtype)
         self.moe_ws = moe.new_workspace(batch, H, I, E, top_k)
@@ -72,7 +80,7 @@ class DecodeBlock:
         B, Hq, Hkv, D = self.B, self.Hq, self.Hkv, self.D
         qkv = torch.addmm(self.b_qkv, norm(x), self.w_qkv).view(B, Hq + 2 * Hkv, D)
         at = self.lengths.long()
-        slots = self.table.gather(1, (at // self.page)[:, None])[:, 0].long() * self.page + at % self.page
+        slots = next_slots(self.table, at, self.page, self.k.shape[0])
         q = moe.rotate_append(qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], at, slots, self.k, self.v, self.inv_freq,
                               k_scale=self.ks, v_scale=self.vs, status=self.status)
         self.lengths += 1
