@@ -253,16 +253,16 @@ __device__ __forceinline__ void add_scaled(float4& a, float f, const float4& b, 
 }
 
 // 1 / (sum with the head's sink), about the larger of the two exponents: what
-// sums taken about m are multiplied by.  0 for a row without tokens.
+// sums taken about m are multiplied by.  0 for a row without tokens; NaN stays NaN.
 __device__ __forceinline__ float final_weight(const AttendParams& p, int head, float m, float l) {
     float w = 1.f;
     if (p.sinks) {
         const float k = __ldg(p.sinks + head) * 1.4426950408889634f;
         const float n = fmaxf(m, k);
         w = n == -INFINITY ? 0.f : ex2_approx(m - n);
-        l = n == -INFINITY ? 0.f : l * w + ex2_approx(k - n);
+        l = n == -INFINITY ? 0.f : l * w + (k == n ? 1.f : ex2_approx(k - n));  // (an infinite sink too)
     }
-    return l > 0.f ? w / l : 0.f;
+    return l == 0.f ? 0.f : w / l;
 }
 
 }  // namespace
