@@ -1036,8 +1036,8 @@ moe_status moe_read_device_status(void* workspace, void* stream) {
     uint32_t word = 0;
     if (cudaMemcpy(&word, workspace, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
     if (cudaMemset(workspace, 0, 4) != cudaSuccess) return MOE_ERR_CUDA;
-    if (word & kErrBadIndex) return MOE_ERR_INDEX;
-    return word ? MOE_ERR_DEVICE_TIMEOUT : MOE_OK;
+    if (word & ~kErrBadIndex) return MOE_ERR_DEVICE_TIMEOUT;  // the graver of two
+    return word ? MOE_ERR_INDEX : MOE_OK;
 }
 
 moe_status moe_test_bounded_wait(uint64_t timeout_ns, int arrivals, uint32_t* result_dev, void* stream) {
