@@ -161,6 +161,12 @@ def _dev(t: torch.Tensor, dtype, name: str):
     return t.data_ptr()
 
 
+def _same_device(like: torch.Tensor, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != like.device:
+            raise ValueError(f"{name} is on another device")
+
+
 def workspace_size(T: int, H: int, I: int, E: int, top_k: int, mx: bool = False) -> int:
     """Workspace bytes of moe_forward (mx=True: moe_forward_mx)."""
     f = lib().moe_workspace_size_mx if mx else lib().moe_workspace_size
@@ -559,21 +565,23 @@ def forward_gated(x, logits, w13, s13, b13, w2, s2, b2, top_k: int, score: str =
     if x.shape[0] != T:
         raise ValueError("x and logits must have the same number of tokens")
     _check_weights(fmt, w13, s13, w2, s2, E, H, I)
-    with torch.cuda.stream(stream):  # what is allocated and dropped here stays in that stream's order
+    _same_device(logits, x=x, bias=bias, w13=w13, s13=s13, b13=b13, w2=w2, s2=s2, b2=b2, out=out, workspace=workspace)
+    # what is allocated and dropped here stays in the stream's order, on the tensors' device
+    with torch.cuda.device(logits.device), torch.cuda.stream(stream):
         if out is None:
             out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-        if workspace is None and T:
+        if T == 0:
+            return out
+        if workspace is None:
             workspace = new_workspace(T, H, I, E, top_k, x.device, mx)
-    if T == 0:
-        return out
-    sdt = torch.uint8 if mx else torch.float32
-    _check(lib().moe_forward_gated(ctypes.byref(g), logits.data_ptr(), dt, logits.stride(0) if T > 1 else E,
-                                   _dev(x, torch.bfloat16, "x"), _FORMATS[fmt], _dev(w13, torch.uint8, "w13"),
-                                   _dev(s13, sdt, "s13"), _dev(b13, torch.bfloat16, "b13"),
-                                   _dev(w2, torch.uint8, "w2"), _dev(s2, sdt, "s2"), _dev(b2, torch.bfloat16, "b2"),
-                                   T, H, I, E, top_k, _dev(out, torch.bfloat16, "out"),
-                                   _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)),
-           "moe_forward_gated")
+        sdt = torch.uint8 if mx else torch.float32
+        _check(lib().moe_forward_gated(ctypes.byref(g), logits.data_ptr(), dt, logits.stride(0) if T > 1 else E,
+                                       _dev(x, torch.bfloat16, "x"), _FORMATS[fmt], _dev(w13, torch.uint8, "w13"),
+                                       _dev(s13, sdt, "s13"), _dev(b13, torch.bfloat16, "b13"),
+                                       _dev(w2, torch.uint8, "w2"), _dev(s2, sdt, "s2"), _dev(b2, torch.bfloat16, "b2"),
+                                       T, H, I, E, top_k, _dev(out, torch.bfloat16, "out"),
+                                       _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)),
+               "moe_forward_gated")
     return out
 
 
