@@ -344,8 +344,13 @@ typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2, MOE_E4M3 = 3 } moe_dtyp
  *   of its group_top (1 or 2) largest c; the top_groups best groups stay open
  *   (groups = 1: all open); the top_k largest c in them are chosen
  *   w_j = s_j, divided by (sum_j s_j + 1e-20) if renormalize, times scale
- * Ties go to the lower index (of the group, of the expert); choices are those
- * of the formula in 64 bits.  The chosen are stored in ascending expert order.
+ * Ties go to the lower index (of the group, of the expert).  Without a bias
+ * experts, and groups by one best, are ordered by their logits (scores rise with
+ * them, also where 64 bits round two to one: sigmoid above 37, softmax 745 below
+ * the largest); with one, and for sums of two, choices are those of the formula in
+ * 64 bits.  The chosen are stored in ascending expert order.  Weights are computed
+ * in fp32: off by at most (32 + 3 d) 2^-24 of themselves, d the logit's distance from
+ * the row's largest (softmax) or from 0 (sigmoid), twice that if renormalised.
  * A NaN logit counts as -inf, +inf as the largest finite value; scores of a
  * softmax row that is -inf throughout are 0.
  * A bias, and a group's sum, count as at most 2^126 and at least -2^126 (NaN as

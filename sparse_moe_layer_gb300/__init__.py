@@ -548,7 +548,8 @@ def route_experts(logits, top_k: int, score: str = "softmax", bias=None, groups:
     weights; with groups > 1 only the top_groups groups with the largest sum of their
     group_top (1 or 2) best choices stay open; renormalize divides the weights by their sum.
     The defaults are the layer's own rule, softmax over the chosen logits.  Ties go to the
-    lower index."""
+    lower index; without a bias experts are ordered by their logits, also where their scores
+    round to one value."""
     return (_calls or _entries()).route_experts(logits, top_k, _SCORES.get(score, -1), bias, groups, top_groups, group_top,
                                                 renormalize, scale, None if stream is None else stream.cuda_stream)
 

@@ -11,11 +11,12 @@
 //   the top_groups best groups stay open; the k largest c in them are chosen
 //   w_j = s_j  [/ (sum_j s_j + 1e-20)]  * scale
 //
-// Ties go to the lower index, and choices are those of the formula in 64 bits:
-// without a bias c orders like the logits, so the logits themselves are
-// compared (exact); with one, fp32 scores are compared, and where a candidate
-// lies within the fp32 error of the border the same warp ranks those few again
-// in 64 bits.
+// Ties go to the lower index.  Without a bias c rises with the logit, so experts
+// (and groups by one best) are ordered by the logits themselves, whole -- also
+// where 64 bits would round two scores to one.  With a bias, and for sums of two,
+// choices are those of the formula in 64 bits: fp32 scores are compared, and where
+// a candidate lies within the fp32 error of the border the same warp ranks those
+// few again in 64 bits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
