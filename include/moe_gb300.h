@@ -443,9 +443,9 @@ moe_status moe_rotate_append(const moe_kv_cache* cache, const void* q, const voi
  * (NULL sinks: no such term), fp32 statistics and sums.  The products are of 16
  * bits: probabilities are rounded to the cache's type (fp16: 2^-31 of the row's
  * largest is the smallest step); over an e4m3 cache, to fp16 after a power of two
- * of its row, queries (2^-24 of the row's largest value is the smallest step) and
- * probabilities times value scales (2^-29 of the row's largest, or 2^-128 where
- * all are smaller still).
+ * of its row, queries (exact down to 2^-30 of the row's largest value) and
+ * probabilities times value scales (2^-29 of the row's largest is the smallest
+ * step, or 2^-128 where all are smaller still).
  * Token t of sequence b is at place t % page_size of page
  * page_table[b * table_ld + t / page_size]; entries past the length are not
  * read, nor are the cache's unused places.  No tokens: out is 0.  A length

@@ -689,8 +689,9 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[d][j] = 0.f;
         if constexpr (KV == kKvE4m3) {
-            // the products run in fp16: each query row is scaled by a power of two to
-            // below 2 (exact but for values 2^-24 below the largest)
+            // the products run in fp16: each query row is scaled by a power of two to below 2^15, fp16's
+            // upper end, so that every fp16 value and bf16 values down to 2^-30 of the largest are exact (its
+            // smallest step is 2^-39 of the largest; sums of 256 products by codes stay below 2^32)
             float a0 = 0.f, a1 = 0.f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
@@ -707,13 +708,13 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
             a0 = fmaxf(a0, __shfl_xor_sync(kAllLanes, a0, 2));
             a1 = fmaxf(a1, __shfl_xor_sync(kAllLanes, a1, 1));
             a1 = fmaxf(a1, __shfl_xor_sync(kAllLanes, a1, 2));
-            // 2^-floor(log2 amax), exponent field kept within [1, 253]
-            const uint32_t e0 = min(max(__float_as_uint(a0) >> 23, 1u), 253u);
-            const uint32_t e1 = min(max(__float_as_uint(a1) >> 23, 1u), 253u);
-            const float f0 = __uint_as_float((254u - e0) << 23), f1 = __uint_as_float((254u - e1) << 23);
+            // 2^(14 - floor(log2 amax)) and its inverse, exponent fields kept within [1, 253]
+            const uint32_t e0 = min(max(__float_as_uint(a0) >> 23, 15u), 253u);
+            const uint32_t e1 = min(max(__float_as_uint(a1) >> 23, 15u), 253u);
+            const float f0 = __uint_as_float((268u - e0) << 23), f1 = __uint_as_float((268u - e1) << 23);
             // not 0, which would make NaN of a masked score
-            qf0 = fmaxf(p.scale_log2 * __uint_as_float(e0 << 23), 0x1p-126f);
-            qf1 = fmaxf(p.scale_log2 * __uint_as_float(e1 << 23), 0x1p-126f);
+            qf0 = fmaxf(p.scale_log2 * __uint_as_float((e0 - 14u) << 23), 0x1p-126f);
+            qf1 = fmaxf(p.scale_log2 * __uint_as_float((e1 - 14u) << 23), 0x1p-126f);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 uint32_t a[4];
