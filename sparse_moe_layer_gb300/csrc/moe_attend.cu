@@ -6,8 +6,8 @@
 //   o = sum_t p_t v_t / (sum_t p_t + 2^(sink log2 e - m)),  p_t = 2^(s_t - m),
 //   s_t = (q . k_t) scale log2 e,  t over the last `window` of `length` tokens
 //
-// Bound by the cache's bytes: each key and value is read once, for all (up to
-// 16) query heads that share it, so the products need G flops a byte (8 to 16,
+// Bound by the cache's bytes: each key and value is read once for (up to 16)
+// query heads that share it, so the products need G flops a byte (8 to 16,
 // above what the fp32 pipes give at full bandwidth, far below the matrix
 // instructions): m16n8k16 with the group's heads as the 16 rows, scores and
 // probabilities staying in registers between the two products.  A 64- or
@@ -30,6 +30,8 @@
 // tiles that a warp has. One sequence of 90 tokens: 3.5 us, latency.
 // A run per warp instead of per CTA lost 4 % on 128 rows and more; 16-token tiles on
 // e4m3 took 149 us, 12 warps an SM with two stages 132 where this shape took 123.
+// More than 16 heads to a key: a row per 16, which reads the cache again (4 x 60000 tokens,
+// 4 key heads of 128, bf16: 64 heads 88 us, 128 heads 166).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -871,7 +873,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
                 m0 = t0;
                 m1 = t1;
             }
-            // --- probabilities (e4m3: weights), rounded to 16 bits for the second product ---
+            // --- probabilities (e4m3: weights), rounded to 16 bits for the second product; e4m3 caches sum
+            // them before (fp32), 16-bit ones after (below) ---
             uint32_t pa[KT][4];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {

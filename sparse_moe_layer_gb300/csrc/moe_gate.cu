@@ -389,8 +389,8 @@ __device__ __forceinline__ bool grid_close(uint32_t w, uint32_t next, float reac
 // only), the next token's logits in flight.
 // 16384 rows of 256 fp32 experts, sigmoid, bias, 4 of 8 groups, top-8: 21 us, 0.8 TB/s:
 // ~800 instructions a row bound it (63 % of issue slots, ALU pipe 50 %); the tail of its
-// 5 close rows is 3 us of that. Softmax without bias or groups: 12.6 us. 256 rows of
-// 128: 2.3 us, of which a launch is most. Rows dealt out beforehand: 26 us (a close row
+// 5 close rows is 3 us of that. Softmax without bias or groups: 11.5 us. 256 rows of
+// 128: 2.4 us, of which a launch is most. Rows dealt out beforehand: 26 us (a close row
 // delays what its warp has left); 4 or 5 CTAs an SM spill: 22.5 and 30 us.
 // p.r.hist != nullptr: the layer's routing step, which also counts the chunk
 // histogram and lets the last CTA scan it.
