@@ -445,7 +445,8 @@ moe_status moe_rotate_append(const moe_kv_cache* cache, const void* q, const voi
  * largest is the smallest step); over an e4m3 cache, to fp16 after a power of two
  * of its row, queries (exact down to 2^-30 of the row's largest value) and
  * probabilities times value scales (2^-29 of the row's largest is the smallest
- * step, or 2^-128 where all are smaller still).
+ * step, or 2^-128 where all are smaller still; a head of zeros with the scale 1, as
+ * moe_rotate_append stores it, does not count there).
  * Token t of sequence b is at place t % page_size of page
  * page_table[b * table_ld + t / page_size]; entries past the length are not
  * read, nor are the cache's unused places.  No tokens: out is 0.  A length

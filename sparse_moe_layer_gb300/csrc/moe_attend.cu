@@ -24,7 +24,7 @@
 // CTA or a warp takes whole ones (attend_plan).
 //
 // 64 sequences of 1 to 16384 tokens, 8 key heads of 64, bf16: 164 us, 6.3 TB/s (92 % of a
-// copy). 4 sequences of 100000 to 131072 tokens, 4 key heads of 128, e4m3: 90 us, 5.5 TB/s;
+// copy). 4 sequences of 100000 to 131072 tokens, 4 key heads of 128, e4m3: 89 us, 5.5 TB/s;
 // 6.8 TB/s while it streams, and 15 us of launch, first tiles, row ends and the join.
 // 256 sequences, window 128, 8 key heads of 64, bf16: 16 us, 4.5 TB/s: latency of the 8
 // tiles that a warp has. One sequence of 90 tokens: 3.5 us, latency.
@@ -47,20 +47,21 @@ constexpr int kAttWarps = 4;  // warps per CTA
 constexpr int kAttRows = 16;  // query heads per row (m16 of the products)
 enum : int { kKvBf16 = 0, kKvFp16 = 1, kKvE4m3 = 2 };
 
-// Powers of two that a score may stand above the maximum that its row's sums are about.
-template <int KV>
-constexpr float kSlack = KV == kKvE4m3 ? 4.f : 8.f;
-// And powers of two that a 16-bit cache's sums lie below that maximum: fp16 probabilities
-// start at 2^7, reach 2^15, and keep their 11 bits down to 2^-21 of the largest (without
-// it a flat tail of probabilities below 2^-25 was lost, however long).
+// 16-bit caches: powers of two that a score may stand above the maximum that its row's sums
+// are about, and that these lie below that maximum: fp16 probabilities start at 2^7, reach
+// 2^15, and keep their 11 bits down to 2^-21 of the largest (without it a flat tail of
+// probabilities below 2^-25 was lost, however long).
+constexpr float kSlack = 8.f;
 template <int KV>
 constexpr float kLift = KV == kKvFp16 ? 7.f : 0.f;
-// e4m3: a weight is probability times value scale, and the row's accumulators are about a
-// power of two of their own, so that the largest weight is at least 2^kNewWeight (kMostLift:
-// powers of two of that about the scores' maximum at most, where all weights are tiny).
-// While the tile's scales times 2^(maximum - that power) are at most 2^kMostScale, weights are
-// at most 2^15 (probabilities 2^kSlack) and fit fp16; else the weights are looked at.
-constexpr float kNewWeight = 5.f, kMostScale = 11.f, kMostLift = 104.f;
+// e4m3: a weight is probability times value scale, and the row's sums and accumulators are
+// about a power of two that makes the largest weight so far at least 2^kNewWeight when it is
+// set (but kMostLift powers of two below the scores' maximum at most, where all weights are
+// tiny). While a tile's largest probability times its largest scale, as they stand to that,
+// is at most 2^kMostWeight the weights fit fp16; else they are looked at and it is set again.
+constexpr float kNewWeight = 5.f, kMostLift = 104.f, kMostWeight = 15.f;
+constexpr float kLeastScale = 0x1p-89f;  // 2^(kMostWeight - kMostLift): the sums' room where scales are smaller
+constexpr float kNoWeights = -0x1p127f;  // the power of two before a row's first
 
 // How the rows are given out: equal runs of tiles, one per CTA; a row per CTA; rows
 // per warp.  attend_plan chooses.
@@ -509,7 +510,6 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
     // positive factors of the scores: |scale| log2 e, times the query row's power of two (e4m3)
     float qf0 = p.scale_log2, qf1 = p.scale_log2;
     float b0 = 0.f, b1 = 0.f;  // powers of two that sums and accumulators are about
-    float vlim = 0.f;          // e4m3: the largest value scale that weights of any row have room for
     uint32_t qr[DP <= 128 ? KS : 1][4];
     uint32_t* qs = reinterpret_cast<uint32_t*>(ring + S * C::STAGE);
     auto qfrag = [&](int k, uint32_t (&a)[4]) {
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
         const int nseg = min(row.ntiles - row.tile, rem);
         m0 = m1 = -INFINITY;
         l0 = l1 = ls[0] = ls[2] = 0.f;
-        b0 = b1 = vlim = 0.f;
+        b0 = b1 = KV == kKvE4m3 ? kNoWeights : 0.f;
 #pragma unroll
         for (int d = 0; d < DP / 8; ++d)
 #pragma unroll
@@ -775,7 +775,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
             }
             // --- key scales, mask, running maximum (of scores before the positive factors qf) ---
             float vr[NT][2];  // e4m3: value scales of the lane's tokens
-            float vmax = 0.f;
+            float vmax = kLeastScale;
             if constexpr (KV == kKvE4m3) {
                 const float* sck = reinterpret_cast<const float*>(stage + 2 * C::TILE);
 #pragma unroll
@@ -791,6 +791,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
                     vmax = fmaxf(vmax, fmaxf(fabsf(vv.x), fabsf(vv.y)));
                 }
             }
+            const float room = kMostWeight - __log2f(vmax);  // for the tile's probabilities
             const uint32_t valid = *reinterpret_cast<const uint32_t*>(stage + 2 * C::TILE + C::SC);
             if (valid != kAllTokens) {
 #pragma unroll
@@ -799,7 +800,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
                     for (int j = 0; j < 4; ++j)
                         if (!((valid >> (t * 8 + 2 * c + (j & 1))) & 1u)) s[t][j] = -INFINITY;
             }
-            float t0 = m0, t1 = m1;
+            float t0 = KV == kKvE4m3 ? -INFINITY : m0, t1 = KV == kKvE4m3 ? -INFINITY : m1;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 t0 = fmaxf(t0, fmaxf(s[t][0], s[t][1]));
@@ -809,56 +810,71 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
             t1 = fmaxf(t1, __shfl_xor_sync(kAllLanes, t1, 1));
             t0 = fmaxf(t0, __shfl_xor_sync(kAllLanes, t0, 2));
             t1 = fmaxf(t1, __shfl_xor_sync(kAllLanes, t1, 2));
-            // The sums stay about an older maximum until a score passes it by kSlack powers of two (one
-            // warp-wide rescaling then): probabilities reach 2^kSlack, exact in the same number of bits.
-            bool far = (t0 - m0) * qf0 > kSlack<KV> || (t1 - m1) * qf1 > kSlack<KV>;  // NaN (both -inf): no
-            if constexpr (KV == kKvE4m3) far = far || vmax > vlim;
-            if (__any_sync(kAllLanes, far)) {
-                const float n0 = t0 == -INFINITY ? 0.f : t0 * qf0, n1 = t1 == -INFINITY ? 0.f : t1 * qf1;
-                float c0, c1;
-                if constexpr (KV == kKvE4m3) {
-                    // The accumulators' powers of two rise with the weights seen, not with the scales: a large
-                    // scale without probability costs the others no bits.  An all-zero head has the scale 1,
-                    // which may be far above theirs: it has no weight.
-                    uint4 any = make_uint4(0, 0, 0, 0);
+            float c0, c1;  // what a rescaling multiplies sums and accumulators by
+            bool rescale;
+            if constexpr (KV == kKvE4m3) {
+                m0 = fmaxf(m0, t0);
+                m1 = fmaxf(m1, t1);
+                rescale = __any_sync(kAllLanes, fmaxf(fmaf(t0, qf0, -b0), fmaf(t1, qf1, -b1)) > room);
+                if (rescale) {
+                    // The power of two rises with the weights seen, not with the scales: a large scale
+                    // without probability costs the others no bits.  A head of zeros, which the append stores
+                    // with a scale of 1 however small the others are, has no weight.
+                    bool one = false;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) one = one || vr[t][0] == 1.f || vr[t][1] == 1.f;
+                    if (__any_sync(kAllLanes, one)) {
+                        uint4 any = make_uint4(0, 0, 0, 0);
 #pragma unroll 4
-                    for (int i = 0; i < C::CH; ++i) {  // lane = token
-                        const uint4 v = *reinterpret_cast<const uint4*>(stage + C::TILE + swz<C>(lane, i));
-                        any.x |= v.x | v.y;
-                        any.y |= v.z | v.w;
+                        for (int i = 0; i < C::CH; ++i) {  // lane = token
+                            const uint4 v = *reinterpret_cast<const uint4*>(stage + C::TILE + swz<C>(lane, i));
+                            any.x |= v.x | v.y;
+                            any.y |= v.z | v.w;
+                        }
+                        const uint32_t some = __ballot_sync(kAllLanes, ((any.x | any.y) & 0x7f7f7f7fu) != 0u);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                if (!((some >> (t * 8 + 2 * c + j)) & 1u)) vr[t][j] = 0.f;
                     }
-                    const uint32_t some = __ballot_sync(kAllLanes, ((any.x | any.y) & 0x7f7f7f7fu) != 0u);
-                    float top0 = 0.f, top1 = 0.f;
+                    float top0 = -INFINITY, top1 = -INFINITY;  // of the weights, in powers of two
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            if (!((some >> (t * 8 + 2 * c + j)) & 1u)) vr[t][j] = 0.f;
-                            top0 = fmaxf(top0, ex2_approx(fmaf(s[t][j], qf0, -n0)) * fabsf(vr[t][j]));
-                            top1 = fmaxf(top1, ex2_approx(fmaf(s[t][2 + j], qf1, -n1)) * fabsf(vr[t][j]));
+                            const float v = __log2f(fabsf(vr[t][j]));
+                            top0 = fmaxf(top0, fmaf(s[t][j], qf0, v));
+                            top1 = fmaxf(top1, fmaf(s[t][2 + j], qf1, v));
                         }
                     top0 = fmaxf(top0, __shfl_xor_sync(kAllLanes, top0, 1));
                     top1 = fmaxf(top1, __shfl_xor_sync(kAllLanes, top1, 1));
                     top0 = fmaxf(top0, __shfl_xor_sync(kAllLanes, top0, 2));
                     top1 = fmaxf(top1, __shfl_xor_sync(kAllLanes, top1, 2));
-                    const float over0 = fmaxf(log2f(top0) - kNewWeight, -kMostLift);  // of the maximum
-                    const float over1 = fmaxf(log2f(top1) - kNewWeight, -kMostLift);
-                    const float r0 = m0 == -INFINITY ? n0 + over0 : fmaxf(b0, n0 + over0);
-                    const float r1 = m1 == -INFINITY ? n1 + over1 : fmaxf(b1, n1 + over1);
-                    c0 = m0 == -INFINITY ? 0.f : ex2_approx(b0 - r0);
-                    c1 = m1 == -INFINITY ? 0.f : ex2_approx(b1 - r1);
+                    // (rows without tokens, m = -inf, stay)
+                    const float r0 = fmaxf(b0, fmaxf(top0 - kNewWeight, m0 * qf0 - kMostLift));
+                    const float r1 = fmaxf(b1, fmaxf(top1 - kNewWeight, m1 * qf1 - kMostLift));
+                    c0 = ex2_approx(b0 - r0);
+                    c1 = ex2_approx(b1 - r1);
                     b0 = r0;
                     b1 = r1;
-                    vlim = fminf(t0 == -INFINITY ? INFINITY : ex2_approx(kMostScale + b0 - n0),
-                                 t1 == -INFINITY ? INFINITY : ex2_approx(kMostScale + b1 - n1));
-#pragma unroll
-                    for (int i = 4; i < 32; i <<= 1) vlim = fminf(vlim, __shfl_xor_sync(kAllLanes, vlim, i));
-                } else {
+                }
+            } else {
+                // The sums stay about an older maximum until a score passes it by kSlack powers of two (one
+                // warp-wide rescaling then): probabilities reach 2^kSlack, exact in the same number of bits.
+                // (NaN, both -inf: no)
+                rescale = __any_sync(kAllLanes, (t0 - m0) * qf0 > kSlack || (t1 - m1) * qf1 > kSlack);
+                if (rescale) {
+                    const float n0 = t0 == -INFINITY ? 0.f : t0 * qf0, n1 = t1 == -INFINITY ? 0.f : t1 * qf1;
                     c0 = ex2_approx(m0 * qf0 - n0);
                     c1 = ex2_approx(m1 * qf1 - n1);
                     b0 = n0 - kLift<KV>;
                     b1 = n1 - kLift<KV>;
+                    m0 = t0;
+                    m1 = t1;
                 }
+            }
+            if (rescale) {
                 l0 *= c0;
                 l1 *= c1;
                 ls[0] *= c0;
@@ -870,8 +886,6 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
                     o[d][2] *= c1;
                     o[d][3] *= c1;
                 }
-                m0 = t0;
-                m1 = t1;
             }
             // --- probabilities (e4m3: weights), rounded to 16 bits for the second product; e4m3 caches sum
             // them before (fp32), 16-bit ones after (below) ---
