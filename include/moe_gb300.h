@@ -434,6 +434,57 @@ moe_status moe_rotate_append(const moe_kv_cache* cache, const void* q, const voi
                              int64_t out_token, int64_t out_head, uint32_t* status, void* stream);
 
 /*
+ * moe_rotate_append with positions of several axes (time, height and width of images
+ * and video): pair i of a token n turns by a_i = positions[axes[i] * axis_stride + n] *
+ * inv_freq[i].  axes int32 [rot_dim / 2]; an axis outside [0, n_axes) counts as 0 and
+ * sets the error word.  Limits: 1 <= n_axes <= 16; N <= axis_stride (n_axes > 1).
+ */
+moe_status moe_rotate_append_axes(const moe_kv_cache* cache, const void* q, const void* k, const void* v, int dtype,
+                                  int64_t q_token, int64_t q_head, int64_t k_token, int64_t k_head, int64_t v_token,
+                                  int64_t v_head, const int64_t* positions, int n_axes, int64_t axis_stride,
+                                  const int32_t* axes, const int64_t* slots, const double* inv_freq, int rot_dim,
+                                  int neighbours, float rope_scale, int N, int q_heads, void* q_out, int64_t out_token,
+                                  int64_t out_head, uint32_t* status, void* stream);
+
+/*
+ * Copies pages of a paged cache: keys, values and scales of the first tokens[i]
+ * places (NULL: all page_size) of page src[i] to page dst[i], in every layer (a
+ * fork's last page; pages moved together).  layer_stride: elements from layer to
+ * layer of k, v and the scales (NULL: one layer, the cache).  A pair with a negative
+ * page is left out; one with a page past the last too, and it sets the error word, as
+ * does a token count outside [0, page_size], which is brought into it.  The pages that
+ * a call writes are distinct and none of them is read by it.
+ *   src, dst, tokens int32 [N]; status: a device error word or NULL
+ * Limits: those of the cache; 1 <= layers <= 65536; layer strides multiples of 16
+ * bytes (scales: 4); N * layers * pieces of 16 KB of a page's keys < 2^30.
+ * Asynchronous on `stream`; no workspace.
+ */
+moe_status moe_copy_pages(const moe_kv_cache* cache, int layers, const int64_t* layer_stride, const int32_t* src,
+                          const int32_t* dst, const int32_t* tokens, int N, uint32_t* status, void* stream);
+
+/*
+ * Closes up the kept drafts of a step in a paged cache.  The last n = starts[b+1] -
+ * starts[b] tokens of sequence b are drafts (as for moe_tree_attention); of these
+ * kept[b, 0], kept[b, 1], ... stay -- strictly ascending, a negative entry ends the
+ * list -- and move, keys, values and scales in every layer, to the first places behind
+ * the context: draft kept[b, j] to token lengths[b] - n + j.  new_lengths[b] = lengths[b]
+ * - n + the number kept; places behind it keep what they hold.  An entry that is no
+ * draft or does not ascend ends the list, a token on a page outside [0, num_pages)
+ * stays where it is, and a sequence with starts that descend, or with more drafts than
+ * tokens or tokens than the table has room for, stays as it is; all three set the error word.
+ *   page_table int32 [B, table_width], rows table_ld apart; lengths int32 [B];
+ *   starts int32 [B + 1]; kept int32 [B, K], rows kept_ld apart; new_lengths int32 [B],
+ *   not lengths itself; layers, layer_stride as for moe_copy_pages
+ * Limits: those of the cache; 1 <= B <= 65536; 1 <= K; table_width * page_size <=
+ * 2^31 - 32; sequences share no page that is moved from or to.
+ * Asynchronous on `stream`; no workspace.
+ */
+moe_status moe_compact_drafts(const moe_kv_cache* cache, int layers, const int64_t* layer_stride,
+                              const int32_t* page_table, int64_t table_ld, int table_width, const int32_t* lengths,
+                              const int32_t* starts, const int32_t* kept, int64_t kept_ld, int B, int K,
+                              int32_t* new_lengths, uint32_t* status, void* stream);
+
+/*
  * Attention of one new token per sequence over a paged cache ("GPT-OSS on Day
  * 0": grouped heads, sink attention, sliding windows).  For sequence b and
  * query head i, key head i / (q_heads / kv_heads), over the tokens t in

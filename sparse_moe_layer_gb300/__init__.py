@@ -24,7 +24,7 @@ __all__ = ["MoeError", "build", "lib", "workspace_size", "workspace_layout", "wo
            "pack_weights_mxfp4", "pack_weights_into_mxfp4", "w13_shape_fp4", "w2_shape_fp4", "unblock_fp4",
            "weight_format", "route_debug", "block_weights", "read_static_scratch_status",
            "route_experts", "forward_gated", "rotate_append", "new_status",
-           "paged_attention", "attention_workspace"]
+           "paged_attention", "attention_workspace", "copy_pages", "compact_drafts"]
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace too small", 4: "CUDA error",
           5: "device wait timed out", 6: "a page, slot or length was out of range"}
@@ -105,11 +105,18 @@ def lib():
         L.moe_rotate_append.argtypes = [vp] * 4 + [i32] + [i64] * 6 + [vp] * 3 + [i32, i32, f32, i32, i32, vp, i64, i64,
                                                                                 vp, vp]
         L.moe_rotate_append.restype = i32
+        L.moe_rotate_append_axes.argtypes = [vp] * 4 + [i32] + [i64] * 6 + [vp, i32, i64] + [vp] * 3 + [i32, i32, f32, i32, i32,
+                                                                                                 vp, i64, i64, vp, vp]
+        L.moe_rotate_append_axes.restype = i32
         L.moe_attention_workspace_size.argtypes = [i32] * 6
         L.moe_attention_workspace_size.restype = sz
         L.moe_paged_attention.argtypes = [vp, vp, i32, i64, i64, vp, i64, i32, vp, i32, i32, f32, vp, i32, vp, i64, i64,
                                           vp, sz, vp, vp]
         L.moe_paged_attention.restype = i32
+        L.moe_copy_pages.argtypes = [vp, i32] + [vp] * 4 + [i32, vp, vp]
+        L.moe_copy_pages.restype = i32
+        L.moe_compact_drafts.argtypes = [vp, i32, vp, vp, i64, i32, vp, vp, vp, i64, i32, i32, vp, vp, vp]
+        L.moe_compact_drafts.restype = i32
         L.moe_read_device_status.argtypes = [vp, vp]
         L.moe_read_device_status.restype = i32
         L.moe_test_bounded_wait.argtypes = [u64, i32, vp, vp]
@@ -592,7 +599,7 @@ def new_status(device=None) -> torch.Tensor:
 
 
 def rotate_append(q, k, v, positions, slots, k_cache, v_cache, inv_freq, k_scale=None, v_scale=None,
-                  interleaved: bool = False, rope_scale: float = 1.0, q_out=None, status=None, stream=None):
+                  interleaved: bool = False, rope_scale: float = 1.0, q_out=None, status=None, stream=None, axes=None):
     """Rotate q [N, Hq, D] and k [N, Hkv, D] by position and append k and v to a paged cache; returns
     the rotated q (a new tensor, or `q_out`, which may be q itself).
 
@@ -601,10 +608,12 @@ def rotate_append(q, k, v, positions, slots, k_cache, v_cache, inv_freq, k_scale
     page, D] of the same type, or uint8 (e4m3 codes) with k_scale, v_scale fp32 [pages, Hkv, page];
     any strides with the last dim contiguous.  inv_freq fp64 [R / 2] rotates the first R dims, in
     pairs (i, i + R/2) or, interleaved, (2i, 2i + 1); cos and sin are multiplied by rope_scale.
-    status (`new_status`): set by a slot past the last page."""
+    With axes int32 [R / 2] positions are [A, N], one row per axis (time, height, width of images and
+    video), and pair i turns by the position of axis axes[i].  status (`new_status`): set by a slot past the
+    last page, or an axis outside [0, A) (it counts as 0)."""
     return (_calls or _entries()).rotate_append(q, k, v, positions, slots, k_cache, v_cache, inv_freq, k_scale, v_scale,
                                                 interleaved, rope_scale, q_out, status,
-                                                None if stream is None else stream.cuda_stream)
+                                                None if stream is None else stream.cuda_stream, axes)
 
 
 def attention_workspace(B: int, q_heads: int, kv_heads: int, head_dim: int, max_tokens: int, dtype=torch.bfloat16,
@@ -629,6 +638,32 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, scale: float, k_sc
     return (_calls or _entries()).paged_attention(q, k_cache, v_cache, page_table, lengths, scale, k_scale, v_scale, sinks,
                                                   window, out, workspace, status,
                                                   None if stream is None else stream.cuda_stream)
+
+
+def copy_pages(k_cache, v_cache, src, dst, tokens=None, k_scale=None, v_scale=None, status=None, stream=None) -> None:
+    """Copy pages of a paged cache, keys, values and scales: the first tokens[i] places (None: all) of page
+    src[i] to page dst[i] -- the last page of a forked sequence, pages moved together.
+
+    Cache as for `rotate_append`, or of several layers at once: [layers, pages, Hkv, page, D], scales [layers,
+    pages, Hkv, page].  src, dst, tokens int32 [N]; a pair with a negative page is left out.  The pages written
+    are distinct, and none of them is read by the call.  status (`new_status`): set by a page past the last (its
+    pair is left out) or a token count outside the page."""
+    return (_calls or _entries()).copy_pages(k_cache, v_cache, src, dst, tokens, k_scale, v_scale, status,
+                                             None if stream is None else stream.cuda_stream)
+
+
+def compact_drafts(k_cache, v_cache, page_table, lengths, starts, kept, k_scale=None, v_scale=None, out=None, status=None,
+                   stream=None):
+    """Close up the kept drafts of a step in a paged cache; returns the sequences' new lengths [B] int32 (a new
+    tensor, or `out`, which is not lengths itself).
+
+    Of the last starts[b + 1] - starts[b] tokens of sequence b, its drafts, number kept[b, 0], kept[b, 1], ...
+    (ascending; a negative entry ends the list) move to the first places behind the context.  Cache of one layer or,
+    as for `copy_pages`, of several; page_table int32 [B, pages], lengths int32 [B] with the drafts, starts int32
+    [B + 1], kept int32 [B, K].  status (`new_status`): set by entries that do not ascend or are no draft (they end
+    the list), pages out of range (those tokens stay) and starts or lengths that do not fit (the sequence stays)."""
+    return (_calls or _entries()).compact_drafts(k_cache, v_cache, page_table, lengths, starts, kept, k_scale, v_scale,
+                                                 out, status, None if stream is None else stream.cuda_stream)
 
 
 class MoeLayer:

@@ -19,7 +19,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_gb300.so")
 BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["moe_api.cu", "moe_route.cu", "moe_gemm.cu", "moe_gemm_decode.cu", "moe_gemm_mx.cu", "moe_gate.cu", "moe_append.cu",
-           "moe_attend.cu"]
+           "moe_attend.cu", "moe_pages.cu"]
 HEADERS = ["moe_device.cuh", "moe_internal.h", "moe_scan.cuh"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "-Xptxas", "-v"]
@@ -119,8 +119,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     library = force or _stale()
     binding = not missing and (force or _binding_stale())
     if missing:
-        warnings.warn(f"no {missing}: route_experts, rotate_append and paged_attention get no Python entries (the C "
-                      "library is not affected)", stacklevel=2)
+        warnings.warn(f"no {missing}: the decoder-block operators (route_experts, rotate_append, paged_attention and those "
+                      "beside them) get no Python entries (the C library is not affected)", stacklevel=2)
     if not library and not binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -185,7 +185,7 @@ PyObject* route_experts(PyObject* const* a) {
 }
 
 // rotate_append(q, k, v, positions, slots, k_cache, v_cache, inv_freq, k_scale, v_scale, interleaved, rope_scale,
-//               q_out, status, stream)
+//               q_out, status, stream, axes)
 PyObject* rotate_append(PyObject* const* a) {
     const moe_kv_cache c = cache_of(a[5], a[6], a[8], a[9]);
     const Tensor& cache = THPVariable_Unpack(a[5]);
@@ -202,8 +202,18 @@ PyObject* rotate_append(PyObject* const* a) {
     const Tensor& inv_freq = tensor(a[7], "inv_freq", &q);
     if (inv_freq.scalar_type() != at::kDouble || !inv_freq.is_contiguous() || inv_freq.numel() > 4096)
         fail("inv_freq must be a contiguous fp64 CUDA tensor [R / 2]");
-    const void* pos = vector_ptr(tensor(a[3], "positions", &q), N, at::kLong,
-                                 "positions must be a contiguous int64 CUDA tensor [N]");
+    const Tensor& position = tensor(a[3], "positions", &q);
+    const Tensor axes = optional(a[15], "axes", q);
+    const void* pos = nullptr;
+    if (axes.defined()) {
+        if (position.scalar_type() != at::kLong || position.dim() != 2 || position.size(0) < 1 ||
+            position.size(0) > 16 || position.size(1) != N || (N > 1 && position.stride(1) != 1))
+            fail("positions must be an int64 CUDA tensor [axes, N] of 1 to 16 contiguous rows");
+        vector_ptr(axes, inv_freq.numel(), at::kInt, "axes must be a contiguous int32 CUDA tensor [R / 2]");
+        pos = position.data_ptr();
+    } else {
+        pos = vector_ptr(position, N, at::kLong, "positions must be a contiguous int64 CUDA tensor [N]");
+    }
     const void* slots =
         vector_ptr(tensor(a[4], "slots", &q), N, at::kLong, "slots must be a contiguous int64 CUDA tensor [N]");
     const OnStream on(a[14], q);
@@ -214,12 +224,22 @@ PyObject* rotate_append(PyObject* const* a) {
         fail("q_out must be like q");
     if (q.stride(2) != 1 || k.stride(2) != 1 || v.stride(2) != 1 || out.stride(2) != 1)
         fail("the last dim of q, k, v and q_out must be contiguous");
-    if (N)
+    const int rot = 2 * (int)inv_freq.numel(), neighbours = truth(a[10]);
+    const float rope_scale = (float)real(a[11]);
+    const int64_t *at = static_cast<const int64_t*>(pos), *to = static_cast<const int64_t*>(slots);
+    const double* freq = static_cast<const double*>(inv_freq.data_ptr());
+    uint32_t* status = status_ptr(a[13], q);
+    if (N && axes.defined())
+        check(moe_rotate_append_axes(&c, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, q.stride(0), q.stride(1),
+                                     k.stride(0), k.stride(1), v.stride(0), v.stride(1), at, (int)position.size(0),
+                                     position.stride(0), static_cast<const int32_t*>(axes.data_ptr()), to, freq, rot,
+                                     neighbours, rope_scale, (int)N, (int)Hq, out.data_ptr(), out.stride(0),
+                                     out.stride(1), status, on.handle),
+              "moe_rotate_append_axes");
+    else if (N)
         check(moe_rotate_append(&c, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, q.stride(0), q.stride(1), k.stride(0),
-                                k.stride(1), v.stride(0), v.stride(1), static_cast<const int64_t*>(pos),
-                                static_cast<const int64_t*>(slots), static_cast<const double*>(inv_freq.data_ptr()),
-                                2 * (int)inv_freq.numel(), truth(a[10]), (float)real(a[11]), (int)N, (int)Hq,
-                                out.data_ptr(), out.stride(0), out.stride(1), status_ptr(a[13], q), on.handle),
+                                k.stride(1), v.stride(0), v.stride(1), at, to, freq, rot, neighbours, rope_scale, (int)N,
+                                (int)Hq, out.data_ptr(), out.stride(0), out.stride(1), status, on.handle),
               "moe_rotate_append");
     return THPVariable_Wrap(out);
 }
@@ -276,6 +296,102 @@ PyObject* paged_attention(PyObject* const* a) {
     return THPVariable_Wrap(out);
 }
 
+// Checked cache tensors of several layers, [layers, pages, heads, page, D] or without the first dim:
+// layer 0 as a cache, the number of layers, the strides from layer to layer of k, v and scales.
+struct Layers {
+    moe_kv_cache cache;
+    int layers = 1;
+    int64_t stride[3] = {0, 0, 0};
+};
+Layers layers_of(PyObject* k_o, PyObject* v_o, PyObject* ks_o, PyObject* vs_o) {
+    Layers r;
+    if (!THPVariable_Check(k_o) || THPVariable_Unpack(k_o).dim() != 5) {
+        r.cache = cache_of(k_o, v_o, ks_o, vs_o);
+        return r;
+    }
+    PyObject* all[4] = {k_o, v_o, ks_o, vs_o};
+    struct Owned {
+        PyObject* o = nullptr;
+        ~Owned() { Py_XDECREF(o); }
+    } first[4];
+    const int64_t n = THPVariable_Unpack(k_o).size(0);
+    if (n < 1 || n > INT_MAX) fail("k_cache and v_cache need at least one layer");
+    for (int i = 0; i < 4; ++i) {
+        if (!THPVariable_Check(all[i])) {  // None, or what cache_of refuses
+            Py_INCREF(all[i]);
+            first[i].o = all[i];
+            continue;
+        }
+        const Tensor& t = THPVariable_Unpack(all[i]);
+        if (t.dim() != (i < 2 ? 5 : 4) || t.size(0) != n)
+            fail("k_cache and v_cache must both be [layers, pages, heads, page, D], scales [layers, pages, heads, page]");
+        if (n > 1) {
+            if (i == 3 && t.stride(0) != r.stride[2]) fail("k_scale and v_scale must have equal strides");
+            r.stride[i < 2 ? i : 2] = t.stride(0);
+        }
+        first[i].o = THPVariable_Wrap(t.select(0, 0));
+        if (!first[i].o) throw Failed();
+    }
+    r.cache = cache_of(first[0].o, first[1].o, first[2].o, first[3].o);
+    r.layers = (int)n;
+    return r;
+}
+const int32_t* ints(const Tensor& t, int64_t n, const char* what) {
+    return static_cast<const int32_t*>(vector_ptr(t, n, at::kInt, what));
+}
+const Tensor& int_rows(PyObject* o, int64_t B, const char* name, const char* what, const Tensor& like) {
+    const Tensor& t = tensor(o, name, &like);
+    if (t.scalar_type() != at::kInt || t.dim() != 2 || t.size(0) != B || t.size(1) > INT_MAX ||
+        (t.size(1) > 1 && t.stride(1) != 1))
+        fail(what);
+    return t;
+}
+
+// copy_pages(k_cache, v_cache, src, dst, tokens, k_scale, v_scale, status, stream)
+PyObject* copy_pages(PyObject* const* a) {
+    const Layers c = layers_of(a[0], a[1], a[5], a[6]);
+    const Tensor& k = THPVariable_Unpack(a[0]);
+    const Tensor& src = tensor(a[2], "src", &k);
+    const int64_t N = src.dim() == 1 ? src.size(0) : -1;
+    if (N > INT_MAX) fail("src is too large");
+    const int32_t* s = ints(src, N, "src must be a contiguous int32 CUDA tensor [N]");
+    const int32_t* d = ints(tensor(a[3], "dst", &k), N, "dst must be a contiguous int32 CUDA tensor [N]");
+    const Tensor tokens = optional(a[4], "tokens", k);
+    const int32_t* t = tokens.defined() ? ints(tokens, N, "tokens must be a contiguous int32 CUDA tensor [N]") : nullptr;
+    const OnStream on(a[8], k);
+    uint32_t* status = status_ptr(a[7], k);
+    if (N) check(moe_copy_pages(&c.cache, c.layers, c.stride, s, d, t, (int)N, status, on.handle), "moe_copy_pages");
+    Py_RETURN_NONE;
+}
+
+// compact_drafts(k_cache, v_cache, page_table, lengths, starts, kept, k_scale, v_scale, out, status, stream)
+PyObject* compact_drafts(PyObject* const* a) {
+    const Layers c = layers_of(a[0], a[1], a[6], a[7]);
+    const Tensor& k = THPVariable_Unpack(a[0]);
+    const Tensor& lengths = tensor(a[3], "lengths", &k);
+    const int64_t B = lengths.dim() == 1 ? lengths.size(0) : -1;
+    if (B > INT_MAX) fail("lengths is too large");
+    const int32_t* lens = ints(lengths, B, "lengths must be a contiguous int32 CUDA tensor [B]");
+    const int32_t* starts = ints(tensor(a[4], "starts", &k), B + 1, "starts must be a contiguous int32 CUDA tensor [B + 1]");
+    const Tensor& table =
+        int_rows(a[2], B, "page_table", "page_table must be an int32 CUDA tensor [B, pages] with contiguous rows", k);
+    const Tensor& kept = int_rows(a[5], B, "kept", "kept must be an int32 CUDA tensor [B, K] with contiguous rows", k);
+    const OnStream on(a[10], k);
+    Tensor out = optional(a[8], "out", k);
+    if (!out.defined())
+        out = empty({B}, at::kInt, k);
+    else if (ints(out, B, "out must be a contiguous int32 CUDA tensor [B]") == lens && B)
+        fail("out cannot be lengths itself");
+    uint32_t* status = status_ptr(a[9], k);
+    if (B)
+        check(moe_compact_drafts(&c.cache, c.layers, c.stride, static_cast<const int32_t*>(table.data_ptr()),
+                                 table.stride(0), (int)table.size(1), lens, starts,
+                                 static_cast<const int32_t*>(kept.data_ptr()), kept.stride(0), (int)B,
+                                 (int)kept.size(1), static_cast<int32_t*>(out.data_ptr()), status, on.handle),
+              "moe_compact_drafts");
+    return THPVariable_Wrap(out);
+}
+
 // No C++ exception leaves an entry: failures of ours have set the Python error,
 // torch's (out of memory among them) become its Python errors.
 template <PyObject* (*F)(PyObject* const*), int N>
@@ -305,8 +421,10 @@ PyCFunction method(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
 }
 PyMethodDef g_methods[] = {
     {"route_experts", method(entry<route_experts, 10>), METH_FASTCALL, nullptr},
-    {"rotate_append", method(entry<rotate_append, 15>), METH_FASTCALL, nullptr},
+    {"rotate_append", method(entry<rotate_append, 16>), METH_FASTCALL, nullptr},
     {"paged_attention", method(entry<paged_attention, 14>), METH_FASTCALL, nullptr},
+    {"copy_pages", method(entry<copy_pages, 9>), METH_FASTCALL, nullptr},
+    {"compact_drafts", method(entry<compact_drafts, 11>), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

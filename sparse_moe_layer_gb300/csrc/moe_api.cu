@@ -841,12 +841,18 @@ static moe_status check_strides(int n, int h, int64_t* token, int64_t* head) {
     return *token % 8 || *head % 8 ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
-extern "C" moe_status moe_rotate_append(const moe_kv_cache* cache, const void* q, const void* k, const void* v,
-                                        int dtype, int64_t q_token, int64_t q_head, int64_t k_token, int64_t k_head,
-                                        int64_t v_token, int64_t v_head, const int64_t* positions,
-                                        const int64_t* slots, const double* inv_freq, int rot_dim, int neighbours,
-                                        float rope_scale, int N, int q_heads, void* q_out, int64_t out_token,
-                                        int64_t out_head, uint32_t* status, void* stream) {
+// Positions of several axes (moe_rotate_append_axes).
+struct AxesInput {
+    const int32_t* axes;
+    int n_axes;
+    int64_t ld;
+};
+
+static moe_status append_impl(const moe_kv_cache* cache, const void* q, const void* k, const void* v, int dtype,
+                              int64_t q_token, int64_t q_head, int64_t k_token, int64_t k_head, int64_t v_token,
+                              int64_t v_head, const int64_t* positions, const AxesInput* ax, const int64_t* slots,
+                              const double* inv_freq, int rot_dim, int neighbours, float rope_scale, int N, int q_heads,
+                              void* q_out, int64_t out_token, int64_t out_head, uint32_t* status, void* stream) {
     AppendParams p;
     memset(&p, 0, sizeof(p));
     const moe_status cs = check_cache(cache, &p.cache);
@@ -873,6 +879,15 @@ extern "C" moe_status moe_rotate_append(const moe_kv_cache* cache, const void* q
     p.q_token = q_token, p.q_head = q_head, p.k_token = k_token, p.k_head = k_head;
     p.v_token = v_token, p.v_head = v_head, p.o_token = out_token, p.o_head = out_head;
     p.positions = positions;
+    if (ax) {
+        if (rot_dim && !ax->axes) return MOE_ERR_INVALID_ARG;
+        if (ax->n_axes < 1 || ax->n_axes > 16 || (ax->n_axes > 1 && (ax->ld < N || ax->ld > (1LL << 40))))
+            return MOE_ERR_INVALID_ARG;
+        if (reinterpret_cast<uintptr_t>(ax->axes) & 3u) return MOE_ERR_UNSUPPORTED;
+        p.axes = ax->axes;
+        p.n_axes = ax->n_axes;
+        p.axis_ld = ax->n_axes > 1 ? ax->ld : 0;
+    }
     p.slots = slots;
     p.inv_freq = inv_freq;
     p.N = N;
@@ -889,6 +904,28 @@ extern "C" moe_status moe_rotate_append(const moe_kv_cache* cache, const void* q
                                 static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
+}
+
+extern "C" moe_status moe_rotate_append(const moe_kv_cache* cache, const void* q, const void* k, const void* v,
+                                        int dtype, int64_t q_token, int64_t q_head, int64_t k_token, int64_t k_head,
+                                        int64_t v_token, int64_t v_head, const int64_t* positions,
+                                        const int64_t* slots, const double* inv_freq, int rot_dim, int neighbours,
+                                        float rope_scale, int N, int q_heads, void* q_out, int64_t out_token,
+                                        int64_t out_head, uint32_t* status, void* stream) {
+    return append_impl(cache, q, k, v, dtype, q_token, q_head, k_token, k_head, v_token, v_head, positions, nullptr, slots,
+                       inv_freq, rot_dim, neighbours, rope_scale, N, q_heads, q_out, out_token, out_head, status, stream);
+}
+
+extern "C" moe_status moe_rotate_append_axes(const moe_kv_cache* cache, const void* q, const void* k, const void* v,
+                                             int dtype, int64_t q_token, int64_t q_head, int64_t k_token,
+                                             int64_t k_head, int64_t v_token, int64_t v_head, const int64_t* positions,
+                                             int n_axes, int64_t axis_stride, const int32_t* axes, const int64_t* slots,
+                                             const double* inv_freq, int rot_dim, int neighbours, float rope_scale, int N,
+                                             int q_heads, void* q_out, int64_t out_token, int64_t out_head,
+                                             uint32_t* status, void* stream) {
+    const AxesInput ax = {axes, n_axes, axis_stride};
+    return append_impl(cache, q, k, v, dtype, q_token, q_head, k_token, k_head, v_token, v_head, positions, &ax, slots,
+                       inv_freq, rot_dim, neighbours, rope_scale, N, q_heads, q_out, out_token, out_head, status, stream);
 }
 
 // A sequence's tokens, at most: a multiple of every tile below 2^31.
@@ -964,6 +1001,97 @@ extern "C" moe_status moe_paged_attention(const moe_kv_cache* cache, const void*
                    cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
+}
+
+// Layer strides of a cache of several layers: out[0..2] of k, v and the scales, 0 for one layer.
+static moe_status check_layers(const moe_kv_cache* c, int layers, const int64_t* stride, long long* out) {
+    out[0] = out[1] = out[2] = 0;
+    if (layers < 1 || layers > 65536 || (layers > 1 && !stride)) return MOE_ERR_INVALID_ARG;
+    if (layers == 1) return MOE_OK;
+    const bool e4m3 = c->dtype == MOE_E4M3;
+    const int el = e4m3 ? 16 : 8;
+    if (stride[0] < 0 || stride[1] < 0 || (e4m3 && stride[2] < 0)) return MOE_ERR_INVALID_ARG;
+    if (stride[0] % el || stride[1] % el) return MOE_ERR_UNSUPPORTED;
+    out[0] = stride[0];
+    out[1] = stride[1];
+    if (e4m3) out[2] = stride[2];
+    return MOE_OK;
+}
+
+extern "C" moe_status moe_copy_pages(const moe_kv_cache* cache, int layers, const int64_t* layer_stride,
+                                     const int32_t* src, const int32_t* dst, const int32_t* tokens, int N,
+                                     uint32_t* status, void* stream) {
+    CopyPagesParams p;
+    memset(&p, 0, sizeof(p));
+    moe_status s = check_cache(cache, &p.cache);
+    if (s != MOE_OK) return s;
+    long long ls[3];
+    s = check_layers(cache, layers, layer_stride, ls);
+    if (s != MOE_OK) return s;
+    if (!src || !dst || N < 1) return MOE_ERR_INVALID_ARG;
+    p.elem = cache->dtype == MOE_E4M3 ? 1 : 2;
+    p.row_pieces = cache->head_dim * p.elem / 16;
+    // pieces of a page's keys are counted in 31 bits, and so are the CTAs
+    const long long pieces = (long long)cache->page_size * p.row_pieces * cache->kv_heads;
+    if (pieces >= (1LL << 31) - 1024) return MOE_ERR_INVALID_ARG;
+    if ((long long)N * layers >= (1LL << 30) || (long long)N * layers * ((pieces + 1023) / 1024) >= (1LL << 30))
+        return MOE_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst) | reinterpret_cast<uintptr_t>(tokens) |
+         reinterpret_cast<uintptr_t>(status)) & 3u)
+        return MOE_ERR_UNSUPPORTED;
+    p.k_layer = ls[0], p.v_layer = ls[1], p.s_layer = ls[2];
+    p.layers = layers;
+    p.num_pages = cache->num_pages;
+    p.page_size = cache->page_size;
+    p.Hkv = cache->kv_heads;
+    p.src = src;
+    p.dst = dst;
+    p.tokens = tokens;
+    p.N = N;
+    p.status = status;
+    return launch_copy_pages(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+extern "C" moe_status moe_compact_drafts(const moe_kv_cache* cache, int layers, const int64_t* layer_stride,
+                                         const int32_t* page_table, int64_t table_ld, int table_width,
+                                         const int32_t* lengths, const int32_t* starts, const int32_t* kept,
+                                         int64_t kept_ld, int B, int K, int32_t* new_lengths, uint32_t* status,
+                                         void* stream) {
+    CompactParams p;
+    memset(&p, 0, sizeof(p));
+    moe_status s = check_cache(cache, &p.cache);
+    if (s != MOE_OK) return s;
+    long long ls[3];
+    s = check_layers(cache, layers, layer_stride, ls);
+    if (s != MOE_OK) return s;
+    if (!page_table || !lengths || !starts || !kept || !new_lengths || new_lengths == lengths) return MOE_ERR_INVALID_ARG;
+    if (B < 1 || B > 65536 || K < 1 || table_width < 1 || (long long)table_width * cache->page_size > kMaxTokens)
+        return MOE_ERR_INVALID_ARG;
+    if (B == 1) table_ld = kept_ld = 0;
+    if (B > 1 && (table_ld < table_width || kept_ld < K)) return MOE_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(lengths) |
+         reinterpret_cast<uintptr_t>(starts) | reinterpret_cast<uintptr_t>(kept) |
+         reinterpret_cast<uintptr_t>(new_lengths) | reinterpret_cast<uintptr_t>(status)) & 3u)
+        return MOE_ERR_UNSUPPORTED;
+    p.elem = cache->dtype == MOE_E4M3 ? 1 : 2;
+    p.row_pieces = cache->head_dim * p.elem / 16;
+    p.k_layer = ls[0], p.v_layer = ls[1], p.s_layer = ls[2];
+    p.layers = layers;
+    p.num_pages = cache->num_pages;
+    p.page_size = cache->page_size;
+    p.Hkv = cache->kv_heads;
+    p.table = page_table;
+    p.table_ld = table_ld;
+    p.max_tokens = table_width * cache->page_size;
+    p.lengths = lengths;
+    p.starts = starts;
+    p.kept = kept;
+    p.kept_ld = kept_ld;
+    p.B = B;
+    p.K = K;
+    p.out = new_lengths;
+    p.status = status;
+    return launch_compact_drafts(p, num_sms(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 extern "C" {

@@ -3,7 +3,8 @@
 // ("GPT-OSS on Day 0", perplexity.ai hub blog, architecture list) and a cache
 // kept heads-major, tokens contiguous ("Hosting Qwen on Blackwell").
 //
-//   a_i = position * inv_freq_i   (64 bits), i < rot / 2
+//   a_i = position * inv_freq_i   (64 bits), i < rot / 2; with several axes (time,
+//         height, width of images and video) the position is that of pair i's axis
 //   (x_i, y_i) -> m (x_i cos a_i - y_i sin a_i, x_i sin a_i + y_i cos a_i)
 //   pairs (i, i + rot/2), or neighbours (2i, 2i+1); dims past rot unchanged
 //   16-bit cache: the rotated k and v, rounded once
@@ -103,8 +104,16 @@ __global__ void __launch_bounds__(kAppendWarps * 32) rotate_append_kernel(Append
         load(r0 + i * rpg, va[i], vb[i]);  // in flight while the angles are computed
     }
     const long long slot = p.slots[n];
-    const double pos = (double)p.positions[n];
+    const double at_n = (double)p.positions[n];  // (axes: of axis 0)
     for (int i = lane; i < half; i += 32) {
+        double pos = at_n;
+        if (p.axes) {
+            const int axis = __ldg(p.axes + i);
+            if ((uint32_t)axis < (uint32_t)p.n_axes)
+                pos = (double)__ldg(p.positions + axis * p.axis_ld + n);
+            else if (p.status)
+                atomicOr(p.status, kErrBadIndex);
+        }
         // whole turns drop out in 64 bits: a float keeps only 2^-24 of the angle, not of its fraction
         const double turn = pos * p.inv_freq[i] * 0.15915494309189533577;
         float s, c;

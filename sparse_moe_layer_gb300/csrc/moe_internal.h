@@ -68,7 +68,10 @@ struct AppendParams {
     const uint16_t* v;
     uint16_t* q_out;
     long long q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
-    const int64_t* positions;  // [N]
+    const int64_t* positions;  // [N]; with axes, [n_axes, N], rows axis_ld apart
+    const int32_t* axes;       // [rot / 2] axis of each pair, or null: one for all
+    long long axis_ld;
+    int n_axes;
     const int64_t* slots;      // [N]; < 0: not appended
     const double* inv_freq;    // [rot / 2]
     int N, Hq, Hkv, D, rot;
@@ -78,6 +81,38 @@ struct AppendParams {
     KvCache cache;
     uint32_t* status;                // error word or null
     int lpr_shift, parts, groups_per_part;  // set at launch
+};
+
+// Moves within a paged cache of several layers (layer strides in elements, the cache's
+// pointers those of layer 0).
+struct CopyPagesParams {
+    KvCache cache;
+    long long k_layer, v_layer, s_layer;
+    int layers, num_pages, page_size, Hkv;
+    int elem, row_pieces;   // bytes of a value; 16-byte pieces of a token's head
+    const int32_t* src;     // [N]; a pair with a negative page is left out
+    const int32_t* dst;     // [N]
+    const int32_t* tokens;  // [N] places copied, or null: all
+    int N;
+    uint32_t* status;  // error word or null
+    int parts;         // set at launch: CTAs of a page's keys (or values) in a layer
+};
+struct CompactParams {
+    KvCache cache;
+    long long k_layer, v_layer, s_layer;
+    int layers, num_pages, page_size, Hkv;
+    int elem, row_pieces;
+    const int32_t* table;  // [B, *] page ids, rows table_ld apart
+    long long table_ld;
+    int max_tokens;          // table columns * page_size
+    const int32_t* lengths;  // [B] tokens of a sequence, its drafts included
+    const int32_t* starts;   // [B + 1] first draft of each sequence
+    const int32_t* kept;     // [B, K] drafts kept, ascending; -1 ends
+    long long kept_ld;
+    int B, K;
+    int32_t* out;  // [B] new lengths
+    uint32_t* status;
+    int lpr_shift, layer_parts;  // set at launch: lanes of a token's head (log2); warps that share the layers
 };
 
 struct AttendParams {
@@ -234,6 +269,8 @@ int router_tc_experts(int T, int H, int E);
 cudaError_t launch_router_tc(const RouteParams& p, const CUtensorMap& tmX, const CUtensorMap& tmW, cudaStream_t st);
 cudaError_t launch_gate(const GateParams& p, int dtype, int sms, cudaStream_t st);
 cudaError_t launch_rotate_append(const AppendParams& p, bool fp16, bool e4m3, int sms, cudaStream_t st);
+cudaError_t launch_copy_pages(const CopyPagesParams& p, cudaStream_t st);
+cudaError_t launch_compact_drafts(const CompactParams& p, int sms, cudaStream_t st);
 // most: tokens that a row can have (its window, or the page table's columns)
 void attend_plan(int B, int Hq, int Hkv, int D, bool e4m3, int most, int sms, AttendPlan* plan);
 cudaError_t launch_attend(const AttendParams& p, const AttendPlan& plan, int kv_dtype, bool fp16, void* workspace,
