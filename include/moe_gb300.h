@@ -523,6 +523,44 @@ moe_status moe_paged_attention(const moe_kv_cache* cache, const void* q, int dty
                                int64_t out_token, int64_t out_head, void* workspace, size_t workspace_bytes,
                                uint32_t* status, void* stream);
 
+/*
+ * Attention of a step's drafted tokens over a paged cache: a tree (or a chain) of
+ * drafts behind the context of each sequence, checked in one pass.  Sequence b has
+ * n = starts[b+1] - starts[b] drafts, rows starts[b] and on of q, whose keys and values
+ * are its last n tokens in the cache; c = lengths[b] - n tokens of context stand before
+ * them.  parents[starts[b] + i] < i is the draft (a number in the sequence) that draft i
+ * follows, -1: the context (NULL: each follows the one before).  Draft i, of d_i
+ * ancestors, sees token t < c of the context if t > c + d_i - window (window 0: all),
+ * and of the drafts itself and its ancestors, of them the nearest window - 1; what
+ * it sees is attended to as in moe_paged_attention, with the same sinks, types,
+ * roundings and limits of e4m3 caches.  Queries are to be rotated by positions c + d_i.
+ * Keys of tokens that a draft does not see may be anything, values of tokens that only
+ * other drafts of the sequence see are to be finite (they are multiplied by 0).
+ * Rows of q outside all sequences are not read, and of out not written.  A draft that
+ * sees nothing gets 0.  A sequence whose starts descend, leave [0, N] or name more than 256
+ * drafts is left out, a length outside [n, table_width * page_size] is brought into it
+ * as far as that goes (no context, and no drafts behind the last token), a parent that is
+ * not before its draft counts as -1, a token on a page outside [0, num_pages) is left
+ * out; all of these set the error word.
+ *   q [N, q_heads, D] bf16 or fp16 (`dtype`; that of a 16-bit cache), strides in elements,
+ *   D contiguous; out likewise; page_table [B, table_width], lengths [B], starts [B + 1],
+ *   parents [N] int32; sinks fp32 [q_heads]
+ *   workspace: moe_tree_attention_workspace_size bytes, 256-byte aligned, any contents;
+ *   calls that may overlap need one each
+ *   status: a device error word for moe_read_device_status, or NULL
+ * Limits: those of the cache; q_heads a multiple of kv_heads, at most 4096; 1 <= N < 2^27;
+ * 1 <= B <= 65536; table_width * page_size at most 2^31 - 256; q and out: pointers and
+ * strides multiples of 16 bytes.  The result is the same for every run of the same call.
+ * Asynchronous on `stream`.
+ */
+size_t moe_tree_attention_workspace_size(int N, int B, int q_heads, int kv_heads, int head_dim, int cache_dtype,
+                                         int max_tokens);
+moe_status moe_tree_attention(const moe_kv_cache* cache, const void* q, int dtype, int64_t q_token, int64_t q_head,
+                              const int32_t* page_table, int64_t table_ld, int table_width, const int32_t* lengths,
+                              const int32_t* starts, const int32_t* parents, int N, int B, int q_heads, float scale,
+                              const float* sinks, int window, void* out, int64_t out_token, int64_t out_head,
+                              void* workspace, size_t workspace_bytes, uint32_t* status, void* stream);
+
 /* Synchronises `stream`, then reads and clears the device error word of
  * `workspace`: MOE_OK, MOE_ERR_DEVICE_TIMEOUT (a bounded wait ran out),
  * MOE_ERR_INDEX (a page, slot or length was out of range), or MOE_ERR_CUDA. */

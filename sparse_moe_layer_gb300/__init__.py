@@ -4,9 +4,9 @@ Thin Python binding of the C ABI in ``include/moe_gb300.h`` (library
 ``libmoe_gb300.so``, built in-tree for sm_103a).  Every step of the layer runs
 in the library's CUDA kernels; this module only checks tensors and passes
 pointers, sizes and the current CUDA stream.  The operators beside the layer
-(route_experts, rotate_append, paged_attention) do that in a compiled module,
-``_binding.so``.  There is no CPU fallback: if the library is missing, importing
-the binding's functions raises.
+(route_experts, rotate_append, paged_attention, tree_attention, copy_pages,
+compact_drafts) do that in a compiled module, ``_binding.so``.  There is no CPU
+fallback: if the library is missing, importing the binding's functions raises.
 """
 from __future__ import annotations
 
@@ -24,7 +24,7 @@ __all__ = ["MoeError", "build", "lib", "workspace_size", "workspace_layout", "wo
            "pack_weights_mxfp4", "pack_weights_into_mxfp4", "w13_shape_fp4", "w2_shape_fp4", "unblock_fp4",
            "weight_format", "route_debug", "block_weights", "read_static_scratch_status",
            "route_experts", "forward_gated", "rotate_append", "new_status",
-           "paged_attention", "attention_workspace", "copy_pages", "compact_drafts"]
+           "paged_attention", "attention_workspace", "tree_attention", "tree_attention_workspace", "copy_pages", "compact_drafts"]
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace too small", 4: "CUDA error",
           5: "device wait timed out", 6: "a page, slot or length was out of range"}
@@ -113,6 +113,11 @@ def lib():
         L.moe_paged_attention.argtypes = [vp, vp, i32, i64, i64, vp, i64, i32, vp, i32, i32, f32, vp, i32, vp, i64, i64,
                                           vp, sz, vp, vp]
         L.moe_paged_attention.restype = i32
+        L.moe_tree_attention_workspace_size.argtypes = [i32] * 7
+        L.moe_tree_attention_workspace_size.restype = sz
+        L.moe_tree_attention.argtypes = [vp, vp, i32, i64, i64, vp, i64, i32, vp, vp, vp, i32, i32, i32, f32, vp, i32, vp, i64,
+                                         i64, vp, sz, vp, vp]
+        L.moe_tree_attention.restype = i32
         L.moe_copy_pages.argtypes = [vp, i32] + [vp] * 4 + [i32, vp, vp]
         L.moe_copy_pages.restype = i32
         L.moe_compact_drafts.argtypes = [vp, i32, vp, vp, i64, i32, vp, vp, vp, i64, i32, i32, vp, vp, vp]
@@ -594,7 +599,7 @@ def forward_gated(x, logits, w13, s13, b13, w2, s2, b2, top_k: int, score: str =
 
 
 def new_status(device=None) -> torch.Tensor:
-    """A zeroed device error word for `rotate_append` and `paged_attention` (read it with `read_device_status`)."""
+    """A zeroed device error word for the operators beside the layer (read it with `read_device_status`)."""
     return torch.zeros(4, dtype=torch.uint8, device=device or "cuda")
 
 
@@ -638,6 +643,33 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, scale: float, k_sc
     return (_calls or _entries()).paged_attention(q, k_cache, v_cache, page_table, lengths, scale, k_scale, v_scale, sinks,
                                                   window, out, workspace, status,
                                                   None if stream is None else stream.cuda_stream)
+
+
+def tree_attention_workspace(N: int, B: int, q_heads: int, kv_heads: int, head_dim: int, max_tokens: int,
+                             dtype=torch.bfloat16, device=None) -> torch.Tensor:
+    """A workspace for `tree_attention` calls of N drafts of B sequences that do not overlap; max_tokens and dtype as
+    for `attention_workspace`."""
+    n = int(lib().moe_tree_attention_workspace_size(N, B, q_heads, kv_heads, head_dim, _DTYPES.get(dtype, -1), max_tokens))
+    if n == 0:
+        raise MoeError(1, "moe_tree_attention_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def tree_attention(q, k_cache, v_cache, page_table, lengths, starts, scale: float, parents=None, k_scale=None,
+                   v_scale=None, sinks=None, window: int = 0, out=None, workspace=None, status=None, stream=None):
+    """Attention of a step's drafted tokens, q [N, Hq, D] (bf16 or fp16), over a paged cache that holds their keys
+    and values already; returns out [N, Hq, D] of q's type.
+
+    Sequence b has rows starts[b] to starts[b + 1] of q (int32 [B + 1]; at most 256), which are the last of its
+    lengths[b] tokens (int32 [B]).  parents int32 [N]: the draft that each one follows, a smaller number in its
+    sequence, or -1 for the context; None: each follows the one before.  A draft sees the context, its ancestors and
+    itself; window > 0: of these only the nearest `window`, itself included, by its place in the tree (rotate drafts
+    by positions context + number of ancestors).  Cache, page_table, sinks, status as for `paged_attention`;
+    status is also set by starts, lengths or parents that do not fit (that sequence, token or parent is left out).
+    Rows outside all sequences are left as they are."""
+    return (_calls or _entries()).tree_attention(q, k_cache, v_cache, page_table, lengths, starts, scale, parents, k_scale,
+                                                 v_scale, sinks, window, out, workspace, status,
+                                                 None if stream is None else stream.cuda_stream)
 
 
 def copy_pages(k_cache, v_cache, src, dst, tokens=None, k_scale=None, v_scale=None, status=None, stream=None) -> None:

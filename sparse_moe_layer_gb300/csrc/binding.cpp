@@ -296,6 +296,71 @@ PyObject* paged_attention(PyObject* const* a) {
     return THPVariable_Wrap(out);
 }
 
+const int32_t* ints(const Tensor& t, int64_t n, const char* what) {
+    return static_cast<const int32_t*>(vector_ptr(t, n, at::kInt, what));
+}
+const Tensor& int_rows(PyObject* o, int64_t B, const char* name, const char* what, const Tensor& like) {
+    const Tensor& t = tensor(o, name, &like);
+    if (t.scalar_type() != at::kInt || t.dim() != 2 || t.size(0) != B || t.size(1) > INT_MAX ||
+        (t.size(1) > 1 && t.stride(1) != 1))
+        fail(what);
+    return t;
+}
+
+// tree_attention(q, k_cache, v_cache, page_table, lengths, starts, scale, parents, k_scale, v_scale, sinks, window,
+//                out, workspace, status, stream)
+PyObject* tree_attention(PyObject* const* a) {
+    const moe_kv_cache c = cache_of(a[1], a[2], a[8], a[9]);
+    const Tensor& q = tensor(a[0], "q", &THPVariable_Unpack(a[1]));
+    const int dt = dtype_of(q);
+    if ((dt != MOE_BF16 && dt != MOE_FP16) || (c.dtype != MOE_E4M3 && c.dtype != dt))
+        fail("q must be a bf16 or fp16 CUDA tensor, and a 16-bit cache of its type");
+    if (q.dim() != 3 || q.size(2) != c.head_dim || q.stride(2) != 1)
+        fail("q must be [N, Hq, D] with the cache's D and a contiguous last dim");
+    const int64_t N = q.size(0), Hq = q.size(1);
+    if (N > INT_MAX || Hq > INT_MAX) fail("q is too large");
+    const Tensor& lengths = tensor(a[4], "lengths", &q);
+    const int64_t B = lengths.dim() == 1 ? lengths.size(0) : -1;
+    if (B > INT_MAX) fail("lengths is too large");
+    const int32_t* lens = ints(lengths, B, "lengths must be a contiguous int32 CUDA tensor [B]");
+    const int32_t* starts = ints(tensor(a[5], "starts", &q), B + 1, "starts must be a contiguous int32 CUDA tensor [B + 1]");
+    const Tensor& table =
+        int_rows(a[3], B, "page_table", "page_table must be an int32 CUDA tensor [B, pages] with contiguous rows", q);
+    const Tensor parents = optional(a[7], "parents", q);
+    const int32_t* up = parents.defined() ? ints(parents, N, "parents must be a contiguous int32 CUDA tensor [N]") : nullptr;
+    const Tensor sinks = optional(a[10], "sinks", q);
+    if (sinks.defined() &&
+        (sinks.scalar_type() != at::kFloat || sinks.dim() != 1 || sinks.size(0) != Hq || !sinks.is_contiguous()))
+        fail("sinks must be a contiguous fp32 tensor [Hq]");
+    const int window = small(a[11]);
+    const float scale = (float)real(a[6]);
+    const OnStream on(a[15], q);
+    uint32_t* status = status_ptr(a[14], q);
+    Tensor out = optional(a[12], "out", q);
+    if (!out.defined())
+        out = empty(q.sizes(), q.scalar_type(), q);
+    else if (out.sizes() != q.sizes() || out.scalar_type() != q.scalar_type() || out.stride(2) != 1)
+        fail("out must be like q, its last dim contiguous");
+    if (N == 0 || B == 0) return THPVariable_Wrap(out);
+    Tensor ws = optional(a[13], "workspace", q);
+    if (ws.defined()) {
+        if (ws.scalar_type() != at::kByte || !ws.is_contiguous()) fail("workspace must be a contiguous uint8 tensor");
+    } else {
+        const long long most = table.size(1) * c.page_size;
+        const size_t bytes = moe_tree_attention_workspace_size(
+            (int)N, (int)B, (int)Hq, c.kv_heads, c.head_dim, c.dtype,
+            (int)(window > 0 && window < most ? window : most < INT_MAX ? most : INT_MAX));
+        if (bytes > 256) ws = empty({(int64_t)bytes}, at::kByte, q);
+    }
+    check(moe_tree_attention(&c, q.data_ptr(), dt, q.stride(0), q.stride(1), static_cast<const int32_t*>(table.data_ptr()),
+                             table.stride(0), (int)table.size(1), lens, starts, up, (int)N, (int)B, (int)Hq, scale,
+                             sinks.defined() ? static_cast<const float*>(sinks.data_ptr()) : nullptr, window,
+                             out.data_ptr(), out.stride(0), out.stride(1), ws.defined() ? ws.data_ptr() : nullptr,
+                             ws.defined() ? (size_t)ws.numel() : 0, status, on.handle),
+          "moe_tree_attention");
+    return THPVariable_Wrap(out);
+}
+
 // Checked cache tensors of several layers, [layers, pages, heads, page, D] or without the first dim:
 // layer 0 as a cache, the number of layers, the strides from layer to layer of k, v and scales.
 struct Layers {
@@ -335,16 +400,6 @@ Layers layers_of(PyObject* k_o, PyObject* v_o, PyObject* ks_o, PyObject* vs_o) {
     r.cache = cache_of(first[0].o, first[1].o, first[2].o, first[3].o);
     r.layers = (int)n;
     return r;
-}
-const int32_t* ints(const Tensor& t, int64_t n, const char* what) {
-    return static_cast<const int32_t*>(vector_ptr(t, n, at::kInt, what));
-}
-const Tensor& int_rows(PyObject* o, int64_t B, const char* name, const char* what, const Tensor& like) {
-    const Tensor& t = tensor(o, name, &like);
-    if (t.scalar_type() != at::kInt || t.dim() != 2 || t.size(0) != B || t.size(1) > INT_MAX ||
-        (t.size(1) > 1 && t.stride(1) != 1))
-        fail(what);
-    return t;
 }
 
 // copy_pages(k_cache, v_cache, src, dst, tokens, k_scale, v_scale, status, stream)
@@ -423,6 +478,7 @@ PyMethodDef g_methods[] = {
     {"route_experts", method(entry<route_experts, 10>), METH_FASTCALL, nullptr},
     {"rotate_append", method(entry<rotate_append, 16>), METH_FASTCALL, nullptr},
     {"paged_attention", method(entry<paged_attention, 14>), METH_FASTCALL, nullptr},
+    {"tree_attention", method(entry<tree_attention, 16>), METH_FASTCALL, nullptr},
     {"copy_pages", method(entry<copy_pages, 9>), METH_FASTCALL, nullptr},
     {"compact_drafts", method(entry<compact_drafts, 11>), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},

@@ -1003,6 +1003,79 @@ extern "C" moe_status moe_paged_attention(const moe_kv_cache* cache, const void*
                : MOE_ERR_CUDA;
 }
 
+static bool tree_ok(int N, int B, int q_heads, int kv_heads, int head_dim) {
+    return N >= 1 && N < (1 << 27) && B >= 1 && B <= 65536 && kv_heads >= 1 && kv_heads <= 256 && q_heads >= 1 &&
+           q_heads <= 4096 && q_heads % kv_heads == 0 && head_dim >= 16 && head_dim <= 256 && head_dim % 16 == 0;
+}
+
+extern "C" size_t moe_tree_attention_workspace_size(int N, int B, int q_heads, int kv_heads, int head_dim,
+                                                    int cache_dtype, int max_tokens) {
+    if (!tree_ok(N, B, q_heads, kv_heads, head_dim) || max_tokens < 1) return 0;
+    if (cache_dtype != MOE_BF16 && cache_dtype != MOE_FP16 && cache_dtype != MOE_E4M3) return 0;
+    TreePlan w;
+    tree_plan(N, B, q_heads, kv_heads, head_dim, cache_dtype == MOE_E4M3, max_tokens, num_sms(), &w);
+    return w.total ? w.total : 256;
+}
+
+extern "C" moe_status moe_tree_attention(const moe_kv_cache* cache, const void* q, int dtype, int64_t q_token,
+                                         int64_t q_head, const int32_t* page_table, int64_t table_ld, int table_width,
+                                         const int32_t* lengths, const int32_t* starts, const int32_t* parents, int N,
+                                         int B, int q_heads, float scale, const float* sinks, int window, void* out,
+                                         int64_t out_token, int64_t out_head, void* workspace, size_t workspace_bytes,
+                                         uint32_t* status, void* stream) {
+    TreeParams p;
+    memset(&p, 0, sizeof(p));
+    const moe_status cs = check_cache(cache, &p.cache);
+    if (cs != MOE_OK) return cs;
+    if (!q || !page_table || !lengths || !starts || !out) return MOE_ERR_INVALID_ARG;
+    if (!tree_ok(N, B, q_heads, cache->kv_heads, cache->head_dim) || table_width < 1 || window < 0 || scale != scale)
+        return MOE_ERR_INVALID_ARG;
+    // token numbers, rounded up to a tile, fit 31 bits
+    const long long most = (long long)table_width * cache->page_size;
+    if (most > (1LL << 31) - 256 || (B > 1 && table_ld < table_width)) return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_BF16 && dtype != MOE_FP16) return MOE_ERR_UNSUPPORTED;
+    if (cache->dtype != MOE_E4M3 && cache->dtype != dtype) return MOE_ERR_UNSUPPORTED;
+    if (B == 1) table_ld = 0;
+    const moe_status ss[] = {check_strides(N, q_heads, &q_token, &q_head), check_strides(N, q_heads, &out_token, &out_head)};
+    for (moe_status e : ss)
+        if (e != MOE_OK) return e;
+    if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return MOE_ERR_UNSUPPORTED;
+    if ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(lengths) |
+         reinterpret_cast<uintptr_t>(starts) | reinterpret_cast<uintptr_t>(parents) |
+         reinterpret_cast<uintptr_t>(sinks) | reinterpret_cast<uintptr_t>(status)) & 3u)
+        return MOE_ERR_UNSUPPORTED;
+    TreePlan w;
+    tree_plan(N, B, q_heads, cache->kv_heads, cache->head_dim, cache->dtype == MOE_E4M3,
+              (int)(window > 0 && window < most ? window : most), num_sms(), &w);
+    if (w.total && !workspace) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < w.total) return MOE_ERR_WORKSPACE;
+    p.q = static_cast<const uint16_t*>(q);
+    p.out = static_cast<uint16_t*>(out);
+    p.q_token = q_token, p.q_head = q_head, p.o_token = out_token, p.o_head = out_head;
+    p.table = page_table;
+    p.table_ld = table_ld;
+    p.lengths = lengths;
+    p.starts = starts;
+    p.parents = parents;
+    p.sinks = sinks;
+    p.N = N;
+    p.B = B;
+    p.Hq = q_heads;
+    p.Hkv = cache->kv_heads;
+    p.D = cache->head_dim;
+    p.num_pages = cache->num_pages;
+    p.page_size = cache->page_size;
+    p.max_tokens = (int)most;
+    p.window = window;
+    // a scale of 0 becomes the smallest normal: the scores' factor must not turn -inf into NaN
+    p.scale_log2 = fmaxf(fabsf(scale) * 1.4426950408889634f, 1.17549435e-38f);
+    p.q_sign = scale < 0.f ? 0x80008000u : 0u;
+    p.status = status;
+    return launch_tree(p, w, cache->dtype, dtype == MOE_FP16, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
 // Layer strides of a cache of several layers: out[0..2] of k, v and the scales, 0 for one layer.
 static moe_status check_layers(const moe_kv_cache* c, int layers, const int64_t* stride, long long* out) {
     out[0] = out[1] = out[2] = 0;

@@ -32,36 +32,15 @@
 // e4m3 took 149 us, 12 warps an SM with two stages 132 where this shape took 123.
 // More than 16 heads to a key: a row per 16, which reads the cache again (4 x 60000 tokens,
 // 4 key heads of 128, bf16: 64 heads 88 us, 128 heads 166).
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "moe_device.cuh"
+#include "moe_attend.cuh"
 #include "moe_internal.h"
 
 namespace moe {
 
 namespace {
 
-constexpr uint32_t kAllLanes = 0xffffffffu;
 constexpr int kAttWarps = 4;  // warps per CTA
 constexpr int kAttRows = 16;  // query heads per row (m16 of the products)
-enum : int { kKvBf16 = 0, kKvFp16 = 1, kKvE4m3 = 2 };
-
-// 16-bit caches: powers of two that a score may stand above the maximum that its row's sums
-// are about, and that these lie below that maximum: fp16 probabilities start at 2^7, reach
-// 2^15, and keep their 11 bits down to 2^-21 of the largest (without it a flat tail of
-// probabilities below 2^-25 was lost, however long).
-constexpr float kSlack = 8.f;
-template <int KV>
-constexpr float kLift = KV == kKvFp16 ? 7.f : 0.f;
-// e4m3: a weight is probability times value scale, and the row's sums and accumulators are
-// about a power of two that makes the largest weight so far at least 2^kNewWeight when it is
-// set (but kMostLift powers of two below the scores' maximum at most, where all weights are
-// tiny). While a tile's largest probability times its largest scale, as they stand to that,
-// is at most 2^kMostWeight the weights fit fp16; else they are looked at and it is set again.
-constexpr float kNewWeight = 5.f, kMostLift = 104.f, kMostWeight = 15.f;
-constexpr float kLeastScale = 0x1p-89f;  // 2^(kMostWeight - kMostLift): the sums' room where scales are smaller
-constexpr float kNoWeights = -0x1p127f;  // the power of two before a row's first
 
 // How the rows are given out: equal runs of tiles, one per CTA; a row per CTA; rows
 // per warp.  attend_plan chooses.
@@ -121,20 +100,6 @@ struct AttCfg {
     static constexpr int CTAS = ctas_per_sm(DP, KV == kKvE4m3, LIGHT);
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, bool valid) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async4z(uint32_t dst, const void* src, bool valid) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -159,27 +124,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two e4m3 codes (low half of v) -> two fp16 values, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
-    return r;
-}
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    if (F16) {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <bool F16>
-__device__ __forceinline__ float2 unpack2(uint32_t v) {
-    if (F16) return __half22float2(*reinterpret_cast<const __half2*>(&v));
-    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-}
-
 // Byte of chunk c (16 bytes) of token row r in a tile: 8 rows of one chunk
 // column fall on 8 different bank groups, for the loads and for ldmatrix.
 template <typename C>
@@ -245,27 +189,6 @@ __device__ __forceinline__ Quad quad(const float (&u)[4], const float (&v)[4], i
 template <int KV>
 __device__ __forceinline__ int quad_at(int c) {
     return KV == kKvE4m3 ? 4 * c : 2 * c;
-}
-
-// a = a f + b h
-__device__ __forceinline__ void add_scaled(float4& a, float f, const float4& b, float h) {
-    a.x = a.x * f + b.x * h;
-    a.y = a.y * f + b.y * h;
-    a.z = a.z * f + b.z * h;
-    a.w = a.w * f + b.w * h;
-}
-
-// 1 / (sum with the head's sink), about the larger of the two exponents: what
-// sums taken about m are multiplied by.  0 for a row without tokens; NaN stays NaN.
-__device__ __forceinline__ float final_weight(const AttendParams& p, int head, float m, float l) {
-    float w = 1.f;
-    if (p.sinks) {
-        const float k = __ldg(p.sinks + head) * 1.4426950408889634f;
-        const float n = fmaxf(m, k);
-        w = n == -INFINITY ? 0.f : ex2_approx(m - n);
-        l = n == -INFINITY ? 0.f : l * w + (k == n ? 1.f : ex2_approx(k - n));  // (an infinite sink too)
-    }
-    return l == 0.f ? 0.f : w / l;
 }
 
 }  // namespace
@@ -592,8 +515,8 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
                 if (ends && !starts) p.last[at] = run;
             }
             if (by_row) {
-                float w0 = g < heads ? final_weight(p, head0 + g, m0, l0) : 0.f;
-                float w1 = g + 8 < heads ? final_weight(p, head0 + g + 8, m1, l1) : 0.f;
+                float w0 = g < heads ? final_weight(p.sinks, head0 + g, m0, l0) : 0.f;
+                float w1 = g + 8 < heads ? final_weight(p.sinks, head0 + g + 8, m1, l1) : 0.f;
                 if constexpr (KV == kKvE4m3) {
                     w0 *= f0;
                     w1 *= f1;
@@ -655,7 +578,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, AttCfg<DP, KV, LIGHT>::CTAS) a
                         e[w] = m == -INFINITY ? 0.f : ex2_approx(s_ml[w][r].x - m);
                         l += e[w] * s_ml[w][r].y;
                     }
-                    const float fw = done ? final_weight(p, head0 + r, m, l) : 1.f;
+                    const float fw = done ? final_weight(p.sinks, head0 + r, m, l) : 1.f;
                     if (!done && lane % LPR == 0) *reinterpret_cast<float2*>(part + 2 * r) = make_float2(m, l);
 #pragma unroll
                     for (int q = 0; q < (DP + 127) / 128; ++q) {
@@ -1050,7 +973,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(AttendPara
             }
     }
     if (nparts && sub == 0 && lane < lp) {
-        const float w = final_weight(p, head0 + head, a.m, a.l);
+        const float w = final_weight(p.sinks, head0 + head, a.m, a.l);
         uint16_t* dst = p.out + b * p.o_token + (long long)(head0 + head) * p.o_head + d;
 #pragma unroll
         for (int k = 0; k < 2; ++k)

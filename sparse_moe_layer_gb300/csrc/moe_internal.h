@@ -144,6 +144,38 @@ struct AttendPlan {
     size_t cont, first, last, partial, total;  // workspace; total 0: none needed
 };
 
+struct TreeParams {
+    const uint16_t* q;  // [N, Hq, D]
+    uint16_t* out;
+    long long q_token, q_head, o_token, o_head;
+    KvCache cache;
+    const int32_t* table;  // [B, *] page ids, rows table_ld apart
+    long long table_ld;
+    const int32_t* lengths;  // [B] tokens of a sequence, its drafts included
+    const int32_t* starts;   // [B + 1] first draft of each sequence
+    const int32_t* parents;  // [N] each draft's, a number in its sequence, -1: none; null: the draft before
+    const float* sinks;      // [Hq] or null
+    int N, B, Hq, Hkv, D;
+    int num_pages, page_size, max_tokens;  // max_tokens: table columns * page_size
+    int window;                            // 0: none
+    float scale_log2;                      // |scale| log2(e), not 0
+    uint32_t q_sign;                       // the queries' sign bits to flip (a negative scale)
+    uint32_t* status;                      // error word or null
+    // set at launch
+    int group;      // query heads per key head
+    int page_shift; // log2(page_size), -1 if none
+    int whole;      // items are not cut
+    int runs;
+    int4* cont;      // [runs] item that the run continues (sequence, key head, row tile, 1), or w = 0
+    float* partial;  // [runs, 2] parts: rows (max, sum), then [D / 4, rows] four sums each
+};
+struct TreePlan {
+    int tiles;  // row tiles of 128 that a CTA takes together: 1 or 2
+    int whole, ctas;
+    size_t cont, partial, total;  // workspace; total 0: none needed
+};
+constexpr int kMaxDrafts = 256;  // of a sequence
+
 struct PermuteParams {
     const uint16_t* x;
     int T, H, Hp, E, k;
@@ -275,6 +307,10 @@ cudaError_t launch_compact_drafts(const CompactParams& p, int sms, cudaStream_t 
 void attend_plan(int B, int Hq, int Hkv, int D, bool e4m3, int most, int sms, AttendPlan* plan);
 cudaError_t launch_attend(const AttendParams& p, const AttendPlan& plan, int kv_dtype, bool fp16, void* workspace,
                           cudaStream_t st);
+// most: context tokens that a draft can see (its window, or the page table's columns)
+void tree_plan(int N, int B, int Hq, int Hkv, int D, bool e4m3, int most, int sms, TreePlan* plan);
+cudaError_t launch_tree(const TreeParams& p, const TreePlan& plan, int kv_dtype, bool fp16, void* workspace,
+                        cudaStream_t st);
 cudaError_t launch_permute_quant(const PermuteParams& p, cudaStream_t st);
 cudaError_t launch_combine(const float* part, int T, int H, int ldp, int k, uint16_t* out, int num_sms,
                            cudaStream_t st);
