@@ -12,8 +12,8 @@
 // A key is read once for all drafts and all query heads that share it, so the rows of
 // the products are the n x group (draft, head) pairs: 128 of them are the rows of a
 // tcgen05 tile.  S = Q K^T goes to tensor memory, where a thread has a whole row: no
-// exchange for maximum and sum.  Probabilities go back in 16 bits over the scores they
-// come from and are the first operand of P V, whose sums stay in tensor memory; they are
+// exchange for maximum and sum.  Probabilities go back in 16 bits, over the scores they
+// come from, or beside them, and are the first operand of P V, whose sums stay in tensor memory; they are
 // rescaled only when a row's maximum rises by more than 2^kSlack.
 //
 // One CTA: a warp that issues the products, four warps that copy keys and values by
@@ -60,8 +60,12 @@ struct TreeCfg {
     static constexpr int META_AT = RAW_AT + NR * RAW_STRIDE;
     static constexpr int ANC_AT = META_AT + META * META_BYTES;
     static constexpr int SMEM = ANC_AT + ANC + 1024;  // (aligned to 1024 in the kernel)
+    // tensor memory: two score buffers, the sums of each row tile, and probabilities (16 bits) in columns of
+    // their own where there are any left, else over the scores that they come from
     static constexpr int S_COLS = 2 * TT;
-    static constexpr int COLS = S_COLS + TILES * DP <= 256 ? 256 : 512;  // tensor memory
+    static constexpr int COLS = S_COLS + TILES * DP <= 256 ? 256 : 512;
+    static constexpr bool OVER = S_COLS + TILES * DP + TT > COLS;
+    static constexpr int P_AT = OVER ? 0 : S_COLS + TILES * DP, P_STEP = OVER ? TT : TT / 2;
     static constexpr int TPW = TT / kTreeLoaders;  // tokens of a loading warp
 };
 
@@ -255,83 +259,110 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES>::THREADS, TreeCfg<DP, K
     TreeSeg g;
 
     if (warp == kMmaWarp) {
-        if (lane == 0) {
-            // ------------------------------------------------ the products
-            constexpr uint32_t ID_S = idesc_f16_f32(F16, kTreeRows, TT, false);
-            const uint32_t id_o = idesc_f16_f32(F16, kTreeRows, p.D, true);
-            const int ksteps = p.D / 16;
-            int c = 0;  // buffers taken from the ring
-            uint32_t q_phase = 0, p_phase = 0;  // bit i: phase of row tile (score buffer) i
-            bool ok = true;
-            auto full = [&](int i) {
-                return mbar_wait(smem_u32(&full_bar[i % NB]), (uint32_t)(i / NB) & 1u, abort_p, p.status, kErrTimeoutMma);
-            };
-            auto scores = [&](int w, int buf, int kbuf) {
-                const uint32_t a = smem_s + C::Q_AT + w * C::Q_TILE, b = smem_s + C::KV_AT + (kbuf % NB) * C::KV_TILE;
-                for (int k = 0; k < ksteps; ++k)
-                    mma_bf16(tmem + buf * TT, smem_desc_sw128(a + (k >> 2) * kTreeRows * 128 + (k & 3) * 32),
-                             smem_desc_sw128(b + (k >> 2) * TT * 128 + (k & 3) * 32), ID_S, k != 0);
+        // ------------------------------------------------ the products
+        // (the warp stays together, one lane issues: what describes the operands is uniform)
+        constexpr uint32_t ID_S = idesc_f16_f32(F16, kTreeRows, TT, false);
+        const uint32_t id_o = idesc_f16_f32(F16, kTreeRows, p.D, true);
+        const int ksteps = p.D / 16;
+        const bool issuer = elect_one();
+        int c = 0;                          // buffers taken from the ring
+        uint32_t o_count[TILES] = {};       // products with values so far
+        uint32_t q_phase = 0, p_phase = 0;  // bit i: phase of row tile (score buffer) i
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t phase) {
+            const bool r = mbar_wait(smem_u32(bar), phase & 1u, abort_p, p.status, kErrTimeoutMma);
+            return __all_sync(kAllLanes, r) != 0;
+        };
+        auto full = [&](int i) { return wait(&full_bar[i % NB], i / NB); };
+        // descriptors: a start address in 16-byte units in the low bits, so steps are additions
+        const uint64_t q_desc = smem_desc_sw128(smem_s + C::Q_AT), k_desc = smem_desc_sw128(smem_s + C::KV_AT),
+                       v_desc = smem_desc_sw128_mn(smem_s + C::KV_AT, TT * 128);
+        auto scores = [&](int w, int buf, int kbuf) {
+            if (issuer) {
+                const uint64_t a = q_desc + w * (C::Q_TILE >> 4), b = k_desc + (kbuf % NB) * (C::KV_TILE >> 4);
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    if (k < ksteps)
+                        mma_bf16(tmem + buf * TT, a + (((k >> 2) * kTreeRows * 128 + (k & 3) * 32) >> 4),
+                                 b + (((k >> 2) * TT * 128 + (k & 3) * 32) >> 4), ID_S, k != 0);
                 mma_commit(smem_u32(&s_bar[buf]));
-            };
-            auto values = [&](int w, int buf, int vbuf, bool first) {
-                const uint32_t b = smem_s + C::KV_AT + (vbuf % NB) * C::KV_TILE;
+            }
+        };
+        auto values = [&](int w, int buf, int vbuf, bool first) {
+            if (issuer) {
+                const uint64_t b = v_desc + (vbuf % NB) * (C::KV_TILE >> 4);
+#pragma unroll
                 for (int k = 0; k < TT / 16; ++k)
-                    mma_16bit_tmem_a(tmem + C::S_COLS + w * DP, tmem + buf * TT + 8 * k,
-                                     smem_desc_sw128_mn(b + k * 2048, TT * 128), id_o, !(first && k == 0));
+                    mma_16bit_tmem_a(tmem + C::S_COLS + w * DP, tmem + C::P_AT + buf * C::P_STEP + 8 * k,
+                                     b + ((k * 2048) >> 4), id_o, k > 0 || !first);
                 mma_commit(smem_u32(&o_bar[w]));
-            };
-            auto probabilities = [&](int buf) {
-                const bool r = mbar_wait(smem_u32(&p_bar[buf]), (p_phase >> buf) & 1u, abort_p, p.status, kErrTimeoutMma);
-                p_phase ^= 1u << buf;
-                return r;
-            };
-            while (ok && walk.next(g)) {
-                const int act = TILES == 2 && g.s.n * p.group - g.rt * 2 * kTreeRows > kTreeRows ? 2 : 1;
-                for (int w = 0; w < act && ok; ++w) {
-                    ok = mbar_wait(smem_u32(&q_bar[w]), (q_phase >> w) & 1u, abort_p, p.status, kErrTimeoutMma);
+            }
+            ++o_count[w];
+        };
+        auto release = [&](int i) {
+            if (issuer) mma_commit(smem_u32(&empty_bar[i % NB]));
+        };
+        // Scores over probabilities: products of different accumulators keep no order, so the ones that read
+        // them are waited for.  (The phase before has passed: the row tile's threads waited for it.)
+        auto free_scores = [&](int w) { return !C::OVER || wait(&o_bar[w], o_count[w] - 1); };
+        auto probabilities = [&](int buf) {
+            const bool r = wait(&p_bar[buf], p_phase >> buf);
+            p_phase ^= 1u << buf;
+            return r;
+        };
+        while (ok && walk.next(g)) {
+            const int act = TILES == 2 && g.s.n * p.group - g.rt * 2 * kTreeRows > kTreeRows ? 2 : 1;
+#pragma unroll
+            for (int w = 0; w < TILES; ++w)
+                if (w < act && ok) {
+                    ok = wait(&q_bar[w], q_phase >> w);
                     q_phase ^= 1u << w;
                 }
-                if (!ok || !(ok = full(c))) break;
-                tc_fence_after();
-                for (int w = 0; w < act; ++w) scores(w, w, c);
-                mma_commit(smem_u32(&empty_bar[c % NB]));
-                for (int j = 0; j < g.n && ok; ++j, c += 2) {
-                    // ring: keys of tile j are buffer c, its values c + 1, the next keys c + 2
-                    const bool more = j + 1 < g.n;
-                    if constexpr (TILES == 1) {
-                        if (more) {
-                            if (!(ok = full(c + 2))) break;
-                            tc_fence_after();
-                            scores(0, (j + 1) & 1, c + 2);
-                            mma_commit(smem_u32(&empty_bar[(c + 2) % NB]));
-                        }
-                        ok = probabilities(j & 1) && full(c + 1);
+            if (!ok || !(ok = full(c))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int w = 0; w < TILES; ++w)
+                if (w < act) scores(w, w, c);
+            release(c);
+            for (int j = 0; j < g.n && ok; ++j, c += 2) {
+                // ring: keys of tile j are buffer c, its values c + 1, the next keys c + 2
+                const bool more = j + 1 < g.n;
+                if constexpr (TILES == 1) {
+                    if (more) {
+                        if (!(ok = full(c + 2) && (j == 0 || free_scores(0)))) break;
+                        tc_fence_after();
+                        scores(0, (j + 1) & 1, c + 2);
+                        release(c + 2);
+                    }
+                    ok = probabilities(j & 1) && full(c + 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    values(0, j & 1, c + 1, j == 0);
+                } else {
+#pragma unroll
+                    for (int w = 0; w < TILES; ++w) {
+                        if (w >= act) continue;
+                        ok = ok && probabilities(w) && (w > 0 || full(c + 1));
                         if (!ok) break;
                         tc_fence_after();
-                        values(0, j & 1, c + 1, j == 0);
-                    } else {
-                        for (int w = 0; w < act; ++w) {
-                            ok = probabilities(w) && (w > 0 || full(c + 1));
-                            if (!ok) break;
+                        values(w, w, c + 1, j == 0);
+                        if (more) {
+                            if (!(ok = (w > 0 || full(c + 2)) && free_scores(w))) break;
                             tc_fence_after();
-                            values(w, w, c + 1, j == 0);
-                            if (more) {
-                                if (w == 0 && !(ok = full(c + 2))) break;
-                                tc_fence_after();
-                                scores(w, w, c + 2);
-                            }
+                            scores(w, w, c + 2);
                         }
-                        if (!ok) break;
-                        if (more) mma_commit(smem_u32(&empty_bar[(c + 2) % NB]));
                     }
-                    mma_commit(smem_u32(&empty_bar[(c + 1) % NB]));
+                    if (!ok) break;
+                    if (more) release(c + 2);
                 }
+                release(c + 1);
             }
-            // every issued product has finished once this commit lands
-            mma_commit(smem_u32(&end_bar));
-            int dummy = 0;
-            mbar_wait(smem_u32(&end_bar), 0, &dummy, p.status, kErrTimeoutMma);
         }
+        // every issued product has finished once this commit lands
+        if (issuer) mma_commit(smem_u32(&end_bar));
+        int dummy = 0;
+        mbar_wait(smem_u32(&end_bar), 0, &dummy, p.status, kErrTimeoutMma);
+        __syncwarp();
     } else if (warp >= TILES * 4) {
         // ------------------------------------------------ keys and values
         constexpr int ES = E4M3 ? 1 : 2, CH = DP * ES / 16;  // 16-byte chunks of a token's head
@@ -399,7 +430,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES>::THREADS, TreeCfg<DP, K
         if constexpr (!E4M3) {
             // copies in flight behind the one issued last: a buffer is free again once the products that read
             // it are done, which wait for no copy but the next
-            constexpr int DEPTH = NB - 2;
+            constexpr int DEPTH = NB / 2;
             auto copy = [&](bool is_k) {
                 const uint8_t* base = static_cast<const uint8_t*>(is_k ? p.cache.k : p.cache.v) +
                                       (long long)h * (is_k ? p.cache.k_head : p.cache.v_head) * ES + ch * 16;
@@ -768,7 +799,13 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES>::THREADS, TreeCfg<DP, K
                             }
                         }
                     }
-                    // --- probabilities (e4m3: weights), rounded to 16 bits, over the scores ---
+                    // --- probabilities (e4m3: weights), rounded to 16 bits ---
+                    if (TILES == 2 && !C::OVER) {  // their columns are read by the products of the tile before
+                        reach();
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    const uint32_t t_p = tmem + C::P_AT + buf * C::P_STEP + lanes;
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int k = 0; k < TT / 32; ++k) {
@@ -793,7 +830,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES>::THREADS, TreeCfg<DP, K
                             x[i / 2] = pack2<F16>(e[0], e[1]);
                             x[i / 2 + 1] = pack2<F16>(e[2], e[3]);
                         }
-                        tmem_st16(t_s + 16 * k, x);
+                        tmem_st16(t_p + 16 * k, x);
                     }
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     tmem_st_wait();
