@@ -19,8 +19,9 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_gb300.so")
 BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["moe_api.cu", "moe_route.cu", "moe_gemm.cu", "moe_gemm_decode.cu", "moe_gemm_mx.cu", "moe_gate.cu", "moe_append.cu",
-           "moe_attend.cu", "moe_pages.cu", "moe_tree.cu"]
-HEADERS = ["moe_device.cuh", "moe_attend.cuh", "moe_internal.h", "moe_scan.cuh"]
+           "moe_attend.cu", "moe_pages.cu", "moe_tree.cu", "moe_tree_bf16.cu",
+           "moe_tree_fp16.cu", "moe_tree_e4m3.cu"]
+HEADERS = ["moe_device.cuh", "moe_attend.cuh", "moe_tree.cuh", "moe_internal.h", "moe_scan.cuh"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "-Xptxas", "-v"]
 

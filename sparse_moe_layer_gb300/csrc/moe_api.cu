@@ -132,6 +132,26 @@ bool make_map_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t col
     return r == CUDA_SUCCESS;
 }
 
+// The keys (or values) of a paged cache, [pages, heads, page, D] with strides in elements (0 for dims of
+// one): boxes of `tokens` tokens of a head, 64 values each in the 128-byte swizzle, or all D codes (e4m3).
+bool make_map_pages(CUtensorMap* m, const void* base, const moe_kv_cache* c, const long long* stride, uint32_t tokens) {
+    auto enc = encoder();
+    if (!enc) return false;
+    const bool e4m3 = c->dtype == MOE_E4M3;
+    const cuuint64_t el = e4m3 ? 1 : 2;
+    cuuint64_t dims[4] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->page_size, (cuuint64_t)c->kv_heads,
+                          (cuuint64_t)c->num_pages};
+    cuuint64_t strides[3] = {(cuuint64_t)stride[2] * el, (cuuint64_t)stride[1] * el, (cuuint64_t)stride[0] * el};
+    for (cuuint64_t& s : strides)
+        if (s == 0) s = 16;  // (never stepped)
+    cuuint32_t box[4] = {e4m3 ? (cuuint32_t)c->head_dim : 64u, tokens, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int num_sms() {
     static std::atomic<int> known[64];  // by device; a device's count does not change
     int dev = 0;
@@ -1013,7 +1033,7 @@ extern "C" size_t moe_tree_attention_workspace_size(int N, int B, int q_heads, i
     if (!tree_ok(N, B, q_heads, kv_heads, head_dim) || max_tokens < 1) return 0;
     if (cache_dtype != MOE_BF16 && cache_dtype != MOE_FP16 && cache_dtype != MOE_E4M3) return 0;
     TreePlan w;
-    tree_plan(N, B, q_heads, kv_heads, head_dim, cache_dtype == MOE_E4M3, max_tokens, num_sms(), &w);
+    tree_plan(N, B, q_heads, kv_heads, head_dim, cache_dtype == MOE_E4M3, 1, 0, max_tokens, num_sms(), &w);
     return w.total ? w.total : 256;
 }
 
@@ -1045,7 +1065,7 @@ extern "C" moe_status moe_tree_attention(const moe_kv_cache* cache, const void* 
          reinterpret_cast<uintptr_t>(sinks) | reinterpret_cast<uintptr_t>(status)) & 3u)
         return MOE_ERR_UNSUPPORTED;
     TreePlan w;
-    tree_plan(N, B, q_heads, cache->kv_heads, cache->head_dim, cache->dtype == MOE_E4M3,
+    tree_plan(N, B, q_heads, cache->kv_heads, cache->head_dim, cache->dtype == MOE_E4M3, cache->page_size, window,
               (int)(window > 0 && window < most ? window : most), num_sms(), &w);
     if (w.total && !workspace) return MOE_ERR_INVALID_ARG;
     if (workspace_bytes < w.total) return MOE_ERR_WORKSPACE;
@@ -1071,7 +1091,17 @@ extern "C" moe_status moe_tree_attention(const moe_kv_cache* cache, const void* 
     p.scale_log2 = fmaxf(fabsf(scale) * 1.4426950408889634f, 1.17549435e-38f);
     p.q_sign = scale < 0.f ? 0x80008000u : 0u;
     p.status = status;
-    return launch_tree(p, w, cache->dtype, dtype == MOE_FP16, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess
+    CUtensorMap tmK, tmV;
+    memset(&tmK, 0, sizeof(tmK));
+    memset(&tmV, 0, sizeof(tmV));
+    if (w.box) {
+        const long long ks[3] = {p.cache.k_page, p.cache.k_head, p.cache.k_token},
+                        vs[3] = {p.cache.v_page, p.cache.v_head, p.cache.v_token};
+        if (!make_map_pages(&tmK, cache->k, cache, ks, w.box) || !make_map_pages(&tmV, cache->v, cache, vs, w.box))
+            w.box = 0;  // strides beyond what a map holds
+    }
+    return launch_tree(tmK, tmV, p, w, cache->dtype, dtype == MOE_FP16, workspace, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }

@@ -164,13 +164,16 @@ struct TreeParams {
     // set at launch
     int group;      // query heads per key head
     int page_shift; // log2(page_size), -1 if none
+    int fp16;       // q and out are fp16, not bf16
     int whole;      // items are not cut
+    int box;        // tokens of a tensor-map copy, which lie on one page; 0: copies of 16 bytes by threads
     int runs;
     int4* cont;      // [runs] item that the run continues (sequence, key head, row tile, 1), or w = 0
     float* partial;  // [runs, 2] parts: rows (max, sum), then [D / 4, rows] four sums each
 };
 struct TreePlan {
     int tiles;  // row tiles of 128 that a CTA takes together: 1 or 2
+    int box;    // as in TreeParams
     int whole, ctas;
     size_t cont, partial, total;  // workspace; total 0: none needed
 };
@@ -308,9 +311,19 @@ void attend_plan(int B, int Hq, int Hkv, int D, bool e4m3, int most, int sms, At
 cudaError_t launch_attend(const AttendParams& p, const AttendPlan& plan, int kv_dtype, bool fp16, void* workspace,
                           cudaStream_t st);
 // most: context tokens that a draft can see (its window, or the page table's columns)
-void tree_plan(int N, int B, int Hq, int Hkv, int D, bool e4m3, int most, int sms, TreePlan* plan);
-cudaError_t launch_tree(const TreeParams& p, const TreePlan& plan, int kv_dtype, bool fp16, void* workspace,
-                        cudaStream_t st);
+void tree_plan(int N, int B, int Hq, int Hkv, int D, bool e4m3, int page_size, int window, int most, int sms,
+               TreePlan* plan);
+// tmK, tmV: with plan.box, maps of [pages, heads, page, D] with boxes of [1, 1, box, 64] (128-byte swizzle), for
+// e4m3 [1, 1, box, D] (none)
+cudaError_t launch_tree(const CUtensorMap& tmK, const CUtensorMap& tmV, const TreeParams& p, const TreePlan& plan,
+                        int kv_dtype, bool fp16, void* workspace, cudaStream_t st);
+// ... its kernel, by the cache's type
+cudaError_t launch_tree_bf16(const CUtensorMap& tmK, const CUtensorMap& tmV, const TreeParams& p, const TreePlan& w,
+                             cudaStream_t st);
+cudaError_t launch_tree_fp16(const CUtensorMap& tmK, const CUtensorMap& tmV, const TreeParams& p, const TreePlan& w,
+                             cudaStream_t st);
+cudaError_t launch_tree_e4m3(const CUtensorMap& tmK, const CUtensorMap& tmV, const TreeParams& p, const TreePlan& w,
+                             cudaStream_t st);
 cudaError_t launch_permute_quant(const PermuteParams& p, cudaStream_t st);
 cudaError_t launch_combine(const float* part, int T, int H, int ldp, int k, uint16_t* out, int num_sms,
                            cudaStream_t st);

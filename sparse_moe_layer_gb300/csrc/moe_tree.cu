@@ -1,899 +1,8 @@
-// Attention of a step's drafted tokens over a paged key-value cache: each sequence
-// has a few drafts that form a tree (or a chain) behind its context, their keys and
-// values already in the cache, and every draft sees the context, its ancestors and
-// itself ("GPT-OSS on Day 0", perplexity.ai hub blog: grouped heads, sink attention,
-// sliding windows).
-//
-//   draft i of n, depth d_i, context of c tokens: sees token t < c if t > c + d_i - window,
-//   and draft j (token c + j) if j is i or an ancestor and d_i - d_j < window
-//   o = sum_t p_t v_t / (sum_t p_t + 2^(sink log2 e - m)),  p_t = 2^(s_t - m),
-//   s_t = (q . k_t) scale log2 e
-//
-// A key is read once for all drafts and all query heads that share it, so the rows of
-// the products are the n x group (draft, head) pairs: 128 of them are the rows of a
-// tcgen05 tile.  S = Q K^T goes to tensor memory, where a thread has a whole row: no
-// exchange for maximum and sum.  Probabilities go back in 16 bits, over the scores they
-// come from, or beside them, and are the first operand of P V, whose sums stay in tensor memory; they are
-// rescaled only when a row's maximum rises by more than 2^kSlack.
-//
-// One CTA: a warp that issues the products, four warps that copy keys and values by
-// cp.async (any page size, strides; e4m3 codes become fp16 on the way from a raw ring),
-// and a warpgroup for each row tile.  One row tile: two CTAs an SM, tiles of 64 tokens,
-// two score buffers, so that the next scores are there when the exponentials of the
-// last are done.  Two row tiles (more than 128 rows): one CTA, tiles of 128 tokens, the two
-// tiles' products and exponentials alternate and share the keys and values in shared memory.
-//
-// The list of items (sequence, key head, row tiles) and their token tiles is cut into
-// equal runs, one per CTA; an item cut by a run's border leaves fp32 parts that a second,
-// dependent launch joins in a fixed order.
-#include "moe_attend.cuh"
-#include "moe_internal.h"
+// Attention of drafted tokens: how the work is split, the launches, and the join of cut items (moe_tree.cuh has
+// the kernel).
+#include "moe_tree.cuh"
 
 namespace moe {
-
-namespace {
-
-constexpr int kTreeRows = 128;  // rows of a tile
-constexpr int kTreeLoaders = 4; // warps
-constexpr int kMinTiles = 4;    // token tiles of a run, at least, where there are so many
-
-// KV: the cache's type; TILES: row tiles of a CTA.
-template <int DP, int KV, int TILES>
-struct TreeCfg {
-    static constexpr bool E4M3 = KV == kKvE4m3;
-    static constexpr int TT = TILES == 2 ? 128 : 64;  // tokens of a tile
-    static constexpr int CTAS = TILES == 2 || DP == 256 ? 1 : 2;
-    static constexpr int THREADS = TILES * kTreeRows + kTreeLoaders * 32 + 32;
-    static constexpr int Q_TILE = kTreeRows * DP * 2;
-    static constexpr int KV_TILE = TT * DP * 2;  // 16-bit keys (or values) of a token tile
-    // buffers of the ring (keys and values in turn), and of the raw codes' ring
-    static constexpr int NB = E4M3 ? (DP == 64 ? 6 : 3) : DP == 64 ? 10 : 4;
-    static constexpr int NR = !E4M3 ? 0 : DP == 64 ? 8 : 3;
-    static constexpr int RAW = TT * DP;
-    static constexpr int RAW_STRIDE = RAW + TT * 4 + 16;  // codes, scales, valid tokens of each loading warp
-    static constexpr int META = NB / 2 + 2;  // what the softmax knows of a tile: valid tokens, scales
-    static constexpr int META_BYTES = E4M3 ? 32 + 2 * TT * 4 : 32;
-    static constexpr int ANC = TILES * kTreeRows * (kMaxDrafts / 32) * 4;
-    static constexpr int Q_AT = 0;
-    static constexpr int KV_AT = TILES * Q_TILE;
-    static constexpr int RAW_AT = KV_AT + NB * KV_TILE;
-    static constexpr int META_AT = RAW_AT + NR * RAW_STRIDE;
-    static constexpr int ANC_AT = META_AT + META * META_BYTES;
-    static constexpr int SMEM = ANC_AT + ANC + 1024;  // (aligned to 1024 in the kernel)
-    // tensor memory: two score buffers, the sums of each row tile, and probabilities (16 bits) in columns of
-    // their own where there are any left, else over the scores that they come from
-    static constexpr int S_COLS = 2 * TT;
-    static constexpr int COLS = S_COLS + TILES * DP <= 256 ? 256 : 512;
-    static constexpr bool OVER = S_COLS + TILES * DP + TT > COLS;
-    static constexpr int P_AT = OVER ? 0 : S_COLS + TILES * DP, P_STEP = OVER ? TT : TT / 2;
-    static constexpr int TPW = TT / kTreeLoaders;  // tokens of a loading warp
-};
-
-struct TreeSeq {
-    int first;         // first row of q
-    int n, len, ctx;   // drafts, tokens, tokens before the drafts
-    int lo;            // first token that any draft sees
-    int start, ntiles; // first token of the first tile (a multiple of 16), token tiles
-    int rtiles;        // row tiles (of TILES * 128 rows)
-};
-
-template <int TT, int TILES>
-__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
-    TreeSeq s;
-    const int lo = __ldg(p.starts + b), hi = __ldg(p.starts + b + 1), raw = __ldg(p.lengths + b);
-    const bool fine = lo >= 0 && hi >= lo && hi <= p.N && hi - lo <= kMaxDrafts;
-    s.first = lo;
-    s.n = fine ? hi - lo : 0;
-    s.len = min(max(raw, 0), p.max_tokens);
-    s.ctx = max(s.len - s.n, 0);
-    if ((!fine || s.len != raw || s.len < s.n) && p.status) atomicOr(p.status, kErrBadIndex);
-    s.lo = p.window > 0 && s.ctx >= p.window ? s.ctx - p.window + 1 : 0;
-    s.start = s.lo & ~15;
-    s.ntiles = max(1, (int)((unsigned)(s.len - s.start + TT - 1) / TT));
-    s.rtiles = (s.n * p.group + TILES * kTreeRows - 1) / (TILES * kTreeRows);
-    return s;
-}
-
-// Where a run begins, and what it has: token tiles, or items where they are not cut.
-struct TreeWork {
-    int b, h, rt, tile;
-    long long rem;
-};
-// A part of an item: token tiles [tile, tile + n) of it.
-struct TreeSeg {
-    TreeSeq s;
-    int b, h, rt, tile, n;
-    bool starts, ends;
-};
-
-template <int TT, int TILES>
-struct TreeWalk {
-    const TreeParams& p;
-    TreeWork w;
-    TreeSeq s;
-    __device__ __forceinline__ TreeWalk(const TreeParams& p_, const TreeWork& w_) : p(p_), w(w_) {
-        if (w.rem > 0) s = tree_seq<TT, TILES>(p, w.b);
-    }
-    __device__ __forceinline__ bool next(TreeSeg& g) {
-        if (w.rem <= 0) return false;
-        const int left = s.ntiles - w.tile;
-        g.s = s;
-        g.b = w.b;
-        g.h = w.h;
-        g.rt = w.rt;
-        g.tile = w.tile;
-        g.n = p.whole || left < w.rem ? left : (int)w.rem;
-        g.starts = w.tile == 0;
-        g.ends = g.n == left;
-        w.rem -= p.whole ? 1 : g.n;
-        w.tile += g.n;
-        if (g.ends) {
-            w.tile = 0;
-            if (++w.rt == s.rtiles) {
-                w.rt = 0;
-                if (++w.h == p.Hkv) {
-                    w.h = 0;
-                    if (w.rem > 0) do s = tree_seq<TT, TILES>(p, ++w.b);
-                        while (s.rtiles == 0);
-                }
-            }
-        }
-        return true;
-    }
-};
-
-// Byte of 16-byte chunk c of row r in a block of `rows` rows: blocks of 64 values a row, 128-byte swizzle.
-__device__ __forceinline__ uint32_t tile_at(int rows, int r, int c) {
-    return (uint32_t)((c >> 3) * rows * 128 + r * 128 + ((c ^ r) & 7) * 16);
-}
-
-}  // namespace
-
-template <int DP, int KV, bool QF16, int TILES>
-__global__ void __launch_bounds__(TreeCfg<DP, KV, TILES>::THREADS, TreeCfg<DP, KV, TILES>::CTAS)
-    tree_kernel(TreeParams p) {
-    using C = TreeCfg<DP, KV, TILES>;
-    constexpr bool E4M3 = C::E4M3, F16 = KV != kKvBf16;
-    constexpr int TT = C::TT, NB = C::NB, THREADS = C::THREADS;
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full_bar[NB], empty_bar[NB], meta_bar[C::META], q_bar[TILES], s_bar[2], p_bar[2],
-        o_bar[TILES], end_bar;
-    __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag;
-    __shared__ TreeWork s_work;
-    __shared__ float s_qf[TILES][kTreeRows];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kMmaWarp = TILES * 4 + kTreeLoaders;
-    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const uint32_t smem_s = smem_u32(smem);
-    long long* s_pre = reinterpret_cast<long long*>(smem);  // [THREADS + 1], before the tiles come
-
-    if (tid == 0) {
-        for (int i = 0; i < NB; ++i) {
-            mbar_init(smem_u32(&full_bar[i]), kTreeLoaders);
-            mbar_init(smem_u32(&empty_bar[i]), 1);
-        }
-        for (int i = 0; i < C::META; ++i) mbar_init(smem_u32(&meta_bar[i]), kTreeLoaders);
-        for (int i = 0; i < TILES; ++i) {
-            mbar_init(smem_u32(&q_bar[i]), kTreeRows);
-            mbar_init(smem_u32(&o_bar[i]), 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&s_bar[i]), 1);
-            mbar_init(smem_u32(&p_bar[i]), 4);
-        }
-        mbar_init(smem_u32(&end_bar), 1);
-        abort_flag = 0;
-        fence_barrier_init();
-    }
-    if (warp == kMmaWarp) tmem_alloc(smem_u32(&tmem_slot), C::COLS);
-    pdl_wait();
-    pdl_allow_dependents();
-
-    // --- the run: each thread counts a slice of the sequences ---
-    const int slice = (p.B + THREADS - 1) / THREADS;
-    long long mine = 0;
-    for (int i = 0; i < slice; ++i) {
-        const int b = tid * slice + i;
-        if (b < p.B) {
-            const TreeSeq s = tree_seq<TT, TILES>(p, b);
-            mine += (long long)p.Hkv * s.rtiles * (p.whole ? 1 : s.ntiles);
-        }
-    }
-    s_pre[tid + 1] = mine;
-    if (tid == 0) s_pre[0] = 0;
-    __syncthreads();
-    if (warp == 0) {  // prefix sums, 32 at a time
-        long long before = 0;
-        for (int base = 0; base < THREADS; base += 32) {
-            long long v = s_pre[base + lane + 1];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(kAllLanes, v, o);
-                if (lane >= o) v += u;
-            }
-            v += before;
-            s_pre[base + lane + 1] = v;
-            before = __shfl_sync(kAllLanes, v, 31);
-        }
-        __syncwarp();
-        const long long total = before, least = p.whole ? 1 : kMinTiles;
-        const long long want = (total + least - 1) / least;
-        const int n = (int)(want < p.runs ? want : p.runs), run = blockIdx.x;
-        TreeWork w = {0, 0, 0, 0, 0};
-        if (run < n) {
-            const long long each = total / n, more = total - each * n;
-            long long u = each * run + more * run / n;
-            w.rem = each + more * (run + 1) / n - more * run / n;
-            int sl = 0;
-            for (int base = 0; base < THREADS; base += 32)
-                sl += __popc(__ballot_sync(kAllLanes, s_pre[base + lane + 1] <= u));
-            u -= s_pre[sl];
-            w.b = sl * slice;
-            while (true) {
-                const TreeSeq s = tree_seq<TT, TILES>(p, w.b);
-                const int nt = p.whole ? 1 : s.ntiles;
-                const long long here = (long long)p.Hkv * s.rtiles * nt;
-                if (u < here) {
-                    const int item = (int)(u / nt);
-                    w.tile = (int)(u - (long long)item * nt);
-                    w.h = item / s.rtiles;
-                    w.rt = item - w.h * s.rtiles;
-                    break;
-                }
-                u -= here;
-                ++w.b;
-            }
-        }
-        if (lane == 0) {
-            s_work = w;
-            if (!p.whole) p.cont[run] = make_int4(w.b, w.h, w.rt, w.tile > 0);
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_slot;
-    volatile int* abort_p = &abort_flag;
-    TreeWalk<TT, TILES> walk(p, s_work);
-    TreeSeg g;
-
-    if (warp == kMmaWarp) {
-        // ------------------------------------------------ the products
-        // (the warp stays together, one lane issues: what describes the operands is uniform)
-        constexpr uint32_t ID_S = idesc_f16_f32(F16, kTreeRows, TT, false);
-        const uint32_t id_o = idesc_f16_f32(F16, kTreeRows, p.D, true);
-        const int ksteps = p.D / 16;
-        const bool issuer = elect_one();
-        int c = 0;                          // buffers taken from the ring
-        uint32_t o_count[TILES] = {};       // products with values so far
-        uint32_t q_phase = 0, p_phase = 0;  // bit i: phase of row tile (score buffer) i
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t phase) {
-            const bool r = mbar_wait(smem_u32(bar), phase & 1u, abort_p, p.status, kErrTimeoutMma);
-            return __all_sync(kAllLanes, r) != 0;
-        };
-        auto full = [&](int i) { return wait(&full_bar[i % NB], i / NB); };
-        // descriptors: a start address in 16-byte units in the low bits, so steps are additions
-        const uint64_t q_desc = smem_desc_sw128(smem_s + C::Q_AT), k_desc = smem_desc_sw128(smem_s + C::KV_AT),
-                       v_desc = smem_desc_sw128_mn(smem_s + C::KV_AT, TT * 128);
-        auto scores = [&](int w, int buf, int kbuf) {
-            if (issuer) {
-                const uint64_t a = q_desc + w * (C::Q_TILE >> 4), b = k_desc + (kbuf % NB) * (C::KV_TILE >> 4);
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-                    if (k < ksteps)
-                        mma_bf16(tmem + buf * TT, a + (((k >> 2) * kTreeRows * 128 + (k & 3) * 32) >> 4),
-                                 b + (((k >> 2) * TT * 128 + (k & 3) * 32) >> 4), ID_S, k != 0);
-                mma_commit(smem_u32(&s_bar[buf]));
-            }
-        };
-        auto values = [&](int w, int buf, int vbuf, bool first) {
-            if (issuer) {
-                const uint64_t b = v_desc + (vbuf % NB) * (C::KV_TILE >> 4);
-#pragma unroll
-                for (int k = 0; k < TT / 16; ++k)
-                    mma_16bit_tmem_a(tmem + C::S_COLS + w * DP, tmem + C::P_AT + buf * C::P_STEP + 8 * k,
-                                     b + ((k * 2048) >> 4), id_o, k > 0 || !first);
-                mma_commit(smem_u32(&o_bar[w]));
-            }
-            ++o_count[w];
-        };
-        auto release = [&](int i) {
-            if (issuer) mma_commit(smem_u32(&empty_bar[i % NB]));
-        };
-        // Scores over probabilities: products of different accumulators keep no order, so the ones that read
-        // them are waited for.  (The phase before has passed: the row tile's threads waited for it.)
-        auto free_scores = [&](int w) { return !C::OVER || wait(&o_bar[w], o_count[w] - 1); };
-        auto probabilities = [&](int buf) {
-            const bool r = wait(&p_bar[buf], p_phase >> buf);
-            p_phase ^= 1u << buf;
-            return r;
-        };
-        while (ok && walk.next(g)) {
-            const int act = TILES == 2 && g.s.n * p.group - g.rt * 2 * kTreeRows > kTreeRows ? 2 : 1;
-#pragma unroll
-            for (int w = 0; w < TILES; ++w)
-                if (w < act && ok) {
-                    ok = wait(&q_bar[w], q_phase >> w);
-                    q_phase ^= 1u << w;
-                }
-            if (!ok || !(ok = full(c))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int w = 0; w < TILES; ++w)
-                if (w < act) scores(w, w, c);
-            release(c);
-            for (int j = 0; j < g.n && ok; ++j, c += 2) {
-                // ring: keys of tile j are buffer c, its values c + 1, the next keys c + 2
-                const bool more = j + 1 < g.n;
-                if constexpr (TILES == 1) {
-                    if (more) {
-                        if (!(ok = full(c + 2) && (j == 0 || free_scores(0)))) break;
-                        tc_fence_after();
-                        scores(0, (j + 1) & 1, c + 2);
-                        release(c + 2);
-                    }
-                    ok = probabilities(j & 1) && full(c + 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    values(0, j & 1, c + 1, j == 0);
-                } else {
-#pragma unroll
-                    for (int w = 0; w < TILES; ++w) {
-                        if (w >= act) continue;
-                        ok = ok && probabilities(w) && (w > 0 || full(c + 1));
-                        if (!ok) break;
-                        tc_fence_after();
-                        values(w, w, c + 1, j == 0);
-                        if (more) {
-                            if (!(ok = (w > 0 || full(c + 2)) && free_scores(w))) break;
-                            tc_fence_after();
-                            scores(w, w, c + 2);
-                        }
-                    }
-                    if (!ok) break;
-                    if (more) release(c + 2);
-                }
-                release(c + 1);
-            }
-        }
-        // every issued product has finished once this commit lands
-        if (issuer) mma_commit(smem_u32(&end_bar));
-        int dummy = 0;
-        mbar_wait(smem_u32(&end_bar), 0, &dummy, p.status, kErrTimeoutMma);
-        __syncwarp();
-    } else if (warp >= TILES * 4) {
-        // ------------------------------------------------ keys and values
-        constexpr int ES = E4M3 ? 1 : 2, CH = DP * ES / 16;  // 16-byte chunks of a token's head
-        constexpr int RPS = 32 / CH, STEPS = C::TPW / RPS;   // tokens of a step of the warp
-        const int lw = warp - TILES * 4, ch = lane % CH, r0 = lane / CH;
-        const bool in = ch * (16 / ES) < p.D;
-        const int lt = lane < C::TPW ? lane : 0;  // the lane's token (others: the first, unused)
-        int c = 0, raw = 0;                       // buffers filled, raw copies issued
-        int tiles = 0;                            // tiles begun: slots of what the softmax knows
-        bool ok = true;
-        int tile = 0;
-        struct Token {
-            int pid, off;
-            bool in;
-        };
-        // the lane's token of the tile at `tile` of g, its page looked up before the copies need it
-        auto fetch = [&]() {
-            Token t = {-1, 0, false};
-            const int tok = g.s.start + (g.tile + tile) * TT + lw * C::TPW + lt;
-            if (tok >= g.s.lo && tok < g.s.len) {
-                const int pi = p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_size;
-                t.off = tok - pi * p.page_size;
-                t.pid = __ldg(p.table + (long long)g.b * p.table_ld + pi);
-                t.in = true;
-            }
-            return t;
-        };
-        auto wait_empty = [&](int i) {
-            const bool r = i < NB || mbar_wait(smem_u32(&empty_bar[i % NB]), (uint32_t)(i / NB - 1) & 1u, abort_p, p.status,
-                                               kErrTimeoutProducer);
-            return __all_sync(kAllLanes, r) != 0;
-        };
-        // the copies of buffer i have landed (all lanes waited for theirs)
-        auto signal = [&](int i) {
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&full_bar[i % NB]));
-        };
-        auto meta = [&](int i) { return smem + C::META_AT + (i % C::META) * C::META_BYTES; };
-        bool any = walk.next(g);
-        Token next = {-1, 0, false};
-        if (any) next = fetch();
-        int h = 0;
-        long long k_off = 0, v_off = 0, s_off = 0;  // of the lane's token
-        uint32_t mask = 0;                          // valid tokens of the warp
-        auto begin_tile = [&]() {
-            Token t = next;
-            if (t.in && (uint32_t)t.pid >= (uint32_t)p.num_pages) {
-                if (p.status && lane < C::TPW) atomicOr(p.status, kErrBadIndex);
-                t.in = false;
-            }
-            mask = __ballot_sync(kAllLanes, t.in && lane < C::TPW);
-            h = g.h;
-            if (!t.in) t.pid = t.off = 0;
-            k_off = t.pid * p.cache.k_page + t.off * p.cache.k_token;
-            v_off = t.pid * p.cache.v_page + t.off * p.cache.v_token;
-            if (E4M3) s_off = t.pid * p.cache.s_page + t.off * p.cache.s_token;
-            // the next tile
-            if (++tile == g.n) {
-                tile = 0;
-                any = walk.next(g);
-            }
-            if (any) next = fetch();
-        };
-        if constexpr (!E4M3) {
-            // copies in flight behind the one issued last: a buffer is free again once the products that read
-            // it are done, which wait for no copy but the next
-            constexpr int DEPTH = NB / 2;
-            auto copy = [&](bool is_k) {
-                const uint8_t* base = static_cast<const uint8_t*>(is_k ? p.cache.k : p.cache.v) +
-                                      (long long)h * (is_k ? p.cache.k_head : p.cache.v_head) * ES + ch * 16;
-                const uint32_t dst = smem_s + C::KV_AT + (c % NB) * C::KV_TILE;
-                const long long off = is_k ? k_off : v_off;
-#pragma unroll
-                for (int i = 0; i < STEPS; ++i) {
-                    const int r = i * RPS + r0;
-                    const long long o = __shfl_sync(kAllLanes, off, r);
-                    if (in) cp_async16z(dst + tile_at(TT, lw * C::TPW + r, ch), base + o * ES, (mask >> r) & 1u);
-                }
-            };
-            auto step = [&](bool is_k) {
-                if (!wait_empty(c)) return false;
-                copy(is_k);
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                cp_async_wait<DEPTH>();
-                if (c >= DEPTH) signal(c - DEPTH);
-                ++c;
-                return true;
-            };
-            while (any) {
-                begin_tile();
-                if (lane == 0) reinterpret_cast<uint32_t*>(meta(tiles))[lw] = mask;
-                if (lane == 0) mbar_arrive(smem_u32(&meta_bar[tiles % C::META]));
-                ++tiles;
-                if (!(ok = step(true) && step(false))) break;
-            }
-            cp_async_wait<0>();
-            if (ok)
-                for (int i = max(0, c - DEPTH); i < c; ++i) signal(i);
-        } else {
-            // raw codes: a lane copies, and later converts, pieces of its own; slot layout [step][thread] 16 bytes
-            constexpr int NR = C::NR;
-            const int lt128 = lw * 32 + lane;
-            auto slot = [&](int i) { return smem + C::RAW_AT + (i % NR) * C::RAW_STRIDE; };
-            auto issue = [&](bool is_k) {
-                const uint8_t* base = static_cast<const uint8_t*>(is_k ? p.cache.k : p.cache.v) +
-                                      (long long)h * (is_k ? p.cache.k_head : p.cache.v_head) + ch * 16;
-                uint8_t* at = slot(raw);
-                const uint32_t dst = smem_u32(at);
-                const long long off = is_k ? k_off : v_off;
-#pragma unroll
-                for (int i = 0; i < STEPS; ++i) {
-                    const int r = i * RPS + r0;
-                    const long long o = __shfl_sync(kAllLanes, off, r);
-                    cp_async16z(dst + (i * 128 + lt128) * 16, in ? base + o : base - ch * 16, in && ((mask >> r) & 1u));
-                }
-                if (lane < C::TPW) {
-                    const float* sc = (is_k ? p.cache.k_scale : p.cache.v_scale) + (long long)h * p.cache.s_head;
-                    cp_async4z(dst + C::RAW + (lw * C::TPW + lane) * 4, sc + s_off, (mask >> lane) & 1u);
-                }
-                if (lane == 0) *reinterpret_cast<uint32_t*>(at + C::RAW + TT * 4 + lw * 4) = mask;
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                ++raw;
-            };
-            // buffer c from raw slot c
-            auto convert = [&](bool is_k) {
-                const uint8_t* at = slot(c);
-                const uint32_t dst = smem_s + C::KV_AT + (c % NB) * C::KV_TILE;
-                const int t = lw * C::TPW + lt;
-                float sc = *reinterpret_cast<const float*>(at + C::RAW + t * 4);
-                uint32_t some = 0;  // V: lanes' tokens with a value that is not 0
-#pragma unroll
-                for (int i = 0; i < STEPS; ++i) {
-                    const int r = i * RPS + r0;
-                    const uint4 v = *reinterpret_cast<const uint4*>(at + (i * 128 + lt128) * 16);
-                    if (in) {
-                        const uint32_t d = dst + tile_at(TT, lw * C::TPW + r, 2 * ch),
-                                       e = dst + tile_at(TT, lw * C::TPW + r, 2 * ch + 1);
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(d), "r"(e4m3x2_to_f16x2(v.x)),
-                                     "r"(e4m3x2_to_f16x2(v.x >> 16)), "r"(e4m3x2_to_f16x2(v.y)),
-                                     "r"(e4m3x2_to_f16x2(v.y >> 16))
-                                     : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(e), "r"(e4m3x2_to_f16x2(v.z)),
-                                     "r"(e4m3x2_to_f16x2(v.z >> 16)), "r"(e4m3x2_to_f16x2(v.w)),
-                                     "r"(e4m3x2_to_f16x2(v.w >> 16))
-                                     : "memory");
-                    }
-                    if (!is_k) {
-                        const uint32_t b =
-                            __ballot_sync(kAllLanes, in && ((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) != 0u);
-#pragma unroll
-                        for (int k = 0; k < RPS; ++k)
-                            some |= ((b >> (k * CH)) & (CH == 32 ? kAllLanes : (1u << (CH & 31)) - 1u)) ? 1u << (i * RPS + k) : 0u;
-                    }
-                }
-                uint8_t* m = meta(c >> 1);
-                float* scales = reinterpret_cast<float*>(m + 32) + (is_k ? 0 : TT);
-                // a head of zeros, which the append stores with a scale of 1 however small the others are,
-                // has no weight
-                if (!is_k && !((some >> lt) & 1u)) sc = 0.f;
-                if (lane < C::TPW) scales[t] = sc;
-                if (is_k) {
-                    if (lane == 0)
-                        reinterpret_cast<uint32_t*>(m)[lw] = *reinterpret_cast<const uint32_t*>(at + C::RAW + TT * 4 + lw * 4);
-                } else {
-                    float top = lane < C::TPW ? fabsf(sc) : 0.f;
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAllLanes, top, o));
-                    if (lane == 0) reinterpret_cast<float*>(m)[4 + lw] = top;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&meta_bar[(c >> 1) % C::META]));
-                }
-            };
-            bool is_k_raw = true;
-            auto issue_next = [&]() {  // an empty group where nothing is left
-                if (is_k_raw) {
-                    if (!any) {
-                        asm volatile("cp.async.commit_group;" ::: "memory");
-                        return;
-                    }
-                    begin_tile();
-                }
-                issue(is_k_raw);
-                is_k_raw = !is_k_raw;
-            };
-#pragma unroll 1
-            for (int i = 0; i < NR - 1; ++i) issue_next();
-#pragma unroll 1
-            while (c < raw) {
-                cp_async_wait<NR - 2>();
-                __syncwarp();
-                if (!(ok = wait_empty(c))) break;
-                convert((c & 1) == 0);
-                signal(c);  // (and the warp is done with the raw slot)
-                ++c;
-                issue_next();
-            }
-            cp_async_wait<0>();
-        }
-    } else {
-        // ------------------------------------------------ softmax: a thread has a row
-        const int w = warp >> 2, r = tid & (kTreeRows - 1);
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t t_o = tmem + C::S_COLS + w * DP + lanes;
-        uint32_t q_phase = 0, s_phase = 0, o_phase = 0;
-        int tiles = 0;
-        uint32_t* anc = reinterpret_cast<uint32_t*>(smem + C::ANC_AT) + w * kTreeRows + r;  // words 128 * TILES apart
-        bool ok = true;
-        while (ok && walk.next(g)) {
-            const int rows = g.s.n * p.group - (g.rt * TILES + w) * kTreeRows;  // of this tile
-            if (rows <= 0) {
-                tiles += g.n;
-                continue;
-            }
-            // --- the queries: the tile's rows, 16 bytes a lane ---
-            {
-                constexpr int LPR = DP / 8;  // lanes of a row
-                const int ch = r % LPR;
-#pragma unroll 4
-                for (int i = 0; i < LPR; ++i) {
-                    const int row = r / LPR + i * (kTreeRows / LPR);
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (row < rows && ch * 8 < p.D) {
-                        const int at = (g.rt * TILES + w) * kTreeRows + row, d = at / p.group;
-                        v = *reinterpret_cast<const uint4*>(p.q + (g.s.first + d) * p.q_token +
-                                                            (long long)(g.h * p.group + at - d * p.group) * p.q_head + ch * 8);
-                    }
-                    v.x ^= p.q_sign, v.y ^= p.q_sign, v.z ^= p.q_sign, v.w ^= p.q_sign;
-                    if constexpr (E4M3) {
-                        // the products run in fp16: each row is scaled by a power of two to below 2^15, so that
-                        // fp16 values, and bf16 values down to 2^-30 of the largest, are exact
-                        uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                        float a = 0.f;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 x = unpack2<QF16>(u[j]);
-                            a = fmaxf(a, fmaxf(fabsf(x.x), fabsf(x.y)));
-                        }
-#pragma unroll
-                        for (int o = LPR / 2; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kAllLanes, a, o));
-                        const uint32_t e = min(max(__float_as_uint(a) >> 23, 15u), 253u);
-                        const float f = __uint_as_float((268u - e) << 23);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 x = unpack2<QF16>(u[j]);
-                            u[j] = pack2<true>(x.x * f, x.y * f);
-                        }
-                        v = make_uint4(u[0], u[1], u[2], u[3]);
-                        // not 0, which would make NaN of a masked score
-                        if (ch == 0) s_qf[w][row] = fmaxf(p.scale_log2 * __uint_as_float((e - 14u) << 23), 0x1p-126f);
-                    }
-                    *reinterpret_cast<uint4*>(smem + C::Q_AT + w * C::Q_TILE + tile_at(kTreeRows, row, ch)) = v;
-                }
-                fence_async_shared();
-                mbar_arrive(smem_u32(&q_bar[w]));
-            }
-            // --- the row's place in the tree ---
-            const bool act = r < rows, warp_act = (r & ~31) < rows;
-            const int at = (g.rt * TILES + w) * kTreeRows + min(r, rows - 1), draft = at / p.group;
-            const int head = g.h * p.group + at - draft * p.group;
-            const bool sees_drafts = g.s.start + (long long)(g.tile + g.n) * TT > g.s.ctx;
-            int depth = draft;
-            if (p.parents && (sees_drafts || p.window > 0)) {
-                uint32_t bits[kMaxDrafts / 32];
-#pragma unroll
-                for (int k = 0; k < kMaxDrafts / 32; ++k) bits[k] = 0;
-                depth = -1;
-                for (int a = draft; a >= 0;) {
-                    ++depth;
-                    if (p.window <= 0 || depth < p.window) {
-#pragma unroll
-                        for (int k = 0; k < kMaxDrafts / 32; ++k)
-                            if (a >> 5 == k) bits[k] |= 1u << (a & 31);
-                    }
-                    const int up = __ldg(p.parents + g.s.first + a);
-                    if (up >= a || up < -1) {
-                        if (p.status) atomicOr(p.status, kErrBadIndex);
-                        break;
-                    }
-                    a = up;
-                }
-#pragma unroll
-                for (int k = 0; k < kMaxDrafts / 32; ++k) anc[k * TILES * kTreeRows] = bits[k];
-            }
-            // the first token that the row sees of the context (of all, in a chain)
-            const int since = p.window > 0 ? max(g.s.ctx + depth - p.window + 1, 0) : 0;
-            ok = __all_sync(kAllLanes, mbar_wait(smem_u32(&q_bar[w]), q_phase, abort_p, p.status, kErrTimeoutEpilogue));
-            q_phase ^= 1u;
-            if (!ok) break;
-            const float qf = E4M3 ? s_qf[w][r] : p.scale_log2;  // positive factor of the scores
-
-            float m = -INFINITY, l = 0.f;          // largest score (before qf) that the sums know, sum
-            float base = E4M3 ? kNoWeights : 0.f;  // power of two that sums are about
-#pragma unroll 1
-            for (int j = 0; j < g.n; ++j, ++tiles) {
-                const int buf = TILES == 2 ? w : j & 1;
-                ok = __all_sync(kAllLanes, mbar_wait(smem_u32(&meta_bar[tiles % C::META]), (uint32_t)(tiles / C::META) & 1u,
-                                                     abort_p, p.status, kErrTimeoutEpilogue) &&
-                                               mbar_wait(smem_u32(&s_bar[buf]), (s_phase >> buf) & 1u, abort_p, p.status,
-                                                         kErrTimeoutEpilogue));
-                s_phase ^= 1u << buf;
-                if (!ok) break;
-                tc_fence_after();
-                // the products of the tile before have reached the accumulators (each phase is waited for: a
-                // parity tells only neighbours apart)
-                bool reached = j == 0;
-                auto reach = [&]() {
-                    if (!reached)
-                        ok = __all_sync(kAllLanes, mbar_wait(smem_u32(&o_bar[w]), o_phase ^ 1u, abort_p, p.status,
-                                                             kErrTimeoutEpilogue));
-                    reached = true;
-                };
-                if (warp_act) {
-                    const uint8_t* meta = smem + C::META_AT + (tiles % C::META) * C::META_BYTES;
-                    const uint32_t t_s = tmem + buf * TT + lanes;
-                    // --- which of the tile's tokens the row sees ---
-                    const int t0 = g.s.start + (g.tile + j) * TT;
-                    uint32_t see[TT / 32];
-                    bool all = true;
-#pragma unroll
-                    for (int k = 0; k < TT / 32; ++k) {
-                        const uint32_t* v = reinterpret_cast<const uint32_t*>(meta);
-                        see[k] = C::TPW == 32 ? v[k] : v[2 * k] | v[2 * k + 1] << 16;
-                        all = all && see[k] == kAllLanes;
-                    }
-                    const bool masked = g.s.ctx - t0 < TT || !all || __any_sync(kAllLanes, since > t0);
-                    if (masked) {
-                        // bits lo and on of 32
-                        auto from = [](int lo) { return lo <= 0 ? kAllLanes : lo >= 32 ? 0u : kAllLanes << lo; };
-#pragma unroll
-                        for (int k = 0; k < TT / 32; ++k) {
-                            const int t = t0 + 32 * k, past = g.s.ctx - t;  // bits from `past` on are drafts
-                            uint32_t of = from(since - t);
-                            if (past < 32) {
-                                if (p.parents) {
-                                    const int o = -past;  // draft of bit 0
-                                    uint32_t d = 0;
-                                    if (o < 0) {
-                                        d = anc[0] << -o;
-                                    } else if (o < kMaxDrafts) {
-                                        const uint32_t lo = anc[(o >> 5) * TILES * kTreeRows];
-                                        const uint32_t hi =
-                                            o < kMaxDrafts - 32 ? anc[((o >> 5) + 1) * TILES * kTreeRows] : 0u;
-                                        d = __funnelshift_r(lo, hi, o & 31);
-                                    }
-                                    const uint32_t drafts = from(past);
-                                    of = (of & ~drafts) | (d & drafts);
-                                } else {
-                                    of &= ~from(past + draft + 1);
-                                }
-                            }
-                            see[k] &= of;
-                        }
-                    }
-                    // --- the scores, 32 at a time ---
-                    const float* scales = reinterpret_cast<const float*>(meta + 32);
-                    auto scores = [&](int k, float (&s)[32]) {
-                        uint32_t x[32];
-                        tmem_ld32(t_s + 32 * k, x);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(x[i]);
-                        if constexpr (E4M3) {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 f = *reinterpret_cast<const float4*>(scales + 32 * k + i);
-                                s[i] *= f.x;
-                                s[i + 1] *= f.y;
-                                s[i + 2] *= f.z;
-                                s[i + 3] *= f.w;
-                            }
-                        }
-                        if (masked) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (!((see[k] >> i) & 1u)) s[i] = -INFINITY;
-                        }
-                    };
-                    float top = E4M3 ? -INFINITY : m;
-#pragma unroll
-                    for (int k = 0; k < TT / 32; ++k) {
-                        float s[32];
-                        scores(k, s);
-                        float a = fmaxf(s[0], s[1]), b = fmaxf(s[2], s[3]);
-#pragma unroll
-                        for (int i = 4; i < 32; i += 4) {
-                            a = fmaxf(a, fmaxf(s[i], s[i + 1]));
-                            b = fmaxf(b, fmaxf(s[i + 2], s[i + 3]));
-                        }
-                        top = fmaxf(top, fmaxf(a, b));
-                    }
-                    // --- what the sums are about; seldom moved (see kSlack, kNewWeight) ---
-                    float f = 1.f;  // sums' factor
-                    bool moved = false;
-                    if constexpr (!E4M3) {
-                        if ((top - m) * qf > kSlack) {  // (NaN, both -inf: no)
-                            const float n = top * qf;
-                            f = ex2_approx(m * qf - n);
-                            base = n - kLift<KV>;
-                            m = top;
-                            moved = true;
-                        }
-                    } else {
-                        m = fmaxf(m, top);
-                        const float* vm = reinterpret_cast<const float*>(meta) + 4;
-                        const float vmax = fmaxf(kLeastScale, fmaxf(fmaxf(vm[0], vm[1]), fmaxf(vm[2], vm[3])));
-                        const bool over = fmaf(top, qf, -base) > kMostWeight - __log2f(vmax);
-                        if (__any_sync(kAllLanes, over)) {
-                            float best = -INFINITY;  // of the weights, in powers of two
-                            for (int k = 0; k < TT / 32; ++k) {
-                                float s[32];
-                                scores(k, s);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    best = fmaxf(best, fmaf(s[i], qf, __log2f(fabsf(scales[TT + 32 * k + i]))));
-                            }
-                            const float n = fmaxf(base, fmaxf(best - kNewWeight, m * qf - kMostLift));
-                            f = ex2_approx(base - n);
-                            base = n;
-                            moved = true;
-                        }
-                    }
-                    if (__any_sync(kAllLanes, moved)) {
-                        l *= f;
-                        if (j > 0) {
-                            reach();
-                            if (!ok) break;
-                            tc_fence_after();
-                            for (int d = 0; d < p.D; d += 16) {
-                                uint32_t x[16];
-                                tmem_ld16(t_o + d, x);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                                tmem_st16(t_o + d, x);
-                            }
-                        }
-                    }
-                    // --- probabilities (e4m3: weights), rounded to 16 bits ---
-                    if (TILES == 2 && !C::OVER) {  // their columns are read by the products of the tile before
-                        reach();
-                        if (!ok) break;
-                        tc_fence_after();
-                    }
-                    const uint32_t t_p = tmem + C::P_AT + buf * C::P_STEP + lanes;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int k = 0; k < TT / 32; ++k) {
-                        float s[32];
-                        scores(k, s);
-                        uint32_t x[16];
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            float e[4];
-#pragma unroll
-                            for (int n = 0; n < 4; ++n) {
-                                e[n] = ex2_approx(fmaf(s[i + n], qf, -base));
-                                sum[n] += e[n];
-                            }
-                            if constexpr (E4M3) {
-                                const float4 v = *reinterpret_cast<const float4*>(scales + TT + 32 * k + i);
-                                e[0] *= v.x;
-                                e[1] *= v.y;
-                                e[2] *= v.z;
-                                e[3] *= v.w;
-                            }
-                            x[i / 2] = pack2<F16>(e[0], e[1]);
-                            x[i / 2 + 1] = pack2<F16>(e[2], e[3]);
-                        }
-                        tmem_st16(t_p + 16 * k, x);
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tmem_st_wait();
-                    tc_fence_before();
-                }
-                reach();
-                if (!ok) break;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&p_bar[buf]));
-                o_phase ^= 1u;  // the phase of this tile's products
-            }
-            if (!ok) break;
-            ok = __all_sync(kAllLanes, mbar_wait(smem_u32(&o_bar[w]), o_phase ^ 1u, abort_p, p.status, kErrTimeoutEpilogue));
-            if (!ok) break;
-            tc_fence_after();
-            // --- the row, or the run's part of it ---
-            if (warp_act) {
-                m = m * qf - kLift<KV>;  // in powers of two, what the sums are about
-                const float f = !E4M3 ? 1.f : m == -INFINITY ? 0.f : ex2_approx(base - m);
-                l *= f;
-                const bool done = p.whole || (g.starts && g.ends);
-                if (done) {
-                    const float fw = final_weight(p.sinks, head, m, l) * f;
-                    uint16_t* dst = p.out + (g.s.first + draft) * p.o_token + (long long)head * p.o_head;
-                    for (int d = 0; d < p.D; d += 16) {
-                        uint32_t x[16], y[8];
-                        tmem_ld16(t_o + d, x);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            y[i] = pack2<QF16>(__uint_as_float(x[2 * i]) * fw, __uint_as_float(x[2 * i + 1]) * fw);
-                        if (act) {
-                            *reinterpret_cast<uint4*>(dst + d) = make_uint4(y[0], y[1], y[2], y[3]);
-                            *reinterpret_cast<uint4*>(dst + d + 8) = make_uint4(y[4], y[5], y[6], y[7]);
-                        }
-                    }
-                } else {
-                    constexpr int ROWS = TILES * kTreeRows;
-                    float* part = p.partial + ((long long)blockIdx.x * 2 + (g.starts ? 1 : 0)) * (ROWS * (p.D + 2));
-                    if (act) reinterpret_cast<float2*>(part)[w * kTreeRows + r] = make_float2(m, l);
-                    float4* sums = reinterpret_cast<float4*>(part + 2 * ROWS) + w * kTreeRows + r;
-                    for (int d = 0; d < p.D; d += 16) {
-                        uint32_t x[16];
-                        tmem_ld16(t_o + d, x);
-                        if (act) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                sums[(d / 4 + i) * ROWS] =
-                                    make_float4(__uint_as_float(x[4 * i]) * f, __uint_as_float(x[4 * i + 1]) * f,
-                                                __uint_as_float(x[4 * i + 2]) * f, __uint_as_float(x[4 * i + 3]) * f);
-                        }
-                    }
-                }
-            }
-            tc_fence_before();
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == kMmaWarp) {
-        tc_fence_after();
-        tmem_dealloc(tmem, C::COLS);
-    }
-}
 
 // Joins the parts of items cut by a run's border.  blockIdx.x: a run that continues an
 // item as the first to do so; blockIdx.y: 32 rows, one a lane; a warp has every 8th
@@ -948,46 +57,29 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(TreePara
     }
 }
 
-namespace {
-
-template <int DP, int KV, bool QF16, int TILES>
-cudaError_t launch_tree_t(const TreeParams& p, const TreePlan& w, cudaStream_t st) {
-    using C = TreeCfg<DP, KV, TILES>;
-    // (a CTA's fixed arrays and what the system keeps of its shared memory: 1 KB each)
-    static_assert((C::SMEM + 2048) * C::CTAS <= 228 * 1024, "shared memory of the resident CTAs");
-    static_assert(C::S_COLS + TILES * DP <= C::COLS && C::COLS * C::CTAS <= 512, "tensor memory");
-    const auto kernel = tree_kernel<DP, KV, QF16, TILES>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(w.ctas), dim3(C::THREADS), C::SMEM, st, p);
-}
-template <int KV, bool QF16>
-cudaError_t launch_tree_d(const TreeParams& p, const TreePlan& w, cudaStream_t st) {
-    if (p.D <= 64)
-        return w.tiles == 2 ? launch_tree_t<64, KV, QF16, 2>(p, w, st) : launch_tree_t<64, KV, QF16, 1>(p, w, st);
-    if (p.D <= 128)
-        return w.tiles == 2 ? launch_tree_t<128, KV, QF16, 2>(p, w, st) : launch_tree_t<128, KV, QF16, 1>(p, w, st);
-    return launch_tree_t<256, KV, QF16, 1>(p, w, st);
-}
-
-}  // namespace
-
-void tree_plan(int N, int B, int Hq, int Hkv, int D, bool e4m3, int most, int sms, TreePlan* w) {
-    (void)e4m3;
+void tree_plan(int N, int B, int Hq, int Hkv, int D, bool e4m3, int page_size, int window, int most, int sms,
+               TreePlan* w) {
     const long long rows = ((long long)N * (Hq / Hkv) + B - 1) / B;  // of a sequence and key head, on average
     w->tiles = D <= 128 && rows > kTreeRows ? 2 : 1;
     w->ctas = w->tiles == 2 || D > 128 ? sms : 2 * sms;
     w->whole = 0;
-    (void)most;
+    (void)most, (void)e4m3;
+    // pieces that divide a page, and tiles, which start at a multiple of 16 in a window
+    const int largest = window > 0 ? 16 : w->tiles == 2 ? 128 : 64;
+    w->box = page_size & -page_size;
+    if (w->box > largest) w->box = largest;
+    if (w->box < 8) w->box = 0;
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     w->cont = 0;
     w->partial = up((size_t)w->ctas * 16);
     w->total = w->whole ? 0 : w->partial + (size_t)w->ctas * 2 * w->tiles * kTreeRows * (D + 2) * 4;
 }
 
-cudaError_t launch_tree(const TreeParams& p_in, const TreePlan& w, int kv_dtype, bool fp16, void* workspace,
-                        cudaStream_t st) {
+cudaError_t launch_tree(const CUtensorMap& tmK, const CUtensorMap& tmV, const TreeParams& p_in, const TreePlan& w,
+                        int kv_dtype, bool fp16, void* workspace, cudaStream_t st) {
     TreeParams p = p_in;
+    p.box = w.box;
+    p.fp16 = fp16;
     p.group = p.Hq / p.Hkv;
     p.whole = w.whole;
     p.runs = w.ctas;
@@ -1001,9 +93,9 @@ cudaError_t launch_tree(const TreeParams& p_in, const TreePlan& w, int kv_dtype,
     }
     cudaError_t e;
     if (kv_dtype == kDtE4m3)
-        e = fp16 ? launch_tree_d<kKvE4m3, true>(p, w, st) : launch_tree_d<kKvE4m3, false>(p, w, st);
+        e = launch_tree_e4m3(tmK, tmV, p, w, st);
     else
-        e = fp16 ? launch_tree_d<kKvFp16, true>(p, w, st) : launch_tree_d<kKvBf16, false>(p, w, st);
+        e = fp16 ? launch_tree_fp16(tmK, tmV, p, w, st) : launch_tree_bf16(tmK, tmV, p, w, st);
     if (e != cudaSuccess || w.whole || p.runs < 2) return e;
     const int rows = w.tiles * kTreeRows;
     const dim3 grid(p.runs - 1, rows / 32), block(kTreeJoinWarps * 32);
