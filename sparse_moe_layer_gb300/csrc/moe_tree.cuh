@@ -27,6 +27,8 @@
 // equal runs, one per CTA; an item cut by a run's border leaves fp32 parts that a second,
 // dependent launch joins in a fixed order.
 #pragma once
+#include <type_traits>
+
 #include "moe_attend.cuh"
 #include "moe_internal.h"
 
@@ -68,9 +70,8 @@ struct TreeCfg {
     static constexpr int COLS = S_COLS + TILES * DP <= 256 ? 256 : 512;
     static constexpr bool OVER = S_COLS + TILES * DP + TT > COLS;
     static constexpr int P_AT = OVER ? 0 : S_COLS + TILES * DP, P_STEP = OVER ? TT : TT / 2;
-    // the next 32 scores are on their way while the last are worked on (two sets of registers: without loading
-    // warps a thread has 168)
-    static constexpr bool AHEAD = LOADERS == 0;
+    // scores that a thread works on at a time (with loading warps it has 128 registers, without 168)
+    static constexpr int WIDE = LOADERS ? 32 : 64;
 };
 
 struct TreeSeq {
@@ -164,11 +165,13 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
     constexpr int kFillers = C::LOADERS ? C::LOADERS : 1;  // arrivals that fill a buffer (and its tokens' slot)
     extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[NB], empty_bar[NB], meta_bar[C::META], q_bar[TILES], s_bar[2], p_bar[2],
-        o_bar[TILES], end_bar, raw_full_bar[NR ? NR : 1], raw_empty_bar[NR ? NR : 1];
+        o_bar[TILES], end_bar, raw_full_bar[NR ? NR : 1], raw_empty_bar[NR ? NR : 1], x_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ TreeWork s_work;
     __shared__ float s_qf[TILES][kTreeRows];
+    __shared__ int16_t s_up[TILES][kMaxDrafts];  // parents
+    __shared__ float2 s_ml[TILES == 1 ? kTreeRows : 1];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t smem_s = smem_u32(smem);
@@ -193,6 +196,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             mbar_init(smem_u32(&p_bar[i]), 4);
         }
         mbar_init(smem_u32(&end_bar), 1);
+        mbar_init(smem_u32(&x_bar), kTreeRows);
         abort_flag = 0;
         fence_barrier_init();
     }
@@ -688,7 +692,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
         const int w = warp >> 2, r = tid & (kTreeRows - 1);
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_o = tmem + C::S_COLS + w * DP + lanes;
-        uint32_t q_phase = 0, s_phase = 0, o_phase = 0;
+        uint32_t q_phase = 0, s_phase = 0, o_phase = 0, x_phase = 0;
         int tiles = 0;
         uint32_t* anc = reinterpret_cast<uint32_t*>(smem + C::ANC_AT) + w * kTreeRows + r;  // words 128 * TILES apart
         bool ok = true;
@@ -696,27 +700,45 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             const bool r = mbar_wait(smem_u32(bar), phase & 1u, abort_p, p.status, kErrTimeoutEpilogue);
             return __all_sync(kAllLanes, r) != 0;
         };
+        // all of the row tile's threads (one row tile) have come so far
+        auto meet = [&]() {
+            mbar_arrive(smem_u32(&x_bar));
+            x_phase ^= 1u;
+            return wait(&x_bar, x_phase ^ 1u);
+        };
         while (ok && walk.next(g)) {
             const int rows = g.s.n * p.group - (g.rt * TILES + w) * kTreeRows;  // of this tile
             if (rows <= 0) {
                 tiles += g.n;
                 continue;
             }
-            // --- the queries: the tile's rows, 16 bytes a lane ---
+            // Few rows stand several times in the tile, and each copy's warps take a part of the tokens (with
+            // sums of their own that meet at the end): the exponentials use all four schedulers.
+            const int rep = TILES == 2 || rows > 64 ? 1 : rows > 32 ? 2 : 4;
+            const int fold = kTreeRows / rep - 1, lr = r & fold;  // the thread's row
+            const int cols = TT / rep, col0 = r / (fold + 1) * cols;
+            // --- the queries: the tile's rows, 16 bytes a lane; the parents ---
             {
+                const bool tree = p.parents != nullptr;
+                int up[2] = {-1, -1};
+                if (tree) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (r + i * kTreeRows < g.s.n) up[i] = __ldg(p.parents + g.s.first + r + i * kTreeRows);
+                }
                 constexpr int LPR = DP / 8, RPI = kTreeRows / LPR;  // lanes of a row, rows of a round
-                constexpr int BATCH = C::AHEAD ? 8 : 4;             // rounds in flight
+                constexpr int BATCH = C::LOADERS ? 4 : 8;           // rounds in flight
                 const int ch = r % LPR;
 #pragma unroll
                 for (int i0 = 0; i0 < LPR; i0 += BATCH) {
-                    if (i0 * RPI >= rows) break;  // rows past the last have any values
+                    if (rep == 1 && i0 * RPI >= rows) break;  // rows past the last have any values
                     uint4 q[BATCH];
 #pragma unroll
                     for (int i = 0; i < BATCH; ++i) {
                         const int row = r / LPR + (i0 + i) * RPI;
                         q[i] = make_uint4(0, 0, 0, 0);
-                        if (row < rows && ch * 8 < p.D) {
-                            const int at = (g.rt * TILES + w) * kTreeRows + row, d = at / p.group;
+                        if (ch * 8 < p.D && (row & fold) < rows) {
+                            const int at = (g.rt * TILES + w) * kTreeRows + (row & fold), d = at / p.group;
                             q[i] = *reinterpret_cast<const uint4*>(
                                 p.q + (g.s.first + d) * p.q_token +
                                 (long long)(g.h * p.group + at - d * p.group) * p.q_head + ch * 8);
@@ -754,46 +776,55 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                         *reinterpret_cast<uint4*>(smem + C::Q_AT + w * C::Q_TILE + tile_at(kTreeRows, row, ch)) = v;
                     }
                 }
+                if (tree) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int d = r + i * kTreeRows;
+                        if (d < g.s.n && (up[i] >= d || up[i] < -1)) {
+                            if (p.status) atomicOr(p.status, kErrBadIndex);
+                            up[i] = -1;
+                        }
+                        s_up[w][d] = (int16_t)up[i];
+                    }
+                }
                 fence_async_shared();
                 mbar_arrive(smem_u32(&q_bar[w]));
             }
             // --- the row's place in the tree ---
-            const bool act = r < rows, warp_act = (r & ~31) < rows;
-            const int at = (g.rt * TILES + w) * kTreeRows + min(r, rows - 1), draft = at / p.group;
+            const bool act = lr < rows, warp_act = (lr & ~31) < rows;
+            const int at = (g.rt * TILES + w) * kTreeRows + min(lr, rows - 1), draft = at / p.group;
             const int head = g.h * p.group + at - draft * p.group;
             const bool sees_drafts = g.s.start + (long long)(g.tile + g.n) * TT > g.s.ctx;
+            if (!(ok = wait(&q_bar[w], q_phase))) break;
+            q_phase ^= 1u;
             int depth = draft;
             if (p.parents && (sees_drafts || p.window > 0)) {
                 uint32_t bits[kMaxDrafts / 32];
 #pragma unroll
                 for (int k = 0; k < kMaxDrafts / 32; ++k) bits[k] = 0;
                 depth = -1;
-                for (int a = draft; a >= 0;) {
+                for (int a = draft; a >= 0; a = s_up[w][a]) {
                     ++depth;
                     if (p.window <= 0 || depth < p.window) {
 #pragma unroll
                         for (int k = 0; k < kMaxDrafts / 32; ++k)
                             if (a >> 5 == k) bits[k] |= 1u << (a & 31);
                     }
-                    const int up = __ldg(p.parents + g.s.first + a);
-                    if (up >= a || up < -1) {
-                        if (p.status) atomicOr(p.status, kErrBadIndex);
-                        break;
-                    }
-                    a = up;
                 }
 #pragma unroll
                 for (int k = 0; k < kMaxDrafts / 32; ++k) anc[k * TILES * kTreeRows] = bits[k];
             }
             // the first token that the row sees of the context (of all, in a chain)
             const int since = p.window > 0 ? max(g.s.ctx + depth - p.window + 1, 0) : 0;
-            ok = wait(&q_bar[w], q_phase);
-            q_phase ^= 1u;
-            if (!ok) break;
             const float qf = E4M3 ? s_qf[w][r] : p.scale_log2;  // positive factor of the scores
+            if (!C::OVER && rep > 1) {  // probabilities of the other copies' tokens
+                const uint32_t z[16] = {};
+                for (int k = 0; k < TT; k += 16) tmem_st16(tmem + C::P_AT + lanes + k, z);
+                tmem_st_wait();
+            }
 
             float m = -INFINITY;  // e4m3: largest score (before qf)
-            // the power of two that sums are about, a whole number; their two halves
+            // the power of two that sums are about; their two halves
             float base = kNoWeights;
             uint64_t sum = 0;
 #pragma unroll 1
@@ -811,13 +842,9 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                     reached = true;
                 };
                 const uint8_t* meta = smem + C::META_AT + (tiles % C::META) * C::META_BYTES;
-                uint32_t see[TT / 32];  // the tile's tokens that the row sees
-                bool all = true;
+                bool all = true;  // the tile's tokens are there
 #pragma unroll
-                for (int k = 0; k < TT / 32; ++k) {
-                    see[k] = reinterpret_cast<const uint32_t*>(meta)[k];
-                    all = all && see[k] == kAllLanes;
-                }
+                for (int k = 0; k < TT / 32; ++k) all = all && reinterpret_cast<const uint32_t*>(meta)[k] == kAllLanes;
                 if (TMA && !E4M3 && !all && w == 0) {
                     // a copied piece may hold anything behind the last token (before the first, on a bad page):
                     // such values become 0, whose product with a probability of 0 is 0
@@ -831,36 +858,8 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 }
                 if (warp_act) {
                     const uint32_t t_s = tmem + buf * TT + lanes, t_p = tmem + C::P_AT + buf * C::P_STEP + lanes;
-                    uint32_t x[C::AHEAD ? 2 : 1][32];
-                    if (C::AHEAD) tmem_ld32_issue(t_s, x[0]);
                     const int t0 = g.s.start + (g.tile + j) * TT;
                     const bool masked = g.s.ctx - t0 < TT || !all || __any_sync(kAllLanes, since > t0);
-                    if (masked) {
-#pragma unroll
-                        for (int k = 0; k < TT / 32; ++k) {
-                            const int t = t0 + 32 * k, past = g.s.ctx - t;  // bits from `past` on are drafts
-                            uint32_t of = bits_from(since - t);
-                            if (past < 32) {
-                                if (p.parents) {
-                                    const int o = -past;  // draft of bit 0
-                                    uint32_t d = 0;
-                                    if (o < 0) {
-                                        d = anc[0] << -o;
-                                    } else if (o < kMaxDrafts) {
-                                        const uint32_t lo = anc[(o >> 5) * TILES * kTreeRows];
-                                        const uint32_t hi =
-                                            o < kMaxDrafts - 32 ? anc[((o >> 5) + 1) * TILES * kTreeRows] : 0u;
-                                        d = __funnelshift_r(lo, hi, o & 31);
-                                    }
-                                    const uint32_t drafts = bits_from(past);
-                                    of = (of & ~drafts) | (d & drafts);
-                                } else {
-                                    of &= ~bits_from(past + draft + 1);
-                                }
-                            }
-                            see[k] &= of;
-                        }
-                    }
                     const float* scales = reinterpret_cast<const float*>(meta + 32);
                     float room = kSlack + kLift<KV>;  // above base, for a score (e4m3: for a weight, less the scales)
                     if constexpr (E4M3) {
@@ -869,62 +868,86 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                         if (C::LOADERS == 4) most = fmaxf(most, fmaxf(v[2], v[3]));
                         room = kMostWeight - __log2f(most);
                     }
-                    // the columns of the probabilities are read by the products of the tile before
-                    if (TILES == 2 && !C::OVER) reach();
-                    // --- 32 scores at a time: what the sums are about, seldom moved; probabilities (e4m3:
-                    // weights), rounded to 16 bits ---
+                    // W scores from column c0 on: what the sums are about, seldom moved; probabilities (e4m3: weights),
+                    // rounded to 16 bits
+                    auto part = [&](auto wide, int c0) {
+                        constexpr int W = decltype(wide)::value;
+                        uint32_t y[W];
+                        if constexpr (W == 16) tmem_ld16(t_s + c0, y);
+                        if constexpr (W == 32) tmem_ld32(t_s + c0, y);
+                        if constexpr (W == 64) tmem_ld64(t_s + c0, y);
+                        uint64_t s[W / 2];
 #pragma unroll
-                    for (int k = 0; k < TT / 32; ++k) {
-                        uint32_t(&y)[32] = x[C::AHEAD ? k & 1 : 0];
-                        if (!C::AHEAD) tmem_ld32_issue(t_s + 32 * k, y);
-                        tmem_ld32_wait(y);
-                        if (C::AHEAD && k + 1 < TT / 32) tmem_ld32_issue(t_s + 32 * (k + 1), x[C::AHEAD ? (k + 1) & 1 : 0]);
-                        uint64_t s[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) s[i] = f32x2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
+                        for (int i = 0; i < W / 2; ++i) s[i] = f32x2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
                         if constexpr (E4M3) {
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const float4 f = *reinterpret_cast<const float4*>(scales + 32 * k + 2 * i);
+                            for (int i = 0; i < W / 2; i += 2) {
+                                const float4 f = *reinterpret_cast<const float4*>(scales + c0 + 2 * i);
                                 s[i] = f32x2_mul(s[i], f32x2(f.x, f.y));
                                 s[i + 1] = f32x2_mul(s[i + 1], f32x2(f.z, f.w));
                             }
                         }
                         if (masked) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float2 v = f32x2_get(s[i]);
-                                s[i] = f32x2((see[k] >> (2 * i)) & 1u ? v.x : -INFINITY,
-                                             (see[k] >> (2 * i + 1)) & 1u ? v.y : -INFINITY);
+                            for (int k = 0; k < W; k += 32) {
+                                // the tokens that the row sees, from t on
+                                const int t = t0 + c0 + k, past = g.s.ctx - t;  // bits from `past` on are drafts
+                                uint32_t see = bits_from(since - t);
+                                if (past < 32) {
+                                    if (p.parents) {
+                                        const int o = -past;  // draft of bit 0
+                                        uint32_t d = 0;
+                                        if (o < 0) {
+                                            d = anc[0] << -o;
+                                        } else if (o < kMaxDrafts) {
+                                            const uint32_t lo = anc[(o >> 5) * TILES * kTreeRows];
+                                            const uint32_t hi =
+                                                o < kMaxDrafts - 32 ? anc[((o >> 5) + 1) * TILES * kTreeRows] : 0u;
+                                            d = __funnelshift_r(lo, hi, o & 31);
+                                        }
+                                        const uint32_t drafts = bits_from(past);
+                                        see = (see & ~drafts) | (d & drafts);
+                                    } else {
+                                        see &= ~bits_from(past + draft + 1);
+                                    }
+                                }
+                                const uint16_t* there = reinterpret_cast<const uint16_t*>(meta) + (c0 + k) / 16;
+                                see &= W == 16 ? there[0] : there[0] | (uint32_t)there[1] << 16;
+#pragma unroll
+                                for (int i = 0; i < (W < 32 ? W : 32); i += 2) {
+                                    const float2 v = f32x2_get(s[(k + i) / 2]);
+                                    s[(k + i) / 2] = f32x2((see >> i) & 1u ? v.x : -INFINITY, (see >> (i + 1)) & 1u ? v.y : -INFINITY);
+                                }
                             }
                         }
                         float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int i = 0; i < W / 2; ++i) {
                             const float2 v = f32x2_get(s[i]);
-                            t[i & 3] = fmaxf(t[i & 3], fmaxf(v.x, v.y));
+                            t[i & 3] = max3(t[i & 3], v.x, v.y);
                         }
-                        const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+                        const float top = fmaxf(max3(t[0], t[1], t[2]), t[3]);
                         if (E4M3) m = fmaxf(m, top);
-                        if (__any_sync(kAllLanes, fmaf(top, qf, -base) > room)) {  // (NaN, -inf: no)
+                        const bool over = fmaf(top, qf, -base) > room;  // (NaN, -inf: no)
+                        if (__any_sync(kAllLanes, over)) {
                             float n = base;
                             if constexpr (!E4M3) {
-                                if (fmaf(top, qf, -base) > room) n = ceilf(top * qf) - kLift<KV>;
+                                if (over) n = top * qf - kLift<KV>;
                             } else {
                                 float best = -INFINITY;  // of the weights, in powers of two
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) {
+                                for (int i = 0; i < W / 2; ++i) {
                                     const float2 v = f32x2_get(s[i]);
-                                    best = fmaxf(best, fmaf(v.x, qf, __log2f(fabsf(scales[TT + 32 * k + 2 * i]))));
-                                    best = fmaxf(best, fmaf(v.y, qf, __log2f(fabsf(scales[TT + 32 * k + 2 * i + 1]))));
+                                    best = fmaxf(best, fmaf(v.x, qf, __log2f(fabsf(scales[TT + c0 + 2 * i]))));
+                                    best = fmaxf(best, fmaf(v.y, qf, __log2f(fabsf(scales[TT + c0 + 2 * i + 1]))));
                                 }
-                                n = fmaxf(base, ceilf(fmaxf(best - kNewWeight, m * qf - kMostLift)));
+                                if (over) n = fmaxf(base, fmaxf(best - kNewWeight, m * qf - kMostLift));
                             }
-                            const float f = ex2_approx(base - n);  // a power of two: exact
+                            const float f = ex2_approx(base - n);
                             base = n;
                             sum = f32x2_mul(sum, f32x2(f, f));
                             reach();
-                            if (!ok) break;
+                            if (!ok) return;
                             tc_fence_after();
                             if (j > 0) {
                                 for (int d = 0; d < p.D; d += 16) {
@@ -935,38 +958,61 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                                     tmem_st16(t_o + d, z);
                                 }
                             }
-                            if (k > 0) {  // and the tile's probabilities so far
+                            if (c0 > col0) {  // and the tile's probabilities so far (rounded again: they are small now)
                                 tmem_st_wait();
-                                for (int d = 0; d < k; ++d) {
+                                for (int d = col0 / 2; d < c0 / 2; d += 16) {
                                     uint32_t z[16];
-                                    tmem_ld16(t_p + 16 * d, z);
+                                    tmem_ld16(t_p + d, z);
 #pragma unroll
                                     for (int i = 0; i < 16; ++i) {
                                         const float2 v = unpack2<F16>(z[i]);
                                         z[i] = pack2<F16>(v.x * f, v.y * f);
                                     }
-                                    tmem_st16(t_p + 16 * d, z);
+                                    tmem_st16(t_p + d, z);
                                 }
                             }
                         }
                         const uint64_t qq = f32x2(qf, qf), bb = f32x2(-base, -base);
-                        uint32_t z[16];
+                        uint64_t sum2 = 0;
+                        uint32_t z[W / 2];
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
+                        for (int i = 0; i < W / 2; i += 2) {
                             const float2 a = f32x2_get(f32x2_fma(s[i], qq, bb)), b = f32x2_get(f32x2_fma(s[i + 1], qq, bb));
                             uint64_t e0 = f32x2(ex2_approx(a.x), ex2_approx(a.y)),
                                      e1 = f32x2(ex2_approx(b.x), ex2_approx(b.y));
-                            sum = f32x2_add(sum, f32x2_add(e0, e1));
+                            sum = f32x2_add(sum, e0);
+                            sum2 = f32x2_add(sum2, e1);
                             if constexpr (E4M3) {
-                                const float4 v = *reinterpret_cast<const float4*>(scales + TT + 32 * k + 2 * i);
+                                const float4 v = *reinterpret_cast<const float4*>(scales + TT + c0 + 2 * i);
                                 e0 = f32x2_mul(e0, f32x2(v.x, v.y));
                                 e1 = f32x2_mul(e1, f32x2(v.z, v.w));
                             }
-                            const float2 c0 = f32x2_get(e0), c1 = f32x2_get(e1);
-                            z[i] = pack2<F16>(c0.x, c0.y);
-                            z[i + 1] = pack2<F16>(c1.x, c1.y);
+                            const float2 u0 = f32x2_get(e0), u1 = f32x2_get(e1);
+                            z[i] = pack2<F16>(u0.x, u0.y);
+                            z[i + 1] = pack2<F16>(u1.x, u1.y);
                         }
-                        tmem_st16(t_p + 16 * k, z);
+                        sum = f32x2_add(sum, sum2);
+                        if constexpr (W == 16) tmem_st8(t_p + c0 / 2, z);
+                        if constexpr (W == 32) tmem_st16(t_p + c0 / 2, z);
+                        if constexpr (W == 64) tmem_st32(t_p + c0 / 2, z);
+                    };
+                    // the columns of the probabilities are read by the products of the tile before
+                    if (TILES == 2 && !C::OVER) reach();
+                    if constexpr (TILES == 1) {
+                        if (rep == 4) {
+                            part(std::integral_constant<int, 16>(), col0);
+                        } else if (rep == 2) {
+                            part(std::integral_constant<int, 32>(), col0);
+                        }
+                    }
+                    if (rep == 1) {
+#pragma unroll
+                        for (int c0 = 0; c0 < TT; c0 += C::WIDE)
+                            if (ok) part(std::integral_constant<int, C::WIDE>(), c0);
+                    } else if (C::OVER) {  // the scores of the other copies' tokens become probabilities of 0
+                        const uint32_t z[8] = {};
+                        for (int k = 0; k < TT; k += 16)
+                            if (k < col0 || k >= col0 + cols) tmem_st8(t_p + k / 2, z);
                     }
                     if (!ok) break;
                     tmem_st_wait();
@@ -982,45 +1028,103 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             if (!(ok = wait(&o_bar[w], o_phase ^ 1u))) break;
             tc_fence_after();
             // --- the row, or the run's part of it ---
-            if (warp_act) {
-                const float2 halves = f32x2_get(sum);
-                const float l = halves.x + halves.y;
-                if (base == kNoWeights) base = -INFINITY;  // no tokens
-                const bool done = p.whole || (g.starts && g.ends);
-                if (done) {
-                    const float fw = final_weight(p.sinks, head, base, l);
-                    uint16_t* dst = p.out + (g.s.first + draft) * p.o_token + (long long)head * p.o_head;
-                    for (int d = 0; d < p.D; d += 16) {
-                        uint32_t x[16], y[8];
-                        tmem_ld16(t_o + d, x);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            {
-                                const float u0 = __uint_as_float(x[2 * i]) * fw, u1 = __uint_as_float(x[2 * i + 1]) * fw;
-                                y[i] = qf16 ? pack2<true>(u0, u1) : pack2<false>(u0, u1);
-                            }
-                        if (act) {
-                            *reinterpret_cast<uint4*>(dst + d) = make_uint4(y[0], y[1], y[2], y[3]);
-                            *reinterpret_cast<uint4*>(dst + d + 8) = make_uint4(y[4], y[5], y[6], y[7]);
-                        }
-                    }
-                } else {
-                    constexpr int ROWS = TILES * kTreeRows;
-                    float* part = p.partial + ((long long)blockIdx.x * 2 + (g.starts ? 1 : 0)) * (ROWS * (p.D + 2));
-                    if (act) reinterpret_cast<float2*>(part)[w * kTreeRows + r] = make_float2(base, l);
-                    float4* sums = reinterpret_cast<float4*>(part + 2 * ROWS) + w * kTreeRows + r;
+            constexpr int ROWS = TILES * kTreeRows;
+            const float2 halves = f32x2_get(sum);
+            float l = halves.x + halves.y;
+            if (base == kNoWeights) base = -INFINITY;  // no tokens
+            const bool done = p.whole || (g.starts && g.ends);
+            uint16_t* dst = p.out + (g.s.first + draft) * p.o_token + (long long)head * p.o_head;
+            float* part = p.partial + ((long long)blockIdx.x * 2 + (g.starts ? 1 : 0)) * (ROWS * (p.D + 2));
+            float4* sums = reinterpret_cast<float4*>(part + 2 * ROWS) + w * kTreeRows + lr;
+            auto pack = [&](float a, float b) { return qf16 ? pack2<true>(a, b) : pack2<false>(a, b); };
+            if (TILES == 2 || rep == 1) {
+                if (warp_act) {
+                    const float fw = done ? final_weight(p.sinks, head, base, l) : 1.f;
+                    if (!done && act) reinterpret_cast<float2*>(part)[w * kTreeRows + r] = make_float2(base, l);
                     for (int d = 0; d < p.D; d += 16) {
                         uint32_t x[16];
                         tmem_ld16(t_o + d, x);
-                        if (act) {
+                        float v[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(x[i]) * fw;
+                        if (act && done) {
+                            *reinterpret_cast<uint4*>(dst + d) =
+                                make_uint4(pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7]));
+                            *reinterpret_cast<uint4*>(dst + d + 8) =
+                                make_uint4(pack(v[8], v[9]), pack(v[10], v[11]), pack(v[12], v[13]), pack(v[14], v[15]));
+                        } else if (act) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                sums[(d / 4 + i) * ROWS] =
-                                    make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]),
-                                                __uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3]));
+                                sums[(d / 4 + i) * ROWS] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                         }
                     }
                 }
+            } else if constexpr (TILES == 1) {
+                // the copies of a row meet where the queries were: each hands the others 8 dims of theirs at a
+                // time and adds up its own, in the order of the copies
+                const int mine = r / (fold + 1);
+                s_ml[r] = make_float2(base, l);
+                if (!(ok = meet())) break;
+                float top = -INFINITY;
+                for (int q = 0; q < rep; ++q) top = fmaxf(top, s_ml[q * (fold + 1) + lr].x);
+                l = 0.f;
+                for (int q = 0; q < rep; ++q) {
+                    const float2 ml = s_ml[q * (fold + 1) + lr];
+                    if (top != -INFINITY) l += ml.y * ex2_approx(ml.x - top);
+                }
+                const float f = top == -INFINITY ? 0.f : ex2_approx(base - top);
+                const float fw = done ? final_weight(p.sinks, head, top, l) : 1.f;
+                if (!done && act && mine == 0) reinterpret_cast<float2*>(part)[lr] = make_float2(top, l);
+                float* room = reinterpret_cast<float*>(smem + C::Q_AT);  // [to, from, row, 8]
+                auto slot = [&](int to, int from) { return room + ((to * rep + from) * (fold + 1) + lr) * 8; };
+                for (int d0 = 0; d0 < p.D; d0 += 8 * rep) {
+                    uint32_t x[16];
+                    float own[8];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (half * 16 >= 8 * rep) continue;
+                        tmem_ld16(t_o + d0 + half * 16, x);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            float* to = slot(2 * half + q, mine);
+                            float v[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(x[8 * q + i]) * f;
+                            if (2 * half + q == mine) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) own[i] = v[i];
+                            } else if (act) {
+                                *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+                                *reinterpret_cast<float4*>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+                            }
+                        }
+                    }
+                    if (!(ok = meet())) break;
+                    const int d = d0 + 8 * mine;
+                    if (act && d < p.D) {
+                        float v[8] = {};
+                        for (int q = 0; q < rep; ++q) {
+                            float4 a = make_float4(own[0], own[1], own[2], own[3]), b = make_float4(own[4], own[5], own[6], own[7]);
+                            if (q != mine) {
+                                a = *reinterpret_cast<const float4*>(slot(mine, q));
+                                b = *reinterpret_cast<const float4*>(slot(mine, q) + 4);
+                            }
+                            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+                            v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] *= fw;
+                        if (done) {
+                            *reinterpret_cast<uint4*>(dst + d) =
+                                make_uint4(pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7]));
+                        } else {
+                            sums[d / 4 * ROWS] = make_float4(v[0], v[1], v[2], v[3]);
+                            sums[(d / 4 + 1) * ROWS] = make_float4(v[4], v[5], v[6], v[7]);
+                        }
+                    }
+                    if (!(ok = meet())) break;
+                }
+                if (!ok) break;
             }
             tc_fence_before();
         }
