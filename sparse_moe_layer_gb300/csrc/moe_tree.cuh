@@ -12,16 +12,20 @@
 // A key is read once for all drafts and all query heads that share it, so the rows of
 // the products are the n x group (draft, head) pairs: 128 of them are the rows of a
 // tcgen05 tile.  S = Q K^T goes to tensor memory, where a thread has a whole row: no
-// exchange for maximum and sum.  Probabilities go back in 16 bits, over the scores they
-// come from, or beside them, and are the first operand of P V, whose sums stay in tensor memory; they are
-// rescaled only when a row's maximum rises by more than 2^kSlack.
+// exchange for maximum and sum.  Probabilities go back in 16 bits beside the scores and
+// are the first operand of P V, whose sums stay in tensor memory; they are rescaled only
+// when a row's maximum rises by more than 2^kSlack.
 //
 // One CTA: a warp that issues the products, a warp that copies keys and values by TMA
-// (pieces of tokens that lie on one page), four more that turn e4m3 codes into fp16, and a
+// (pieces of tokens that lie on one page), warps that turn e4m3 codes into fp16, and a
 // warpgroup for each row tile.  Pages of which 8 is no divisor are copied 16 bytes a
-// thread, by the four warps.  One row tile: two CTAs an SM, tiles of 64 tokens, two score
-// buffers, so that the next scores are there when the exponentials of the last are done.  Two row tiles (more than 128 rows): one CTA, tiles of 128 tokens, the two
-// tiles' products and exponentials alternate and share the keys and values in shared memory.
+// thread, by as many warps.  One row tile: two score buffers, so that the next scores are
+// there when the exponentials of the last are done.  Two row tiles (more than 128 rows)
+// share the keys and values in shared memory, and their scores are made anew as soon as
+// a row tile has read its own.
+//
+// A wait on a barrier takes 100 to 150 cycles even when it has come, so there are few: one
+// for a tile's keys and values, one for its scores, one for its probabilities.
 //
 // The list of items (sequence, key head, row tiles) and their token tiles is cut into
 // equal runs, one per CTA; an item cut by a run's border leaves fp32 parts that a second,
@@ -41,37 +45,36 @@ constexpr int kMinTiles = 4;    // token tiles of a run, at least, where there a
 template <int DP, int KV, int TILES, bool TMA>
 struct TreeCfg {
     static constexpr bool E4M3 = KV == kKvE4m3;
-    static constexpr int TT = TILES == 2 ? 128 : 64;  // tokens of a tile
-    static constexpr int CTAS = TILES == 2 || DP == 256 ? 1 : 2;
-    // warps: row tiles, then those that copy or convert, a TMA warp, the products' warp
-    static constexpr int LOADERS = E4M3 || !TMA ? TT / 32 : 0;  // a token a lane
+    static constexpr int TT = DP == 256 ? 32 : TILES == 2 && DP == 64 ? 128 : 64;  // tokens of a tile
+    static constexpr int CTAS = TILES == 1 && DP == 64 ? 2 : 1;
+    // warps: row tiles, then those that copy or convert (a token a lane), a TMA warp, the products' warp
+    static constexpr int LOADERS = E4M3 || !TMA ? TT / 32 : 0;
     static constexpr int TMA_WARP = TILES * 4 + LOADERS, MMA_WARP = TMA_WARP + (TMA ? 1 : 0);
     static constexpr int THREADS = (MMA_WARP + 1) * 32;
+    // scores that a thread works on at a time, by its registers
+    static constexpr int WARPS_EACH = ((MMA_WARP + 1) * CTAS + 3) / 4;  // of a scheduler
+    static constexpr int WIDE = TT < 64 || WARPS_EACH > 3 ? 32 : 64;
     static constexpr int Q_TILE = kTreeRows * DP * 2;
-    static constexpr int KV_TILE = TT * DP * 2;  // 16-bit keys (or values) of a token tile
-    // buffers of the ring (keys and values in turn), and of the raw codes' ring
-    static constexpr int NB = E4M3 ? (DP == 64 ? 6 : 3) : DP == 64 ? 10 : 4;
-    static constexpr int NR = !E4M3 ? 0 : DP == 64 ? 8 : 3;
-    static constexpr int RAW = TT * DP;
-    // codes; by threads, also scales and valid tokens of each loading warp
-    static constexpr int RAW_STRIDE = TMA ? RAW : RAW + TT * 4 + 16;
-    static constexpr int META = NB / 2 + 2;  // what the softmax knows of a tile: valid tokens, scales
-    static constexpr int META_BYTES = E4M3 ? 32 + 2 * TT * 4 : 32;
+    static constexpr int KV_TILE = TT * DP * 2;     // 16-bit keys (or values) of a token tile
+    static constexpr int RAW_TILE = TT * DP;        // their codes
+    static constexpr int STAGE = 2 * KV_TILE;       // keys, values
+    static constexpr int NS = E4M3 ? 3 : DP == 64 || TILES == 1 && DP == 128 ? 5 : 4;
+    // the raw codes' ring; by threads also scales and valid tokens
+    static constexpr int NR = !E4M3 ? 0 : DP == 64 ? 4 : DP == 128 && TILES == 1 ? 5 : 3;
+    static constexpr int RAW_STAGE = 2 * RAW_TILE + (TMA ? 0 : 2 * TT * 4 + 16);
+    // what the softmax knows of a tile: valid tokens; e4m3: each loading warp's largest value scale, scales
+    static constexpr int META = E4M3 ? 32 + 2 * TT * 4 : 32;
     static constexpr int ANC = TILES * kTreeRows * (kMaxDrafts / 32) * 4;
     static constexpr int Q_AT = 0;
     static constexpr int KV_AT = TILES * Q_TILE;
-    static constexpr int RAW_AT = KV_AT + NB * KV_TILE;
-    static constexpr int META_AT = RAW_AT + NR * RAW_STRIDE;
-    static constexpr int ANC_AT = META_AT + META * META_BYTES;
+    static constexpr int RAW_AT = KV_AT + NS * STAGE;
+    static constexpr int META_AT = RAW_AT + NR * RAW_STAGE;
+    static constexpr int ANC_AT = META_AT + NS * META;
     static constexpr int SMEM = ANC_AT + ANC + 1024;  // (aligned to 1024 in the kernel)
-    // tensor memory: two score buffers, the sums of each row tile, and probabilities (16 bits) in columns of
-    // their own where there are any left, else over the scores that they come from
-    static constexpr int S_COLS = 2 * TT;
-    static constexpr int COLS = S_COLS + TILES * DP <= 256 ? 256 : 512;
-    static constexpr bool OVER = S_COLS + TILES * DP + TT > COLS;
-    static constexpr int P_AT = OVER ? 0 : S_COLS + TILES * DP, P_STEP = OVER ? TT : TT / 2;
-    // scores that a thread works on at a time (with loading warps it has 128 registers, without 168)
-    static constexpr int WIDE = LOADERS ? 32 : 64;
+    // tensor memory: two score buffers (a row tile's own, or in turn), the sums of each row tile, two of
+    // probabilities (16 bits)
+    static constexpr int O_AT = 2 * TT, P_AT = O_AT + TILES * DP;
+    static constexpr int COLS = P_AT + TT <= 256 ? 256 : 512;
 };
 
 struct TreeSeq {
@@ -147,6 +150,11 @@ struct TreeWalk {
     }
 };
 
+// a / b of numbers >= 0, in 32 bits where they fit
+__device__ __forceinline__ long long tree_quotient(long long a, int b) {
+    return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
 // Bits lo and on of 32.
 __device__ __forceinline__ uint32_t bits_from(int lo) { return lo <= 0 ? kAllLanes : lo >= 32 ? 0u : kAllLanes << lo; }
 
@@ -161,11 +169,11 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
     using C = TreeCfg<DP, KV, TILES, TMA>;
     constexpr bool E4M3 = C::E4M3, F16 = KV != kKvBf16;  // F16: type of the products
     const bool qf16 = E4M3 ? p.fp16 : F16;               // of q and out
-    constexpr int TT = C::TT, NB = C::NB, NR = C::NR, THREADS = C::THREADS;
-    constexpr int kFillers = C::LOADERS ? C::LOADERS : 1;  // arrivals that fill a buffer (and its tokens' slot)
+    constexpr int TT = C::TT, NS = C::NS, NR = C::NR ? C::NR : 1, THREADS = C::THREADS;
+    constexpr int kFillers = C::LOADERS ? C::LOADERS : 1;  // arrivals that fill a stage
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full_bar[NB], empty_bar[NB], meta_bar[C::META], q_bar[TILES], s_bar[2], p_bar[2],
-        o_bar[TILES], end_bar, raw_full_bar[NR ? NR : 1], raw_empty_bar[NR ? NR : 1], x_bar;
+    __shared__ __align__(8) uint64_t full_bar[NS], empty_bar[NS], q_bar[TILES], s_bar[2], p_bar[2], o_bar[TILES], end_bar,
+        raw_full_bar[NR], raw_empty_bar[NR], read_bar[TILES], x_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ TreeWork s_work;
@@ -178,11 +186,10 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
     long long* s_pre = reinterpret_cast<long long*>(smem);  // [THREADS + 1], before the tiles come
 
     if (tid == 0) {
-        for (int i = 0; i < NB; ++i) {
+        for (int i = 0; i < NS; ++i) {
             mbar_init(smem_u32(&full_bar[i]), kFillers);
             mbar_init(smem_u32(&empty_bar[i]), 1);
         }
-        for (int i = 0; i < C::META; ++i) mbar_init(smem_u32(&meta_bar[i]), kFillers);
         for (int i = 0; i < NR; ++i) {
             mbar_init(smem_u32(&raw_full_bar[i]), 1);
             mbar_init(smem_u32(&raw_empty_bar[i]), kFillers);
@@ -190,6 +197,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
         for (int i = 0; i < TILES; ++i) {
             mbar_init(smem_u32(&q_bar[i]), kTreeRows);
             mbar_init(smem_u32(&o_bar[i]), 1);
+            mbar_init(smem_u32(&read_bar[i]), 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&s_bar[i]), 1);
@@ -219,7 +227,8 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
     __syncthreads();
     if (warp == 0) {  // prefix sums, 32 at a time
         long long before = 0;
-        for (int base = 0; base < THREADS; base += 32) {
+        const int slices = (p.B + slice - 1) / slice;
+        for (int base = 0; base < slices; base += 32) {
             long long v = s_pre[base + lane + 1];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -232,15 +241,16 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
         }
         __syncwarp();
         const long long total = before, least = p.whole ? 1 : kMinTiles;
-        const long long want = (total + least - 1) / least;
+        const long long want = tree_quotient(total + least - 1, (int)least);
         const int n = (int)(want < p.runs ? want : p.runs), run = blockIdx.x;
         TreeWork w = {0, 0, 0, 0, 0};
         if (run < n) {
-            const long long each = total / n, more = total - each * n;
-            long long u = each * run + more * run / n;
-            w.rem = each + more * (run + 1) / n - more * run / n;
+            const long long each = tree_quotient(total, n);
+            const int more = (int)(total - each * n), from = more * run / n;  // (n is small)
+            long long u = each * run + from;
+            w.rem = each + more * (run + 1) / n - from;
             int sl = 0;
-            for (int base = 0; base < THREADS; base += 32)
+            for (int base = 0; base < slices; base += 32)
                 sl += __popc(__ballot_sync(kAllLanes, s_pre[base + lane + 1] <= u));
             u -= s_pre[sl];
             w.b = sl * slice;
@@ -249,7 +259,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 const int nt = p.whole ? 1 : s.ntiles;
                 const long long here = (long long)p.Hkv * s.rtiles * nt;
                 if (u < here) {
-                    const int item = (int)(u / nt);
+                    const int item = (int)tree_quotient(u, nt);
                     w.tile = (int)(u - (long long)item * nt);
                     w.h = item / s.rtiles;
                     w.rt = item - w.h * s.rtiles;
@@ -279,21 +289,20 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
         const uint32_t id_o = idesc_f16_f32(F16, kTreeRows, p.D, true);
         const int ksteps = p.D / 16;
         const bool issuer = elect_one();
-        int c = 0;                          // buffers taken from the ring
-        uint32_t o_count[TILES] = {};       // products with values so far
-        uint32_t q_phase = 0, p_phase = 0;  // bit i: phase of row tile (score buffer) i
+        int c = 0;  // tiles so far: stages of the ring
+        uint32_t q_phase = 0, p_phase = 0, read_phase = 0;  // bit i: phase of row tile (score buffer) i
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t phase) {
             const bool r = mbar_wait(smem_u32(bar), phase & 1u, abort_p, p.status, kErrTimeoutMma);
             return __all_sync(kAllLanes, r) != 0;
         };
-        auto full = [&](int i) { return wait(&full_bar[i % NB], i / NB); };
+        auto full = [&](int i) { return wait(&full_bar[i % NS], i / NS); };
         // descriptors: a start address in 16-byte units in the low bits, so steps are additions
         const uint64_t q_desc = smem_desc_sw128(smem_s + C::Q_AT), k_desc = smem_desc_sw128(smem_s + C::KV_AT),
-                       v_desc = smem_desc_sw128_mn(smem_s + C::KV_AT, TT * 128);
-        auto scores = [&](int w, int buf, int kbuf) {
+                       v_desc = smem_desc_sw128_mn(smem_s + C::KV_AT + C::KV_TILE, TT * 128);
+        auto scores = [&](int w, int buf, int stage) {
             if (issuer) {
-                const uint64_t a = q_desc + w * (C::Q_TILE >> 4), b = k_desc + (kbuf % NB) * (C::KV_TILE >> 4);
+                const uint64_t a = q_desc + w * (C::Q_TILE >> 4), b = k_desc + (stage % NS) * (C::STAGE >> 4);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
                     if (k < ksteps)
@@ -302,23 +311,19 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 mma_commit(smem_u32(&s_bar[buf]));
             }
         };
-        auto values = [&](int w, int buf, int vbuf, bool first) {
+        auto values = [&](int w, int buf, int stage, bool first) {
             if (issuer) {
-                const uint64_t b = v_desc + (vbuf % NB) * (C::KV_TILE >> 4);
+                const uint64_t b = v_desc + (stage % NS) * (C::STAGE >> 4);
 #pragma unroll
                 for (int k = 0; k < TT / 16; ++k)
-                    mma_16bit_tmem_a(tmem + C::S_COLS + w * DP, tmem + C::P_AT + buf * C::P_STEP + 8 * k,
+                    mma_16bit_tmem_a(tmem + C::O_AT + w * DP, tmem + C::P_AT + buf * (TT / 2) + 8 * k,
                                      b + ((k * 2048) >> 4), id_o, k > 0 || !first);
                 mma_commit(smem_u32(&o_bar[w]));
             }
-            ++o_count[w];
         };
         auto release = [&](int i) {
-            if (issuer) mma_commit(smem_u32(&empty_bar[i % NB]));
+            if (issuer) mma_commit(smem_u32(&empty_bar[i % NS]));
         };
-        // Scores over probabilities: products of different accumulators keep no order, so the ones that read
-        // them are waited for.  (The phase before has passed: the row tile's threads waited for it.)
-        auto free_scores = [&](int w) { return !C::OVER || wait(&o_bar[w], o_count[w] - 1); };
         auto probabilities = [&](int buf) {
             const bool r = wait(&p_bar[buf], p_phase >> buf);
             p_phase ^= 1u << buf;
@@ -337,39 +342,39 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
 #pragma unroll
             for (int w = 0; w < TILES; ++w)
                 if (w < act) scores(w, w, c);
-            release(c);
-            for (int j = 0; j < g.n && ok; ++j, c += 2) {
-                // ring: keys of tile j are buffer c, its values c + 1, the next keys c + 2
+            // Products of different accumulators keep no order: what a product writes over has been read, by
+            // the row tile's threads (scores), or by products that they waited for (probabilities).
+            for (int j = 0; j < g.n && ok; ++j, ++c) {
                 const bool more = j + 1 < g.n;
                 if constexpr (TILES == 1) {
                     if (more) {
-                        if (!(ok = full(c + 2) && (j == 0 || free_scores(0)))) break;
+                        if (!(ok = full(c + 1))) break;
                         tc_fence_after();
-                        scores(0, (j + 1) & 1, c + 2);
-                        release(c + 2);
+                        scores(0, (j + 1) & 1, c + 1);
                     }
-                    ok = probabilities(j & 1) && full(c + 1);
-                    if (!ok) break;
+                    if (!(ok = probabilities(j & 1))) break;
                     tc_fence_after();
-                    values(0, j & 1, c + 1, j == 0);
+                    values(0, j & 1, c, j == 0);
                 } else {
 #pragma unroll
                     for (int w = 0; w < TILES; ++w) {
-                        if (w >= act) continue;
-                        ok = ok && probabilities(w) && (w > 0 || full(c + 1));
-                        if (!ok) break;
+                        if (w >= act || !ok) continue;
+                        ok = wait(&read_bar[w], read_phase >> w) && (w > 0 || !more || full(c + 1));
+                        read_phase ^= 1u << w;
+                        if (!ok || !more) continue;
                         tc_fence_after();
-                        values(w, w, c + 1, j == 0);
-                        if (more) {
-                            if (!(ok = (w > 0 || full(c + 2)) && free_scores(w))) break;
-                            tc_fence_after();
-                            scores(w, w, c + 2);
-                        }
+                        scores(w, w, c + 1);
+                    }
+#pragma unroll
+                    for (int w = 0; w < TILES; ++w) {
+                        if (w >= act || !ok) continue;
+                        if (!(ok = probabilities(w))) continue;
+                        tc_fence_after();
+                        values(w, w, c, j == 0);
                     }
                     if (!ok) break;
-                    if (more) release(c + 2);
                 }
-                release(c + 1);
+                release(c);
             }
         }
         // every issued product has finished once this commit lands
@@ -383,20 +388,21 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
         constexpr int RPS = 32 / CH, STEPS = 32 / RPS;       // tokens of a step of a loading warp
         const int lw = warp - TILES * 4, ch = lane % CH, r0 = lane / CH;
         const bool in = ch * (16 / ES) < p.D;
-        int c = 0;  // buffers filled
+        int c = 0;  // tiles begun: stages filled
         bool ok = true;
         auto wait = [&](uint64_t* bar, int phase) {
             const bool r = mbar_wait(smem_u32(bar), (uint32_t)phase & 1u, abort_p, p.status, kErrTimeoutProducer);
             return __all_sync(kAllLanes, r) != 0;
         };
-        auto wait_empty = [&](int i) { return i < NB || wait(&empty_bar[i % NB], i / NB - 1); };
-        // buffer i is filled (all lanes did, or waited for, their part)
+        auto wait_empty = [&](int i) { return i < NS || wait(&empty_bar[i % NS], i / NS - 1); };
+        // stage i is filled (all lanes did, or waited for, their part)
         auto signal = [&](int i) {
             fence_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&full_bar[i % NB]));
+            if (lane == 0) mbar_arrive(smem_u32(&full_bar[i % NS]));
         };
-        auto meta = [&](int i) { return smem + C::META_AT + (i % C::META) * C::META_BYTES; };
+        auto stage = [&](int i) { return smem_s + C::KV_AT + (i % NS) * C::STAGE; };
+        auto meta = [&](int i) { return smem + C::META_AT + (i % NS) * C::META; };
         // a token (or piece of box tokens) of a lane, its page looked up before the copies need it
         struct Token {
             int pid, off, h;
@@ -439,139 +445,148 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             // a lane has a piece of box tokens of the tile
             const int pieces = TT / p.box;
             const int blocks = E4M3 ? 1 : (p.D + 63) / 64;
+            const bool issuer = elect_one();
             bool has;
             Token t = take(has, lane * p.box, p.box, lane < pieces);
-            for (int tiles = 0; has && ok; ++tiles) {
+            for (; has; ++c) {
                 const Token u = t;
                 t = take(has, lane * p.box, p.box, lane < pieces);
                 const bool good = on_page(u);
                 const uint32_t copied = __ballot_sync(kAllLanes, good), bad = __ballot_sync(kAllLanes, u.in && !good);
-                if (!E4M3) {
-                    if (lane < TT / 32) {  // valid tokens, 32 a lane
-                        const int w0 = u.t0 + 32 * lane;
-                        uint32_t v = bits_from(u.lo - w0) & ~bits_from(u.len - w0);
-                        for (uint32_t b = bad; b; b &= b - 1) {
-                            const int at = (__ffs(b) - 1) * p.box - 32 * lane;
-                            v &= ~(bits_from(at) & ~bits_from(at + p.box));
-                        }
-                        reinterpret_cast<uint32_t*>(meta(tiles))[lane] = v;
+                ok = E4M3 ? c < NR || wait(&raw_empty_bar[c % NR], c / NR - 1) : wait_empty(c);
+                if (!ok) break;
+                if (!E4M3 && lane < TT / 32) {  // valid tokens, 32 a lane
+                    const int w0 = u.t0 + 32 * lane;
+                    uint32_t v = bits_from(u.lo - w0) & ~bits_from(u.len - w0);
+                    for (uint32_t b = bad; b; b &= b - 1) {
+                        const int at = (__ffs(b) - 1) * p.box - 32 * lane;
+                        v &= ~(bits_from(at) & ~bits_from(at + p.box));
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&meta_bar[tiles % C::META]));
+                    reinterpret_cast<uint32_t*>(meta(c))[lane] = v;
                 }
-                const uint32_t bytes = __popc(copied) * p.box * (E4M3 ? p.D : 128 * blocks);
+                __syncwarp();
+                const uint32_t bar = smem_u32(E4M3 ? &raw_full_bar[c % NR] : &full_bar[c % NS]);
+                const uint32_t to = E4M3 ? smem_s + C::RAW_AT + (c % NR) * C::RAW_STAGE : stage(c);
+                if (issuer) mbar_arrive_expect_tx(bar, 2 * __popc(copied) * p.box * (E4M3 ? p.D : 128 * blocks));
+                // one lane issues all (lanes that issue a piece each take 100 cycles a piece), four at a time
+                for (int i0 = 0; i0 < pieces; i0 += 4) {
+                    int pid[4], off[4];
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++c) {
-                    uint64_t* bar = E4M3 ? &raw_full_bar[c % (NR ? NR : 1)] : &full_bar[c % NB];
-                    ok = E4M3 ? c < NR || wait(&raw_empty_bar[c % (NR ? NR : 1)], c / (NR ? NR : 1) - 1) : wait_empty(c);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(smem_u32(bar), bytes);
-                    __syncwarp();
-                    if (good) {
-                        const CUtensorMap* m = kv ? &tmV : &tmK;
-                        if (E4M3) {
-                            tma_load_4d(smem_s + C::RAW_AT + (c % (NR ? NR : 1)) * C::RAW_STRIDE + lane * p.box * p.D, m, 0,
-                                        u.off, u.h, u.pid, smem_u32(bar));
-                        } else {
-                            const uint32_t dst = smem_s + C::KV_AT + (c % NB) * C::KV_TILE + lane * p.box * 128;
+                    for (int i = 0; i < 4; ++i) {
+                        pid[i] = __shfl_sync(kAllLanes, u.pid, i0 + i);
+                        off[i] = __shfl_sync(kAllLanes, u.off, i0 + i);
+                    }
+                    if (issuer) {
 #pragma unroll
-                            for (int k = 0; k < DP / 64; ++k)
-                                if (k < blocks) tma_load_4d(dst + k * TT * 128, m, k * 64, u.off, u.h, u.pid, smem_u32(bar));
+                        for (int i = 0; i < 4; ++i) {
+                            if (!((copied >> (i0 + i)) & 1u)) continue;
+                            if (E4M3) {
+                                const uint32_t at = to + (i0 + i) * p.box * p.D;
+                                tma_load_4d(at, &tmK, 0, off[i], u.h, pid[i], bar);
+                                tma_load_4d(at + C::RAW_TILE, &tmV, 0, off[i], u.h, pid[i], bar);
+                            } else {
+                                const uint32_t at = to + (i0 + i) * p.box * 128;
+#pragma unroll
+                                for (int k = 0; k < DP / 64; ++k) {
+                                    if (k >= blocks) continue;
+                                    tma_load_4d(at + k * TT * 128, &tmK, k * 64, off[i], u.h, pid[i], bar);
+                                    tma_load_4d(at + C::KV_TILE + k * TT * 128, &tmV, k * 64, off[i], u.h, pid[i], bar);
+                                }
+                            }
                         }
                     }
                 }
+                __syncwarp();
             }
             // the last copies have landed before the CTA may exit
-            constexpr int LAST = E4M3 ? (NR ? NR : 1) : NB;
+            constexpr int LAST = E4M3 ? NR : NS;
             int dummy = 0;
             for (int i = max(0, c - LAST); i < c; ++i)
                 mbar_wait(smem_u32(E4M3 ? &raw_full_bar[i % LAST] : &full_bar[i % LAST]), (uint32_t)(i / LAST) & 1u, &dummy,
                           p.status, kErrTimeoutProducer);
         } else if constexpr (!E4M3) {
-            int h = 0;
-            long long k_off = 0, v_off = 0;  // of the lane's token
-            uint32_t mask = 0;               // valid tokens of the warp
-            // copies in flight behind the one issued last: a buffer is free again once the products that read
-            // it are done, which wait for no copy but the next
-            constexpr int DEPTH = NB / 2;
-            auto copy = [&](bool is_k) {
-                const uint8_t* base = static_cast<const uint8_t*>(is_k ? p.cache.k : p.cache.v) +
-                                      (long long)h * (is_k ? p.cache.k_head : p.cache.v_head) * ES + ch * 16;
-                const uint32_t dst = smem_s + C::KV_AT + (c % NB) * C::KV_TILE;
-                const long long off = is_k ? k_off : v_off;
-#pragma unroll
-                for (int i = 0; i < STEPS; ++i) {
-                    const int r = i * RPS + r0;
-                    const long long o = __shfl_sync(kAllLanes, off, r);
-                    if (in) cp_async16z(dst + tile_at(TT, lw * 32 + r, ch), base + o * ES, (mask >> r) & 1u);
-                }
-            };
-            auto step = [&](bool is_k) {
-                if (!wait_empty(c)) return false;
-                copy(is_k);
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                cp_async_wait<DEPTH>();
-                if (c >= DEPTH) signal(c - DEPTH);
-                ++c;
-                return true;
-            };
+            // copies of tiles in flight behind the one issued last: a stage is free again once the products that
+            // read it are done, which wait for no tile but the next
+            constexpr int DEPTH = NS - 2;
             bool has;
             Token t = take(has, lw * 32 + lane, 1, true);
-            for (int tiles = 0; has; ++tiles) {
+            for (; has; ++c) {
                 Token u = t;
                 t = take(has, lw * 32 + lane, 1, true);
                 u.in = on_page(u);
-                mask = __ballot_sync(kAllLanes, u.in);
-                h = u.h;
+                const uint32_t mask = __ballot_sync(kAllLanes, u.in);  // valid tokens of the warp
                 if (!u.in) u.pid = u.off = 0;
-                k_off = u.pid * p.cache.k_page + u.off * p.cache.k_token;
-                v_off = u.pid * p.cache.v_page + u.off * p.cache.v_token;
-                if (lane == 0) {
-                    reinterpret_cast<uint32_t*>(meta(tiles))[lw] = mask;
-                    mbar_arrive(smem_u32(&meta_bar[tiles % C::META]));
+                if (!(ok = wait_empty(c))) break;
+                if (lane == 0) reinterpret_cast<uint32_t*>(meta(c))[lw] = mask;
+                const uint8_t* kb = static_cast<const uint8_t*>(p.cache.k) + (u.h * p.cache.k_head) * 2 + ch * 16;
+                const uint8_t* vb = static_cast<const uint8_t*>(p.cache.v) + (u.h * p.cache.v_head) * 2 + ch * 16;
+                const long long k_off = u.pid * p.cache.k_page + u.off * p.cache.k_token,
+                                v_off = u.pid * p.cache.v_page + u.off * p.cache.v_token;
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i) {
+                    const int r = i * RPS + r0;
+                    const long long ko = __shfl_sync(kAllLanes, k_off, r), vo = __shfl_sync(kAllLanes, v_off, r);
+                    const uint32_t at = stage(c) + tile_at(TT, lw * 32 + r, ch);
+                    if (in) {
+                        cp_async16z(at, kb + ko * 2, (mask >> r) & 1u);
+                        cp_async16z(at + C::KV_TILE, vb + vo * 2, (mask >> r) & 1u);
+                    }
                 }
-                if (!(ok = step(true) && step(false))) break;
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                cp_async_wait<DEPTH>();
+                if (c >= DEPTH) signal(c - DEPTH);
             }
             cp_async_wait<0>();
             if (ok)
                 for (int i = max(0, c - DEPTH); i < c; ++i) signal(i);
         } else {
             // e4m3: raw codes become fp16.  By TMA: [token][D].  By threads: a lane copies, and later converts,
-            // pieces of its own, [step][thread] 16 bytes.
-            constexpr int LANES = C::LOADERS * 32;
-            auto slot = [&](int i) { return smem + C::RAW_AT + (i % NR) * C::RAW_STRIDE; };
-            // buffer c from raw slot c; sc: the scale of the lane's token, mask: the warp's valid tokens
+            // pieces of its own, [step][lane] 16 bytes.
+            constexpr int LANES = C::LOADERS * 32, BATCH = STEPS < 8 ? STEPS : 8;
+            auto slot = [&](int i) { return smem + C::RAW_AT + (i % NR) * C::RAW_STAGE; };
+            // the keys (values) of stage c from raw slot c; sc: the scale of the lane's token, mask: the warp's
+            // valid tokens
             auto convert = [&](bool is_k, float sc, uint32_t mask) {
-                const uint8_t* at = slot(c);
-                const uint32_t dst = smem_s + C::KV_AT + (c % NB) * C::KV_TILE;
+                const uint8_t* at = slot(c) + (is_k ? 0 : C::RAW_TILE);
+                const uint32_t dst = stage(c) + (is_k ? 0 : C::KV_TILE);
                 uint32_t some = 0;  // V: tokens with a value that is not 0
 #pragma unroll
-                for (int i = 0; i < STEPS; ++i) {
-                    const int r = i * RPS + r0;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (TMA ? in && ((mask >> r) & 1u) : true)
-                        v = *reinterpret_cast<const uint4*>(at + (TMA ? (lw * 32 + r) * p.D + ch * 16 : (i * LANES + lw * 32 + lane) * 16));
-                    if (in) {
-                        const uint32_t d = dst + tile_at(TT, lw * 32 + r, 2 * ch),
-                                       e = dst + tile_at(TT, lw * 32 + r, 2 * ch + 1);
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(d), "r"(e4m3x2_to_f16x2(v.x)),
-                                     "r"(e4m3x2_to_f16x2(v.x >> 16)), "r"(e4m3x2_to_f16x2(v.y)),
-                                     "r"(e4m3x2_to_f16x2(v.y >> 16))
-                                     : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(e), "r"(e4m3x2_to_f16x2(v.z)),
-                                     "r"(e4m3x2_to_f16x2(v.z >> 16)), "r"(e4m3x2_to_f16x2(v.w)),
-                                     "r"(e4m3x2_to_f16x2(v.w >> 16))
-                                     : "memory");
-                    }
-                    if (!is_k) {
-                        const uint32_t b =
-                            __ballot_sync(kAllLanes, in && ((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) != 0u);
+                for (int i0 = 0; i0 < STEPS; i0 += BATCH) {
+                    uint4 v[BATCH];
 #pragma unroll
-                        for (int k = 0; k < RPS; ++k)
-                            some |= ((b >> (k * CH)) & (CH == 32 ? kAllLanes : (1u << (CH & 31)) - 1u)) ? 1u << (i * RPS + k) : 0u;
+                    for (int i = 0; i < BATCH; ++i) {
+                        const int r = (i0 + i) * RPS + r0;
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (!TMA || (in && ((mask >> r) & 1u)))
+                            v[i] = *reinterpret_cast<const uint4*>(
+                                at + (TMA ? (lw * 32 + r) * p.D + ch * 16 : ((i0 + i) * LANES + lw * 32 + lane) * 16));
+                    }
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) {
+                        const int r = (i0 + i) * RPS + r0;
+                        if (in) {
+                            const uint32_t d = dst + tile_at(TT, lw * 32 + r, 2 * ch), e = dst + tile_at(TT, lw * 32 + r, 2 * ch + 1);
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(d), "r"(e4m3x2_to_f16x2(v[i].x)),
+                                         "r"(e4m3x2_to_f16x2(v[i].x >> 16)), "r"(e4m3x2_to_f16x2(v[i].y)),
+                                         "r"(e4m3x2_to_f16x2(v[i].y >> 16))
+                                         : "memory");
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(e), "r"(e4m3x2_to_f16x2(v[i].z)),
+                                         "r"(e4m3x2_to_f16x2(v[i].z >> 16)), "r"(e4m3x2_to_f16x2(v[i].w)),
+                                         "r"(e4m3x2_to_f16x2(v[i].w >> 16))
+                                         : "memory");
+                        }
+                        if (!is_k) {
+                            const uint32_t b =
+                                __ballot_sync(kAllLanes, in && ((v[i].x | v[i].y | v[i].z | v[i].w) & 0x7f7f7f7fu) != 0u);
+#pragma unroll
+                            for (int k = 0; k < RPS; ++k)
+                                some |= ((b >> (k * CH)) & (CH == 32 ? kAllLanes : (1u << (CH & 31)) - 1u))
+                                            ? 1u << ((i0 + i) * RPS + k)
+                                            : 0u;
+                        }
                     }
                 }
-                uint8_t* m = meta(c >> 1);
+                uint8_t* m = meta(c);
                 // a head of zeros, which the append stores with a scale of 1 however small the others are,
                 // has no weight
                 if (!is_k && !((some >> lane) & 1u)) sc = 0.f;
@@ -579,12 +594,9 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 if (is_k) {
                     if (lane == 0) reinterpret_cast<uint32_t*>(m)[lw] = mask;
                 } else {
-                    float top = fabsf(sc);
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAllLanes, top, o));
-                    if (lane == 0) reinterpret_cast<float*>(m)[4 + lw] = top;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&meta_bar[(c >> 1) % C::META]));
+                    // (floats of one sign order as whole numbers do; NaN above all)
+                    const uint32_t top = __reduce_max_sync(kAllLanes, __float_as_uint(sc) & 0x7fffffffu);
+                    if (lane == 0) reinterpret_cast<uint32_t*>(m)[4 + lw] = top;
                 }
             };
             if constexpr (TMA) {
@@ -606,82 +618,66 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 Token t = take(has_s, lw * 32 + lane, 1, true);
                 Scales s = scales(t);
                 t = take(has_t, lw * 32 + lane, 1, true);
-                while (has_s && ok) {
+                for (; has_s; ++c) {
                     const Scales u = s;
                     has_s = has_t;
                     s = scales(t);
                     t = take(has_t, lw * 32 + lane, 1, true);
                     const uint32_t mask = __ballot_sync(kAllLanes, u.in);
-#pragma unroll 1
-                    for (int kv = 0; kv < 2; ++kv, ++c) {
-                        ok = wait(&raw_full_bar[c % NR], c / NR) && wait_empty(c);
-                        if (!ok) break;
-                        convert(kv == 0, kv ? u.v : u.k, mask);
-                        signal(c);
-                        if (lane == 0) mbar_arrive(smem_u32(&raw_empty_bar[c % NR]));
-                    }
+                    ok = wait_empty(c) && wait(&raw_full_bar[c % NR], c / NR);
+                    if (!ok) break;
+                    convert(true, u.k, mask);
+                    convert(false, u.v, mask);
+                    signal(c);
+                    if (lane == 0) mbar_arrive(smem_u32(&raw_empty_bar[c % NR]));
                 }
             } else {
-                int raw = 0, h = 0;  // raw copies issued
-                long long k_off = 0, v_off = 0, s_off = 0;
-                uint32_t mask = 0;
                 bool has;
                 Token t = take(has, lw * 32 + lane, 1, true);
-                auto begin_tile = [&]() {
-                    Token u = t;
-                    t = take(has, lw * 32 + lane, 1, true);
-                    u.in = on_page(u);
-                    mask = __ballot_sync(kAllLanes, u.in);
-                    h = u.h;
-                    if (!u.in) u.pid = u.off = 0;
-                    k_off = u.pid * p.cache.k_page + u.off * p.cache.k_token;
-                    v_off = u.pid * p.cache.v_page + u.off * p.cache.v_token;
-                    s_off = u.pid * p.cache.s_page + u.off * p.cache.s_token;
-                };
-                auto issue = [&](bool is_k) {
-                    const uint8_t* base = static_cast<const uint8_t*>(is_k ? p.cache.k : p.cache.v) +
-                                          (long long)h * (is_k ? p.cache.k_head : p.cache.v_head) + ch * 16;
-                    uint8_t* at = slot(raw);
-                    const uint32_t dst = smem_u32(at);
-                    const long long off = is_k ? k_off : v_off;
+                int raw = 0;  // tiles whose copies are issued
+                auto issue_next = [&]() {
+                    if (has) {
+                        Token u = t;
+                        t = take(has, lw * 32 + lane, 1, true);
+                        u.in = on_page(u);
+                        const uint32_t mask = __ballot_sync(kAllLanes, u.in);
+                        if (!u.in) u.pid = u.off = 0;
+                        const uint8_t* kb = static_cast<const uint8_t*>(p.cache.k) + u.h * p.cache.k_head;
+                        const uint8_t* vb = static_cast<const uint8_t*>(p.cache.v) + u.h * p.cache.v_head;
+                        const long long k_off = u.pid * p.cache.k_page + u.off * p.cache.k_token,
+                                        v_off = u.pid * p.cache.v_page + u.off * p.cache.v_token;
+                        uint8_t* at = slot(raw);
+                        const uint32_t dst = smem_u32(at);
 #pragma unroll
-                    for (int i = 0; i < STEPS; ++i) {
-                        const int r = i * RPS + r0;
-                        const long long o = __shfl_sync(kAllLanes, off, r);
-                        cp_async16z(dst + (i * LANES + lw * 32 + lane) * 16, in ? base + o : base - ch * 16, in && ((mask >> r) & 1u));
-                    }
-                    {
-                        const float* sc = (is_k ? p.cache.k_scale : p.cache.v_scale) + (long long)h * p.cache.s_head;
-                        cp_async4z(dst + C::RAW + (lw * 32 + lane) * 4, sc + s_off, (mask >> lane) & 1u);
-                    }
-                    if (lane == 0) *reinterpret_cast<uint32_t*>(at + C::RAW + TT * 4 + lw * 4) = mask;
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    ++raw;
-                };
-                bool is_k_raw = true;
-                auto issue_next = [&]() {  // an empty group where nothing is left
-                    if (is_k_raw) {
-                        if (!has) {
-                            asm volatile("cp.async.commit_group;" ::: "memory");
-                            return;
+                        for (int i = 0; i < STEPS; ++i) {
+                            const int r = i * RPS + r0;
+                            const long long ko = __shfl_sync(kAllLanes, k_off, r), vo = __shfl_sync(kAllLanes, v_off, r);
+                            const uint32_t to = dst + (i * LANES + lw * 32 + lane) * 16;
+                            const bool there = in && ((mask >> r) & 1u);
+                            cp_async16z(to, in ? kb + ko + ch * 16 : kb, there);
+                            cp_async16z(to + C::RAW_TILE, in ? vb + vo + ch * 16 : vb, there);
                         }
-                        begin_tile();
+                        const long long s_off = u.pid * p.cache.s_page + u.h * p.cache.s_head + u.off * p.cache.s_token;
+                        const uint32_t sc = dst + 2 * C::RAW_TILE + (lw * 32 + lane) * 4;
+                        cp_async4z(sc, p.cache.k_scale + s_off, u.in);
+                        cp_async4z(sc + TT * 4, p.cache.v_scale + s_off, u.in);
+                        if (lane == 0) *reinterpret_cast<uint32_t*>(at + 2 * C::RAW_TILE + 2 * TT * 4 + lw * 4) = mask;
+                        ++raw;
                     }
-                    issue(is_k_raw);
-                    is_k_raw = !is_k_raw;
+                    asm volatile("cp.async.commit_group;" ::: "memory");  // (empty where nothing is left)
                 };
 #pragma unroll 1
                 for (int i = 0; i < NR - 1; ++i) issue_next();
 #pragma unroll 1
-                while (c < raw) {
+                for (; c < raw; ++c) {
                     cp_async_wait<NR - 2>();
                     __syncwarp();
                     if (!(ok = wait_empty(c))) break;
-                    const uint8_t* at = slot(c);
-                    convert((c & 1) == 0, *reinterpret_cast<const float*>(at + C::RAW + (lw * 32 + lane) * 4),
-                            *reinterpret_cast<const uint32_t*>(at + C::RAW + TT * 4 + lw * 4));
+                    const uint8_t* sc = slot(c) + 2 * C::RAW_TILE;
+                    const uint32_t mask = *reinterpret_cast<const uint32_t*>(sc + 2 * TT * 4 + lw * 4);
+                    convert(true, *reinterpret_cast<const float*>(sc + (lw * 32 + lane) * 4), mask);
+                    convert(false, *reinterpret_cast<const float*>(sc + (TT + lw * 32 + lane) * 4), mask);
                     signal(c);  // (and the warp is done with the raw slot)
-                    ++c;
                     issue_next();
                 }
                 cp_async_wait<0>();
@@ -691,9 +687,11 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
         // ------------------------------------------------ softmax: a thread has a row
         const int w = warp >> 2, r = tid & (kTreeRows - 1);
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t t_o = tmem + C::S_COLS + w * DP + lanes;
-        uint32_t q_phase = 0, s_phase = 0, o_phase = 0, x_phase = 0;
-        int tiles = 0;
+        const uint32_t t_o = tmem + C::O_AT + w * DP + lanes;
+        uint32_t q_phase = 0, s_phase = 0, x_phase = 0;
+        // products with values: of the tiles so far, and those known to have reached the accumulators
+        uint32_t tiles_done = 0, reached = 0;
+        int tiles = 0;  // stages of the ring
         uint32_t* anc = reinterpret_cast<uint32_t*>(smem + C::ANC_AT) + w * kTreeRows + r;  // words 128 * TILES apart
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t phase) {
@@ -714,7 +712,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             }
             // Few rows stand several times in the tile, and each copy's warps take a part of the tokens (with
             // sums of their own that meet at the end): the exponentials use all four schedulers.
-            const int rep = TILES == 2 || rows > 64 ? 1 : rows > 32 ? 2 : 4;
+            const int rep = TILES == 2 || TT < 64 || rows > 64 ? 1 : rows > 32 ? 2 : 4;
             const int fold = kTreeRows / rep - 1, lr = r & fold;  // the thread's row
             const int cols = TT / rep, col0 = r / (fold + 1) * cols;
             // --- the queries: the tile's rows, 16 bytes a lane; the parents ---
@@ -727,7 +725,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                         if (r + i * kTreeRows < g.s.n) up[i] = __ldg(p.parents + g.s.first + r + i * kTreeRows);
                 }
                 constexpr int LPR = DP / 8, RPI = kTreeRows / LPR;  // lanes of a row, rows of a round
-                constexpr int BATCH = C::LOADERS ? 4 : 8;           // rounds in flight
+                constexpr int BATCH = 8;                            // rounds in flight
                 const int ch = r % LPR;
 #pragma unroll
                 for (int i0 = 0; i0 < LPR; i0 += BATCH) {
@@ -817,57 +815,63 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             // the first token that the row sees of the context (of all, in a chain)
             const int since = p.window > 0 ? max(g.s.ctx + depth - p.window + 1, 0) : 0;
             const float qf = E4M3 ? s_qf[w][r] : p.scale_log2;  // positive factor of the scores
-            if (!C::OVER && rep > 1) {  // probabilities of the other copies' tokens
+            if (rep > 1) {  // probabilities of the other copies' tokens
                 const uint32_t z[16] = {};
                 for (int k = 0; k < TT; k += 16) tmem_st16(tmem + C::P_AT + lanes + k, z);
                 tmem_st_wait();
             }
 
             float m = -INFINITY;  // e4m3: largest score (before qf)
-            // the power of two that sums are about; their two halves
-            float base = kNoWeights;
-            uint64_t sum = 0;
+            float base = kNoWeights;       // the power of two that sums are about
+            uint64_t sum[4] = {0, 0, 0, 0};  // in eight parts
+            // all products so far have reached the accumulators (a parity tells only neighbours apart: each phase is
+            // waited for, or known to have passed)
+            auto reach = [&]() {
+                for (; reached != tiles_done && ok; ++reached) ok = wait(&o_bar[w], reached);
+            };
 #pragma unroll 1
             for (int j = 0; j < g.n; ++j, ++tiles) {
                 const int buf = TILES == 2 ? w : j & 1;
-                ok = wait(&meta_bar[tiles % C::META], tiles / C::META) && wait(&s_bar[buf], s_phase >> buf);
+                ok = wait(&s_bar[buf], s_phase >> buf);
                 s_phase ^= 1u << buf;
                 if (!ok) break;
                 tc_fence_after();
-                // the products of the tile before have reached the accumulators (each phase is waited for: a
-                // parity tells only neighbours apart)
-                bool reached = j == 0;
-                auto reach = [&]() {
-                    if (!reached) ok = wait(&o_bar[w], o_phase ^ 1u);
-                    reached = true;
-                };
-                const uint8_t* meta = smem + C::META_AT + (tiles % C::META) * C::META_BYTES;
+                // The tile's keys, values and scales are there (its scores waited for them), and the products issued
+                // before its scores, up to those of the tile before the last, are done.
+                if (j > 0) reached = tiles_done - 1;
+                const uint8_t* meta = smem + C::META_AT + (tiles % NS) * C::META;
                 bool all = true;  // the tile's tokens are there
 #pragma unroll
                 for (int k = 0; k < TT / 32; ++k) all = all && reinterpret_cast<const uint32_t*>(meta)[k] == kAllLanes;
                 if (TMA && !E4M3 && !all && w == 0) {
                     // a copied piece may hold anything behind the last token (before the first, on a bad page):
                     // such values become 0, whose product with a probability of 0 is 0
-                    const int i = (2 * tiles + 1) % NB;
-                    if (!(ok = wait(&full_bar[i], (2 * tiles + 1) / NB))) break;
+                    if (!(ok = wait(&full_bar[tiles % NS], tiles / NS))) break;
                     if (r < TT && !((reinterpret_cast<const uint32_t*>(meta)[r >> 5] >> (r & 31)) & 1u))
                         for (int k = 0; k < p.D / 8; ++k)
-                            *reinterpret_cast<uint4*>(smem + C::KV_AT + i * C::KV_TILE + tile_at(TT, r, k)) =
+                            *reinterpret_cast<uint4*>(smem + C::KV_AT + (tiles % NS) * C::STAGE + C::KV_TILE + tile_at(TT, r, k)) =
                                 make_uint4(0, 0, 0, 0);
                     fence_async_shared();
                 }
                 if (warp_act) {
-                    const uint32_t t_s = tmem + buf * TT + lanes, t_p = tmem + C::P_AT + buf * C::P_STEP + lanes;
+                    const uint32_t t_s = tmem + buf * TT + lanes, t_p = tmem + C::P_AT + buf * (TT / 2) + lanes;
                     const int t0 = g.s.start + (g.tile + j) * TT;
                     const bool masked = g.s.ctx - t0 < TT || !all || __any_sync(kAllLanes, since > t0);
                     const float* scales = reinterpret_cast<const float*>(meta + 32);
                     float room = kSlack + kLift<KV>;  // above base, for a score (e4m3: for a weight, less the scales)
                     if constexpr (E4M3) {
                         const float* v = reinterpret_cast<const float*>(meta + 16);  // largest, of each loading warp
-                        float most = fmaxf(kLeastScale, fmaxf(v[0], v[1]));
-                        if (C::LOADERS == 4) most = fmaxf(most, fmaxf(v[2], v[3]));
+                        float most = kLeastScale;
+#pragma unroll
+                        for (int i = 0; i < C::LOADERS; ++i) most = fmaxf(most, v[i]);
                         room = kMostWeight - __log2f(most);
                     }
+                    // the row tile's next scores may come (two row tiles)
+                    auto read_scores = [&]() {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&read_bar[w]));
+                    };
                     // W scores from column c0 on: what the sums are about, seldom moved; probabilities (e4m3: weights),
                     // rounded to 16 bits
                     auto part = [&](auto wide, int c0) {
@@ -876,6 +880,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                         if constexpr (W == 16) tmem_ld16(t_s + c0, y);
                         if constexpr (W == 32) tmem_ld32(t_s + c0, y);
                         if constexpr (W == 64) tmem_ld64(t_s + c0, y);
+                        if (TILES == 2 && c0 + W == TT) read_scores();
                         uint64_t s[W / 2];
 #pragma unroll
                         for (int i = 0; i < W / 2; ++i) s[i] = f32x2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
@@ -945,7 +950,8 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                             }
                             const float f = ex2_approx(base - n);
                             base = n;
-                            sum = f32x2_mul(sum, f32x2(f, f));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) sum[i] = f32x2_mul(sum[i], f32x2(f, f));
                             reach();
                             if (!ok) return;
                             tc_fence_after();
@@ -973,15 +979,19 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                             }
                         }
                         const uint64_t qq = f32x2(qf, qf), bb = f32x2(-base, -base);
-                        uint64_t sum2 = 0;
+                        if (TILES == 2) {  // the columns of the probabilities are read by the products of the tile before
+                            reach();
+                            if (!ok) return;
+                            tc_fence_after();
+                        }
                         uint32_t z[W / 2];
 #pragma unroll
                         for (int i = 0; i < W / 2; i += 2) {
                             const float2 a = f32x2_get(f32x2_fma(s[i], qq, bb)), b = f32x2_get(f32x2_fma(s[i + 1], qq, bb));
                             uint64_t e0 = f32x2(ex2_approx(a.x), ex2_approx(a.y)),
                                      e1 = f32x2(ex2_approx(b.x), ex2_approx(b.y));
-                            sum = f32x2_add(sum, e0);
-                            sum2 = f32x2_add(sum2, e1);
+                            sum[i & 2] = f32x2_add(sum[i & 2], e0);
+                            sum[(i & 2) + 1] = f32x2_add(sum[(i & 2) + 1], e1);
                             if constexpr (E4M3) {
                                 const float4 v = *reinterpret_cast<const float4*>(scales + TT + c0 + 2 * i);
                                 e0 = f32x2_mul(e0, f32x2(v.x, v.y));
@@ -991,14 +1001,11 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                             z[i] = pack2<F16>(u0.x, u0.y);
                             z[i + 1] = pack2<F16>(u1.x, u1.y);
                         }
-                        sum = f32x2_add(sum, sum2);
                         if constexpr (W == 16) tmem_st8(t_p + c0 / 2, z);
                         if constexpr (W == 32) tmem_st16(t_p + c0 / 2, z);
                         if constexpr (W == 64) tmem_st32(t_p + c0 / 2, z);
                     };
-                    // the columns of the probabilities are read by the products of the tile before
-                    if (TILES == 2 && !C::OVER) reach();
-                    if constexpr (TILES == 1) {
+                    if constexpr (TILES == 1 && TT == 64) {
                         if (rep == 4) {
                             part(std::integral_constant<int, 16>(), col0);
                         } else if (rep == 2) {
@@ -1009,27 +1016,27 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
 #pragma unroll
                         for (int c0 = 0; c0 < TT; c0 += C::WIDE)
                             if (ok) part(std::integral_constant<int, C::WIDE>(), c0);
-                    } else if (C::OVER) {  // the scores of the other copies' tokens become probabilities of 0
-                        const uint32_t z[8] = {};
-                        for (int k = 0; k < TT; k += 16)
-                            if (k < col0 || k >= col0 + cols) tmem_st8(t_p + k / 2, z);
                     }
                     if (!ok) break;
                     tmem_st_wait();
                     tc_fence_before();
                 }
-                reach();
+                if (TILES == 2 && !warp_act && lane == 0) mbar_arrive(smem_u32(&read_bar[w]));
+                // Two row tiles: the next scores may come before the others' probabilities, a warp without rows keeps
+                // behind them.  The last tile: one phase is left to wait for afterwards.
+                if (TILES == 2 || j == g.n - 1) reach();
                 if (!ok) break;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&p_bar[buf]));
-                o_phase ^= 1u;  // the phase of this tile's products
+                ++tiles_done;
             }
             if (!ok) break;
-            if (!(ok = wait(&o_bar[w], o_phase ^ 1u))) break;
+            reach();
+            if (!ok) break;
             tc_fence_after();
             // --- the row, or the run's part of it ---
             constexpr int ROWS = TILES * kTreeRows;
-            const float2 halves = f32x2_get(sum);
+            const float2 halves = f32x2_get(f32x2_add(f32x2_add(sum[0], sum[1]), f32x2_add(sum[2], sum[3])));
             float l = halves.x + halves.y;
             if (base == kNoWeights) base = -INFINITY;  // no tokens
             const bool done = p.whole || (g.starts && g.ends);
@@ -1143,7 +1150,7 @@ cudaError_t launch_tree_t(const CUtensorMap& tmK, const CUtensorMap& tmV, const 
     using C = TreeCfg<DP, KV, TILES, TMA>;
     // (a CTA's fixed arrays and what the system keeps of its shared memory: 1 KB each)
     static_assert((C::SMEM + 2048) * C::CTAS <= 228 * 1024, "shared memory of the resident CTAs");
-    static_assert(C::S_COLS + TILES * DP <= C::COLS && C::COLS * C::CTAS <= 512, "tensor memory");
+    static_assert(C::P_AT + C::TT <= C::COLS && C::COLS * C::CTAS <= 512, "tensor memory");
     const auto kernel = tree_kernel<DP, KV, TILES, TMA>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
