@@ -549,9 +549,10 @@ moe_status moe_paged_attention(const moe_kv_cache* cache, const void* q, int dty
  *   calls that may overlap need one each
  *   status: a device error word for moe_read_device_status, or NULL
  * Limits: those of the cache; q_heads a multiple of kv_heads, at most 4096; 1 <= N < 2^27;
- * 1 <= B <= 65536; table_width * page_size at most 2^31 - 256; q and out: pointers and
- * strides multiples of 16 bytes.  The result is the same for every run of the same call.
- * Asynchronous on `stream`.
+ * 1 <= B <= 65536; table_width * page_size at most 2^31 - 256; (N * q_heads / kv_heads /
+ * 128 + B) * kv_heads * (tokens that a draft can see / 32 + 16) < 2^31; q and out:
+ * pointers and strides multiples of 16 bytes.  The result is the same for every run of the
+ * same call.  Asynchronous on `stream`.
  */
 size_t moe_tree_attention_workspace_size(int N, int B, int q_heads, int kv_heads, int head_dim, int cache_dtype,
                                          int max_tokens);

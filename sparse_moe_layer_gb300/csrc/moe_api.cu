@@ -1053,6 +1053,11 @@ extern "C" moe_status moe_tree_attention(const moe_kv_cache* cache, const void* 
     // token numbers, rounded up to a tile, fit 31 bits
     const long long most = (long long)table_width * cache->page_size;
     if (most > (1LL << 31) - 256 || (B > 1 && table_ld < table_width)) return MOE_ERR_INVALID_ARG;
+    // and so do the tiles of all drafts, 128 rows by 32 tokens or more
+    const int group = q_heads / cache->kv_heads;
+    const long long seen = window > 0 && window < most ? window : most;
+    if ((double)((long long)N * group / 128 + B) * cache->kv_heads * (double)(seen / 32 + 16) > 2147000000.0)
+        return MOE_ERR_INVALID_ARG;
     if (dtype != MOE_BF16 && dtype != MOE_FP16) return MOE_ERR_UNSUPPORTED;
     if (cache->dtype != MOE_E4M3 && cache->dtype != dtype) return MOE_ERR_UNSUPPORTED;
     if (B == 1) table_ld = 0;
@@ -1066,7 +1071,7 @@ extern "C" moe_status moe_tree_attention(const moe_kv_cache* cache, const void* 
         return MOE_ERR_UNSUPPORTED;
     TreePlan w;
     tree_plan(N, B, q_heads, cache->kv_heads, cache->head_dim, cache->dtype == MOE_E4M3, cache->page_size, window,
-              (int)(window > 0 && window < most ? window : most), num_sms(), &w);
+              (int)seen, num_sms(), &w);
     if (w.total && !workspace) return MOE_ERR_INVALID_ARG;
     if (workspace_bytes < w.total) return MOE_ERR_WORKSPACE;
     p.q = static_cast<const uint16_t*>(q);

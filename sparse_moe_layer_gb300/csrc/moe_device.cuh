@@ -240,6 +240,16 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
+// The same with the wait itself out of line: for kernels with many waits.
+static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err,
+                                                   uint32_t err_bit) {
+    return mbar_wait(bar, parity, abort, err, err_bit);
+}
+__device__ __forceinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err,
+                                             uint32_t err_bit) {
+    return mbar_try_wait(bar, parity) || mbar_wait_long(bar, parity, abort, err, err_bit);
+}
+
 // ------------------------------------------------------- thread-block cluster ----
 __device__ __forceinline__ uint32_t cluster_ctarank() {
     uint32_t r;

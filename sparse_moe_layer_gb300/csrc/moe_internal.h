@@ -163,6 +163,7 @@ struct TreeParams {
     uint32_t* status;                      // error word or null
     // set at launch
     int group;      // query heads per key head
+    float inv_group;
     int page_shift; // log2(page_size), -1 if none
     int fp16;       // q and out are fp16, not bf16
     int whole;      // items are not cut

@@ -81,6 +81,7 @@ cudaError_t launch_tree(const CUtensorMap& tmK, const CUtensorMap& tmV, const Tr
     p.box = w.box;
     p.fp16 = fp16;
     p.group = p.Hq / p.Hkv;
+    p.inv_group = 1.f / (float)p.group;
     p.whole = w.whole;
     p.runs = w.ctas;
     p.page_shift = -1;

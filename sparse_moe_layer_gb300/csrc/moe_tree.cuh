@@ -104,8 +104,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
 
 // Where a run begins, and what it has: token tiles, or items where they are not cut.
 struct TreeWork {
-    int b, h, rt, tile;
-    long long rem;
+    int b, h, rt, tile, rem;
 };
 // A part of an item: token tiles [tile, tile + n) of it.
 struct TreeSeg {
@@ -114,46 +113,53 @@ struct TreeSeg {
     bool starts, ends;
 };
 
-template <int TT, int TILES>
+// Where a run is: the sequence of its next part, and what is left.
 struct TreeWalk {
-    const TreeParams& p;
     TreeWork w;
     TreeSeq s;
-    __device__ __forceinline__ TreeWalk(const TreeParams& p_, const TreeWork& w_) : p(p_), w(w_) {
-        if (w.rem > 0) s = tree_seq<TT, TILES>(p, w.b);
-    }
-    __device__ __forceinline__ bool next(TreeSeg& g) {
-        if (w.rem <= 0) return false;
-        const int left = s.ntiles - w.tile;
-        g.s = s;
-        g.b = w.b;
-        g.h = w.h;
-        g.rt = w.rt;
-        g.tile = w.tile;
-        g.n = p.whole || left < w.rem ? left : (int)w.rem;
-        g.starts = w.tile == 0;
-        g.ends = g.n == left;
-        w.rem -= p.whole ? 1 : g.n;
-        w.tile += g.n;
-        if (g.ends) {
-            w.tile = 0;
-            if (++w.rt == s.rtiles) {
-                w.rt = 0;
-                if (++w.h == p.Hkv) {
-                    w.h = 0;
-                    if (w.rem > 0) do s = tree_seq<TT, TILES>(p, ++w.b);
-                        while (s.rtiles == 0);
-                }
+};
+// The next part of the run; false: none.
+template <int TT, int TILES>
+__device__ __forceinline__ bool tree_next(const TreeParams& p, TreeWalk& k, TreeSeg& g) {
+    TreeWork& w = k.w;
+    if (w.rem <= 0) return false;
+    const int left = k.s.ntiles - w.tile;
+    g.s = k.s;
+    g.b = w.b;
+    g.h = w.h;
+    g.rt = w.rt;
+    g.tile = w.tile;
+    g.n = p.whole || left < w.rem ? left : w.rem;
+    g.starts = w.tile == 0;
+    g.ends = g.n == left;
+    w.rem -= p.whole ? 1 : g.n;
+    w.tile += g.n;
+    if (g.ends) {
+        w.tile = 0;
+        if (++w.rt == k.s.rtiles) {
+            w.rt = 0;
+            if (++w.h == p.Hkv) {
+                w.h = 0;
+                if (w.rem > 0) do k.s = tree_seq<TT, TILES>(p, ++w.b);
+                    while (k.s.rtiles == 0);
             }
         }
-        return true;
+    }
+    return true;
+}
+
+// A place in a ring of N stages.
+template <int N>
+struct TreeRing {
+    int at = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) at = 0, phase ^= 1u;
     }
 };
 
-// a / b of numbers >= 0, in 32 bits where they fit
-__device__ __forceinline__ long long tree_quotient(long long a, int b) {
-    return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
-}
+// Draft of row `at` of a sequence (rounded once, and far from a border: rows are below 2^20).
+__device__ __forceinline__ int tree_draft(const TreeParams& p, int at) { return (int)(((float)at + 0.5f) * p.inv_group); }
 
 // Bits lo and on of 32.
 __device__ __forceinline__ uint32_t bits_from(int lo) { return lo <= 0 ? kAllLanes : lo >= 32 ? 0u : kAllLanes << lo; }
@@ -165,7 +171,8 @@ __device__ __forceinline__ uint32_t tile_at(int rows, int r, int c) {
 
 template <int DP, int KV, int TILES, bool TMA>
 __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<DP, KV, TILES, TMA>::CTAS)
-    tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, TreeParams p) {
+    tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                const __grid_constant__ TreeParams p) {
     using C = TreeCfg<DP, KV, TILES, TMA>;
     constexpr bool E4M3 = C::E4M3, F16 = KV != kKvBf16;  // F16: type of the products
     const bool qf16 = E4M3 ? p.fp16 : F16;               // of q and out
@@ -183,7 +190,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t smem_s = smem_u32(smem);
-    long long* s_pre = reinterpret_cast<long long*>(smem);  // [THREADS + 1], before the tiles come
+    int* s_pre = reinterpret_cast<int*>(smem);  // [THREADS + 1], before the tiles come
 
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -214,25 +221,27 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
 
     // --- the run: each thread counts a slice of the sequences ---
     const int slice = (p.B + THREADS - 1) / THREADS;
-    long long mine = 0;
+    int mine = 0;
+#pragma unroll 1
     for (int i = 0; i < slice; ++i) {
         const int b = tid * slice + i;
         if (b < p.B) {
             const TreeSeq s = tree_seq<TT, TILES>(p, b);
-            mine += (long long)p.Hkv * s.rtiles * (p.whole ? 1 : s.ntiles);
+            mine += p.Hkv * s.rtiles * (p.whole ? 1 : s.ntiles);
         }
     }
     s_pre[tid + 1] = mine;
     if (tid == 0) s_pre[0] = 0;
     __syncthreads();
     if (warp == 0) {  // prefix sums, 32 at a time
-        long long before = 0;
+        int before = 0;
         const int slices = (p.B + slice - 1) / slice;
+#pragma unroll 1
         for (int base = 0; base < slices; base += 32) {
-            long long v = s_pre[base + lane + 1];
+            int v = s_pre[base + lane + 1];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(kAllLanes, v, o);
+                const int u = __shfl_up_sync(kAllLanes, v, o);
                 if (lane >= o) v += u;
             }
             v += before;
@@ -240,27 +249,26 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             before = __shfl_sync(kAllLanes, v, 31);
         }
         __syncwarp();
-        const long long total = before, least = p.whole ? 1 : kMinTiles;
-        const long long want = tree_quotient(total + least - 1, (int)least);
-        const int n = (int)(want < p.runs ? want : p.runs), run = blockIdx.x;
+        const int total = before, n = min(p.whole ? total : (total + kMinTiles - 1) / kMinTiles, p.runs), run = blockIdx.x;
         TreeWork w = {0, 0, 0, 0, 0};
         if (run < n) {
-            const long long each = tree_quotient(total, n);
-            const int more = (int)(total - each * n), from = more * run / n;  // (n is small)
-            long long u = each * run + from;
+            const int each = total / n, more = total - each * n, from = more * run / n;  // (n is small)
+            int u = each * run + from;
             w.rem = each + more * (run + 1) / n - from;
             int sl = 0;
+#pragma unroll 1
             for (int base = 0; base < slices; base += 32)
                 sl += __popc(__ballot_sync(kAllLanes, s_pre[base + lane + 1] <= u));
             u -= s_pre[sl];
             w.b = sl * slice;
+#pragma unroll 1
             while (true) {
                 const TreeSeq s = tree_seq<TT, TILES>(p, w.b);
                 const int nt = p.whole ? 1 : s.ntiles;
-                const long long here = (long long)p.Hkv * s.rtiles * nt;
+                const int here = p.Hkv * s.rtiles * nt;
                 if (u < here) {
-                    const int item = (int)tree_quotient(u, nt);
-                    w.tile = (int)(u - (long long)item * nt);
+                    const int item = u / nt;
+                    w.tile = u - item * nt;
                     w.h = item / s.rtiles;
                     w.rt = item - w.h * s.rtiles;
                     break;
@@ -279,8 +287,11 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     volatile int* abort_p = &abort_flag;
-    TreeWalk<TT, TILES> walk(p, s_work);
+    TreeWalk walk;
     TreeSeg g;
+    walk.w = s_work;
+    if (walk.w.rem > 0) walk.s = tree_seq<TT, TILES>(p, walk.w.b);
+    auto next_part = [&]() { return tree_next<TT, TILES>(p, walk, g); };
 
     if (warp == C::MMA_WARP) {
         // ------------------------------------------------ the products
@@ -289,20 +300,20 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
         const uint32_t id_o = idesc_f16_f32(F16, kTreeRows, p.D, true);
         const int ksteps = p.D / 16;
         const bool issuer = elect_one();
-        int c = 0;  // tiles so far: stages of the ring
+        TreeRing<NS> c, ahead;  // stages of the tile whose values are next, and whose keys are
         uint32_t q_phase = 0, p_phase = 0, read_phase = 0;  // bit i: phase of row tile (score buffer) i
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t phase) {
-            const bool r = mbar_wait(smem_u32(bar), phase & 1u, abort_p, p.status, kErrTimeoutMma);
+            const bool r = mbar_wait_on(smem_u32(bar), phase & 1u, abort_p, p.status, kErrTimeoutMma);
             return __all_sync(kAllLanes, r) != 0;
         };
-        auto full = [&](int i) { return wait(&full_bar[i % NS], i / NS); };
+        auto full = [&]() { return wait(&full_bar[ahead.at], ahead.phase); };
         // descriptors: a start address in 16-byte units in the low bits, so steps are additions
         const uint64_t q_desc = smem_desc_sw128(smem_s + C::Q_AT), k_desc = smem_desc_sw128(smem_s + C::KV_AT),
                        v_desc = smem_desc_sw128_mn(smem_s + C::KV_AT + C::KV_TILE, TT * 128);
-        auto scores = [&](int w, int buf, int stage) {
+        auto scores = [&](int w, int buf) {
             if (issuer) {
-                const uint64_t a = q_desc + w * (C::Q_TILE >> 4), b = k_desc + (stage % NS) * (C::STAGE >> 4);
+                const uint64_t a = q_desc + w * (C::Q_TILE >> 4), b = k_desc + ahead.at * (C::STAGE >> 4);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
                     if (k < ksteps)
@@ -311,9 +322,9 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 mma_commit(smem_u32(&s_bar[buf]));
             }
         };
-        auto values = [&](int w, int buf, int stage, bool first) {
+        auto values = [&](int w, int buf, bool first) {
             if (issuer) {
-                const uint64_t b = v_desc + (stage % NS) * (C::STAGE >> 4);
+                const uint64_t b = v_desc + c.at * (C::STAGE >> 4);
 #pragma unroll
                 for (int k = 0; k < TT / 16; ++k)
                     mma_16bit_tmem_a(tmem + C::O_AT + w * DP, tmem + C::P_AT + buf * (TT / 2) + 8 * k,
@@ -321,15 +332,12 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 mma_commit(smem_u32(&o_bar[w]));
             }
         };
-        auto release = [&](int i) {
-            if (issuer) mma_commit(smem_u32(&empty_bar[i % NS]));
-        };
         auto probabilities = [&](int buf) {
             const bool r = wait(&p_bar[buf], p_phase >> buf);
             p_phase ^= 1u << buf;
             return r;
         };
-        while (ok && walk.next(g)) {
+        while (ok && next_part()) {
             const int act = TILES == 2 && g.s.n * p.group - g.rt * 2 * kTreeRows > kTreeRows ? 2 : 1;
 #pragma unroll
             for (int w = 0; w < TILES; ++w)
@@ -337,50 +345,55 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                     ok = wait(&q_bar[w], q_phase >> w);
                     q_phase ^= 1u << w;
                 }
-            if (!ok || !(ok = full(c))) break;
+            if (!ok || !(ok = full())) break;
             tc_fence_after();
 #pragma unroll
             for (int w = 0; w < TILES; ++w)
-                if (w < act) scores(w, w, c);
+                if (w < act) scores(w, w);
+            ahead.next();
             // Products of different accumulators keep no order: what a product writes over has been read, by
             // the row tile's threads (scores), or by products that they waited for (probabilities).
-            for (int j = 0; j < g.n && ok; ++j, ++c) {
+#pragma unroll 1
+            for (int j = 0; j < g.n && ok; ++j) {
                 const bool more = j + 1 < g.n;
                 if constexpr (TILES == 1) {
                     if (more) {
-                        if (!(ok = full(c + 1))) break;
+                        if (!(ok = full())) break;
                         tc_fence_after();
-                        scores(0, (j + 1) & 1, c + 1);
+                        scores(0, (j + 1) & 1);
+                        ahead.next();
                     }
                     if (!(ok = probabilities(j & 1))) break;
                     tc_fence_after();
-                    values(0, j & 1, c, j == 0);
+                    values(0, j & 1, j == 0);
                 } else {
 #pragma unroll
                     for (int w = 0; w < TILES; ++w) {
                         if (w >= act || !ok) continue;
-                        ok = wait(&read_bar[w], read_phase >> w) && (w > 0 || !more || full(c + 1));
+                        ok = wait(&read_bar[w], read_phase >> w) && (w > 0 || !more || full());
                         read_phase ^= 1u << w;
                         if (!ok || !more) continue;
                         tc_fence_after();
-                        scores(w, w, c + 1);
+                        scores(w, w);
                     }
+                    if (more) ahead.next();
 #pragma unroll
                     for (int w = 0; w < TILES; ++w) {
                         if (w >= act || !ok) continue;
                         if (!(ok = probabilities(w))) continue;
                         tc_fence_after();
-                        values(w, w, c, j == 0);
+                        values(w, w, j == 0);
                     }
                     if (!ok) break;
                 }
-                release(c);
+                if (issuer) mma_commit(smem_u32(&empty_bar[c.at]));
+                c.next();
             }
         }
         // every issued product has finished once this commit lands
         if (issuer) mma_commit(smem_u32(&end_bar));
         int dummy = 0;
-        mbar_wait(smem_u32(&end_bar), 0, &dummy, p.status, kErrTimeoutMma);
+        mbar_wait_on(smem_u32(&end_bar), 0, &dummy, p.status, kErrTimeoutMma);
         __syncwarp();
     } else if (warp >= TILES * 4) {
         // ------------------------------------------------ keys and values
@@ -388,41 +401,37 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
         constexpr int RPS = 32 / CH, STEPS = 32 / RPS;       // tokens of a step of a loading warp
         const int lw = warp - TILES * 4, ch = lane % CH, r0 = lane / CH;
         const bool in = ch * (16 / ES) < p.D;
-        int c = 0;  // tiles begun: stages filled
+        TreeRing<NS> c;  // the stage to fill
+        int filled = 0;
         bool ok = true;
-        auto wait = [&](uint64_t* bar, int phase) {
-            const bool r = mbar_wait(smem_u32(bar), (uint32_t)phase & 1u, abort_p, p.status, kErrTimeoutProducer);
+        auto wait = [&](uint64_t* bar, uint32_t phase) {
+            const bool r = mbar_wait_on(smem_u32(bar), phase & 1u, abort_p, p.status, kErrTimeoutProducer);
             return __all_sync(kAllLanes, r) != 0;
         };
-        auto wait_empty = [&](int i) { return i < NS || wait(&empty_bar[i % NS], i / NS - 1); };
-        // stage i is filled (all lanes did, or waited for, their part)
-        auto signal = [&](int i) {
+        auto wait_empty = [&]() { return filled < NS || wait(&empty_bar[c.at], c.phase ^ 1u); };
+        // a stage is filled (all lanes did, or waited for, their part)
+        auto signal = [&](int at) {
             fence_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&full_bar[i % NS]));
+            if (lane == 0) mbar_arrive(smem_u32(&full_bar[at]));
         };
-        auto stage = [&](int i) { return smem_s + C::KV_AT + (i % NS) * C::STAGE; };
-        auto meta = [&](int i) { return smem + C::META_AT + (i % NS) * C::META; };
-        // a token (or piece of box tokens) of a lane, its page looked up before the copies need it
+        auto stage = [&]() { return smem_s + C::KV_AT + c.at * C::STAGE; };
+        auto meta = [&]() { return smem + C::META_AT + c.at * C::META; };
+        // a lane's token, its page looked up before the copies need it
         struct Token {
             int pid, off, h;
-            int t0;  // first token of the tile, from the sequence's first seen one and last on: lo, len
-            int lo, len;
             bool in;
         };
         int tile = 0;
-        bool any = walk.next(g);
-        // the next tile's, of lane's token `at` of `n`
-        auto take = [&](bool& has, int at, int n, bool used) {
-            Token t = {-1, 0, 0, 0, 0, 0, false};
+        bool any = next_part();
+        // token `at` of the next tile
+        auto take = [&](bool& has, int at) {
+            Token t = {-1, 0, 0, false};
             has = any;
             if (!any) return t;
-            t.t0 = g.s.start + (g.tile + tile) * TT;
-            t.lo = g.s.lo;
-            t.len = g.s.len;
             t.h = g.h;
-            const int tok = t.t0 + at;
-            if (used && tok + n > t.lo && tok < t.len) {
+            const int tok = g.s.start + (g.tile + tile) * TT + at;
+            if (tok >= g.s.lo && tok < g.s.len) {
                 const int pi = p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_size;
                 t.off = tok - pi * p.page_size;
                 t.pid = __ldg(p.table + (long long)g.b * p.table_ld + pi);
@@ -430,7 +439,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             }
             if (++tile == g.n) {
                 tile = 0;
-                any = walk.next(g);
+                any = next_part();
             }
             return t;
         };
@@ -442,82 +451,138 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
         };
 
         if (TMA && warp == C::TMA_WARP) {
-            // a lane has a piece of box tokens of the tile
-            const int pieces = TT / p.box;
+            // pieces of box tokens; 32 of them, a lane's each, are looked up together, a batch of tiles ahead
+            const int pieces = TT / p.box, per = 32 / pieces;
             const int blocks = E4M3 ? 1 : (p.D + 63) / 64;
             const bool issuer = elect_one();
-            bool has;
-            Token t = take(has, lane * p.box, p.box, lane < pieces);
-            for (; has; ++c) {
-                const Token u = t;
-                t = take(has, lane * p.box, p.box, lane < pieces);
-                const bool good = on_page(u);
-                const uint32_t copied = __ballot_sync(kAllLanes, good), bad = __ballot_sync(kAllLanes, u.in && !good);
-                ok = E4M3 ? c < NR || wait(&raw_empty_bar[c % NR], c / NR - 1) : wait_empty(c);
-                if (!ok) break;
-                if (!E4M3 && lane < TT / 32) {  // valid tokens, 32 a lane
-                    const int w0 = u.t0 + 32 * lane;
-                    uint32_t v = bits_from(u.lo - w0) & ~bits_from(u.len - w0);
-                    for (uint32_t b = bad; b; b &= b - 1) {
-                        const int at = (__ffs(b) - 1) * p.box - 32 * lane;
-                        v &= ~(bits_from(at) & ~bits_from(at + p.box));
-                    }
-                    reinterpret_cast<uint32_t*>(meta(c))[lane] = v;
+            TreeRing<NR> raw;
+            struct Batch {
+                int pid, off, h, t0, lo, len, n;
+                bool in;
+            };
+            auto look_up = [&]() {
+                Batch t;
+                t.n = 0;
+                if (!any) return t;
+                t.n = min(per, g.n - tile);
+                t.t0 = g.s.start + (g.tile + tile) * TT;
+                t.lo = g.s.lo;
+                t.len = g.s.len;
+                t.h = g.h;
+                t.pid = t.off = 0;
+                const int tok = t.t0 + lane * p.box;
+                t.in = lane < t.n * pieces && tok + p.box > t.lo && tok < t.len;
+                if (t.in) {
+                    const int pi = p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_size;
+                    t.off = tok - pi * p.page_size;
+                    t.pid = __ldg(p.table + (long long)g.b * p.table_ld + pi);
                 }
-                __syncwarp();
-                const uint32_t bar = smem_u32(E4M3 ? &raw_full_bar[c % NR] : &full_bar[c % NS]);
-                const uint32_t to = E4M3 ? smem_s + C::RAW_AT + (c % NR) * C::RAW_STAGE : stage(c);
-                if (issuer) mbar_arrive_expect_tx(bar, 2 * __popc(copied) * p.box * (E4M3 ? p.D : 128 * blocks));
-                // one lane issues all (lanes that issue a piece each take 100 cycles a piece), four at a time
-                for (int i0 = 0; i0 < pieces; i0 += 4) {
-                    int pid[4], off[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        pid[i] = __shfl_sync(kAllLanes, u.pid, i0 + i);
-                        off[i] = __shfl_sync(kAllLanes, u.off, i0 + i);
+                tile += t.n;
+                if (tile == g.n) {
+                    tile = 0;
+                    any = next_part();
+                }
+                return t;
+            };
+            Batch u;
+            u.n = 0;
+#pragma unroll 1
+            while (true) {
+                const Batch following = look_up();
+                const bool there = u.n && u.in && (uint32_t)u.pid < (uint32_t)p.num_pages;
+                if (u.n && u.in && !there && p.status) atomicOr(p.status, kErrBadIndex);
+                uint32_t copied = __ballot_sync(kAllLanes, there), bad = __ballot_sync(kAllLanes, u.n && u.in && !there);
+#pragma unroll 1
+                for (int j = 0; j < u.n; ++j) {
+                    ok = E4M3 ? filled < NR || wait(&raw_empty_bar[raw.at], raw.phase ^ 1u) : wait_empty();
+                    if (!ok) break;
+                    const uint32_t mine = pieces == 32 ? kAllLanes : (1u << pieces) - 1u;
+                    if (!E4M3) {
+                        if (lane < TT / 32) {  // valid tokens, 32 a lane
+                            const int w0 = u.t0 + j * TT + 32 * lane;
+                            uint32_t v = bits_from(u.lo - w0) & ~bits_from(u.len - w0);
+#pragma unroll 1
+                            for (uint32_t b = bad & mine; b; b &= b - 1) {
+                                const int at = (__ffs(b) - 1) * p.box - 32 * lane;
+                                v &= ~(bits_from(at) & ~bits_from(at + p.box));
+                            }
+                            reinterpret_cast<uint32_t*>(meta())[lane] = v;
+                        }
+                        __syncwarp();
                     }
-                    if (issuer) {
+                    const uint32_t bar = smem_u32(E4M3 ? &raw_full_bar[raw.at] : &full_bar[c.at]);
+                    const uint32_t to = E4M3 ? smem_s + C::RAW_AT + raw.at * C::RAW_STAGE : stage();
+                    if (issuer)
+                        mbar_arrive_expect_tx(bar, 2 * __popc(copied & mine) * p.box * (E4M3 ? p.D : 128 * blocks));
+                    // one lane issues all (lanes that issue a piece each take 100 cycles a piece), four at a time
+#pragma unroll 1
+                    for (int i0 = 0; i0 < pieces; i0 += 4) {
+                        int pid[4], off[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            if (!((copied >> (i0 + i)) & 1u)) continue;
-                            if (E4M3) {
-                                const uint32_t at = to + (i0 + i) * p.box * p.D;
-                                tma_load_4d(at, &tmK, 0, off[i], u.h, pid[i], bar);
-                                tma_load_4d(at + C::RAW_TILE, &tmV, 0, off[i], u.h, pid[i], bar);
-                            } else {
-                                const uint32_t at = to + (i0 + i) * p.box * 128;
+                            pid[i] = __shfl_sync(kAllLanes, u.pid, j * pieces + i0 + i);
+                            off[i] = __shfl_sync(kAllLanes, u.off, j * pieces + i0 + i);
+                        }
+                        if (issuer) {
 #pragma unroll
-                                for (int k = 0; k < DP / 64; ++k) {
-                                    if (k >= blocks) continue;
-                                    tma_load_4d(at + k * TT * 128, &tmK, k * 64, off[i], u.h, pid[i], bar);
-                                    tma_load_4d(at + C::KV_TILE + k * TT * 128, &tmV, k * 64, off[i], u.h, pid[i], bar);
+                            for (int i = 0; i < 4; ++i) {
+                                if (!(((copied & mine) >> (i0 + i)) & 1u)) continue;
+                                if (E4M3) {
+                                    const uint32_t at = to + (i0 + i) * p.box * p.D;
+                                    tma_load_4d(at, &tmK, 0, off[i], u.h, pid[i], bar);
+                                    tma_load_4d(at + C::RAW_TILE, &tmV, 0, off[i], u.h, pid[i], bar);
+                                } else {
+                                    const uint32_t at = to + (i0 + i) * p.box * 128;
+#pragma unroll
+                                    for (int k = 0; k < DP / 64; ++k) {
+                                        if (k >= blocks) continue;
+                                        tma_load_4d(at + k * TT * 128, &tmK, k * 64, off[i], u.h, pid[i], bar);
+                                        tma_load_4d(at + C::KV_TILE + k * TT * 128, &tmV, k * 64, off[i], u.h, pid[i], bar);
+                                    }
                                 }
                             }
                         }
                     }
+                    __syncwarp();
+                    copied = pieces == 32 ? 0u : copied >> pieces;
+                    bad = pieces == 32 ? 0u : bad >> pieces;
+                    ++filled;
+                    if (E4M3)
+                        raw.next();
+                    else
+                        c.next();
                 }
-                __syncwarp();
+                u = following;
+                if (!ok || u.n == 0) break;
             }
             // the last copies have landed before the CTA may exit
             constexpr int LAST = E4M3 ? NR : NS;
             int dummy = 0;
-            for (int i = max(0, c - LAST); i < c; ++i)
-                mbar_wait(smem_u32(E4M3 ? &raw_full_bar[i % LAST] : &full_bar[i % LAST]), (uint32_t)(i / LAST) & 1u, &dummy,
-                          p.status, kErrTimeoutProducer);
+#pragma unroll 1
+            for (int i = max(0, filled - LAST); i < filled; ++i)
+                mbar_wait_on(smem_u32(E4M3 ? &raw_full_bar[i % LAST] : &full_bar[i % LAST]), (uint32_t)(i / LAST) & 1u, &dummy,
+                             p.status, kErrTimeoutProducer);
         } else if constexpr (!E4M3) {
             // copies of tiles in flight behind the one issued last: a stage is free again once the products that
             // read it are done, which wait for no tile but the next
             constexpr int DEPTH = NS - 2;
-            bool has;
-            Token t = take(has, lw * 32 + lane, 1, true);
-            for (; has; ++c) {
+            TreeRing<NS> landed;
+            bool has = false;
+            Token t = {};
+#pragma unroll 1
+            while (true) {
                 Token u = t;
-                t = take(has, lw * 32 + lane, 1, true);
+                const bool had = has;
+                t = take(has, lw * 32 + lane);
+                if (!had) {
+                    if (!has) break;
+                    continue;
+                }
                 u.in = on_page(u);
                 const uint32_t mask = __ballot_sync(kAllLanes, u.in);  // valid tokens of the warp
                 if (!u.in) u.pid = u.off = 0;
-                if (!(ok = wait_empty(c))) break;
-                if (lane == 0) reinterpret_cast<uint32_t*>(meta(c))[lw] = mask;
+                if (!(ok = wait_empty())) break;
+                if (lane == 0) reinterpret_cast<uint32_t*>(meta())[lw] = mask;
                 const uint8_t* kb = static_cast<const uint8_t*>(p.cache.k) + (u.h * p.cache.k_head) * 2 + ch * 16;
                 const uint8_t* vb = static_cast<const uint8_t*>(p.cache.v) + (u.h * p.cache.v_head) * 2 + ch * 16;
                 const long long k_off = u.pid * p.cache.k_page + u.off * p.cache.k_token,
@@ -526,7 +591,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 for (int i = 0; i < STEPS; ++i) {
                     const int r = i * RPS + r0;
                     const long long ko = __shfl_sync(kAllLanes, k_off, r), vo = __shfl_sync(kAllLanes, v_off, r);
-                    const uint32_t at = stage(c) + tile_at(TT, lw * 32 + r, ch);
+                    const uint32_t at = stage() + tile_at(TT, lw * 32 + r, ch);
                     if (in) {
                         cp_async16z(at, kb + ko * 2, (mask >> r) & 1u);
                         cp_async16z(at + C::KV_TILE, vb + vo * 2, (mask >> r) & 1u);
@@ -534,21 +599,32 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
                 cp_async_wait<DEPTH>();
-                if (c >= DEPTH) signal(c - DEPTH);
+                if (filled >= DEPTH) {
+                    signal(landed.at);
+                    landed.next();
+                }
+                ++filled;
+                c.next();
+                if (!has) break;
             }
             cp_async_wait<0>();
             if (ok)
-                for (int i = max(0, c - DEPTH); i < c; ++i) signal(i);
+#pragma unroll 1
+                for (int i = min(DEPTH, filled); i > 0; --i) {
+                    signal(landed.at);
+                    landed.next();
+                }
         } else {
             // e4m3: raw codes become fp16.  By TMA: [token][D].  By threads: a lane copies, and later converts,
             // pieces of its own, [step][lane] 16 bytes.
             constexpr int LANES = C::LOADERS * 32, BATCH = STEPS < 8 ? STEPS : 8;
-            auto slot = [&](int i) { return smem + C::RAW_AT + (i % NR) * C::RAW_STAGE; };
-            // the keys (values) of stage c from raw slot c; sc: the scale of the lane's token, mask: the warp's
+            TreeRing<NR> raw;  // the slot to convert
+            auto slot = [&](int at) { return smem + C::RAW_AT + at * C::RAW_STAGE; };
+            // the keys (values) of a stage from a raw slot; sc: the scale of the lane's token, mask: the warp's
             // valid tokens
             auto convert = [&](bool is_k, float sc, uint32_t mask) {
-                const uint8_t* at = slot(c) + (is_k ? 0 : C::RAW_TILE);
-                const uint32_t dst = stage(c) + (is_k ? 0 : C::KV_TILE);
+                const uint8_t* at = slot(raw.at) + (is_k ? 0 : C::RAW_TILE);
+                const uint32_t dst = stage() + (is_k ? 0 : C::KV_TILE);
                 uint32_t some = 0;  // V: tokens with a value that is not 0
 #pragma unroll
                 for (int i0 = 0; i0 < STEPS; i0 += BATCH) {
@@ -586,7 +662,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                         }
                     }
                 }
-                uint8_t* m = meta(c);
+                uint8_t* m = meta();
                 // a head of zeros, which the append stores with a scale of 1 however small the others are,
                 // has no weight
                 if (!is_k && !((some >> lane) & 1u)) sc = 0.f;
@@ -614,31 +690,41 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                     }
                     return s;
                 };
-                bool has_t, has_s;
-                Token t = take(has_s, lw * 32 + lane, 1, true);
-                Scales s = scales(t);
-                t = take(has_t, lw * 32 + lane, 1, true);
-                for (; has_s; ++c) {
+                bool has_t = false, has_s = false;
+                Token t = {};
+                Scales s = {};
+#pragma unroll 1
+                while (true) {
                     const Scales u = s;
+                    const bool now = has_s;
                     has_s = has_t;
-                    s = scales(t);
-                    t = take(has_t, lw * 32 + lane, 1, true);
+                    if (has_s) s = scales(t);
+                    t = take(has_t, lw * 32 + lane);
+                    if (!now) {
+                        if (!has_s && !has_t) break;
+                        continue;
+                    }
                     const uint32_t mask = __ballot_sync(kAllLanes, u.in);
-                    ok = wait_empty(c) && wait(&raw_full_bar[c % NR], c / NR);
+                    ok = wait_empty() && wait(&raw_full_bar[raw.at], raw.phase);
                     if (!ok) break;
                     convert(true, u.k, mask);
                     convert(false, u.v, mask);
-                    signal(c);
-                    if (lane == 0) mbar_arrive(smem_u32(&raw_empty_bar[c % NR]));
+                    signal(c.at);
+                    if (lane == 0) mbar_arrive(smem_u32(&raw_empty_bar[raw.at]));
+                    ++filled;
+                    c.next();
+                    raw.next();
+                    if (!has_s) break;
                 }
             } else {
                 bool has;
-                Token t = take(has, lw * 32 + lane, 1, true);
-                int raw = 0;  // tiles whose copies are issued
+                Token t = take(has, lw * 32 + lane);
+                TreeRing<NR> issued;
+                int ahead = 0;  // tiles whose copies are issued
                 auto issue_next = [&]() {
                     if (has) {
                         Token u = t;
-                        t = take(has, lw * 32 + lane, 1, true);
+                        t = take(has, lw * 32 + lane);
                         u.in = on_page(u);
                         const uint32_t mask = __ballot_sync(kAllLanes, u.in);
                         if (!u.in) u.pid = u.off = 0;
@@ -646,7 +732,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                         const uint8_t* vb = static_cast<const uint8_t*>(p.cache.v) + u.h * p.cache.v_head;
                         const long long k_off = u.pid * p.cache.k_page + u.off * p.cache.k_token,
                                         v_off = u.pid * p.cache.v_page + u.off * p.cache.v_token;
-                        uint8_t* at = slot(raw);
+                        uint8_t* at = slot(issued.at);
                         const uint32_t dst = smem_u32(at);
 #pragma unroll
                         for (int i = 0; i < STEPS; ++i) {
@@ -662,22 +748,26 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                         cp_async4z(sc, p.cache.k_scale + s_off, u.in);
                         cp_async4z(sc + TT * 4, p.cache.v_scale + s_off, u.in);
                         if (lane == 0) *reinterpret_cast<uint32_t*>(at + 2 * C::RAW_TILE + 2 * TT * 4 + lw * 4) = mask;
-                        ++raw;
+                        ++ahead;
+                        issued.next();
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");  // (empty where nothing is left)
                 };
 #pragma unroll 1
                 for (int i = 0; i < NR - 1; ++i) issue_next();
 #pragma unroll 1
-                for (; c < raw; ++c) {
+                while (filled < ahead) {
                     cp_async_wait<NR - 2>();
                     __syncwarp();
-                    if (!(ok = wait_empty(c))) break;
-                    const uint8_t* sc = slot(c) + 2 * C::RAW_TILE;
+                    if (!(ok = wait_empty())) break;
+                    const uint8_t* sc = slot(raw.at) + 2 * C::RAW_TILE;
                     const uint32_t mask = *reinterpret_cast<const uint32_t*>(sc + 2 * TT * 4 + lw * 4);
                     convert(true, *reinterpret_cast<const float*>(sc + (lw * 32 + lane) * 4), mask);
                     convert(false, *reinterpret_cast<const float*>(sc + (TT + lw * 32 + lane) * 4), mask);
-                    signal(c);  // (and the warp is done with the raw slot)
+                    signal(c.at);  // (and the warp is done with the raw slot)
+                    ++filled;
+                    c.next();
+                    raw.next();
                     issue_next();
                 }
                 cp_async_wait<0>();
@@ -691,11 +781,11 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
         uint32_t q_phase = 0, s_phase = 0, x_phase = 0;
         // products with values: of the tiles so far, and those known to have reached the accumulators
         uint32_t tiles_done = 0, reached = 0;
-        int tiles = 0;  // stages of the ring
+        TreeRing<NS> c;  // the tile's stage
         uint32_t* anc = reinterpret_cast<uint32_t*>(smem + C::ANC_AT) + w * kTreeRows + r;  // words 128 * TILES apart
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t phase) {
-            const bool r = mbar_wait(smem_u32(bar), phase & 1u, abort_p, p.status, kErrTimeoutEpilogue);
+            const bool r = mbar_wait_on(smem_u32(bar), phase & 1u, abort_p, p.status, kErrTimeoutEpilogue);
             return __all_sync(kAllLanes, r) != 0;
         };
         // all of the row tile's threads (one row tile) have come so far
@@ -704,10 +794,10 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             x_phase ^= 1u;
             return wait(&x_bar, x_phase ^ 1u);
         };
-        while (ok && walk.next(g)) {
+        while (ok && next_part()) {
             const int rows = g.s.n * p.group - (g.rt * TILES + w) * kTreeRows;  // of this tile
             if (rows <= 0) {
-                tiles += g.n;
+                for (int i = g.n % (2 * NS); i > 0; --i) c.next();
                 continue;
             }
             // Few rows stand several times in the tile, and each copy's warps take a part of the tokens (with
@@ -736,7 +826,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                         const int row = r / LPR + (i0 + i) * RPI;
                         q[i] = make_uint4(0, 0, 0, 0);
                         if (ch * 8 < p.D && (row & fold) < rows) {
-                            const int at = (g.rt * TILES + w) * kTreeRows + (row & fold), d = at / p.group;
+                            const int at = (g.rt * TILES + w) * kTreeRows + (row & fold), d = tree_draft(p, at);
                             q[i] = *reinterpret_cast<const uint4*>(
                                 p.q + (g.s.first + d) * p.q_token +
                                 (long long)(g.h * p.group + at - d * p.group) * p.q_head + ch * 8);
@@ -790,7 +880,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             }
             // --- the row's place in the tree ---
             const bool act = lr < rows, warp_act = (lr & ~31) < rows;
-            const int at = (g.rt * TILES + w) * kTreeRows + min(lr, rows - 1), draft = at / p.group;
+            const int at = (g.rt * TILES + w) * kTreeRows + min(lr, rows - 1), draft = tree_draft(p, at);
             const int head = g.h * p.group + at - draft * p.group;
             const bool sees_drafts = g.s.start + (long long)(g.tile + g.n) * TT > g.s.ctx;
             if (!(ok = wait(&q_bar[w], q_phase))) break;
@@ -801,6 +891,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
 #pragma unroll
                 for (int k = 0; k < kMaxDrafts / 32; ++k) bits[k] = 0;
                 depth = -1;
+#pragma unroll 1
                 for (int a = draft; a >= 0; a = s_up[w][a]) {
                     ++depth;
                     if (p.window <= 0 || depth < p.window) {
@@ -817,6 +908,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             const float qf = E4M3 ? s_qf[w][r] : p.scale_log2;  // positive factor of the scores
             if (rep > 1) {  // probabilities of the other copies' tokens
                 const uint32_t z[16] = {};
+#pragma unroll 1
                 for (int k = 0; k < TT; k += 16) tmem_st16(tmem + C::P_AT + lanes + k, z);
                 tmem_st_wait();
             }
@@ -827,10 +919,11 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             // all products so far have reached the accumulators (a parity tells only neighbours apart: each phase is
             // waited for, or known to have passed)
             auto reach = [&]() {
+#pragma unroll 1
                 for (; reached != tiles_done && ok; ++reached) ok = wait(&o_bar[w], reached);
             };
 #pragma unroll 1
-            for (int j = 0; j < g.n; ++j, ++tiles) {
+            for (int j = 0; j < g.n; ++j, c.next()) {
                 const int buf = TILES == 2 ? w : j & 1;
                 ok = wait(&s_bar[buf], s_phase >> buf);
                 s_phase ^= 1u << buf;
@@ -839,17 +932,18 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 // The tile's keys, values and scales are there (its scores waited for them), and the products issued
                 // before its scores, up to those of the tile before the last, are done.
                 if (j > 0) reached = tiles_done - 1;
-                const uint8_t* meta = smem + C::META_AT + (tiles % NS) * C::META;
+                const uint8_t* meta = smem + C::META_AT + c.at * C::META;
                 bool all = true;  // the tile's tokens are there
 #pragma unroll
                 for (int k = 0; k < TT / 32; ++k) all = all && reinterpret_cast<const uint32_t*>(meta)[k] == kAllLanes;
                 if (TMA && !E4M3 && !all && w == 0) {
                     // a copied piece may hold anything behind the last token (before the first, on a bad page):
                     // such values become 0, whose product with a probability of 0 is 0
-                    if (!(ok = wait(&full_bar[tiles % NS], tiles / NS))) break;
+                    if (!(ok = wait(&full_bar[c.at], c.phase))) break;
                     if (r < TT && !((reinterpret_cast<const uint32_t*>(meta)[r >> 5] >> (r & 31)) & 1u))
+#pragma unroll 1
                         for (int k = 0; k < p.D / 8; ++k)
-                            *reinterpret_cast<uint4*>(smem + C::KV_AT + (tiles % NS) * C::STAGE + C::KV_TILE + tile_at(TT, r, k)) =
+                            *reinterpret_cast<uint4*>(smem + C::KV_AT + c.at * C::STAGE + C::KV_TILE + tile_at(TT, r, k)) =
                                 make_uint4(0, 0, 0, 0);
                     fence_async_shared();
                 }
@@ -956,6 +1050,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                             if (!ok) return;
                             tc_fence_after();
                             if (j > 0) {
+#pragma unroll 1
                                 for (int d = 0; d < p.D; d += 16) {
                                     uint32_t z[16];
                                     tmem_ld16(t_o + d, z);
@@ -966,6 +1061,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                             }
                             if (c0 > col0) {  // and the tile's probabilities so far (rounded again: they are small now)
                                 tmem_st_wait();
+#pragma unroll 1
                                 for (int d = col0 / 2; d < c0 / 2; d += 16) {
                                     uint32_t z[16];
                                     tmem_ld16(t_p + d, z);
@@ -1048,6 +1144,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 if (warp_act) {
                     const float fw = done ? final_weight(p.sinks, head, base, l) : 1.f;
                     if (!done && act) reinterpret_cast<float2*>(part)[w * kTreeRows + r] = make_float2(base, l);
+#pragma unroll 1
                     for (int d = 0; d < p.D; d += 16) {
                         uint32_t x[16];
                         tmem_ld16(t_o + d, x);
@@ -1073,8 +1170,10 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 s_ml[r] = make_float2(base, l);
                 if (!(ok = meet())) break;
                 float top = -INFINITY;
+#pragma unroll 1
                 for (int q = 0; q < rep; ++q) top = fmaxf(top, s_ml[q * (fold + 1) + lr].x);
                 l = 0.f;
+#pragma unroll 1
                 for (int q = 0; q < rep; ++q) {
                     const float2 ml = s_ml[q * (fold + 1) + lr];
                     if (top != -INFINITY) l += ml.y * ex2_approx(ml.x - top);
@@ -1084,6 +1183,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 if (!done && act && mine == 0) reinterpret_cast<float2*>(part)[lr] = make_float2(top, l);
                 float* room = reinterpret_cast<float*>(smem + C::Q_AT);  // [to, from, row, 8]
                 auto slot = [&](int to, int from) { return room + ((to * rep + from) * (fold + 1) + lr) * 8; };
+#pragma unroll 1
                 for (int d0 = 0; d0 < p.D; d0 += 8 * rep) {
                     uint32_t x[16];
                     float own[8];
@@ -1110,6 +1210,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                     const int d = d0 + 8 * mine;
                     if (act && d < p.D) {
                         float v[8] = {};
+#pragma unroll 1
                         for (int q = 0; q < rep; ++q) {
                             float4 a = make_float4(own[0], own[1], own[2], own[3]), b = make_float4(own[4], own[5], own[6], own[7]);
                             if (q != mine) {
