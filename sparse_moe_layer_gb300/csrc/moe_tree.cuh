@@ -40,6 +40,9 @@ namespace moe {
 
 constexpr int kTreeRows = 128;  // rows of a tile
 constexpr int kMinTiles = 4;    // token tiles of a run, at least, where there are so many
+// What an item costs beside its tiles (queries, the place in the tree, the row's end), in tiles: runs are cut into
+// equal sums of both.
+constexpr int kItemTiles = 4;
 
 // KV: the cache's type; TILES: row tiles of a CTA; TMA: copies by tensor maps.
 template <int DP, int KV, int TILES, bool TMA>
@@ -58,15 +61,18 @@ struct TreeCfg {
     static constexpr int KV_TILE = TT * DP * 2;     // 16-bit keys (or values) of a token tile
     static constexpr int RAW_TILE = TT * DP;        // their codes
     static constexpr int STAGE = 2 * KV_TILE;       // keys, values
-    static constexpr int NS = E4M3 ? 3 : DP == 64 || TILES == 1 && DP == 128 ? 5 : 4;
+    static constexpr int NS = E4M3 ? 3 : TILES == 2 && DP == 64 ? 5 : 4;
     // the raw codes' ring; by threads also scales and valid tokens
-    static constexpr int NR = !E4M3 ? 0 : DP == 64 ? 4 : DP == 128 && TILES == 1 ? 5 : 3;
+    static constexpr int NR = !E4M3 ? 0 : DP == 64 && TILES == 2 ? 4 : DP == 64 && !TMA ? 2 : 3;
     static constexpr int RAW_STAGE = 2 * RAW_TILE + (TMA ? 0 : 2 * TT * 4 + 16);
     // what the softmax knows of a tile: valid tokens; e4m3: each loading warp's largest value scale, scales
     static constexpr int META = E4M3 ? 32 + 2 * TT * 4 : 32;
     static constexpr int ANC = TILES * kTreeRows * (kMaxDrafts / 32) * 4;
+    // where copies of rows meet: each one's sums in fp32, over the queries and behind them
+    static constexpr bool COPIES = TILES == 1 && TT == 64;
+    static constexpr int MEET = COPIES ? kTreeRows * DP * 4 - Q_TILE : 0;
     static constexpr int Q_AT = 0;
-    static constexpr int KV_AT = TILES * Q_TILE;
+    static constexpr int KV_AT = TILES * Q_TILE + MEET;
     static constexpr int RAW_AT = KV_AT + NS * STAGE;
     static constexpr int META_AT = RAW_AT + NR * RAW_STAGE;
     static constexpr int ANC_AT = META_AT + NS * META;
@@ -102,9 +108,10 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
     return s;
 }
 
-// Where a run begins, and what it has: token tiles, or items where they are not cut.
+// Where a run begins, and what it has: token tiles and items' costs, or items where they are not cut.
 struct TreeWork {
-    int b, h, rt, tile, rem;
+    int b, h, rt, tile;
+    int lead, rem;  // what the item costs before its first tile; what the run has left, of both
 };
 // A part of an item: token tiles [tile, tile + n) of it.
 struct TreeSeg {
@@ -122,17 +129,19 @@ struct TreeWalk {
 template <int TT, int TILES>
 __device__ __forceinline__ bool tree_next(const TreeParams& p, TreeWalk& k, TreeSeg& g) {
     TreeWork& w = k.w;
-    if (w.rem <= 0) return false;
+    const int have = w.rem - w.lead;  // (none: the next run begins the item)
+    if (have <= 0) return false;
     const int left = k.s.ntiles - w.tile;
     g.s = k.s;
     g.b = w.b;
     g.h = w.h;
     g.rt = w.rt;
     g.tile = w.tile;
-    g.n = p.whole || left < w.rem ? left : w.rem;
+    g.n = p.whole || left < have ? left : have;
     g.starts = w.tile == 0;
     g.ends = g.n == left;
-    w.rem -= p.whole ? 1 : g.n;
+    w.rem = have - (p.whole ? 1 : g.n);
+    w.lead = p.whole ? 0 : kItemTiles;
     w.tile += g.n;
     if (g.ends) {
         w.tile = 0;
@@ -227,7 +236,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
         const int b = tid * slice + i;
         if (b < p.B) {
             const TreeSeq s = tree_seq<TT, TILES>(p, b);
-            mine += p.Hkv * s.rtiles * (p.whole ? 1 : s.ntiles);
+            mine += p.Hkv * s.rtiles * (p.whole ? 1 : s.ntiles + kItemTiles);
         }
     }
     s_pre[tid + 1] = mine;
@@ -249,12 +258,13 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             before = __shfl_sync(kAllLanes, v, 31);
         }
         __syncwarp();
-        const int total = before, n = min(p.whole ? total : (total + kMinTiles - 1) / kMinTiles, p.runs), run = blockIdx.x;
-        TreeWork w = {0, 0, 0, 0, 0};
+        const int least = p.whole ? 1 : kMinTiles + kItemTiles;
+        const int total = before, n = min((total + least - 1) / least, p.runs), run = blockIdx.x;
+        TreeWork w = {0, 0, 0, 0, 0, 0};
         if (run < n) {
-            const int each = total / n, more = total - each * n, from = more * run / n;  // (n is small)
-            int u = each * run + from;
-            w.rem = each + more * (run + 1) / n - from;
+            const int most = total / n, more = total - most * n, from = more * run / n;  // (n is small)
+            int u = most * run + from;
+            w.rem = most + more * (run + 1) / n - from;
             int sl = 0;
 #pragma unroll 1
             for (int base = 0; base < slices; base += 32)
@@ -264,11 +274,12 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
 #pragma unroll 1
             while (true) {
                 const TreeSeq s = tree_seq<TT, TILES>(p, w.b);
-                const int nt = p.whole ? 1 : s.ntiles;
-                const int here = p.Hkv * s.rtiles * nt;
+                const int each = p.whole ? 1 : s.ntiles + kItemTiles;
+                const int here = p.Hkv * s.rtiles * each;
                 if (u < here) {
-                    const int item = u / nt;
-                    w.tile = u - item * nt;
+                    const int item = u / each, at = u - item * each;
+                    w.lead = p.whole ? 0 : max(kItemTiles - at, 0);
+                    w.tile = p.whole ? 0 : max(at - kItemTiles, 0);
                     w.h = item / s.rtiles;
                     w.rt = item - w.h * s.rtiles;
                     break;
@@ -279,6 +290,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
         }
         if (lane == 0) {
             s_work = w;
+            // (a run whose part of an item is all cost has none of it)
             if (!p.whole) p.cont[run] = make_int4(w.b, w.h, w.rt, w.tile > 0);
         }
     }
@@ -802,7 +814,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             }
             // Few rows stand several times in the tile, and each copy's warps take a part of the tokens (with
             // sums of their own that meet at the end): the exponentials use all four schedulers.
-            const int rep = TILES == 2 || TT < 64 || rows > 64 ? 1 : rows > 32 ? 2 : 4;
+            const int rep = !C::COPIES || rows > 64 ? 1 : rows > 32 ? 2 : 4;
             const int fold = kTreeRows / rep - 1, lr = r & fold;  // the thread's row
             const int cols = TT / rep, col0 = r / (fold + 1) * cols;
             // --- the queries: the tile's rows, 16 bytes a lane; the parents ---
@@ -975,15 +987,16 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                         if constexpr (W == 32) tmem_ld32(t_s + c0, y);
                         if constexpr (W == 64) tmem_ld64(t_s + c0, y);
                         if (TILES == 2 && c0 + W == TT) read_scores();
-                        uint64_t s[W / 2];
-#pragma unroll
-                        for (int i = 0; i < W / 2; ++i) s[i] = f32x2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1]));
+                        auto score = [&](int i) { return __uint_as_float(y[i]); };
+                        auto pair = [&](int i) { return f32x2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])); };
                         if constexpr (E4M3) {
 #pragma unroll
-                            for (int i = 0; i < W / 2; i += 2) {
-                                const float4 f = *reinterpret_cast<const float4*>(scales + c0 + 2 * i);
-                                s[i] = f32x2_mul(s[i], f32x2(f.x, f.y));
-                                s[i + 1] = f32x2_mul(s[i + 1], f32x2(f.z, f.w));
+                            for (int i = 0; i < W; i += 4) {
+                                const float4 f = *reinterpret_cast<const float4*>(scales + c0 + i);
+                                const float2 u = f32x2_get(f32x2_mul(pair(i), f32x2(f.x, f.y))),
+                                             v = f32x2_get(f32x2_mul(pair(i + 2), f32x2(f.z, f.w)));
+                                y[i] = __float_as_uint(u.x), y[i + 1] = __float_as_uint(u.y);
+                                y[i + 2] = __float_as_uint(v.x), y[i + 3] = __float_as_uint(v.y);
                             }
                         }
                         if (masked) {
@@ -1013,18 +1026,13 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                                 const uint16_t* there = reinterpret_cast<const uint16_t*>(meta) + (c0 + k) / 16;
                                 see &= W == 16 ? there[0] : there[0] | (uint32_t)there[1] << 16;
 #pragma unroll
-                                for (int i = 0; i < (W < 32 ? W : 32); i += 2) {
-                                    const float2 v = f32x2_get(s[(k + i) / 2]);
-                                    s[(k + i) / 2] = f32x2((see >> i) & 1u ? v.x : -INFINITY, (see >> (i + 1)) & 1u ? v.y : -INFINITY);
-                                }
+                                for (int i = 0; i < (W < 32 ? W : 32); ++i)
+                                    if (!((see >> i) & 1u)) y[k + i] = __float_as_uint(-INFINITY);
                             }
                         }
                         float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int i = 0; i < W / 2; ++i) {
-                            const float2 v = f32x2_get(s[i]);
-                            t[i & 3] = max3(t[i & 3], v.x, v.y);
-                        }
+                        for (int i = 0; i < W / 2; ++i) t[i & 3] = max3(t[i & 3], score(2 * i), score(2 * i + 1));
                         const float top = fmaxf(max3(t[0], t[1], t[2]), t[3]);
                         if (E4M3) m = fmaxf(m, top);
                         const bool over = fmaf(top, qf, -base) > room;  // (NaN, -inf: no)
@@ -1035,11 +1043,8 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                             } else {
                                 float best = -INFINITY;  // of the weights, in powers of two
 #pragma unroll
-                                for (int i = 0; i < W / 2; ++i) {
-                                    const float2 v = f32x2_get(s[i]);
-                                    best = fmaxf(best, fmaf(v.x, qf, __log2f(fabsf(scales[TT + c0 + 2 * i]))));
-                                    best = fmaxf(best, fmaf(v.y, qf, __log2f(fabsf(scales[TT + c0 + 2 * i + 1]))));
-                                }
+                                for (int i = 0; i < W; ++i)
+                                    best = fmaxf(best, fmaf(score(i), qf, __log2f(fabsf(scales[TT + c0 + i]))));
                                 if (over) n = fmaxf(base, fmaxf(best - kNewWeight, m * qf - kMostLift));
                             }
                             const float f = ex2_approx(base - n);
@@ -1083,7 +1088,8 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                         uint32_t z[W / 2];
 #pragma unroll
                         for (int i = 0; i < W / 2; i += 2) {
-                            const float2 a = f32x2_get(f32x2_fma(s[i], qq, bb)), b = f32x2_get(f32x2_fma(s[i + 1], qq, bb));
+                            const float2 a = f32x2_get(f32x2_fma(pair(2 * i), qq, bb)),
+                                         b = f32x2_get(f32x2_fma(pair(2 * i + 2), qq, bb));
                             uint64_t e0 = f32x2(ex2_approx(a.x), ex2_approx(a.y)),
                                      e1 = f32x2(ex2_approx(b.x), ex2_approx(b.y));
                             sum[i & 2] = f32x2_add(sum[i & 2], e0);
@@ -1101,7 +1107,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                         if constexpr (W == 32) tmem_st16(t_p + c0 / 2, z);
                         if constexpr (W == 64) tmem_st32(t_p + c0 / 2, z);
                     };
-                    if constexpr (TILES == 1 && TT == 64) {
+                    if constexpr (C::COPIES) {
                         if (rep == 4) {
                             part(std::integral_constant<int, 16>(), col0);
                         } else if (rep == 2) {
@@ -1140,7 +1146,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             float* part = p.partial + ((long long)blockIdx.x * 2 + (g.starts ? 1 : 0)) * (ROWS * (p.D + 2));
             float4* sums = reinterpret_cast<float4*>(part + 2 * ROWS) + w * kTreeRows + lr;
             auto pack = [&](float a, float b) { return qf16 ? pack2<true>(a, b) : pack2<false>(a, b); };
-            if (TILES == 2 || rep == 1) {
+            if (rep == 1) {
                 if (warp_act) {
                     const float fw = done ? final_weight(p.sinks, head, base, l) : 1.f;
                     if (!done && act) reinterpret_cast<float2*>(part)[w * kTreeRows + r] = make_float2(base, l);
@@ -1163,9 +1169,8 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                         }
                     }
                 }
-            } else if constexpr (TILES == 1) {
-                // the copies of a row meet where the queries were: each hands the others 8 dims of theirs at a
-                // time and adds up its own, in the order of the copies
+            } else if constexpr (C::COPIES) {
+                // the copies of a row meet where the queries were; sums are in the order of the copies
                 const int mine = r / (fold + 1);
                 s_ml[r] = make_float2(base, l);
                 if (!(ok = meet())) break;
@@ -1181,58 +1186,39 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 const float f = top == -INFINITY ? 0.f : ex2_approx(base - top);
                 const float fw = done ? final_weight(p.sinks, head, top, l) : 1.f;
                 if (!done && act && mine == 0) reinterpret_cast<float2*>(part)[lr] = make_float2(top, l);
-                float* room = reinterpret_cast<float*>(smem + C::Q_AT);  // [to, from, row, 8]
-                auto slot = [&](int to, int from) { return room + ((to * rep + from) * (fold + 1) + lr) * 8; };
+                // [four dims, copy, row]; eight dims in turn are a copy's to add up
+                float4* room = reinterpret_cast<float4*>(smem + C::Q_AT);
 #pragma unroll 1
-                for (int d0 = 0; d0 < p.D; d0 += 8 * rep) {
+                for (int d = 0; d < p.D; d += 16) {
                     uint32_t x[16];
-                    float own[8];
+                    tmem_ld16(t_o + d, x);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (half * 16 >= 8 * rep) continue;
-                        tmem_ld16(t_o + d0 + half * 16, x);
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            float* to = slot(2 * half + q, mine);
-                            float v[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(x[8 * q + i]) * f;
-                            if (2 * half + q == mine) {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) own[i] = v[i];
-                            } else if (act) {
-                                *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
-                                *reinterpret_cast<float4*>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
-                            }
-                        }
-                    }
-                    if (!(ok = meet())) break;
-                    const int d = d0 + 8 * mine;
-                    if (act && d < p.D) {
-                        float v[8] = {};
-#pragma unroll 1
-                        for (int q = 0; q < rep; ++q) {
-                            float4 a = make_float4(own[0], own[1], own[2], own[3]), b = make_float4(own[4], own[5], own[6], own[7]);
-                            if (q != mine) {
-                                a = *reinterpret_cast<const float4*>(slot(mine, q));
-                                b = *reinterpret_cast<const float4*>(slot(mine, q) + 4);
-                            }
-                            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-                            v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] *= fw;
-                        if (done) {
-                            *reinterpret_cast<uint4*>(dst + d) =
-                                make_uint4(pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7]));
-                        } else {
-                            sums[d / 4 * ROWS] = make_float4(v[0], v[1], v[2], v[3]);
-                            sums[(d / 4 + 1) * ROWS] = make_float4(v[4], v[5], v[6], v[7]);
-                        }
-                    }
-                    if (!(ok = meet())) break;
+                    for (int i = 0; i < 4; ++i)
+                        room[(d / 4 + i) * kTreeRows + r] =
+                            make_float4(__uint_as_float(x[4 * i]) * f, __uint_as_float(x[4 * i + 1]) * f,
+                                        __uint_as_float(x[4 * i + 2]) * f, __uint_as_float(x[4 * i + 3]) * f);
                 }
-                if (!ok) break;
+                if (!(ok = meet())) break;
+                if (act) {
+#pragma unroll 1
+                    for (int q = 2 * mine; q < p.D / 4; q += 2 * rep) {  // 8 dims
+                        float4 u = room[q * kTreeRows + lr], v = room[(q + 1) * kTreeRows + lr];
+                        for (int k = 1; k < rep; ++k) {
+                            add_scaled(u, 1.f, room[q * kTreeRows + k * (fold + 1) + lr], 1.f);
+                            add_scaled(v, 1.f, room[(q + 1) * kTreeRows + k * (fold + 1) + lr], 1.f);
+                        }
+                        u = make_float4(u.x * fw, u.y * fw, u.z * fw, u.w * fw);
+                        v = make_float4(v.x * fw, v.y * fw, v.z * fw, v.w * fw);
+                        if (done) {
+                            *reinterpret_cast<uint4*>(dst + 4 * q) =
+                                make_uint4(pack(u.x, u.y), pack(u.z, u.w), pack(v.x, v.y), pack(v.z, v.w));
+                        } else {
+                            sums[q * ROWS] = u;
+                            sums[(q + 1) * ROWS] = v;
+                        }
+                    }
+                }
+                if (!(ok = meet())) break;
             }
             tc_fence_before();
         }
