@@ -53,9 +53,10 @@ struct TreeCfg {
     // warps: row tiles, then those that copy or convert (a token a lane), a TMA warp, the products' warp
     static constexpr int LOADERS = E4M3 || !TMA ? TT / 32 : 0;
     static constexpr int TMA_WARP = TILES * 4 + LOADERS, MMA_WARP = TMA_WARP + (TMA ? 1 : 0);
-    static constexpr int THREADS = (MMA_WARP + 1) * 32;
+    static constexpr int MMAS = LOADERS ? 1 : TILES;  // a warp for each row tile's products, where there is room
+    static constexpr int THREADS = (MMA_WARP + MMAS) * 32;
     // scores that a thread works on at a time, by its registers
-    static constexpr int WARPS_EACH = ((MMA_WARP + 1) * CTAS + 3) / 4;  // of a scheduler
+    static constexpr int WARPS_EACH = ((MMA_WARP + MMAS) * CTAS + 3) / 4;  // of a scheduler
     static constexpr int WIDE = TT < 64 || WARPS_EACH > 3 ? 32 : 64;
     static constexpr int Q_TILE = kTreeRows * DP * 2;
     static constexpr int KV_TILE = TT * DP * 2;     // 16-bit keys (or values) of a token tile
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(smem_u32(&full_bar[i]), kFillers);
-            mbar_init(smem_u32(&empty_bar[i]), 1);
+            mbar_init(smem_u32(&empty_bar[i]), C::MMAS);
         }
         for (int i = 0; i < NR; ++i) {
             mbar_init(smem_u32(&raw_full_bar[i]), 1);
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             mbar_init(smem_u32(&s_bar[i]), 1);
             mbar_init(smem_u32(&p_bar[i]), 4);
         }
-        mbar_init(smem_u32(&end_bar), 1);
+        mbar_init(smem_u32(&end_bar), C::MMAS);
         mbar_init(smem_u32(&x_bar), kTreeRows);
         abort_flag = 0;
         fence_barrier_init();
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
     if (walk.w.rem > 0) walk.s = tree_seq<TT, TILES>(p, walk.w.b);
     auto next_part = [&]() { return tree_next<TT, TILES>(p, walk, g); };
 
-    if (warp == C::MMA_WARP) {
+    if (warp >= C::MMA_WARP) {
         // ------------------------------------------------ the products
         // (the warp stays together, one lane issues: what describes the operands is uniform)
         constexpr uint32_t ID_S = idesc_f16_f32(F16, kTreeRows, TT, false);
@@ -349,11 +350,23 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             p_phase ^= 1u << buf;
             return r;
         };
+        // the warp's row tiles: one of two, or all
+        const int first = C::MMAS == 2 ? warp - C::MMA_WARP : 0, last = C::MMAS == 2 ? first + 1 : TILES;
         while (ok && next_part()) {
-            const int act = TILES == 2 && g.s.n * p.group - g.rt * 2 * kTreeRows > kTreeRows ? 2 : 1;
+            const int both = TILES == 2 && g.s.n * p.group - g.rt * 2 * kTreeRows > kTreeRows ? 2 : 1;
+            const int end = min(last, both);
+            if (first >= end) {  // no rows: the warp lets the stages go as they are filled
+                for (int j = 0; j < g.n && ok; ++j) {
+                    if (!(ok = full())) break;
+                    if (issuer) mbar_arrive(smem_u32(&empty_bar[c.at]));
+                    ahead.next();
+                    c.next();
+                }
+                continue;
+            }
 #pragma unroll
             for (int w = 0; w < TILES; ++w)
-                if (w < act && ok) {
+                if (w >= first && w < end && ok) {
                     ok = wait(&q_bar[w], q_phase >> w);
                     q_phase ^= 1u << w;
                 }
@@ -361,7 +374,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             tc_fence_after();
 #pragma unroll
             for (int w = 0; w < TILES; ++w)
-                if (w < act) scores(w, w);
+                if (w >= first && w < end) scores(w, w);
             ahead.next();
             // Products of different accumulators keep no order: what a product writes over has been read, by
             // the row tile's threads (scores), or by products that they waited for (probabilities).
@@ -381,8 +394,8 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 } else {
 #pragma unroll
                     for (int w = 0; w < TILES; ++w) {
-                        if (w >= act || !ok) continue;
-                        ok = wait(&read_bar[w], read_phase >> w) && (w > 0 || !more || full());
+                        if (w < first || w >= end || !ok) continue;
+                        ok = wait(&read_bar[w], read_phase >> w) && (w > first || !more || full());
                         read_phase ^= 1u << w;
                         if (!ok || !more) continue;
                         tc_fence_after();
@@ -391,7 +404,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                     if (more) ahead.next();
 #pragma unroll
                     for (int w = 0; w < TILES; ++w) {
-                        if (w >= act || !ok) continue;
+                        if (w < first || w >= end || !ok) continue;
                         if (!(ok = probabilities(w))) continue;
                         tc_fence_after();
                         values(w, w, j == 0);
@@ -636,8 +649,11 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             // valid tokens
             auto convert = [&](bool is_k, float sc, uint32_t mask) {
                 const uint8_t* at = slot(raw.at) + (is_k ? 0 : C::RAW_TILE);
-                const uint32_t dst = stage() + (is_k ? 0 : C::KV_TILE);
-                uint32_t some = 0;  // V: tokens with a value that is not 0
+                uint8_t* dst = smem + C::KV_AT + c.at * C::STAGE + (is_k ? 0 : C::KV_TILE);
+                auto codes = [&](int r, int k) {  // 16 of token r of the warp
+                    return *reinterpret_cast<const uint4*>(
+                        at + (TMA ? (lw * 32 + r) * p.D + k * 16 : (r / RPS * LANES + lw * 32 + r % RPS * CH + k) * 16));
+                };
 #pragma unroll
                 for (int i0 = 0; i0 < STEPS; i0 += BATCH) {
                     uint4 v[BATCH];
@@ -645,39 +661,32 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                     for (int i = 0; i < BATCH; ++i) {
                         const int r = (i0 + i) * RPS + r0;
                         v[i] = make_uint4(0, 0, 0, 0);
-                        if (!TMA || (in && ((mask >> r) & 1u)))
-                            v[i] = *reinterpret_cast<const uint4*>(
-                                at + (TMA ? (lw * 32 + r) * p.D + ch * 16 : ((i0 + i) * LANES + lw * 32 + lane) * 16));
+                        if (in && ((mask >> r) & 1u)) v[i] = codes(r, ch);
                     }
 #pragma unroll
                     for (int i = 0; i < BATCH; ++i) {
-                        const int r = (i0 + i) * RPS + r0;
-                        if (in) {
-                            const uint32_t d = dst + tile_at(TT, lw * 32 + r, 2 * ch), e = dst + tile_at(TT, lw * 32 + r, 2 * ch + 1);
-                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(d), "r"(e4m3x2_to_f16x2(v[i].x)),
-                                         "r"(e4m3x2_to_f16x2(v[i].x >> 16)), "r"(e4m3x2_to_f16x2(v[i].y)),
-                                         "r"(e4m3x2_to_f16x2(v[i].y >> 16))
-                                         : "memory");
-                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(e), "r"(e4m3x2_to_f16x2(v[i].z)),
-                                         "r"(e4m3x2_to_f16x2(v[i].z >> 16)), "r"(e4m3x2_to_f16x2(v[i].w)),
-                                         "r"(e4m3x2_to_f16x2(v[i].w >> 16))
-                                         : "memory");
-                        }
-                        if (!is_k) {
-                            const uint32_t b =
-                                __ballot_sync(kAllLanes, in && ((v[i].x | v[i].y | v[i].z | v[i].w) & 0x7f7f7f7fu) != 0u);
-#pragma unroll
-                            for (int k = 0; k < RPS; ++k)
-                                some |= ((b >> (k * CH)) & (CH == 32 ? kAllLanes : (1u << (CH & 31)) - 1u))
-                                            ? 1u << ((i0 + i) * RPS + k)
-                                            : 0u;
-                        }
+                        const int r = lw * 32 + (i0 + i) * RPS + r0;
+                        if (!in) continue;
+                        *reinterpret_cast<uint4*>(dst + tile_at(TT, r, 2 * ch)) =
+                            make_uint4(e4m3x2_to_f16x2(v[i].x), e4m3x2_to_f16x2(v[i].x >> 16), e4m3x2_to_f16x2(v[i].y),
+                                       e4m3x2_to_f16x2(v[i].y >> 16));
+                        *reinterpret_cast<uint4*>(dst + tile_at(TT, r, 2 * ch + 1)) =
+                            make_uint4(e4m3x2_to_f16x2(v[i].z), e4m3x2_to_f16x2(v[i].z >> 16), e4m3x2_to_f16x2(v[i].w),
+                                       e4m3x2_to_f16x2(v[i].w >> 16));
                     }
                 }
                 uint8_t* m = meta();
                 // a head of zeros, which the append stores with a scale of 1 however small the others are,
                 // has no weight
-                if (!is_k && !((some >> lane) & 1u)) sc = 0.f;
+                if (!is_k && __any_sync(kAllLanes, sc == 1.f)) {
+                    uint32_t some = 0;
+#pragma unroll 1
+                    for (int k = 0; k < p.D / 16; ++k) {
+                        const uint4 v = codes(lane, k);
+                        some |= (v.x | v.y | v.z | v.w) & 0x7f7f7f7fu;
+                    }
+                    if (sc == 1.f && !some) sc = 0.f;
+                }
                 reinterpret_cast<float*>(m + 32)[(is_k ? 0 : TT) + lw * 32 + lane] = sc;
                 if (is_k) {
                     if (lane == 0) reinterpret_cast<uint32_t*>(m)[lw] = mask;
@@ -806,114 +815,145 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             x_phase ^= 1u;
             return wait(&x_bar, x_phase ^ 1u);
         };
-        while (ok && next_part()) {
-            const int rows = g.s.n * p.group - (g.rt * TILES + w) * kTreeRows;  // of this tile
-            if (rows <= 0) {
+        constexpr int LPR = DP / 8, RPI = kTreeRows / LPR;  // lanes of a row of queries, rows of a round
+        constexpr int BATCH = 8;                            // rounds in flight
+        const int q_ch = r % LPR;
+        int rows = 0;  // of the part's row tile
+        // Few rows stand several times in the tile, and each copy's warps take a part of the tokens (with sums of
+        // their own that meet at the end): the exponentials use all four schedulers.
+        auto copies = [&]() { return !C::COPIES || rows > 64 ? 1 : rows > 32 ? 2 : 4; };
+        // the next part that has rows in this tile
+        auto advance = [&]() {
+            while (next_part()) {
+                rows = g.s.n * p.group - (g.rt * TILES + w) * kTreeRows;
+                if (rows > 0) return true;
                 for (int i = g.n % (2 * NS); i > 0; --i) c.next();
-                continue;
             }
-            // Few rows stand several times in the tile, and each copy's warps take a part of the tokens (with
-            // sums of their own that meet at the end): the exponentials use all four schedulers.
-            const int rep = !C::COPIES || rows > 64 ? 1 : rows > 32 ? 2 : 4;
-            const int fold = kTreeRows / rep - 1, lr = r & fold;  // the thread's row
+            return false;
+        };
+        // rounds i0 and on of its queries, 16 bytes a lane
+        auto load_q = [&](int i0, uint4 (&q)[BATCH]) {
+            const int fold = kTreeRows / copies() - 1;
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int row = (r / LPR + (i0 + i) * RPI) & fold;
+                q[i] = make_uint4(0, 0, 0, 0);
+                if (q_ch * 8 < p.D && row < rows) {
+                    const int at = (g.rt * TILES + w) * kTreeRows + row, d = tree_draft(p, at);
+                    q[i] = *reinterpret_cast<const uint4*>(p.q + (g.s.first + d) * p.q_token +
+                                                           (long long)(g.h * p.group + at - d * p.group) * p.q_head + q_ch * 8);
+                }
+            }
+        };
+        auto store_q = [&](int i0, const uint4 (&q)[BATCH]) {
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int row = r / LPR + (i0 + i) * RPI;
+                uint4 v = q[i];
+                v.x ^= p.q_sign, v.y ^= p.q_sign, v.z ^= p.q_sign, v.w ^= p.q_sign;
+                if constexpr (E4M3) {
+                    // the products run in fp16: each row is scaled by a power of two to below 2^15, so that
+                    // fp16 values, and bf16 values down to 2^-30 of the largest, are exact
+                    uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                    float a = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 x = (qf16 ? unpack2<true>(u[j]) : unpack2<false>(u[j]));
+                        a = fmaxf(a, fmaxf(fabsf(x.x), fabsf(x.y)));
+                    }
+#pragma unroll
+                    for (int o = LPR / 2; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kAllLanes, a, o));
+                    const uint32_t e = min(max(__float_as_uint(a) >> 23, 15u), 253u);
+                    const float f = __uint_as_float((268u - e) << 23);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 x = (qf16 ? unpack2<true>(u[j]) : unpack2<false>(u[j]));
+                        u[j] = pack2<true>(x.x * f, x.y * f);
+                    }
+                    v = make_uint4(u[0], u[1], u[2], u[3]);
+                    // not 0, which would make NaN of a masked score
+                    if (q_ch == 0)
+                        s_qf[w][row] = fmaxf(p.scale_log2 * __uint_as_float((e - 14u) << 23), 0x1p-126f);
+                }
+                *reinterpret_cast<uint4*>(smem + C::Q_AT + w * C::Q_TILE + tile_at(kTreeRows, row, q_ch)) = v;
+            }
+        };
+        // parents of drafts r and on, the lane's draft's where there are few
+        auto load_up = [&](int (&up)[2]) {
+            const int from = g.s.n <= 32 ? lane : r;
+            up[0] = p.parents && from < g.s.n ? __ldg(p.parents + g.s.first + from) : -1;
+            up[1] = p.parents && from == r && r + kTreeRows < g.s.n ? __ldg(p.parents + g.s.first + r + kTreeRows) : -1;
+        };
+        uint4 q[BATCH];
+        int up[2];
+        bool have = advance();
+        if (have) {
+            load_q(0, q);
+            load_up(up);
+        }
+        while (have && ok) {
+            const int rep = copies(), fold = kTreeRows / rep - 1, lr = r & fold;  // lr: the thread's row
             const int cols = TT / rep, col0 = r / (fold + 1) * cols;
-            // --- the queries: the tile's rows, 16 bytes a lane; the parents ---
-            {
-                const bool tree = p.parents != nullptr;
-                int up[2] = {-1, -1};
-                if (tree) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (r + i * kTreeRows < g.s.n) up[i] = __ldg(p.parents + g.s.first + r + i * kTreeRows);
-                }
-                constexpr int LPR = DP / 8, RPI = kTreeRows / LPR;  // lanes of a row, rows of a round
-                constexpr int BATCH = 8;                            // rounds in flight
-                const int ch = r % LPR;
-#pragma unroll
-                for (int i0 = 0; i0 < LPR; i0 += BATCH) {
-                    if (rep == 1 && i0 * RPI >= rows) break;  // rows past the last have any values
-                    uint4 q[BATCH];
-#pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        const int row = r / LPR + (i0 + i) * RPI;
-                        q[i] = make_uint4(0, 0, 0, 0);
-                        if (ch * 8 < p.D && (row & fold) < rows) {
-                            const int at = (g.rt * TILES + w) * kTreeRows + (row & fold), d = tree_draft(p, at);
-                            q[i] = *reinterpret_cast<const uint4*>(
-                                p.q + (g.s.first + d) * p.q_token +
-                                (long long)(g.h * p.group + at - d * p.group) * p.q_head + ch * 8);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        const int row = r / LPR + (i0 + i) * RPI;
-                        uint4 v = q[i];
-                        v.x ^= p.q_sign, v.y ^= p.q_sign, v.z ^= p.q_sign, v.w ^= p.q_sign;
-                        if constexpr (E4M3) {
-                            // the products run in fp16: each row is scaled by a power of two to below 2^15, so that
-                            // fp16 values, and bf16 values down to 2^-30 of the largest, are exact
-                            uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                            float a = 0.f;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float2 x = (qf16 ? unpack2<true>(u[j]) : unpack2<false>(u[j]));
-                                a = fmaxf(a, fmaxf(fabsf(x.x), fabsf(x.y)));
-                            }
-#pragma unroll
-                            for (int o = LPR / 2; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kAllLanes, a, o));
-                            const uint32_t e = min(max(__float_as_uint(a) >> 23, 15u), 253u);
-                            const float f = __uint_as_float((268u - e) << 23);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float2 x = (qf16 ? unpack2<true>(u[j]) : unpack2<false>(u[j]));
-                                u[j] = pack2<true>(x.x * f, x.y * f);
-                            }
-                            v = make_uint4(u[0], u[1], u[2], u[3]);
-                            // not 0, which would make NaN of a masked score
-                            if (ch == 0)
-                                s_qf[w][row] = fmaxf(p.scale_log2 * __uint_as_float((e - 14u) << 23), 0x1p-126f);
-                        }
-                        *reinterpret_cast<uint4*>(smem + C::Q_AT + w * C::Q_TILE + tile_at(kTreeRows, row, ch)) = v;
-                    }
-                }
-                if (tree) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int d = r + i * kTreeRows;
-                        if (d < g.s.n && (up[i] >= d || up[i] < -1)) {
-                            if (p.status) atomicOr(p.status, kErrBadIndex);
-                            up[i] = -1;
-                        }
-                        s_up[w][d] = (int16_t)up[i];
-                    }
-                }
-                fence_async_shared();
-                mbar_arrive(smem_u32(&q_bar[w]));
+            // --- the queries; the parents ---
+            store_q(0, q);
+#pragma unroll 1
+            for (int i0 = BATCH; i0 < LPR && (rep > 1 || i0 * RPI < rows); i0 += BATCH) {
+                // (rows past the last have any values)
+                load_q(i0, q);
+                store_q(i0, q);
             }
+            const bool few = g.s.n <= 32;  // drafts: a warp has their parents in its lanes
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int d = (few ? lane : r) + i * kTreeRows;
+                if (up[i] >= d || up[i] < -1) {
+                    if (d < g.s.n && p.status) atomicOr(p.status, kErrBadIndex);
+                    up[i] = -1;
+                }
+                if (!few) s_up[w][d] = (int16_t)up[i];
+            }
+            fence_async_shared();
+            mbar_arrive(smem_u32(&q_bar[w]));
             // --- the row's place in the tree ---
             const bool act = lr < rows, warp_act = (lr & ~31) < rows;
             const int at = (g.rt * TILES + w) * kTreeRows + min(lr, rows - 1), draft = tree_draft(p, at);
             const int head = g.h * p.group + at - draft * p.group;
             const bool sees_drafts = g.s.start + (long long)(g.tile + g.n) * TT > g.s.ctx;
-            if (!(ok = wait(&q_bar[w], q_phase))) break;
+            if (E4M3 || !few) {
+                if (!(ok = wait(&q_bar[w], q_phase))) break;
+            }
             q_phase ^= 1u;
             int depth = draft;
             if (p.parents && (sees_drafts || p.window > 0)) {
-                uint32_t bits[kMaxDrafts / 32];
-#pragma unroll
-                for (int k = 0; k < kMaxDrafts / 32; ++k) bits[k] = 0;
                 depth = -1;
-#pragma unroll 1
-                for (int a = draft; a >= 0; a = s_up[w][a]) {
-                    ++depth;
-                    if (p.window <= 0 || depth < p.window) {
-#pragma unroll
-                        for (int k = 0; k < kMaxDrafts / 32; ++k)
-                            if (a >> 5 == k) bits[k] |= 1u << (a & 31);
+                if (few) {
+                    uint32_t bits = 0;
+                    int a = draft;
+                    while (__any_sync(kAllLanes, a >= 0)) {
+                        if (a >= 0) {
+                            ++depth;
+                            if (p.window <= 0 || depth < p.window) bits |= 1u << a;
+                        }
+                        const int above = __shfl_sync(kAllLanes, up[0], a & 31);
+                        a = a >= 0 ? above : -1;
                     }
-                }
+                    anc[0] = bits;  // (what follows is of tokens that are not there)
+                } else {
+                    uint32_t bits[kMaxDrafts / 32];
 #pragma unroll
-                for (int k = 0; k < kMaxDrafts / 32; ++k) anc[k * TILES * kTreeRows] = bits[k];
+                    for (int k = 0; k < kMaxDrafts / 32; ++k) bits[k] = 0;
+#pragma unroll 1
+                    for (int a = draft; a >= 0; a = s_up[w][a]) {
+                        ++depth;
+                        if (p.window <= 0 || depth < p.window) {
+#pragma unroll
+                            for (int k = 0; k < kMaxDrafts / 32; ++k)
+                                if (a >> 5 == k) bits[k] |= 1u << (a & 31);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < kMaxDrafts / 32; ++k) anc[k * TILES * kTreeRows] = bits[k];
+                }
             }
             // the first token that the row sees of the context (of all, in a chain)
             const int since = p.window > 0 ? max(g.s.ctx + depth - p.window + 1, 0) : 0;
@@ -948,9 +988,10 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 bool all = true;  // the tile's tokens are there
 #pragma unroll
                 for (int k = 0; k < TT / 32; ++k) all = all && reinterpret_cast<const uint32_t*>(meta)[k] == kAllLanes;
-                if (TMA && !E4M3 && !all && w == 0) {
+                if (TMA && !E4M3 && !all) {
                     // a copied piece may hold anything behind the last token (before the first, on a bad page):
-                    // such values become 0, whose product with a probability of 0 is 0
+                    // such values become 0 (for each row tile: its products wait for no other), whose product with a
+                    // probability of 0 is 0
                     if (!(ok = wait(&full_bar[c.at], c.phase))) break;
                     if (r < TT && !((reinterpret_cast<const uint32_t*>(meta)[r >> 5] >> (r & 31)) & 1u))
 #pragma unroll 1
@@ -1133,10 +1174,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 ++tiles_done;
             }
             if (!ok) break;
-            reach();
-            if (!ok) break;
-            tc_fence_after();
-            // --- the row, or the run's part of it ---
+            // --- the row, or the run's part of it; the next part's queries come meanwhile ---
             constexpr int ROWS = TILES * kTreeRows;
             const float2 halves = f32x2_get(f32x2_add(f32x2_add(sum[0], sum[1]), f32x2_add(sum[2], sum[3])));
             float l = halves.x + halves.y;
@@ -1145,6 +1183,14 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             uint16_t* dst = p.out + (g.s.first + draft) * p.o_token + (long long)head * p.o_head;
             float* part = p.partial + ((long long)blockIdx.x * 2 + (g.starts ? 1 : 0)) * (ROWS * (p.D + 2));
             float4* sums = reinterpret_cast<float4*>(part + 2 * ROWS) + w * kTreeRows + lr;
+            have = advance();
+            if (have) {
+                load_q(0, q);
+                load_up(up);
+            }
+            reach();
+            if (!ok) break;
+            tc_fence_after();
             auto pack = [&](float a, float b) { return qf16 ? pack2<true>(a, b) : pack2<false>(a, b); };
             if (rep == 1) {
                 if (warp_act) {
@@ -1172,22 +1218,9 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             } else if constexpr (C::COPIES) {
                 // the copies of a row meet where the queries were; sums are in the order of the copies
                 const int mine = r / (fold + 1);
-                s_ml[r] = make_float2(base, l);
-                if (!(ok = meet())) break;
-                float top = -INFINITY;
-#pragma unroll 1
-                for (int q = 0; q < rep; ++q) top = fmaxf(top, s_ml[q * (fold + 1) + lr].x);
-                l = 0.f;
-#pragma unroll 1
-                for (int q = 0; q < rep; ++q) {
-                    const float2 ml = s_ml[q * (fold + 1) + lr];
-                    if (top != -INFINITY) l += ml.y * ex2_approx(ml.x - top);
-                }
-                const float f = top == -INFINITY ? 0.f : ex2_approx(base - top);
-                const float fw = done ? final_weight(p.sinks, head, top, l) : 1.f;
-                if (!done && act && mine == 0) reinterpret_cast<float2*>(part)[lr] = make_float2(top, l);
                 // [four dims, copy, row]; eight dims in turn are a copy's to add up
                 float4* room = reinterpret_cast<float4*>(smem + C::Q_AT);
+                s_ml[r] = make_float2(base, l);
 #pragma unroll 1
                 for (int d = 0; d < p.D; d += 16) {
                     uint32_t x[16];
@@ -1195,26 +1228,43 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         room[(d / 4 + i) * kTreeRows + r] =
-                            make_float4(__uint_as_float(x[4 * i]) * f, __uint_as_float(x[4 * i + 1]) * f,
-                                        __uint_as_float(x[4 * i + 2]) * f, __uint_as_float(x[4 * i + 3]) * f);
+                            make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]),
+                                        __uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3]));
                 }
                 if (!(ok = meet())) break;
+                float f[4];  // what each copy's sums are multiplied by
+                float top = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    f[k] = k < rep ? s_ml[k * (fold + 1) + lr].x : -INFINITY;
+                    top = fmaxf(top, f[k]);
+                }
+                l = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    f[k] = top == -INFINITY ? 0.f : ex2_approx(f[k] - top);
+                    if (k < rep) l += s_ml[k * (fold + 1) + lr].y * f[k];
+                }
+                const float fw = done ? final_weight(p.sinks, head, top, l) : 1.f;
+                if (!done && act && mine == 0) reinterpret_cast<float2*>(part)[lr] = make_float2(top, l);
                 if (act) {
 #pragma unroll 1
-                    for (int q = 2 * mine; q < p.D / 4; q += 2 * rep) {  // 8 dims
-                        float4 u = room[q * kTreeRows + lr], v = room[(q + 1) * kTreeRows + lr];
-                        for (int k = 1; k < rep; ++k) {
-                            add_scaled(u, 1.f, room[q * kTreeRows + k * (fold + 1) + lr], 1.f);
-                            add_scaled(v, 1.f, room[(q + 1) * kTreeRows + k * (fold + 1) + lr], 1.f);
+                    for (int e = 2 * mine; e < p.D / 4; e += 2 * rep) {  // 8 dims
+                        float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (k >= rep) continue;
+                            add_scaled(u, 1.f, room[e * kTreeRows + k * (fold + 1) + lr], f[k]);
+                            add_scaled(v, 1.f, room[(e + 1) * kTreeRows + k * (fold + 1) + lr], f[k]);
                         }
                         u = make_float4(u.x * fw, u.y * fw, u.z * fw, u.w * fw);
                         v = make_float4(v.x * fw, v.y * fw, v.z * fw, v.w * fw);
                         if (done) {
-                            *reinterpret_cast<uint4*>(dst + 4 * q) =
+                            *reinterpret_cast<uint4*>(dst + 4 * e) =
                                 make_uint4(pack(u.x, u.y), pack(u.z, u.w), pack(v.x, v.y), pack(v.z, v.w));
                         } else {
-                            sums[q * ROWS] = u;
-                            sums[(q + 1) * ROWS] = v;
+                            sums[e * ROWS] = u;
+                            sums[(e + 1) * ROWS] = v;
                         }
                     }
                 }
