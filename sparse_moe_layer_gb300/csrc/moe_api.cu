@@ -1033,7 +1033,7 @@ extern "C" size_t moe_tree_attention_workspace_size(int N, int B, int q_heads, i
     if (!tree_ok(N, B, q_heads, kv_heads, head_dim) || max_tokens < 1) return 0;
     if (cache_dtype != MOE_BF16 && cache_dtype != MOE_FP16 && cache_dtype != MOE_E4M3) return 0;
     TreePlan w;
-    tree_plan(N, B, q_heads, kv_heads, head_dim, cache_dtype == MOE_E4M3, 1, 0, max_tokens, num_sms(), &w);
+    tree_plan(N, B, q_heads, kv_heads, head_dim, 1, 0, max_tokens, num_sms(), &w);
     return w.total ? w.total : 256;
 }
 
@@ -1070,8 +1070,7 @@ extern "C" moe_status moe_tree_attention(const moe_kv_cache* cache, const void* 
          reinterpret_cast<uintptr_t>(sinks) | reinterpret_cast<uintptr_t>(status)) & 3u)
         return MOE_ERR_UNSUPPORTED;
     TreePlan w;
-    tree_plan(N, B, q_heads, cache->kv_heads, cache->head_dim, cache->dtype == MOE_E4M3, cache->page_size, window,
-              (int)seen, num_sms(), &w);
+    tree_plan(N, B, q_heads, cache->kv_heads, cache->head_dim, cache->page_size, window, (int)seen, num_sms(), &w);
     if (w.total && !workspace) return MOE_ERR_INVALID_ARG;
     if (workspace_bytes < w.total) return MOE_ERR_WORKSPACE;
     p.q = static_cast<const uint16_t*>(q);

@@ -312,8 +312,7 @@ void attend_plan(int B, int Hq, int Hkv, int D, bool e4m3, int most, int sms, At
 cudaError_t launch_attend(const AttendParams& p, const AttendPlan& plan, int kv_dtype, bool fp16, void* workspace,
                           cudaStream_t st);
 // most: context tokens that a draft can see (its window, or the page table's columns)
-void tree_plan(int N, int B, int Hq, int Hkv, int D, bool e4m3, int page_size, int window, int most, int sms,
-               TreePlan* plan);
+void tree_plan(int N, int B, int Hq, int Hkv, int D, int page_size, int window, int most, int sms, TreePlan* plan);
 // tmK, tmV: with plan.box, maps of [pages, heads, page, D] with boxes of [1, 1, box, 64] (128-byte swizzle), for
 // e4m3 [1, 1, box, D] (none)
 cudaError_t launch_tree(const CUtensorMap& tmK, const CUtensorMap& tmV, const TreeParams& p, const TreePlan& plan,

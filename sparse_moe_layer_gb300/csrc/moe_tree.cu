@@ -57,15 +57,15 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(TreePara
     }
 }
 
-void tree_plan(int N, int B, int Hq, int Hkv, int D, bool e4m3, int page_size, int window, int most, int sms,
-               TreePlan* w) {
+void tree_plan(int N, int B, int Hq, int Hkv, int D, int page_size, int window, int most, int sms, TreePlan* w) {
     const long long rows = ((long long)N * (Hq / Hkv) + B - 1) / B;  // of a sequence and key head, on average
     w->tiles = D <= 128 && rows > kTreeRows ? 2 : 1;
     w->ctas = w->tiles == 2 || D > 64 ? sms : 2 * sms;
-    w->whole = 0;
-    (void)most, (void)e4m3;
+    const int tt = D > 128 ? 32 : w->tiles == 2 && D <= 64 ? 128 : 64;
+    // (a window of `most` tokens begins anywhere in 16, and drafts come behind it)
+    w->whole = (long long)most + 16 + kMaxDrafts <= kWholeTiles * tt;
     // pieces that divide a page, and tiles, which start at a multiple of 16 in a window
-    const int largest = window > 0 ? 16 : D > 128 ? 32 : w->tiles == 2 && D <= 64 ? 128 : 64;
+    const int largest = window > 0 ? 16 : tt;
     w->box = page_size & -page_size;
     if (w->box > largest) w->box = largest;
     if (w->box < 8) w->box = 0;

@@ -43,6 +43,8 @@ constexpr int kMinTiles = 4;    // token tiles of a run, at least, where there a
 // What an item costs beside its tiles (queries, the place in the tree, the row's end), in tiles: runs are cut into
 // equal sums of both.
 constexpr int kItemTiles = 4;
+// Items are not cut where none has more tiles: a cut costs an item's beginning and end once more, and the join.
+constexpr int kWholeTiles = 8;
 
 // KV: the cache's type; TILES: row tiles of a CTA; TMA: copies by tensor maps.
 template <int DP, int KV, int TILES, bool TMA>
@@ -53,10 +55,9 @@ struct TreeCfg {
     // warps: row tiles, then those that copy or convert (a token a lane), a TMA warp, the products' warp
     static constexpr int LOADERS = E4M3 || !TMA ? TT / 32 : 0;
     static constexpr int TMA_WARP = TILES * 4 + LOADERS, MMA_WARP = TMA_WARP + (TMA ? 1 : 0);
-    static constexpr int MMAS = LOADERS ? 1 : TILES;  // a warp for each row tile's products, where there is room
-    static constexpr int THREADS = (MMA_WARP + MMAS) * 32;
+    static constexpr int THREADS = (MMA_WARP + 1) * 32;
     // scores that a thread works on at a time, by its registers
-    static constexpr int WARPS_EACH = ((MMA_WARP + MMAS) * CTAS + 3) / 4;  // of a scheduler
+    static constexpr int WARPS_EACH = ((MMA_WARP + 1) * CTAS + 3) / 4;  // of a scheduler
     static constexpr int WIDE = TT < 64 || WARPS_EACH > 3 ? 32 : 64;
     static constexpr int Q_TILE = kTreeRows * DP * 2;
     static constexpr int KV_TILE = TT * DP * 2;     // 16-bit keys (or values) of a token tile
@@ -128,7 +129,7 @@ struct TreeWalk {
 };
 // The next part of the run; false: none.
 template <int TT, int TILES>
-__device__ __forceinline__ bool tree_next(const TreeParams& p, TreeWalk& k, TreeSeg& g) {
+__device__ __forceinline__ bool tree_next(const TreeParams& p, bool whole, TreeWalk& k, TreeSeg& g) {
     TreeWork& w = k.w;
     const int have = w.rem - w.lead;  // (none: the next run begins the item)
     if (have <= 0) return false;
@@ -138,11 +139,11 @@ __device__ __forceinline__ bool tree_next(const TreeParams& p, TreeWalk& k, Tree
     g.h = w.h;
     g.rt = w.rt;
     g.tile = w.tile;
-    g.n = p.whole || left < have ? left : have;
+    g.n = whole || left < have ? left : have;
     g.starts = w.tile == 0;
     g.ends = g.n == left;
-    w.rem = have - (p.whole ? 1 : g.n);
-    w.lead = p.whole ? 0 : kItemTiles;
+    w.rem = have - (whole ? 1 : g.n);
+    w.lead = whole ? 0 : kItemTiles;
     w.tile += g.n;
     if (g.ends) {
         w.tile = 0;
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
     __shared__ __align__(8) uint64_t full_bar[NS], empty_bar[NS], q_bar[TILES], s_bar[2], p_bar[2], o_bar[TILES], end_bar,
         raw_full_bar[NR], raw_empty_bar[NR], read_bar[TILES], x_bar;
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag;
+    __shared__ int abort_flag, s_longest;
     __shared__ TreeWork s_work;
     __shared__ float s_qf[TILES][kTreeRows];
     __shared__ int16_t s_up[TILES][kMaxDrafts];  // parents
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(smem_u32(&full_bar[i]), kFillers);
-            mbar_init(smem_u32(&empty_bar[i]), C::MMAS);
+            mbar_init(smem_u32(&empty_bar[i]), 1);
         }
         for (int i = 0; i < NR; ++i) {
             mbar_init(smem_u32(&raw_full_bar[i]), 1);
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             mbar_init(smem_u32(&s_bar[i]), 1);
             mbar_init(smem_u32(&p_bar[i]), 4);
         }
-        mbar_init(smem_u32(&end_bar), C::MMAS);
+        mbar_init(smem_u32(&end_bar), 1);
         mbar_init(smem_u32(&x_bar), kTreeRows);
         abort_flag = 0;
         fence_barrier_init();
@@ -231,17 +232,25 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
 
     // --- the run: each thread counts a slice of the sequences ---
     const int slice = (p.B + THREADS - 1) / THREADS;
-    int mine = 0;
+    if (tid == 0) s_longest = 0;
+    __syncthreads();
+    int mine = 0, items = 0, longest = 0;
 #pragma unroll 1
     for (int i = 0; i < slice; ++i) {
         const int b = tid * slice + i;
         if (b < p.B) {
             const TreeSeq s = tree_seq<TT, TILES>(p, b);
-            mine += p.Hkv * s.rtiles * (p.whole ? 1 : s.ntiles + kItemTiles);
+            items += p.Hkv * s.rtiles;
+            mine += p.Hkv * s.rtiles * (s.ntiles + kItemTiles);
+            if (s.rtiles) longest = max(longest, s.ntiles);
         }
     }
-    s_pre[tid + 1] = mine;
+    longest = __reduce_max_sync(kAllLanes, longest);
+    if (lane == 0) atomicMax(&s_longest, longest);
     if (tid == 0) s_pre[0] = 0;
+    __syncthreads();
+    const bool whole = p.whole || s_longest <= kWholeTiles;
+    s_pre[tid + 1] = whole ? items : mine;
     __syncthreads();
     if (warp == 0) {  // prefix sums, 32 at a time
         int before = 0;
@@ -259,7 +268,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             before = __shfl_sync(kAllLanes, v, 31);
         }
         __syncwarp();
-        const int least = p.whole ? 1 : kMinTiles + kItemTiles;
+        const int least = whole ? 1 : kMinTiles + kItemTiles;
         const int total = before, n = min((total + least - 1) / least, p.runs), run = blockIdx.x;
         TreeWork w = {0, 0, 0, 0, 0, 0};
         if (run < n) {
@@ -275,12 +284,12 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
 #pragma unroll 1
             while (true) {
                 const TreeSeq s = tree_seq<TT, TILES>(p, w.b);
-                const int each = p.whole ? 1 : s.ntiles + kItemTiles;
+                const int each = whole ? 1 : s.ntiles + kItemTiles;
                 const int here = p.Hkv * s.rtiles * each;
                 if (u < here) {
                     const int item = u / each, at = u - item * each;
-                    w.lead = p.whole ? 0 : max(kItemTiles - at, 0);
-                    w.tile = p.whole ? 0 : max(at - kItemTiles, 0);
+                    w.lead = whole ? 0 : max(kItemTiles - at, 0);
+                    w.tile = whole ? 0 : max(at - kItemTiles, 0);
                     w.h = item / s.rtiles;
                     w.rt = item - w.h * s.rtiles;
                     break;
@@ -304,9 +313,9 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
     TreeSeg g;
     walk.w = s_work;
     if (walk.w.rem > 0) walk.s = tree_seq<TT, TILES>(p, walk.w.b);
-    auto next_part = [&]() { return tree_next<TT, TILES>(p, walk, g); };
+    auto next_part = [&]() { return tree_next<TT, TILES>(p, whole, walk, g); };
 
-    if (warp >= C::MMA_WARP) {
+    if (warp == C::MMA_WARP) {
         // ------------------------------------------------ the products
         // (the warp stays together, one lane issues: what describes the operands is uniform)
         constexpr uint32_t ID_S = idesc_f16_f32(F16, kTreeRows, TT, false);
@@ -350,23 +359,11 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             p_phase ^= 1u << buf;
             return r;
         };
-        // the warp's row tiles: one of two, or all
-        const int first = C::MMAS == 2 ? warp - C::MMA_WARP : 0, last = C::MMAS == 2 ? first + 1 : TILES;
         while (ok && next_part()) {
-            const int both = TILES == 2 && g.s.n * p.group - g.rt * 2 * kTreeRows > kTreeRows ? 2 : 1;
-            const int end = min(last, both);
-            if (first >= end) {  // no rows: the warp lets the stages go as they are filled
-                for (int j = 0; j < g.n && ok; ++j) {
-                    if (!(ok = full())) break;
-                    if (issuer) mbar_arrive(smem_u32(&empty_bar[c.at]));
-                    ahead.next();
-                    c.next();
-                }
-                continue;
-            }
+            const int act = TILES == 2 && g.s.n * p.group - g.rt * 2 * kTreeRows > kTreeRows ? 2 : 1;
 #pragma unroll
             for (int w = 0; w < TILES; ++w)
-                if (w >= first && w < end && ok) {
+                if (w < act && ok) {
                     ok = wait(&q_bar[w], q_phase >> w);
                     q_phase ^= 1u << w;
                 }
@@ -374,7 +371,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             tc_fence_after();
 #pragma unroll
             for (int w = 0; w < TILES; ++w)
-                if (w >= first && w < end) scores(w, w);
+                if (w < act) scores(w, w);
             ahead.next();
             // Products of different accumulators keep no order: what a product writes over has been read, by
             // the row tile's threads (scores), or by products that they waited for (probabilities).
@@ -394,8 +391,8 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 } else {
 #pragma unroll
                     for (int w = 0; w < TILES; ++w) {
-                        if (w < first || w >= end || !ok) continue;
-                        ok = wait(&read_bar[w], read_phase >> w) && (w > first || !more || full());
+                        if (w >= act || !ok) continue;
+                        ok = wait(&read_bar[w], read_phase >> w) && (w > 0 || !more || full());
                         read_phase ^= 1u << w;
                         if (!ok || !more) continue;
                         tc_fence_after();
@@ -404,7 +401,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                     if (more) ahead.next();
 #pragma unroll
                     for (int w = 0; w < TILES; ++w) {
-                        if (w < first || w >= end || !ok) continue;
+                        if (w >= act || !ok) continue;
                         if (!(ok = probabilities(w))) continue;
                         tc_fence_after();
                         values(w, w, j == 0);
@@ -884,21 +881,16 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             up[0] = p.parents && from < g.s.n ? __ldg(p.parents + g.s.first + from) : -1;
             up[1] = p.parents && from == r && r + kTreeRows < g.s.n ? __ldg(p.parents + g.s.first + r + kTreeRows) : -1;
         };
-        uint4 q[BATCH];
-        int up[2];
-        bool have = advance();
-        if (have) {
-            load_q(0, q);
-            load_up(up);
-        }
-        while (have && ok) {
+        while (ok && advance()) {
             const int rep = copies(), fold = kTreeRows / rep - 1, lr = r & fold;  // lr: the thread's row
             const int cols = TT / rep, col0 = r / (fold + 1) * cols;
             // --- the queries; the parents ---
-            store_q(0, q);
+            int up[2];
+            load_up(up);
 #pragma unroll 1
-            for (int i0 = BATCH; i0 < LPR && (rep > 1 || i0 * RPI < rows); i0 += BATCH) {
+            for (int i0 = 0; i0 < LPR && (rep > 1 || i0 * RPI < rows); i0 += BATCH) {
                 // (rows past the last have any values)
+                uint4 q[BATCH];
                 load_q(i0, q);
                 store_q(i0, q);
             }
@@ -988,10 +980,9 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 bool all = true;  // the tile's tokens are there
 #pragma unroll
                 for (int k = 0; k < TT / 32; ++k) all = all && reinterpret_cast<const uint32_t*>(meta)[k] == kAllLanes;
-                if (TMA && !E4M3 && !all) {
+                if (TMA && !E4M3 && !all && w == 0) {
                     // a copied piece may hold anything behind the last token (before the first, on a bad page):
-                    // such values become 0 (for each row tile: its products wait for no other), whose product with a
-                    // probability of 0 is 0
+                    // such values become 0, whose product with a probability of 0 is 0
                     if (!(ok = wait(&full_bar[c.at], c.phase))) break;
                     if (r < TT && !((reinterpret_cast<const uint32_t*>(meta)[r >> 5] >> (r & 31)) & 1u))
 #pragma unroll 1
@@ -1174,20 +1165,15 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 ++tiles_done;
             }
             if (!ok) break;
-            // --- the row, or the run's part of it; the next part's queries come meanwhile ---
+            // --- the row, or the run's part of it ---
             constexpr int ROWS = TILES * kTreeRows;
             const float2 halves = f32x2_get(f32x2_add(f32x2_add(sum[0], sum[1]), f32x2_add(sum[2], sum[3])));
             float l = halves.x + halves.y;
             if (base == kNoWeights) base = -INFINITY;  // no tokens
-            const bool done = p.whole || (g.starts && g.ends);
+            const bool done = g.starts && g.ends;
             uint16_t* dst = p.out + (g.s.first + draft) * p.o_token + (long long)head * p.o_head;
             float* part = p.partial + ((long long)blockIdx.x * 2 + (g.starts ? 1 : 0)) * (ROWS * (p.D + 2));
             float4* sums = reinterpret_cast<float4*>(part + 2 * ROWS) + w * kTreeRows + lr;
-            have = advance();
-            if (have) {
-                load_q(0, q);
-                load_up(up);
-            }
             reach();
             if (!ok) break;
             tc_fence_after();

@@ -44,8 +44,9 @@ def test_refusals_on_the_host():
         return L.moe_tree_attention(kv_bytes(**cache) if kv is None else kv, q, dt, *qst, table, ld, width, lens, starts,
                                     parents, N, B, Hq, scale, sinks, window, out, *ost, ws, wsb, status, None)
 
-    for name in ("q", "table", "lens", "starts", "out", "ws"):
+    for name in ("q", "table", "lens", "starts", "out"):
         assert call(**{name: None}) == 1, name
+    assert call(width=100, ld=100, ws=None) == 1  # rows that may be cut need a workspace
     assert call(k=0) == 1 and call(B=0) == 1 and call(B=65537) == 1 and call(N=0) == 1 and call(N=1 << 27) == 1
     assert call(Hq=0) == 1 and call(Hq=3) == 1 and call(Hq=4098) == 1 and call(D=72) == 1 and call(D=272) == 1
     assert call(S=0) == 1 and call(H=300) == 1 and call(width=0) == 1 and call(ld=3) == 1
@@ -58,11 +59,11 @@ def test_refusals_on_the_host():
         assert call(**{name: 258}) == 2, name
     assert call(qst=(256, 65)) == 2 and call(ost=(252, 64)) == 2 and call(qst=(-256, 64)) == 1
     assert call(kv=kv_bytes(k=264)) == 2 and call(kv=kv_bytes(strides=(2048, 1024, 68))) == 2
-    assert call(wsb=64) == 3
+    assert call(width=100, ld=100, wsb=64) == 3
     size = L.moe_tree_attention_workspace_size
     assert size(0, 1, 4, 2, 64, 0, 99) == 0 and size(3, 0, 4, 2, 64, 0, 99) == 0 and size(3, 1, 3, 2, 64, 0, 99) == 0
     assert size(3, 1, 4, 2, 72, 0, 99) == 0 and size(3, 1, 4, 2, 64, 2, 99) == 0 and size(3, 1, 4, 2, 64, 0, 0) == 0
-    assert size(3, 1, 4, 2, 64, 3, 99999) > 256
+    assert size(3, 1, 4, 2, 64, 3, 99) == 256 and size(3, 1, 4, 2, 64, 3, 99999) > 256
 
 
 def test_binding_refuses():
@@ -419,8 +420,9 @@ def test_gpu_refusals():
             c.run(**bad)
     with pytest.raises(moe.MoeError):
         c.run(window=-1)
+    long = Case([1000], [2], 8, 2, 64, seed=9)
     with pytest.raises(moe.MoeError):
-        c.run(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+        long.run(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(moe.MoeError):
         moe.tree_attention_workspace(0, 1, 8, 2, 64, 100)
     e = torch.zeros(0, 8, 64, dtype=torch.bfloat16, device="cuda")
