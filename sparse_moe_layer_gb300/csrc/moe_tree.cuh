@@ -43,8 +43,10 @@ constexpr int kMinTiles = 4;    // token tiles of a run, at least, where there a
 // What an item costs beside its tiles (queries, the place in the tree, the row's end), in tiles: runs are cut into
 // equal sums of both.
 constexpr int kItemTiles = 4;
-// Items are not cut where none has more tiles: a cut costs an item's beginning and end once more, and the join.
-constexpr int kWholeTiles = 8;
+// What cutting items adds to every run beside a second item's cost (parts written, the join), in tiles: items stay whole
+// where equal numbers of them take no longer.
+constexpr int kCutTiles = 7;
+constexpr int kWholeTiles = 8;  // tables for so few tiles: never cut, so without workspace and join
 
 // KV: the cache's type; TILES: row tiles of a CTA; TMA: copies by tensor maps.
 template <int DP, int KV, int TILES, bool TMA>
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
     __shared__ __align__(8) uint64_t full_bar[NS], empty_bar[NS], q_bar[TILES], s_bar[2], p_bar[2], o_bar[TILES], end_bar,
         raw_full_bar[NR], raw_empty_bar[NR], read_bar[TILES], x_bar;
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag, s_longest;
+    __shared__ int abort_flag, s_sum[3];  // (all runs': units, items, tiles of the longest)
     __shared__ TreeWork s_work;
     __shared__ float s_qf[TILES][kTreeRows];
     __shared__ int16_t s_up[TILES][kMaxDrafts];  // parents
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
 
     // --- the run: each thread counts a slice of the sequences ---
     const int slice = (p.B + THREADS - 1) / THREADS;
-    if (tid == 0) s_longest = 0;
+    if (tid < 3) s_sum[tid] = 0;
     __syncthreads();
     int mine = 0, items = 0, longest = 0;
 #pragma unroll 1
@@ -245,11 +247,21 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             if (s.rtiles) longest = max(longest, s.ntiles);
         }
     }
+    const int warp_units = __reduce_add_sync(kAllLanes, mine), warp_items = __reduce_add_sync(kAllLanes, items);
     longest = __reduce_max_sync(kAllLanes, longest);
-    if (lane == 0) atomicMax(&s_longest, longest);
-    if (tid == 0) s_pre[0] = 0;
+    if (lane == 0) {
+        atomicAdd(&s_sum[0], warp_units);
+        atomicAdd(&s_sum[1], warp_items);
+        atomicMax(&s_sum[2], longest);
+        if (warp == 0) s_pre[0] = 0;
+    }
     __syncthreads();
-    const bool whole = p.whole || s_longest <= kWholeTiles;
+    bool whole = p.whole;
+    if (!whole) {
+        const int least = kMinTiles + kItemTiles, n = min((s_sum[0] + least - 1) / least, p.runs);
+        const float each = (float)((s_sum[1] + p.runs - 1) / p.runs) * (float)(s_sum[2] + kItemTiles);
+        whole = each <= (float)s_sum[0] / (float)max(n, 1) + (float)(kItemTiles + kCutTiles);
+    }
     s_pre[tid + 1] = whole ? items : mine;
     __syncthreads();
     if (warp == 0) {  // prefix sums, 32 at a time
