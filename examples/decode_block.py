@@ -8,7 +8,13 @@ Norms and the dense projections are plain torch; the cache is bf16 or e4m3.  The
 step runs as one CUDA graph: lengths, slots and positions live in device tensors
 that advance inside it.
 
+With --drafts n each step checks a tree of n drafted tokens a sequence and keeps one
+path of it:
+
+  x -> norm -> q, k, v -> rotate_append -> tree_attention -> + x -> ... ;  compact_drafts
+
   python examples/decode_block.py [--batch 64] [--context 4096] [--steps 32] [--cache bf16|e4m3] [--window 0]
+                                  [--drafts 0]
 """
 import argparse
 import os
@@ -96,7 +102,7 @@ class DecodeBlock:
                                  **self.gate)
 
     def step(self, x):
-        x = x + self.attention(x)[1].reshape(self.B, -1) @ self.w_o
+        x = x + self.attention(x)[1].reshape(x.shape[0], -1) @ self.w_o
         return x + self.mlp(x)
 
     def graphed(self, x):
@@ -115,6 +121,77 @@ class DecodeBlock:
         return static, out, graph
 
 
+class DraftBlock(DecodeBlock):
+    """A block whose step checks drafted tokens, x [batch * n, H]: n drafts of each sequence, which follow one
+    another as `parents` [n] says (-1: the context).  A step appends all of them; `keep` lets a path of them stay.
+    `room` counts a step's drafts, and those of the steps before that stay."""
+
+    def __init__(self, batch, context, room, parents, **kw):
+        super().__init__(batch, context, room, **kw)
+        depth = []
+        for up in parents:
+            depth.append(depth[up] + 1 if up >= 0 else 0)
+        n, most = len(parents), self.table.shape[1] * self.page
+        self.depth = torch.tensor(depth, device="cuda")
+        self.parents = torch.tensor(parents, dtype=torch.int32, device="cuda").repeat(batch)
+        self.starts = torch.arange(0, batch * n + 1, n, dtype=torch.int32, device="cuda")
+        self.att_ws = moe.tree_attention_workspace(batch * n, batch, self.Hq, self.Hkv, self.D, most, self.k.dtype)
+        (H, E), I = self.w_router.shape, self.b13.shape[1] // 2
+        self.moe_ws = moe.new_workspace(batch * n, H, I, E, self.top_k)
+
+    def attention(self, x):
+        """x [batch * n, H] -> (rotated q, attention output before w_o); the drafts' keys and values are appended."""
+        n, Hq, Hkv, D = len(self.depth), self.Hq, self.Hkv, self.D
+        qkv = torch.addmm(self.b_qkv, norm(x), self.w_qkv).view(-1, Hq + 2 * Hkv, D)
+        at = self.lengths.long()[:, None]
+        slots = next_slots(self.table.repeat_interleave(n, 0), (at + torch.arange(n, device="cuda")).view(-1), self.page,
+                           self.k.shape[0])
+        q = moe.rotate_append(qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], (at + self.depth).view(-1), slots, self.k,
+                              self.v, self.inv_freq, k_scale=self.ks, v_scale=self.vs, status=self.status)
+        self.lengths += n
+        return q, moe.tree_attention(q, self.k, self.v, self.table, self.lengths, self.starts, D ** -0.5, self.parents,
+                                     k_scale=self.ks, v_scale=self.vs, sinks=self.sinks, window=self.window,
+                                     workspace=self.att_ws, status=self.status)
+
+    def keep(self, kept):
+        """Of the last step's drafts those numbered kept [batch, K] (ascending; a negative one ends the list) become
+        context, the others are forgotten."""
+        moved = moe.compact_drafts(self.k, self.v, self.table, self.lengths, self.starts, kept, k_scale=self.ks,
+                                   v_scale=self.vs, status=self.status)
+        self.lengths.copy_(moved)
+
+    def fork(self, src, dst):
+        """Sequences dst [m] go on from where sequences src [m] (none of dst) are: full pages are shared, the last one is
+        copied.  (The pages that dst had there are free then.)"""
+        have = self.lengths[src].long()
+        full = have // self.page
+        column = torch.arange(self.table.shape[1], device="cuda")
+        self.table[dst] = torch.where(column < full[:, None], self.table[src], self.table[dst])
+        last = full.clamp(max=self.table.shape[1] - 1)[:, None]
+        moe.copy_pages(self.k, self.v, self.table[src].gather(1, last)[:, 0], self.table[dst].gather(1, last)[:, 0],
+                       (have % self.page).int(), k_scale=self.ks, v_scale=self.vs, status=self.status)
+        self.lengths[dst] = self.lengths[src]
+
+
+def draft_steps(a):
+    """Steps of a.drafts drafts in a binary tree, of which the path of first children is kept each time."""
+    parents = [(i + 1) // 2 - 1 for i in range(a.drafts)]
+    path = [0]
+    while 2 * path[-1] + 1 < a.drafts:
+        path.append(2 * path[-1] + 1)
+    block = DraftBlock(a.batch, a.context, len(path) * (a.steps + 1) + a.drafts, parents, cache=a.cache, window=a.window)
+    kept = torch.tensor([path] * a.batch, dtype=torch.int32, device="cuda")
+    static, out, graph = block.graphed(torch.randn(a.batch * a.drafts, 2880, device="cuda").bfloat16())
+    torch.cuda.synchronize()
+    t = time.perf_counter()
+    for _ in range(a.steps):
+        graph.replay()
+        block.keep(kept)
+        static.copy_(norm(out))
+    torch.cuda.synchronize()
+    return block, (time.perf_counter() - t) / a.steps, len(path)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--batch", type=int, default=64)
@@ -122,7 +199,16 @@ def main():
     ap.add_argument("--steps", type=int, default=32)
     ap.add_argument("--cache", choices=["bf16", "e4m3"], default="bf16")
     ap.add_argument("--window", type=int, default=0)
+    ap.add_argument("--drafts", type=int, default=0)
     a = ap.parse_args()
+    if a.drafts > 0:
+        block, t, kept = draft_steps(a)
+        for word in (block.status, block.moe_ws):
+            if moe.read_device_status(word) != 0:
+                raise SystemExit("a device error word is set")
+        print(f"batch {a.batch}, context {a.context}, {a.drafts} drafts a step, {kept} of them kept, {a.cache} cache, window "
+              f"{a.window}: {t * 1e6:.1f} us a step of one block, {a.batch * kept / t:.0f} tokens/s")
+        return
     block = DecodeBlock(a.batch, a.context, a.steps + 2, cache=a.cache, window=a.window)
     x = torch.randn(a.batch, 2880, device="cuda").bfloat16()
     static, out, graph = block.graphed(x)
