@@ -70,17 +70,20 @@ __device__ __forceinline__ void add_scaled(float4& a, float f, const float4& b, 
     a.w = a.w * f + b.w * h;
 }
 
-// 1 / (sum with the head's sink), about the larger of the two exponents: what
+// 1 / (sum with the head's sink, where there is one), about the larger of the two exponents: what
 // sums taken about m are multiplied by.  0 for a row without tokens; NaN stays NaN.
-__device__ __forceinline__ float final_weight(const float* sinks, int head, float m, float l) {
+__device__ __forceinline__ float final_weight(bool sinks, float sink, float m, float l) {
     float w = 1.f;
     if (sinks) {
-        const float k = __ldg(sinks + head) * 1.4426950408889634f;
+        const float k = sink * 1.4426950408889634f;
         const float n = fmaxf(m, k);
         w = n == -INFINITY ? 0.f : ex2_approx(m - n);
         l = n == -INFINITY ? 0.f : l * w + (k == n ? 1.f : ex2_approx(k - n));  // (an infinite sink too)
     }
     return l == 0.f ? 0.f : w / l;
+}
+__device__ __forceinline__ float final_weight(const float* sinks, int head, float m, float l) {
+    return final_weight(sinks != nullptr, sinks ? __ldg(sinks + head) : 0.f, m, l);
 }
 
 }  // namespace moe

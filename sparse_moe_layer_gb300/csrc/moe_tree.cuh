@@ -819,11 +819,12 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             return __all_sync(kAllLanes, r) != 0;
         };
         // all of the row tile's threads (one row tile) have come so far
-        auto meet = [&]() {
+        auto come = [&]() {
             mbar_arrive(smem_u32(&x_bar));
             x_phase ^= 1u;
-            return wait(&x_bar, x_phase ^ 1u);
         };
+        auto met = [&]() { return wait(&x_bar, x_phase ^ 1u); };
+        bool to_meet = false;  // copies of the part before may still be read where the queries go
         constexpr int LPR = DP / 8, RPI = kTreeRows / LPR;  // lanes of a row of queries, rows of a round
         constexpr int BATCH = 8;                            // rounds in flight
         const int q_ch = r % LPR;
@@ -840,12 +841,11 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             }
             return false;
         };
-        // rounds i0 and on of its queries, 16 bytes a lane
-        auto load_q = [&](int i0, uint4 (&q)[BATCH]) {
-            const int fold = kTreeRows / copies() - 1;
+        // rounds i0 and on of its queries, 16 bytes a lane; rows come again `every` so many (a power of two)
+        auto load_q = [&](int i0, int every, uint4 (&q)[BATCH]) {
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
-                const int row = (r / LPR + (i0 + i) * RPI) & fold;
+                const int row = (r / LPR + (i0 + i) * RPI) & (every - 1);
                 q[i] = make_uint4(0, 0, 0, 0);
                 if (q_ch * 8 < p.D && row < rows) {
                     const int at = (g.rt * TILES + w) * kTreeRows + row, d = tree_draft(p, at);
@@ -903,9 +903,14 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             for (int i0 = 0; i0 < LPR && (rep > 1 || i0 * RPI < rows); i0 += BATCH) {
                 // (rows past the last have any values)
                 uint4 q[BATCH];
-                load_q(i0, q);
+                load_q(i0, fold + 1, q);
+                if (C::COPIES && to_meet) {
+                    if (!(ok = met())) break;
+                    to_meet = false;
+                }
                 store_q(i0, q);
             }
+            if (!ok) break;
             const bool few = g.s.n <= 32;  // drafts: a warp has their parents in its lanes
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -922,6 +927,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             const bool act = lr < rows, warp_act = (lr & ~31) < rows;
             const int at = (g.rt * TILES + w) * kTreeRows + min(lr, rows - 1), draft = tree_draft(p, at);
             const int head = g.h * p.group + at - draft * p.group;
+            const float sink = TILES == 1 && p.sinks ? __ldg(p.sinks + head) : 0.f;  // (in time; two row tiles: registers)
             const bool sees_drafts = g.s.start + (long long)(g.tile + g.n) * TT > g.s.ctx;
             if (E4M3 || !few) {
                 if (!(ok = wait(&q_bar[w], q_phase))) break;
@@ -961,7 +967,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             }
             // the first token that the row sees of the context (of all, in a chain)
             const int since = p.window > 0 ? max(g.s.ctx + depth - p.window + 1, 0) : 0;
-            const float qf = E4M3 ? s_qf[w][r] : p.scale_log2;  // positive factor of the scores
+            const float qf = E4M3 ? s_qf[w][lr] : p.scale_log2;  // positive factor of the scores
             if (rep > 1) {  // probabilities of the other copies' tokens
                 const uint32_t z[16] = {};
 #pragma unroll 1
@@ -1192,7 +1198,9 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             auto pack = [&](float a, float b) { return qf16 ? pack2<true>(a, b) : pack2<false>(a, b); };
             if (rep == 1) {
                 if (warp_act) {
-                    const float fw = done ? final_weight(p.sinks, head, base, l) : 1.f;
+                    const float fw = !done        ? 1.f
+                                     : TILES == 1 ? final_weight(p.sinks != nullptr, sink, base, l)
+                                                  : final_weight(p.sinks, head, base, l);
                     if (!done && act) reinterpret_cast<float2*>(part)[w * kTreeRows + r] = make_float2(base, l);
 #pragma unroll 1
                     for (int d = 0; d < p.D; d += 16) {
@@ -1220,16 +1228,20 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 float4* room = reinterpret_cast<float4*>(smem + C::Q_AT);
                 s_ml[r] = make_float2(base, l);
 #pragma unroll 1
-                for (int d = 0; d < p.D; d += 16) {
-                    uint32_t x[16];
-                    tmem_ld16(t_o + d, x);
+                for (int d = 0; d < p.D; d += 32) {
+                    uint32_t x[32];
+                    tmem_ld32(t_o + d, x);
+                    if (act) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        room[(d / 4 + i) * kTreeRows + r] =
-                            make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]),
-                                        __uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3]));
+                        for (int i = 0; i < 8; ++i)
+                            room[(d / 4 + i) * kTreeRows + r] =
+                                make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]),
+                                            __uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3]));
+                    }
+                    __syncwarp();
                 }
-                if (!(ok = meet())) break;
+                come();
+                if (!(ok = met())) break;
                 float f[4];  // what each copy's sums are multiplied by
                 float top = -INFINITY;
 #pragma unroll
@@ -1243,7 +1255,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                     f[k] = top == -INFINITY ? 0.f : ex2_approx(f[k] - top);
                     if (k < rep) l += s_ml[k * (fold + 1) + lr].y * f[k];
                 }
-                const float fw = done ? final_weight(p.sinks, head, top, l) : 1.f;
+                const float fw = done ? final_weight(p.sinks != nullptr, sink, top, l) : 1.f;
                 if (!done && act && mine == 0) reinterpret_cast<float2*>(part)[lr] = make_float2(top, l);
                 if (act) {
 #pragma unroll 1
@@ -1266,7 +1278,8 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                         }
                     }
                 }
-                if (!(ok = meet())) break;
+                come();
+                to_meet = true;
             }
             tc_fence_before();
         }
