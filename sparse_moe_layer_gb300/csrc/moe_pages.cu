@@ -5,6 +5,10 @@
 // heads-major; "GPT-OSS on Day 0": the layers' own caches).
 //
 // Bound by memory: what moves is read once and written once, in 16-byte pieces.
+// 256 pages of 64 tokens, 4 heads of 128 e4m3 codes, 36 layers: 187.6 us for 1.25 GB,
+// 6.66 TB/s, 98 % of a copy. The used places of 64 last pages of 16, 8 heads of 64, 24
+// layers: 10.5 us for 53 MB. Up to 7 of 24 drafts of 128 sequences, e4m3, 36 layers: 9.7
+// us for 19.5 MB in tokens of 128 bytes, latency; 4 of 8 of one sequence: 2.6.
 #include "moe_device.cuh"
 #include "moe_internal.h"
 
@@ -13,10 +17,10 @@ namespace moe {
 namespace {
 
 constexpr int kCopyThreads = 256;
-constexpr int kCopyPieces = 4;  // 16-byte pieces that a thread has in flight
+constexpr int kCopyPieces = 4;  // 16-byte pieces that a thread has in flight (2: 193 and 12.9 us, 8: 189.5 and 13.0)
 constexpr int kCopyBlock = kCopyThreads * kCopyPieces;
 constexpr int kMoveWarps = 4;   // per CTA
-constexpr int kMoveLayers = 4;  // layers that a warp has in flight
+constexpr int kMoveLayers = 4;  // layers that a warp has in flight (2: 9.8 us, 8: 10.8)
 
 }  // namespace
 
@@ -185,7 +189,8 @@ cudaError_t launch_compact_drafts(const CompactParams& p_in, int sms, cudaStream
     CompactParams p = p_in;
     p.lpr_shift = 0;
     while ((1 << p.lpr_shift) < p.row_pieces) ++p.lpr_shift;
-    // a warp's layers share its index arithmetic; fewer each where that leaves SMs without warps
+    // a warp's layers share its index arithmetic; fewer each where that leaves SMs without warps (one sequence 2.6 us, all
+    // layers in one warp 3.8; 128 sequences 9.7, in one warp 18.2, always in parts of four layers 10.6)
     const long long warps = 2LL * p.B * p.Hkv, most = (p.layers + kMoveLayers - 1) / kMoveLayers;
     const long long parts = (32LL * sms + warps - 1) / warps;
     p.layer_parts = (int)(parts < 1 ? 1 : parts < most ? parts : most);

@@ -27,6 +27,17 @@
 // A wait on a barrier takes 100 to 150 cycles even when it has come, so there are few: one
 // for a tile's keys and values, one for its scores, one for its probabilities.
 //
+// Measured (one GB300): chains of 4 drafts of 64 heads on 8 of 64, 64 sequences of 1 to
+// 16384 tokens: 176 us for 1.08 GB, 6.1 TB/s, 90 % of a copy. Trees of 48 to 64 drafts of
+// the same heads, 32 sequences of 2000 to 8192 tokens: 241 us, 620 TFLOP/s; two row tiles
+// are in turn at their exponentials, 3.1 thousand cycles for 128 tokens of 256 rows where the
+// exponential unit needs 1.0 (without softmax 143 us). 16 drafts of 64 heads on 4 of 128, 4
+// sequences of 100000 to 131072 tokens, e4m3: 298 us, 810 TFLOP/s, bound by conversion and
+// exponentials together (without softmax 245 us). A window of 128 over 256 sequences: 44.8
+// us, a tile's and a row end's latency after another. One short sequence: 7.0 us.
+// One row tile for all: 253 and 452 us for the two wide cases. Copies by threads, which pages
+// of odd sizes take: 277, 322, 313 and 54 us for these four.
+//
 // The list of items (sequence, key head, row tiles) and their token tiles is cut into
 // equal runs, one per CTA; an item cut by a run's border leaves fp32 parts that a second,
 // dependent launch joins in a fixed order.
@@ -39,14 +50,20 @@
 namespace moe {
 
 constexpr int kTreeRows = 128;  // rows of a tile
-constexpr int kMinTiles = 4;    // token tiles of a run, at least, where there are so many
+// Token tiles of a run, at least, where there are so many (8: one sequence of 1000 tokens 24.4 us for 20.0; 2: the same).
+constexpr int kMinTiles = 4;
 // What an item costs beside its tiles (queries, the place in the tree, the row's end), in tiles: runs are cut into
-// equal sums of both.
+// equal sums of both.  (1: ragged lengths up to 16384 204 us, up to 3000 35; 4: 182 and 28; 2: 196; 8: 180, wide trees
+// +2 %.)
 constexpr int kItemTiles = 4;
 // What cutting items adds to every run beside a second item's cost (parts written, the join), in tiles: items stay whole
-// where equal numbers of them take no longer.
+// where equal numbers of them take no longer.  (16 sequences of 1000 and 2000 tokens, 8 key heads of 128: cut 33.8 and
+// 49.0 us, whole 21.0 and 36.0; one sequence: cut 20.0 and 22.1, whole 19.6 and 31.6.  3 cuts 64 sequences of 500: 59.4
+// us for 53.3; 12 leaves one of 2000 with 256 rows whole: 32.9 for 24.1.)
 constexpr int kCutTiles = 7;
-constexpr int kWholeTiles = 8;  // tables for so few tiles: never cut, so without workspace and join
+// Tables for so few tiles are never cut, so without workspace and join: 64 sequences of 500 tokens 22.4 us, cut 24.7;
+// one short sequence 7.5, cut 14.0.
+constexpr int kWholeTiles = 8;
 
 // KV: the cache's type; TILES: row tiles of a CTA; TMA: copies by tensor maps.
 template <int DP, int KV, int TILES, bool TMA>
@@ -65,15 +82,20 @@ struct TreeCfg {
     static constexpr int KV_TILE = TT * DP * 2;     // 16-bit keys (or values) of a token tile
     static constexpr int RAW_TILE = TT * DP;        // their codes
     static constexpr int STAGE = 2 * KV_TILE;       // keys, values
-    static constexpr int NS = E4M3 ? 3 : TILES == 2 && DP == 64 ? 5 : 4;
+    // stages of keys and values: as many as fit (one row tile, 16 bits: 5 where 4 took 181 us, now 176, for the 1.08 GB of
+    // 64 sequences of up to 16384 tokens)
+    static constexpr int NS = E4M3 ? 3 : DP == 64 || (DP == 128 && TILES == 1) ? 5 : 4;
     // the raw codes' ring; by threads also scales and valid tokens
     static constexpr int NR = !E4M3 ? 0 : DP == 64 && TILES == 2 ? 4 : DP == 64 && !TMA ? 2 : 3;
     static constexpr int RAW_STAGE = 2 * RAW_TILE + (TMA ? 0 : 2 * TT * 4 + 16);
     // what the softmax knows of a tile: valid tokens; e4m3: each loading warp's largest value scale, scales
     static constexpr int META = E4M3 ? 32 + 2 * TT * 4 : 32;
     static constexpr int ANC = TILES * kTreeRows * (kMaxDrafts / 32) * 4;
-    // where copies of rows meet: each one's sums in fp32, over the queries and behind them
-    static constexpr bool COPIES = TILES == 1 && TT == 64;
+    // Few rows of e4m3 caches stand 2 or 4 times in their tile, each copy with a part of the tokens, so that conversion
+    // and exponentials share the schedulers evenly (8 rows, 32 sequences of 8000 tokens, 8 key heads of 64: 122 us, once
+    // each 132). 16-bit caches have them once (a window of 128 over 256 sequences: 44.8 us, four times 50.7).
+    // Where the copies meet: each one's sums in fp32, over the queries and behind them.
+    static constexpr bool COPIES = E4M3 && TILES == 1 && TT == 64;
     static constexpr int MEET = COPIES ? kTreeRows * DP * 4 - Q_TILE : 0;
     static constexpr int Q_AT = 0;
     static constexpr int KV_AT = TILES * Q_TILE + MEET;
@@ -153,8 +175,14 @@ __device__ __forceinline__ bool tree_next(const TreeParams& p, bool whole, TreeW
             w.rt = 0;
             if (++w.h == p.Hkv) {
                 w.h = 0;
-                if (w.rem > 0) do k.s = tree_seq<TT, TILES>(p, ++w.b);
-                    while (k.s.rtiles == 0);
+                while (w.rem > 0) {
+                    if (++w.b >= p.B) {  // (starts that descend can make sums of work that overflow)
+                        w.rem = 0;
+                        break;
+                    }
+                    k.s = tree_seq<TT, TILES>(p, w.b);
+                    if (k.s.rtiles) break;
+                }
             }
         }
     }
@@ -294,7 +322,11 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             u -= s_pre[sl];
             w.b = sl * slice;
 #pragma unroll 1
-            while (true) {
+            for (bool found = false; !found;) {
+                if (u < 0 || w.b >= p.B) {  // (as in tree_next)
+                    w.rem = 0;
+                    break;
+                }
                 const TreeSeq s = tree_seq<TT, TILES>(p, w.b);
                 const int each = whole ? 1 : s.ntiles + kItemTiles;
                 const int here = p.Hkv * s.rtiles * each;
@@ -304,10 +336,11 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                     w.tile = whole ? 0 : max(at - kItemTiles, 0);
                     w.h = item / s.rtiles;
                     w.rt = item - w.h * s.rtiles;
-                    break;
+                    found = true;
+                } else {
+                    u -= here;
+                    ++w.b;
                 }
-                u -= here;
-                ++w.b;
             }
         }
         if (lane == 0) {
@@ -829,8 +862,8 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
         constexpr int BATCH = 8;                            // rounds in flight
         const int q_ch = r % LPR;
         int rows = 0;  // of the part's row tile
-        // Few rows stand several times in the tile, and each copy's warps take a part of the tokens (with sums of
-        // their own that meet at the end): the exponentials use all four schedulers.
+        // how often the rows stand in the tile (e4m3): each copy's warps take a part of the tokens, with sums of their own
+        // that meet at the end
         auto copies = [&]() { return !C::COPIES || rows > 64 ? 1 : rows > 32 ? 2 : 4; };
         // the next part that has rows in this tile
         auto advance = [&]() {
