@@ -277,6 +277,20 @@ def test_long_contexts_are_cut_and_joined(contexts, drafts, cache):
 
 
 @gpu
+@pytest.mark.parametrize("Hq,Hkv,D,page,dtype,cache", [(8, 1, 64, 16, "bf16", "bf16"), (32, 2, 128, 24, "fp16", "fp16"),
+                                                       (16, 4, 128, 64, "bf16", "e4m3"), (6, 2, 80, 7, "fp16", "e4m3"),
+                                                       (4, 1, 240, 16, "bf16", "bf16"), (32, 1, 64, 32, "bf16", "e4m3")])
+@pytest.mark.parametrize("contexts,drafts", [([5000], [9]), ([900] * 40, [4] * 40), ([1, 9000, 0, 700], [12, 3, 1, 70]),
+                                             ([2100] * 12, [20] * 12)])
+@pytest.mark.parametrize("window", [0, 3000])
+def test_cut_and_whole_items(Hq, Hkv, D, page, dtype, cache, contexts, drafts, window):
+    c = Case(contexts, drafts, Hq, Hkv, D, page, dtype, cache, seed=len(contexts))
+    out = c.run(True, window)
+    c.check(out, True, window)
+    assert torch.equal(c.run(True, window), out)
+
+
+@gpu
 def test_many_sequences():
     h = torch.Generator().manual_seed(1)
     ctx = torch.randint(0, 200, (700,), generator=h).tolist()
