@@ -1120,17 +1120,27 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                         if (E4M3) m = fmaxf(m, top);
                         const bool over = fmaf(top, qf, -base) > room;  // (NaN, -inf: no)
                         if (__any_sync(kAllLanes, over)) {
-                            float n = base;
+                            // After the first time it moves by whole powers of two, so that the tile's probabilities so
+                            // far, of which some may be as large as the new ones, keep their bits.  (e4m3: down to
+                            // the weights' place, up to the least that it may have; none where the bound was too high.)
+                            float n = base, steps = 0.f;
+                            const bool first = base == kNoWeights;
                             if constexpr (!E4M3) {
-                                if (over) n = top * qf - kLift<KV>;
+                                const float to = top * qf - kLift<KV>;
+                                if (over) steps = rintf(to - base), n = first ? to : base + steps;
                             } else {
                                 float best = -INFINITY;  // of the weights, in powers of two
 #pragma unroll
                                 for (int i = 0; i < W; ++i)
                                     best = fmaxf(best, fmaf(score(i), qf, __log2f(fabsf(scales[TT + c0 + i]))));
-                                if (over) n = fmaxf(base, fmaxf(best - kNewWeight, m * qf - kMostLift));
+                                const float to = best - kNewWeight, least = m * qf - kMostLift;
+                                if (over) {
+                                    steps = fmaxf(fmaxf(floorf(to - base), ceilf(least - base)), 0.f);
+                                    n = first ? fmaxf(base, fmaxf(to, least)) : base + steps;
+                                }
                             }
-                            const float f = ex2_approx(base - n);
+                            // (sums take the difference as it was rounded, probabilities the whole power)
+                            const float f = ex2_approx(base - n), fp = steps < 127.f ? __uint_as_float((127u - (uint32_t)steps) << 23) : 0.f;
                             base = n;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) sum[i] = f32x2_mul(sum[i], f32x2(f, f));
@@ -1147,7 +1157,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                                     tmem_st16(t_o + d, z);
                                 }
                             }
-                            if (c0 > col0) {  // and the tile's probabilities so far (rounded again: they are small now)
+                            if (c0 > col0) {  // and the tile's probabilities so far
                                 tmem_st_wait();
 #pragma unroll 1
                                 for (int d = col0 / 2; d < c0 / 2; d += 16) {
@@ -1156,7 +1166,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
 #pragma unroll
                                     for (int i = 0; i < 16; ++i) {
                                         const float2 v = unpack2<F16>(z[i]);
-                                        z[i] = pack2<F16>(v.x * f, v.y * f);
+                                        z[i] = pack2<F16>(v.x * fp, v.y * fp);
                                     }
                                     tmem_st16(t_p + d, z);
                                 }
