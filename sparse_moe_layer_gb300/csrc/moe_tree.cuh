@@ -1147,6 +1147,9 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                             reach();
                             if (!ok) return;
                             tc_fence_after();
+                            // what an earlier part of the tile stored, probabilities and rescaled sums, is there
+                            // before it is loaded
+                            tmem_st_wait();
                             if (j > 0) {
 #pragma unroll 1
                                 for (int d = 0; d < p.D; d += 16) {
@@ -1158,7 +1161,6 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                                 }
                             }
                             if (c0 > col0) {  // and the tile's probabilities so far
-                                tmem_st_wait();
 #pragma unroll 1
                                 for (int d = col0 / 2; d < c0 / 2; d += 16) {
                                     uint32_t z[16];
