@@ -161,12 +161,20 @@ class DraftBlock(DecodeBlock):
         self.lengths.copy_(moved)
 
     def fork(self, src, dst):
-        """Sequences dst [m] go on from where sequences src [m] (none of dst) are: full pages are shared, the last one is
-        copied.  (The pages that dst had there are free then.)"""
+        """Sequences dst [m] (distinct) go on from where sequences src [m] (none of dst) are: full pages are shared, the
+        last one is copied to a page of dst's own, and so are the places behind it.  Between `keep` and the next step."""
         have = self.lengths[src].long()
         full = have // self.page
-        column = torch.arange(self.table.shape[1], device="cuda")
-        self.table[dst] = torch.where(column < full[:, None], self.table[src], self.table[dst])
+        own = torch.arange(self.table.shape[1], device=self.table.device) >= full[:, None]
+        self.table[dst] = torch.where(own, -1, self.table[src])
+        # dst's own: pages that no sequence names now (what dst had may have been lent, or borrowed). There are enough:
+        # the table has as many places as there are pages.
+        pages = self.k.shape[0]
+        named = torch.zeros(pages + 1, dtype=torch.bool, device=self.table.device)
+        named[torch.where(self.table < 0, pages, self.table).long()] = True
+        free = torch.argsort(named[:pages].int(), stable=True).int()
+        place = (own.view(-1).cumsum(0) - 1).clamp(min=0).view(own.shape)
+        self.table[dst] = torch.where(own, free[place], self.table[dst])
         last = full.clamp(max=self.table.shape[1] - 1)[:, None]
         moe.copy_pages(self.k, self.v, self.table[src].gather(1, last)[:, 0], self.table[dst].gather(1, last)[:, 0],
                        (have % self.page).int(), k_scale=self.ks, v_scale=self.vs, status=self.status)
