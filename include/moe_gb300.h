@@ -545,9 +545,10 @@ moe_status moe_paged_attention(const moe_kv_cache* cache, const void* q, int dty
  *   q [N, q_heads, D] bf16 or fp16 (`dtype`; that of a 16-bit cache), strides in elements,
  *   D contiguous; out likewise; page_table [B, table_width], lengths [B], starts [B + 1],
  *   parents [N] int32; sinks fp32 [q_heads]
- *   workspace: moe_tree_attention_workspace_size bytes, 256-byte aligned, any contents;
- *   calls that may overlap need one each; NULL where the size is 256 (a table for so few
- *   tokens that nothing is split); max_tokens as for moe_attention_workspace_size
+ *   workspace: moe_tree_attention_workspace_size bytes, 256-byte aligned, any contents; it
+ *   serves every call of at most N drafts of B sequences of max_tokens tokens (as for
+ *   moe_attention_workspace_size); calls that may overlap need one each; NULL where the size
+ *   is 256 (a table for so few tokens that nothing is split)
  *   status: a device error word for moe_read_device_status, or NULL
  * Limits: those of the cache; q_heads a multiple of kv_heads, at most 4096; 1 <= N < 2^27;
  * 1 <= B <= 65536; table_width * page_size at most 2^31 - 256; (N * q_heads / kv_heads /

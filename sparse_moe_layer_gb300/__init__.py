@@ -647,8 +647,8 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, scale: float, k_sc
 
 def tree_attention_workspace(N: int, B: int, q_heads: int, kv_heads: int, head_dim: int, max_tokens: int,
                              dtype=torch.bfloat16, device=None) -> torch.Tensor:
-    """A workspace for `tree_attention` calls of N drafts of B sequences that do not overlap; max_tokens and dtype as
-    for `attention_workspace`."""
+    """A workspace for `tree_attention` calls of at most N drafts of at most B sequences that do not overlap;
+    max_tokens and dtype as for `attention_workspace`."""
     n = int(lib().moe_tree_attention_workspace_size(N, B, q_heads, kv_heads, head_dim, _DTYPES.get(dtype, -1), max_tokens))
     if n == 0:
         raise MoeError(1, "moe_tree_attention_workspace_size")

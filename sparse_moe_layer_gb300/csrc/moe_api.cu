@@ -1032,9 +1032,12 @@ extern "C" size_t moe_tree_attention_workspace_size(int N, int B, int q_heads, i
                                                     int cache_dtype, int max_tokens) {
     if (!tree_ok(N, B, q_heads, kv_heads, head_dim) || max_tokens < 1) return 0;
     if (cache_dtype != MOE_BF16 && cache_dtype != MOE_FP16 && cache_dtype != MOE_E4M3) return 0;
-    TreePlan w;
-    tree_plan(N, B, q_heads, kv_heads, head_dim, 1, 0, max_tokens, num_sms(), &w);
-    return w.total ? w.total : 256;
+    // Fewer drafts of a sequence (one row tile) or fewer sequences (two) can need more: a workspace serves both.
+    TreePlan few, many;
+    tree_plan(1, B, q_heads, kv_heads, head_dim, 1, 0, max_tokens, num_sms(), &few);
+    tree_plan(N, 1, q_heads, kv_heads, head_dim, 1, 0, max_tokens, num_sms(), &many);
+    const size_t most = few.total > many.total ? few.total : many.total;
+    return most ? most : 256;
 }
 
 extern "C" moe_status moe_tree_attention(const moe_kv_cache* cache, const void* q, int dtype, int64_t q_token,
