@@ -437,7 +437,8 @@ moe_status moe_rotate_append(const moe_kv_cache* cache, const void* q, const voi
  * moe_rotate_append with positions of several axes (time, height and width of images
  * and video): pair i of a token n turns by a_i = positions[axes[i] * axis_stride + n] *
  * inv_freq[i].  axes int32 [rot_dim / 2]; an axis outside [0, n_axes) counts as 0 and
- * sets the error word.  Limits: 1 <= n_axes <= 16; N <= axis_stride (n_axes > 1).
+ * sets the error word.  Limits: 1 <= n_axes <= 16; axis_stride (n_axes > 1) at least N,
+ * or 0: one row for all axes (the positions of text).
  */
 moe_status moe_rotate_append_axes(const moe_kv_cache* cache, const void* q, const void* k, const void* v, int dtype,
                                   int64_t q_token, int64_t q_head, int64_t k_token, int64_t k_head, int64_t v_token,

@@ -614,8 +614,8 @@ def rotate_append(q, k, v, positions, slots, k_cache, v_cache, inv_freq, k_scale
     any strides with the last dim contiguous.  inv_freq fp64 [R / 2] rotates the first R dims, in
     pairs (i, i + R/2) or, interleaved, (2i, 2i + 1); cos and sin are multiplied by rope_scale.
     With axes int32 [R / 2] positions are [A, N], one row per axis (time, height, width of images and
-    video), and pair i turns by the position of axis axes[i].  status (`new_status`): set by a slot past the
-    last page, or an axis outside [0, A) (it counts as 0)."""
+    video; one row expanded to all will do), and pair i turns by the position of axis axes[i].  status
+    (`new_status`): set by a slot past the last page, or an axis outside [0, A) (it counts as 0)."""
     return (_calls or _entries()).rotate_append(q, k, v, positions, slots, k_cache, v_cache, inv_freq, k_scale, v_scale,
                                                 interleaved, rope_scale, q_out, status,
                                                 None if stream is None else stream.cuda_stream, axes)

@@ -901,7 +901,7 @@ static moe_status append_impl(const moe_kv_cache* cache, const void* q, const vo
     p.positions = positions;
     if (ax) {
         if (rot_dim && !ax->axes) return MOE_ERR_INVALID_ARG;
-        if (ax->n_axes < 1 || ax->n_axes > 16 || (ax->n_axes > 1 && (ax->ld < N || ax->ld > (1LL << 40))))
+        if (ax->n_axes < 1 || ax->n_axes > 16 || (ax->n_axes > 1 && ax->ld && (ax->ld < N || ax->ld > (1LL << 40))))
             return MOE_ERR_INVALID_ARG;
         if (reinterpret_cast<uintptr_t>(ax->axes) & 3u) return MOE_ERR_UNSUPPORTED;
         p.axes = ax->axes;
