@@ -441,7 +441,7 @@ PyObject* compact_drafts(PyObject* const* a) {
     if (B)
         check(moe_compact_drafts(&c.cache, c.layers, c.stride, static_cast<const int32_t*>(table.data_ptr()),
                                  table.stride(0), (int)table.size(1), lens, starts,
-                                 static_cast<const int32_t*>(kept.data_ptr()), kept.stride(0), (int)B,
+                                 kept.size(1) ? static_cast<const int32_t*>(kept.data_ptr()) : nullptr, kept.stride(0), (int)B,
                                  (int)kept.size(1), static_cast<int32_t*>(out.data_ptr()), status, on.handle),
               "moe_compact_drafts");
     return THPVariable_Wrap(out);

@@ -1174,8 +1174,9 @@ extern "C" moe_status moe_compact_drafts(const moe_kv_cache* cache, int layers, 
     long long ls[3];
     s = check_layers(cache, layers, layer_stride, ls);
     if (s != MOE_OK) return s;
-    if (!page_table || !lengths || !starts || !kept || !new_lengths || new_lengths == lengths) return MOE_ERR_INVALID_ARG;
-    if (B < 1 || B > 65536 || K < 1 || table_width < 1 || (long long)table_width * cache->page_size > kMaxTokens)
+    if (!page_table || !lengths || !starts || !new_lengths || new_lengths == lengths) return MOE_ERR_INVALID_ARG;
+    if (K < 0 || (kept != nullptr) != (K > 0)) return MOE_ERR_INVALID_ARG;
+    if (B < 1 || B > 65536 || table_width < 1 || (long long)table_width * cache->page_size > kMaxTokens)
         return MOE_ERR_INVALID_ARG;
     if (B == 1) table_ld = kept_ld = 0;
     if (B > 1 && (table_ld < table_width || kept_ld < K)) return MOE_ERR_INVALID_ARG;

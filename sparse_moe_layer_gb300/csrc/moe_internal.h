@@ -107,7 +107,7 @@ struct CompactParams {
     int max_tokens;          // table columns * page_size
     const int32_t* lengths;  // [B] tokens of a sequence, its drafts included
     const int32_t* starts;   // [B + 1] first draft of each sequence
-    const int32_t* kept;     // [B, K] drafts kept, ascending; -1 ends
+    const int32_t* kept;     // [B, K] drafts kept, ascending; -1 ends; null: K is 0
     long long kept_ld;
     int B, K;
     int32_t* out;  // [B] new lengths
