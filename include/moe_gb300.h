@@ -475,7 +475,7 @@ moe_status moe_copy_pages(const moe_kv_cache* cache, int layers, const int64_t* 
  * tokens or tokens than the table has room for, stays as it is; all three set the error word.
  *   page_table int32 [B, table_width], rows table_ld apart; lengths int32 [B];
  *   starts int32 [B + 1]; kept int32 [B, K], rows kept_ld apart; new_lengths int32 [B],
- *   not lengths itself; layers, layer_stride as for moe_copy_pages
+ *   sharing no memory with these four; layers, layer_stride as for moe_copy_pages
  * Limits: those of the cache; 1 <= B <= 65536; 1 <= K, or K = 0 and kept NULL: no draft
  * is kept; table_width * page_size <= 2^31 - 32; sequences share no page that is moved
  * from or to.

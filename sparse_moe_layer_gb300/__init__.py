@@ -687,7 +687,7 @@ def copy_pages(k_cache, v_cache, src, dst, tokens=None, k_scale=None, v_scale=No
 def compact_drafts(k_cache, v_cache, page_table, lengths, starts, kept, k_scale=None, v_scale=None, out=None, status=None,
                    stream=None):
     """Close up the kept drafts of a step in a paged cache; returns the sequences' new lengths [B] int32 (a new
-    tensor, or `out`, which is not lengths itself).
+    tensor, or `out`, which shares no memory with lengths, starts, kept or page_table).
 
     Of the last starts[b + 1] - starts[b] tokens of sequence b, its drafts, number kept[b, 0], kept[b, 1], ...
     (ascending; a negative entry ends the list) move to the first places behind the context.  Cache of one layer or,

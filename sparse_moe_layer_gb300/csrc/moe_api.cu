@@ -1162,6 +1162,17 @@ extern "C" moe_status moe_copy_pages(const moe_kv_cache* cache, int layers, cons
     return launch_copy_pages(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// Whether [x, x + n) shares a value with `count` rows of `width` values, ld apart.
+static bool meets(const int32_t* x, long long n, const int32_t* rows, long long count, long long width, long long ld) {
+    if (!rows) return false;
+    const long long a = (static_cast<long long>(reinterpret_cast<uintptr_t>(x)) -
+                         static_cast<long long>(reinterpret_cast<uintptr_t>(rows))) / 4;
+    if (a + n <= 0 || a >= (count - 1) * ld + width) return false;
+    if (a <= 0 || count == 1) return true;
+    const long long r = a / ld;  // x begins in this row, or behind it
+    return a - r * ld < width || (r + 1 < count && a + n > (r + 1) * ld);
+}
+
 extern "C" moe_status moe_compact_drafts(const moe_kv_cache* cache, int layers, const int64_t* layer_stride,
                                          const int32_t* page_table, int64_t table_ld, int table_width,
                                          const int32_t* lengths, const int32_t* starts, const int32_t* kept,
@@ -1174,7 +1185,7 @@ extern "C" moe_status moe_compact_drafts(const moe_kv_cache* cache, int layers, 
     long long ls[3];
     s = check_layers(cache, layers, layer_stride, ls);
     if (s != MOE_OK) return s;
-    if (!page_table || !lengths || !starts || !new_lengths || new_lengths == lengths) return MOE_ERR_INVALID_ARG;
+    if (!page_table || !lengths || !starts || !new_lengths) return MOE_ERR_INVALID_ARG;
     if (K < 0 || (kept != nullptr) != (K > 0)) return MOE_ERR_INVALID_ARG;
     if (B < 1 || B > 65536 || table_width < 1 || (long long)table_width * cache->page_size > kMaxTokens)
         return MOE_ERR_INVALID_ARG;
@@ -1184,6 +1195,10 @@ extern "C" moe_status moe_compact_drafts(const moe_kv_cache* cache, int layers, 
          reinterpret_cast<uintptr_t>(starts) | reinterpret_cast<uintptr_t>(kept) |
          reinterpret_cast<uintptr_t>(new_lengths) | reinterpret_cast<uintptr_t>(status)) & 3u)
         return MOE_ERR_UNSUPPORTED;
+    // (a sequence's length is written while others, and other heads of it, still read)
+    if (meets(new_lengths, B, lengths, 1, B, 0) || meets(new_lengths, B, starts, 1, B + 1, 0) ||
+        meets(new_lengths, B, kept, B, K, kept_ld) || meets(new_lengths, B, page_table, B, table_width, table_ld))
+        return MOE_ERR_INVALID_ARG;
     p.elem = cache->dtype == MOE_E4M3 ? 1 : 2;
     p.row_pieces = cache->head_dim * p.elem / 16;
     p.k_layer = ls[0], p.v_layer = ls[1], p.s_layer = ls[2];
