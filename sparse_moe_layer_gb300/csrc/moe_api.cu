@@ -134,6 +134,7 @@ bool make_map_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t col
 
 // The keys (or values) of a paged cache, [pages, heads, page, D] with strides in elements (0 for dims of
 // one): boxes of `tokens` tokens of a head, 64 values each in the 128-byte swizzle, or all D codes (e4m3).
+// False: strides that a map does not hold, 0 (a head expanded to several) among them.
 bool make_map_pages(CUtensorMap* m, const void* base, const moe_kv_cache* c, const long long* stride, uint32_t tokens) {
     auto enc = encoder();
     if (!enc) return false;
@@ -142,8 +143,11 @@ bool make_map_pages(CUtensorMap* m, const void* base, const moe_kv_cache* c, con
     cuuint64_t dims[4] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->page_size, (cuuint64_t)c->kv_heads,
                           (cuuint64_t)c->num_pages};
     cuuint64_t strides[3] = {(cuuint64_t)stride[2] * el, (cuuint64_t)stride[1] * el, (cuuint64_t)stride[0] * el};
-    for (cuuint64_t& s : strides)
-        if (s == 0) s = 16;  // (never stepped)
+    for (int i = 0; i < 3; ++i)
+        if (strides[i] == 0) {
+            if (dims[i + 1] > 1) return false;
+            strides[i] = 16;  // (never stepped)
+        }
     cuuint32_t box[4] = {e4m3 ? (cuuint32_t)c->head_dim : 64u, tokens, 1, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
@@ -1105,7 +1109,7 @@ extern "C" moe_status moe_tree_attention(const moe_kv_cache* cache, const void* 
         const long long ks[3] = {p.cache.k_page, p.cache.k_head, p.cache.k_token},
                         vs[3] = {p.cache.v_page, p.cache.v_head, p.cache.v_token};
         if (!make_map_pages(&tmK, cache->k, cache, ks, w.box) || !make_map_pages(&tmV, cache->v, cache, vs, w.box))
-            w.box = 0;  // strides beyond what a map holds
+            w.box = 0;  // by threads
     }
     return launch_tree(tmK, tmV, p, w, cache->dtype, dtype == MOE_FP16, workspace, static_cast<cudaStream_t>(stream)) ==
                    cudaSuccess
