@@ -7,8 +7,8 @@
 // Bound by memory: what moves is read once and written once, in 16-byte pieces.
 // 256 pages of 64 tokens, 4 heads of 128 e4m3 codes, 36 layers: 187.6 us for 1.25 GB,
 // 6.66 TB/s, 98 % of a copy. The used places of 64 last pages of 16, 8 heads of 64, 24
-// layers: 10.5 us for 53 MB. Up to 7 of 24 drafts of 128 sequences, e4m3, 36 layers: 9.7
-// us for 19.5 MB in tokens of 128 bytes, latency; 4 of 8 of one sequence: 2.6.
+// layers: 10.0 us for 53 MB. Up to 7 of 24 drafts of 128 sequences, e4m3, 36 layers: 10.2
+// us for 19.5 MB in tokens of 128 bytes, latency; 4 of 8 of one sequence: 2.9.
 #include "moe_device.cuh"
 #include "moe_internal.h"
 

@@ -59,15 +59,16 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(TreePara
 
 void tree_plan(int N, int B, int Hq, int Hkv, int D, int page_size, int window, int most, int sms, TreePlan* w) {
     const long long rows = ((long long)N * (Hq / Hkv) + B - 1) / B;  // of a sequence and key head, on average
-    // two row tiles share a tile of keys and values (they fit to 128 dims): 64 drafts of 8 heads 241 us, one by one 253;
-    // 16 drafts of 16 heads of 128, e4m3, converted once instead of twice: 298, 452
+    // two row tiles share a tile of keys and values (they fit to 128 dims): 64 drafts of 8 heads 236 us, one by one 239;
+    // 16 drafts of 16 heads of 128, e4m3, converted once instead of twice: 285, 446.  By the batch's average: one large
+    // tree among many single drafts has one row tile at a time.
     w->tiles = D <= 128 && rows > kTreeRows ? 2 : 1;
     w->ctas = w->tiles == 2 || D > 64 ? sms : 2 * sms;
     const int tt = D > 128 ? 32 : w->tiles == 2 && D <= 64 ? 128 : 64;
     // (a window of `most` tokens begins anywhere in 16, and drafts come behind it)
     w->whole = (long long)most + 16 + kMaxDrafts <= kWholeTiles * tt;
     // TMA pieces of tokens that divide a page, and tiles, which start at a multiple of 16 in a window; from 8 on: pieces
-    // cost the copying warp 17 cycles each (64 sequences of up to 16384 tokens, pages of 16: 176 us, by threads 277)
+    // cost the copying warp 17 cycles each (64 sequences of up to 16384 tokens, pages of 16: 176 us, by threads 286)
     const int largest = window > 0 ? 16 : tt;
     w->box = page_size & -page_size;
     if (w->box > largest) w->box = largest;

@@ -9,12 +9,14 @@
 //   o = sum_t p_t v_t / (sum_t p_t + 2^(sink log2 e - m)),  p_t = 2^(s_t - m),
 //   s_t = (q . k_t) scale log2 e
 //
-// A key is read once for all drafts and all query heads that share it, so the rows of
-// the products are the n x group (draft, head) pairs: 128 of them are the rows of a
-// tcgen05 tile.  S = Q K^T goes to tensor memory, where a thread has a whole row: no
+// Drafts and query heads share a key, so the rows of the products are the n x group
+// (draft, head) pairs: 128 of them are the rows of a tcgen05 tile.  A key is read once for
+// 256 rows (two row tiles), or for 128 with more than 128 dims or where the batch's
+// sequences have at most 128 on average.  S = Q K^T goes to tensor memory, where a thread has a whole row: no
 // exchange for maximum and sum.  Probabilities go back in 16 bits beside the scores and
 // are the first operand of P V, whose sums stay in tensor memory; they are rescaled only
-// when a row's maximum rises by more than 2^kSlack.
+// when a row's maximum rises by more than 2^kSlack, after its first time by a whole power of
+// two, so that probabilities are rounded once.
 //
 // One CTA: a warp that issues the products, a warp that copies keys and values by TMA
 // (pieces of tokens that lie on one page), warps that turn e4m3 codes into fp16, and a
@@ -29,14 +31,17 @@
 //
 // Measured (one GB300): chains of 4 drafts of 64 heads on 8 of 64, 64 sequences of 1 to
 // 16384 tokens: 176 us for 1.08 GB, 6.1 TB/s, 90 % of a copy. Trees of 48 to 64 drafts of
-// the same heads, 32 sequences of 2000 to 8192 tokens: 241 us, 620 TFLOP/s; two row tiles
+// the same heads, 32 sequences of 2000 to 8192 tokens: 236 us, 635 TFLOP/s; two row tiles
 // are in turn at their exponentials, 3.1 thousand cycles for 128 tokens of 256 rows where the
 // exponential unit needs 1.0 (without softmax 143 us). 16 drafts of 64 heads on 4 of 128, 4
-// sequences of 100000 to 131072 tokens, e4m3: 298 us, 810 TFLOP/s, bound by conversion and
+// sequences of 100000 to 131072 tokens, e4m3: 285 us, 850 TFLOP/s, bound by conversion and
 // exponentials together (without softmax 245 us). A window of 128 over 256 sequences: 44.8
 // us, a tile's and a row end's latency after another. One short sequence: 7.0 us.
-// One row tile for all: 253 and 452 us for the two wide cases. Copies by threads, which pages
-// of odd sizes take: 277, 322, 313 and 54 us for these four.
+// One row tile for all: 239 and 446 us for the two wide cases. Copies by threads, which pages
+// of odd sizes take: 286, 322, 304 and 54 us for these four.
+//
+// e4m3 caches with few rows stay behind bf16 ones of the same shape (8 rows, 32 sequences of 8000
+// tokens, 8 key heads of 64: 122 us, bf16 92): a warp converts the codes of 32 tokens by itself.
 //
 // The list of items (sequence, key head, row tiles) and their token tiles is cut into
 // equal runs, one per CTA; an item cut by a run's border leaves fp32 parts that a second,
@@ -93,7 +98,7 @@ struct TreeCfg {
     static constexpr int ANC = TILES * kTreeRows * (kMaxDrafts / 32) * 4;
     // Few rows of e4m3 caches stand 2 or 4 times in their tile, each copy with a part of the tokens, so that conversion
     // and exponentials share the schedulers evenly (8 rows, 32 sequences of 8000 tokens, 8 key heads of 64: 122 us, once
-    // each 132). 16-bit caches have them once (a window of 128 over 256 sequences: 44.8 us, four times 50.7).
+    // each 127). 16-bit caches have them once (a window of 128 over 256 sequences: 44.8 us, four times 50.7).
     // Where the copies meet: each one's sums in fp32, over the queries and behind them.
     static constexpr bool COPIES = E4M3 && TILES == 1 && TT == 64;
     static constexpr int MEET = COPIES ? kTreeRows * DP * 4 - Q_TILE : 0;
