@@ -536,8 +536,9 @@ moe_status moe_paged_attention(const moe_kv_cache* cache, const void* q, int dty
  * and of the drafts itself and its ancestors, of them the nearest window - 1; what
  * it sees is attended to as in moe_paged_attention, with the same sinks, types,
  * roundings and limits of e4m3 caches.  Queries are to be rotated by positions c + d_i.
- * Keys of tokens that a draft does not see may be anything, values of tokens that only
- * other drafts of the sequence see are to be finite (they are multiplied by 0).
+ * Keys and values of tokens that a draft does not see may be anything.  (A value that is not
+ * finite is multiplied by 0 at first; rows that it spoils are computed anew, which takes long,
+ * and not where out shares memory with q.)
  * Rows of q outside all sequences are not read, and of out not written.  A draft that
  * sees nothing gets 0.  A sequence whose starts descend, leave [0, N] or name more than 256
  * drafts is left out, a length outside [n, table_width * page_size] is brought into it

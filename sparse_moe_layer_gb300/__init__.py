@@ -664,9 +664,9 @@ def tree_attention(q, k_cache, v_cache, page_table, lengths, starts, scale: floa
     lengths[b] tokens (int32 [B]).  parents int32 [N]: the draft that each one follows, a smaller number in its
     sequence, or -1 for the context; None: each follows the one before.  A draft sees the context, its ancestors and
     itself; window > 0: of these only the nearest `window`, itself included, by its place in the tree (rotate drafts
-    by positions context + number of ancestors).  Keys that a draft does not see may be anything; values that any
-    draft of the sequence sees are to be finite (others of them are multiplied by 0).  Cache, page_table, sinks, status
-    as for `paged_attention`;
+    by positions context + number of ancestors).  Keys and values that a draft does not see may be anything (rows that
+    an infinite or NaN value of theirs would reach are computed anew, slowly; not where out is q).  Cache, page_table,
+    sinks, status as for `paged_attention`;
     status is also set by starts, lengths or parents that do not fit (that sequence, token or parent is left out).
     Rows outside all sequences are left as they are."""
     return (_calls or _entries()).tree_attention(q, k_cache, v_cache, page_table, lengths, starts, scale, parents, k_scale,

@@ -1102,6 +1102,11 @@ extern "C" moe_status moe_tree_attention(const moe_kv_cache* cache, const void* 
     p.scale_log2 = fmaxf(fabsf(scale) * 1.4426950408889634f, 1.17549435e-38f);
     p.q_sign = scale < 0.f ? 0x80008000u : 0u;
     p.status = status;
+    auto extent = [&](int64_t token, int64_t head) {
+        return ((long long)(N - 1) * token + (long long)(q_heads - 1) * head + cache->head_dim) * 2;
+    };
+    const uintptr_t q_at = reinterpret_cast<uintptr_t>(q), o_at = reinterpret_cast<uintptr_t>(out);
+    p.once = o_at < q_at + extent(q_token, q_head) && q_at < o_at + extent(out_token, out_head);
     CUtensorMap tmK, tmV;
     memset(&tmK, 0, sizeof(tmK));
     memset(&tmV, 0, sizeof(tmV));

@@ -167,6 +167,7 @@ struct TreeParams {
     int page_shift; // log2(page_size), -1 if none
     int fp16;       // q and out are fp16, not bf16
     int whole;      // items are not cut
+    int once;       // no row is computed anew (out shares memory with q)
     int box;        // tokens of a tensor-map copy, which lie on one page; 0: copies of 16 bytes by threads
     int runs;
     int4* cont;      // [runs] item that the run continues (sequence, key head, row tile, 1), or w = 0

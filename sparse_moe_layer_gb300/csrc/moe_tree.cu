@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kTreeJoinWarps * 32) tree_join_kernel(TreePara
 void tree_plan(int N, int B, int Hq, int Hkv, int D, int page_size, int window, int most, int sms, TreePlan* w) {
     const long long rows = ((long long)N * (Hq / Hkv) + B - 1) / B;  // of a sequence and key head, on average
     // two row tiles share a tile of keys and values (they fit to 128 dims): 64 drafts of 8 heads 236 us, one by one 239;
-    // 16 drafts of 16 heads of 128, e4m3, converted once instead of twice: 285, 446.  By the batch's average: one large
+    // 16 drafts of 16 heads of 128, e4m3, converted once instead of twice: 286, 446.  By the batch's average: one large
     // tree among many single drafts has one row tile at a time.
     w->tiles = D <= 128 && rows > kTreeRows ? 2 : 1;
     w->ctas = w->tiles == 2 || D > 64 ? sms : 2 * sms;

@@ -34,7 +34,7 @@
 // the same heads, 32 sequences of 2000 to 8192 tokens: 236 us, 635 TFLOP/s; two row tiles
 // are in turn at their exponentials, 3.1 thousand cycles for 128 tokens of 256 rows where the
 // exponential unit needs 1.0 (without softmax 143 us). 16 drafts of 64 heads on 4 of 128, 4
-// sequences of 100000 to 131072 tokens, e4m3: 285 us, 850 TFLOP/s, bound by conversion and
+// sequences of 100000 to 131072 tokens, e4m3: 286 us, 845 TFLOP/s, bound by conversion and
 // exponentials together (without softmax 245 us). A window of 128 over 256 sequences: 44.8
 // us, a tile's and a row end's latency after another. One short sequence: 7.0 us.
 // One row tile for all: 239 and 446 us for the two wide cases. Copies by threads, which pages
@@ -42,6 +42,13 @@
 //
 // e4m3 caches with few rows stay behind bf16 ones of the same shape (8 rows, 32 sequences of 8000
 // tokens, 8 key heads of 64: 122 us, bf16 92): a warp converts the codes of 32 tokens by itself.
+//
+// A value that is infinite or NaN makes NaN of its product with a weight of 0, so a draft's would
+// reach its siblings, and that of a window's first token those that have passed it.  A row's end
+// looks whether its sums are finite (windows 43.8 -> 44.3 us, one short sequence 6.8 -> 7.0); if some are
+// not, the CTA ends with tree_mend, which computes the rows anew that such a value spoilt. A look at every
+// value of the tiles that hold such tokens took 51 us for the windows, 304 for the e4m3 case, a second
+// run of the CTA with that look where it is needed, 45 and 296: registers of the common path.
 //
 // The list of items (sequence, key head, row tiles) and their token tiles is cut into
 // equal runs, one per CTA; an item cut by a run's border leaves fp32 parts that a second,
@@ -215,6 +222,180 @@ __device__ __forceinline__ uint32_t tile_at(int rows, int r, int c) {
     return (uint32_t)((c >> 3) * rows * 128 + r * 128 + ((c ^ r) & 7) * 16);
 }
 
+// Rows of the CTA's run whose sums are not finite because of a value that other rows see and they do not (a draft of
+// another branch, a token before their window): computed anew, a warp each, in fp32, over what they see.  All of the CTA's
+// threads, seldom, and no faster than it has to be (one such draft in each of 64 sequences of 8000 tokens, 4 drafts of 8
+// heads: 10 ms for 0.19; a bad value that all rows see: 0.22).
+template <int KV, int TT, int TILES>
+static __device__ __noinline__ void tree_mend(const TreeParams& p, const TreeWork* work, bool whole) {
+    constexpr bool E4M3 = KV == kKvE4m3;
+    constexpr int ROWS = TILES * kTreeRows;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int group = 2;  // lanes that have a token's dims, 8 each
+    while (group * 8 < p.D) group *= 2;
+    const int groups = 32 / group, ch = lane % group;
+    const bool in = ch * 8 < p.D;
+    const bool qf16 = E4M3 ? p.fp16 : KV == kKvFp16;
+    TreeWalk walk;
+    TreeSeg g;
+    walk.w = *work;
+    if (walk.w.rem > 0) walk.s = tree_seq<TT, TILES>(p, walk.w.b);
+    auto wide = [](uint16_t v, bool f16) { return f16 ? unpack2<true>(v).x : unpack2<false>(v).x; };
+#pragma unroll 1
+    while (tree_next<TT, TILES>(p, whole, walk, g)) {
+        const TreeSeq& s = g.s;
+        const bool done = g.starts && g.ends;
+        const int rows = min(ROWS, s.n * p.group - g.rt * ROWS);
+        const int t_end = min(s.start + (g.tile + g.n) * TT, s.len), t_begin = max(s.start + g.tile * TT, s.lo);
+        // tokens from here to the context's end are seen by all rows
+        const int edge = p.window > 0 ? s.ctx + s.n - p.window : 0;
+        float* part = p.partial + ((long long)blockIdx.x * 2 + (g.starts ? 1 : 0)) * (ROWS * (p.D + 2));
+#pragma unroll 1
+        for (int row = warp; row < rows; row += warps) {
+            const int at = g.rt * ROWS + row, draft = tree_draft(p, at), head = g.h * p.group + at - draft * p.group;
+            uint16_t* dst = p.out + (s.first + draft) * p.o_token + (long long)head * p.o_head;
+            auto sum = [&](int d) { return part + 2 * ROWS + ((d / 4) * ROWS + row) * 4 + d % 4; };
+            bool odd = false;
+            for (int d = lane; d < p.D; d += 32) odd = odd || !isfinite(done ? wide(dst[d], qf16) : *sum(d));
+            if (!__any_sync(kAllLanes, odd)) continue;
+            // the draft's place; ancestors, and itself: 32 of them a lane
+            uint32_t path = 0;
+            int depth = -1;
+#pragma unroll 1
+            for (int a = draft; a >= 0;) {
+                ++depth;
+                if (a >> 5 == lane && (p.window <= 0 || depth < p.window)) path |= 1u << (a & 31);
+                const int up = p.parents ? __ldg(p.parents + s.first + a) : a - 1;
+                a = up < a && up >= -1 ? up : -1;
+            }
+            const int since = p.window > 0 ? s.ctx + depth - p.window + 1 : 0;
+            // a lane has a token: its page (-1: none, or out of range), whether the row sees it
+            auto page = [&](int t) {
+                const int pid = t < t_end ? __ldg(p.table + (long long)g.b * p.table_ld + t / p.page_size) : -1;
+                return (uint32_t)pid < (uint32_t)p.num_pages ? pid : -1;
+            };
+            auto sees = [&](int t) {
+                const int o = t - s.ctx;
+                const uint32_t word = __shfl_sync(kAllLanes, path, (o >> 5) & 31);
+                return o < 0 ? t >= since : o < kMaxDrafts && ((word >> (o & 31)) & 1u);
+            };
+            auto scale = [&](const float* of, int pid, int t) {
+                if constexpr (!E4M3) return 1.f;
+                return __ldg(of + pid * p.cache.s_page + g.h * p.cache.s_head + t % p.page_size * p.cache.s_token);
+            };
+            auto k_at = [&](int pid, int t) {
+                return pid * p.cache.k_page + g.h * p.cache.k_head + t % p.page_size * p.cache.k_token;
+            };
+            auto v_at = [&](int pid, int t) {
+                return pid * p.cache.v_page + g.h * p.cache.v_head + t % p.page_size * p.cache.v_token;
+            };
+            auto load8 = [&](const void* of, long long i, float (&y)[8]) {
+                uint32_t u[4];
+                if constexpr (E4M3) {
+                    const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(of) + i);
+                    u[0] = e4m3x2_to_f16x2(c.x), u[1] = e4m3x2_to_f16x2(c.x >> 16);
+                    u[2] = e4m3x2_to_f16x2(c.y), u[3] = e4m3x2_to_f16x2(c.y >> 16);
+                } else {
+                    const uint4 c = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(of) + i);
+                    u[0] = c.x, u[1] = c.y, u[2] = c.z, u[3] = c.w;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 x = unpack2<KV != kKvBf16>(u[j]);
+                    y[2 * j] = x.x, y[2 * j + 1] = x.y;
+                }
+            };
+            odd = false;
+#pragma unroll 1
+            for (int t0 = t_begin; t0 < t_end; t0 += 32) {
+                if (t0 >= edge && t0 + 32 <= s.ctx) {  // (all are seen)
+                    t0 += (s.ctx - t0) / 32 * 32 - 32;
+                    continue;
+                }
+                const int t = t0 + lane, pid = page(t);
+                if (sees(t) || pid < 0) continue;
+                odd = odd || !isfinite(scale(p.cache.v_scale, pid, t));
+#pragma unroll 1
+                for (int d = 0; d < p.D; d += 8) {
+                    float y[8];
+                    load8(p.cache.v, v_at(pid, t) + d, y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) odd = odd || !isfinite(y[j]);
+                }
+            }
+            if (!__any_sync(kAllLanes, odd)) continue;
+            // over what it sees, 32 tokens at a time: groups of lanes take a token's key, then its value, 8 dims a lane
+            const float factor = p.q_sign ? -p.scale_log2 : p.scale_log2;
+            float m = -INFINITY, l = 0.f, x[8] = {}, acc[8] = {};  // l: the lane's part
+            if (in) {
+                const uint4 c = *reinterpret_cast<const uint4*>(p.q + (s.first + draft) * p.q_token +
+                                                                (long long)head * p.q_head + 8 * ch);
+                const uint32_t u[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 y = qf16 ? unpack2<true>(u[j]) : unpack2<false>(u[j]);
+                    x[2 * j] = y.x, x[2 * j + 1] = y.y;
+                }
+            }
+#pragma unroll 1
+            for (int t0 = t_begin; t0 < t_end; t0 += 32) {
+                const int t = t0 + lane, pid = page(t);
+                const bool seen = sees(t) && pid >= 0;
+                const uint32_t any = __ballot_sync(kAllLanes, seen);
+                const long long k = seen ? k_at(pid, t) : 0, v = seen ? v_at(pid, t) : 0;
+                float y = 0.f;
+#pragma unroll 4
+                for (int i = 0; i < group; ++i) {
+                    float z[8] = {}, r = 0.f;
+                    const long long at = __shfl_sync(kAllLanes, k, i * groups + lane / group);
+                    if (in) load8(p.cache.k, at + 8 * ch, z);  // (of the first token where none is seen)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) r = fmaf(x[j], z[j], r);
+                    for (int o = group / 2; o; o >>= 1) r += __shfl_xor_sync(kAllLanes, r, o);
+                    r = __shfl_sync(kAllLanes, r, lane % groups * group);
+                    if (lane / groups == i) y = r;
+                }
+                y = seen ? y * (scale(p.cache.k_scale, pid, t) * factor) : -INFINITY;
+                float n = y;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) n = fmaxf(n, __shfl_xor_sync(kAllLanes, n, o));
+                n = fmaxf(m, n);
+                const float f = m == -INFINITY ? 0.f : ex2_approx(m - n), e = y == -INFINITY ? 0.f : ex2_approx(y - n);
+                const float w = seen ? e * scale(p.cache.v_scale, pid, t) : 0.f;
+                m = n;
+                l = l * f + e;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[j] *= f;
+#pragma unroll 4
+                for (int i = 0; i < group; ++i) {
+                    const int from = i * groups + lane / group;
+                    float z[8] = {};
+                    const long long at = __shfl_sync(kAllLanes, v, from);
+                    const float h = __shfl_sync(kAllLanes, w, from);
+                    if (in) load8(p.cache.v, at + 8 * ch, z);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[j] = (any >> from) & 1u ? fmaf(h, z[j], acc[j]) : acc[j];
+                }
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(kAllLanes, l, o);
+            for (int o = 16; o >= group; o >>= 1)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[j] += __shfl_xor_sync(kAllLanes, acc[j], o);
+            const float fw = done ? final_weight(p.sinks, head, m, l) : 1.f;
+            if (!done && lane == 0) reinterpret_cast<float2*>(part)[row] = make_float2(m, l);
+            if (in && lane < group)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (done)
+                        dst[8 * ch + j] = (uint16_t)(qf16 ? pack2<true>(acc[j] * fw, 0.f) : pack2<false>(acc[j] * fw, 0.f));
+                    else
+                        *sum(8 * ch + j) = acc[j];
+                }
+        }
+    }
+}
+
 template <int DP, int KV, int TILES, bool TMA>
 __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<DP, KV, TILES, TMA>::CTAS)
     tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -229,6 +410,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
         raw_full_bar[NR], raw_empty_bar[NR], read_bar[TILES], x_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag, s_sum[3];  // (all runs': units, items, tiles of the longest)
+    __shared__ int s_odd;                 // a row's sums were not finite
     __shared__ TreeWork s_work;
     __shared__ float s_qf[TILES][kTreeRows];
     __shared__ int16_t s_up[TILES][kMaxDrafts];  // parents
@@ -258,7 +440,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
         }
         mbar_init(smem_u32(&end_bar), 1);
         mbar_init(smem_u32(&x_bar), kTreeRows);
-        abort_flag = 0;
+        abort_flag = s_odd = 0;
         fence_barrier_init();
     }
     if (warp == C::MMA_WARP) tmem_alloc(smem_u32(&tmem_slot), C::COLS);
@@ -1246,6 +1428,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
             if (!ok) break;
             tc_fence_after();
             auto pack = [&](float a, float b) { return qf16 ? pack2<true>(a, b) : pack2<false>(a, b); };
+            uint64_t odd = 0;  // NaN where a sum is not finite
             if (rep == 1) {
                 if (warp_act) {
                     const float fw = !done        ? 1.f
@@ -1259,6 +1442,9 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                         float v[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(x[i]) * fw;
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2)
+                            odd = f32x2_fma(f32x2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), 0, odd);
                         if (act && done) {
                             *reinterpret_cast<uint4*>(dst + d) =
                                 make_uint4(pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7]));
@@ -1317,6 +1503,8 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                             add_scaled(u, 1.f, room[e * kTreeRows + k * (fold + 1) + lr], f[k]);
                             add_scaled(v, 1.f, room[(e + 1) * kTreeRows + k * (fold + 1) + lr], f[k]);
                         }
+                        odd = f32x2_fma(f32x2(u.x, u.y), 0, f32x2_fma(f32x2(u.z, u.w), 0, odd));
+                        odd = f32x2_fma(f32x2(v.x, v.y), 0, f32x2_fma(f32x2(v.z, v.w), 0, odd));
                         u = make_float4(u.x * fw, u.y * fw, u.z * fw, u.w * fw);
                         v = make_float4(v.x * fw, v.y * fw, v.z * fw, v.w * fw);
                         if (done) {
@@ -1331,6 +1519,8 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
                 come();
                 to_meet = true;
             }
+            const float2 o = f32x2_get(odd);
+            if (act && o.x + o.y != 0.f) s_odd = 1;
             tc_fence_before();
         }
     }
@@ -1340,6 +1530,7 @@ __global__ void __launch_bounds__(TreeCfg<DP, KV, TILES, TMA>::THREADS, TreeCfg<
         tc_fence_after();
         tmem_dealloc(tmem, C::COLS);
     }
+    if (s_odd && !abort_flag && !p.once) tree_mend<KV, TT, TILES>(p, &s_work, whole);
 }
 
 template <int DP, int KV, int TILES, bool TMA>
